@@ -39,7 +39,9 @@ EXPORTS = ["spec_workspace_bytes", "spec_draft_workspace_bytes", "spec_verify_gr
            "spec_draft_confidence", "spec_prefix_stats", "spec_restore_rows",
            "spec_result_string", "spec_last_cuda_error", "spec_abi_version",
            "spec_step_state_bytes", "spec_step_init", "spec_step_update", "spec_step_query",
-           "spec_step_cost_sps", "spec_step_cost_additive"]
+           "spec_step_cost_sps", "spec_step_cost_additive",
+           "spec_cache_append", "spec_cache_read", "spec_cache_workspace_bytes",
+           "spec_cache_attend", "spec_cache_weights", "spec_cache_evict"]
 
 
 class SpecError(RuntimeError):
@@ -125,6 +127,16 @@ def load_library(path: Optional[str] = None) -> C.CDLL:
     for f in ["spec_verify_greedy", "spec_verify_greedy_noalloc", "spec_verify_relaxed_topk",
               "spec_verify_greedy_margin", "spec_verify_greedy_active", "spec_verify_sample",
               "spec_draft_confidence", "spec_prefix_stats", "spec_abi_version"]:
+        getattr(L, f).restype = C.c_int
+    L.spec_cache_append.argtypes = [vp, vp, vp]
+    L.spec_cache_read.argtypes = [vp, vp, vp]
+    L.spec_cache_workspace_bytes.argtypes = [i32] * 6
+    L.spec_cache_workspace_bytes.restype = C.c_size_t
+    L.spec_cache_attend.argtypes = [vp, vp, vp, vp, vp, C.c_size_t, vp]
+    L.spec_cache_weights.argtypes = [vp, vp, vp, vp, vp]
+    L.spec_cache_evict.argtypes = [vp, vp, vp]
+    for f in ["spec_cache_append", "spec_cache_read", "spec_cache_attend", "spec_cache_weights",
+              "spec_cache_evict"]:
         getattr(L, f).restype = C.c_int
     L.spec_step_state_bytes.restype = C.c_size_t
     L.spec_step_state_bytes.argtypes = []

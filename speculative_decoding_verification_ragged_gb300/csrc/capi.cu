@@ -7,6 +7,7 @@
 
 #include "common.cuh"
 #include "internal.h"
+#include "spec_cache.h"
 
 using namespace specv;
 
@@ -141,6 +142,107 @@ int noalloc_scratch(void **ptr)
     const cudaError_t e = cudaGetSymbolAddress(&p, g_noalloc_scratch);
     if (e != cudaSuccess) return cuda_fail(e);
     *ptr = p;
+    return SPEC_OK;
+}
+
+// ---- the 4-bit paged cache ----
+
+int check_cache(const spec_cache *c, CacheView &v)
+{
+    if (!c || !c->pages || !c->page_table) return SPEC_ERR_INVALID_ARG;
+    if (c->n_pages < 1 || c->n_pages > INT32_MAX || c->H < 1 || c->B < 1 || c->max_pages < 1)
+        return SPEC_ERR_INVALID_ARG;
+    if (c->page_tokens < SPEC_CACHE_BLOCK_TOKENS || c->page_tokens % SPEC_CACHE_BLOCK_TOKENS)
+        return SPEC_ERR_INVALID_ARG;
+    if (reinterpret_cast<uintptr_t>(c->pages) % 16) return SPEC_ERR_INVALID_ARG;
+    if (c->D != 64 && c->D != 128 && c->D != 256) return SPEC_ERR_UNSUPPORTED;
+    // slots are 32-bit; kv heads and requests are the y and z of the grids
+    if (c->page_tokens > 65536 || c->H > 65535 || c->B > 65535) return SPEC_ERR_UNSUPPORTED;
+    if (static_cast<int64_t>(c->max_pages) * c->page_tokens > (1 << 30)) return SPEC_ERR_UNSUPPORTED;
+    v.pages = static_cast<uint8_t *>(c->pages);
+    v.n_pages = c->n_pages;
+    v.page_tokens = c->page_tokens;
+    v.H = c->H;
+    v.D = c->D;
+    v.k_scale = c->k_scale;
+    v.v_scale = c->v_scale;
+    v.B = c->B;
+    v.max_pages = c->max_pages;
+    v.page_table = c->page_table;
+    return SPEC_OK;
+}
+
+// whether every (row, head) of a tensor starts on a 16-byte boundary
+bool rows_aligned(const void *p, int64_t row, int64_t head, size_t elt)
+{
+    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && (row * static_cast<int64_t>(elt)) % 16 == 0 &&
+           (head * static_cast<int64_t>(elt)) % 16 == 0;
+}
+
+int run_cache_rows(const spec_cache *cache, const spec_cache_rows *r, bool append, spec_stream stream)
+{
+    CacheView c;
+    const int rc = check_cache(cache, c);
+    if (rc != SPEC_OK) return rc;
+    if (!r || !r->k || !r->v || !r->cu_rows || !r->start) return SPEC_ERR_INVALID_ARG;
+    if (r->dtype != SPEC_F32 && r->dtype != SPEC_BF16) return SPEC_ERR_UNSUPPORTED;
+    if (r->R_cap < 1 || r->max_rows < 1) return SPEC_ERR_INVALID_ARG;
+    if (r->max_rows > (1 << 30)) return SPEC_ERR_UNSUPPORTED;
+    const size_t elt = elt_bytes(r->dtype);
+    if (reinterpret_cast<uintptr_t>(r->k) % elt || reinterpret_cast<uintptr_t>(r->v) % elt)
+        return SPEC_ERR_INVALID_ARG;
+    CacheRows p;
+    p.k = r->k;
+    p.v = r->v;
+    p.k_row = r->k_row;
+    p.k_head = r->k_head;
+    p.v_row = r->v_row;
+    p.v_head = r->v_head;
+    p.R_cap = r->R_cap;
+    p.max_rows = r->max_rows;
+    p.cu_rows = r->cu_rows;
+    p.start = r->start;
+    p.score = append ? r->score : nullptr;
+    p.slot_pos = append ? r->slot_pos : nullptr;
+    p.pos0 = r->pos0;
+    p.status = r->status;
+    p.k_aligned = rows_aligned(r->k, r->k_row, r->k_head, elt);
+    p.v_aligned = rows_aligned(r->v, r->v_row, r->v_head, elt);
+    const cudaError_t e = launch_cache_rows(c, p, r->dtype, append, reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? SPEC_OK : cuda_fail(e);
+}
+
+int check_attention(const spec_cache *cache, const spec_attention *a, CacheView &c, AttnParams &p)
+{
+    const int rc = check_cache(cache, c);
+    if (rc != SPEC_OK) return rc;
+    if (!a || !a->q || !a->cu_rows || !a->len) return SPEC_ERR_INVALID_ARG;
+    if (a->dtype != SPEC_F32 && a->dtype != SPEC_BF16) return SPEC_ERR_UNSUPPORTED;
+    if (a->Hq < 1 || a->Hq % c.H || a->R_cap < 1 || a->k_max < 0 || a->window < 0 || a->prefix < 0)
+        return SPEC_ERR_INVALID_ARG;
+    if (a->k_max > 31 || a->Hq > 65535) return SPEC_ERR_UNSUPPORTED;
+    if (!(a->scale - a->scale == 0.f) || !(a->cap >= 0.f) || !(a->cap - a->cap == 0.f))
+        return SPEC_ERR_INVALID_ARG;
+    const int64_t room = static_cast<int64_t>(c.max_pages) * c.page_tokens;
+    if (a->max_len < 0 || a->max_len > room) return SPEC_ERR_INVALID_ARG;
+    if (reinterpret_cast<uintptr_t>(a->q) % elt_bytes(a->dtype)) return SPEC_ERR_INVALID_ARG;
+    std::memset(&p, 0, sizeof p);
+    p.q = a->q;
+    p.q_row = a->q_row;
+    p.q_head = a->q_head;
+    p.Hq = a->Hq;
+    p.R_cap = a->R_cap;
+    p.k_max = a->k_max;
+    p.cu_rows = a->cu_rows;
+    p.len = a->len;
+    p.max_len = a->max_len ? a->max_len : static_cast<int32_t>(room);
+    p.scale = a->scale;
+    p.cap = a->cap;
+    p.slopes = a->slopes;
+    p.window = a->window;
+    p.prefix = a->prefix;
+    p.slot_pos = a->slot_pos;
+    p.status = a->status;
     return SPEC_OK;
 }
 
@@ -366,6 +468,83 @@ int spec_restore_rows(const void *compact, int64_t compact_ld, int32_t R_cap,
     const cudaError_t e = launch_restore_rows(compact, compact_ld, R_cap, cu_rows, B, k_max,
                                               row_bytes, out, out_ld, status,
                                               reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? SPEC_OK : cuda_fail(e);
+}
+
+int spec_cache_append(const spec_cache *cache, const spec_cache_rows *rows, spec_stream stream)
+{
+    return run_cache_rows(cache, rows, true, stream);
+}
+
+int spec_cache_read(const spec_cache *cache, const spec_cache_rows *rows, spec_stream stream)
+{
+    return run_cache_rows(cache, rows, false, stream);
+}
+
+size_t spec_cache_workspace_bytes(int32_t B, int32_t k_max, int32_t Hq, int32_t H, int32_t D,
+                                  int32_t max_len)
+{
+    if (B < 1 || k_max < 0 || k_max > 31 || H < 1 || Hq < H || Hq % H || max_len < 1) return 0;
+    if (D != 64 && D != 128 && D != 256) return 0;
+    return 256;
+}
+
+int spec_cache_attend(const spec_cache *cache, const spec_attention *attn, void *out, float *lse,
+                      void *workspace, size_t workspace_bytes, spec_stream stream)
+{
+    CacheView c;
+    AttnParams p;
+    const int rc = check_attention(cache, attn, c, p);
+    if (rc != SPEC_OK) return rc;
+    if (!out) return SPEC_ERR_INVALID_ARG;
+    if (reinterpret_cast<uintptr_t>(out) % elt_bytes(attn->dtype)) return SPEC_ERR_INVALID_ARG;
+    if (!workspace || workspace_bytes < spec_cache_workspace_bytes(c.B, p.k_max, p.Hq, c.H, c.D, p.max_len))
+        return SPEC_ERR_WORKSPACE;
+    p.out = out;
+    p.lse = lse;
+    p.ws = workspace;
+    const cudaError_t e = launch_cache_attend(c, p, attn->dtype, reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? SPEC_OK : cuda_fail(e);
+}
+
+int spec_cache_weights(const spec_cache *cache, const spec_attention *attn, const float *lse,
+                       float *score, spec_stream stream)
+{
+    CacheView c;
+    AttnParams p;
+    const int rc = check_attention(cache, attn, c, p);
+    if (rc != SPEC_OK) return rc;
+    if (!lse || !score) return SPEC_ERR_INVALID_ARG;
+    p.lse = const_cast<float *>(lse);
+    p.score = score;
+    const cudaError_t e = launch_cache_weights(c, p, attn->dtype, reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? SPEC_OK : cuda_fail(e);
+}
+
+int spec_cache_evict(const spec_cache *cache, const spec_eviction *ev, spec_stream stream)
+{
+    CacheView c;
+    const int rc = check_cache(cache, c);
+    if (rc != SPEC_OK) return rc;
+    if (!ev || !ev->score || !ev->len || !ev->dst_table || !ev->kept || !ev->new_len)
+        return SPEC_ERR_INVALID_ARG;
+    if (ev->budget < 1 || ev->recent < 0 || ev->recent > ev->budget || ev->dst_pages < 1)
+        return SPEC_ERR_INVALID_ARG;
+    const int64_t room = static_cast<int64_t>(c.max_pages) * c.page_tokens;
+    const int64_t most = ev->budget < room ? ev->budget : room;
+    if (static_cast<int64_t>(ev->dst_pages) * c.page_tokens < most) return SPEC_ERR_INVALID_ARG;
+    EvictParams p;
+    p.score = ev->score;
+    p.slot_pos = ev->slot_pos;
+    p.len = ev->len;
+    p.budget = ev->budget;
+    p.recent = ev->recent;
+    p.dst_table = ev->dst_table;
+    p.dst_pages = ev->dst_pages;
+    p.kept = ev->kept;
+    p.new_len = ev->new_len;
+    p.status = ev->status;
+    const cudaError_t e = launch_cache_evict(c, p, reinterpret_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? SPEC_OK : cuda_fail(e);
 }
 

@@ -86,6 +86,67 @@ struct AllocParams {
     uint32_t *status;
 };
 
+// ---- the 4-bit paged cache (include/spec_cache.h) ----
+
+// The cache as a batch of requests sees it (passed by value to the kernels).
+struct CacheView {
+    uint8_t *pages;
+    int64_t n_pages;
+    int32_t page_tokens, H, D;
+    const float *k_scale, *v_scale;
+    int32_t B, max_pages;
+    const int32_t *page_table;
+};
+
+// Rows entering (append) or leaving (read) the cache.
+struct CacheRows {
+    void *k, *v;
+    int64_t k_row, k_head, v_row, v_head;
+    int32_t R_cap, max_rows;
+    const int32_t *cu_rows, *start;
+    float *score;
+    int32_t *slot_pos;
+    const int32_t *pos0;
+    uint32_t *status;
+    bool k_aligned, v_aligned;   // every head's first channel lies on a 16-byte boundary
+};
+
+struct AttnParams {
+    const void *q;
+    int64_t q_row, q_head;
+    int32_t Hq, R_cap, k_max;
+    const int32_t *cu_rows, *len;
+    int32_t max_len;
+    float scale, cap;
+    const float *slopes;
+    int32_t window, prefix;
+    const int32_t *slot_pos;
+    uint32_t *status;
+    void *out;
+    float *lse;                  // attend: written; weights: read
+    float *score;                // weights only
+    void *ws;
+};
+
+struct EvictParams {
+    float *score;
+    int32_t *slot_pos;
+    const int32_t *len;
+    int32_t budget, recent;
+    const int32_t *dst_table;
+    int32_t dst_pages;
+    int32_t *kept, *new_len;
+    uint32_t *status;
+};
+
+cudaError_t launch_cache_rows(const CacheView &c, const CacheRows &r, int dtype, bool append,
+                              cudaStream_t stream);
+cudaError_t launch_cache_attend(const CacheView &c, const AttnParams &p, int dtype,
+                                cudaStream_t stream);
+cudaError_t launch_cache_weights(const CacheView &c, const AttnParams &p, int dtype,
+                                 cudaStream_t stream);
+cudaError_t launch_cache_evict(const CacheView &c, const EvictParams &p, cudaStream_t stream);
+
 // Host launchers (return cudaError_t of the launch).
 cudaError_t launch_verify(int mode, int dtype, const VerifyParams &p, cudaStream_t stream);
 // the row path of relaxed top-K (bf16, large batches; called by launch_verify)
