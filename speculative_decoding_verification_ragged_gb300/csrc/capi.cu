@@ -486,7 +486,7 @@ size_t spec_cache_workspace_bytes(int32_t B, int32_t k_max, int32_t Hq, int32_t 
 {
     if (B < 1 || k_max < 0 || k_max > 31 || H < 1 || Hq < H || Hq % H || max_len < 1) return 0;
     if (D != 64 && D != 128 && D != 256) return 0;
-    return 256;
+    return cache_attend_workspace(B, k_max, Hq, H, D, max_len);
 }
 
 int spec_cache_attend(const spec_cache *cache, const spec_attention *attn, void *out, float *lse,

@@ -145,6 +145,8 @@ cudaError_t launch_cache_attend(const CacheView &c, const AttnParams &p, int dty
                                 cudaStream_t stream);
 cudaError_t launch_cache_weights(const CacheView &c, const AttnParams &p, int dtype,
                                  cudaStream_t stream);
+// workspace bytes of the attention (for queries of either type)
+size_t cache_attend_workspace(int B, int k_max, int Hq, int H, int D, int max_len);
 cudaError_t launch_cache_evict(const CacheView &c, const EvictParams &p, cudaStream_t stream);
 
 // Host launchers (return cudaError_t of the launch).
