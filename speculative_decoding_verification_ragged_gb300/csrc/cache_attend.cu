@@ -25,15 +25,12 @@
 // of weights in fp32 before any rounding.
 #include <climits>
 
-#include "cache.cuh"
-#include "tensor.cuh"
+#include "attend.cuh"
 
 namespace specv {
 
 namespace {
 
-constexpr int kAttnThreads = 128;
-constexpr int kTile = 128;                 // tokens of a tile: 4 blocks
 constexpr float kUnset = -1e30f;           // reference of a column that has seen nothing yet
 constexpr float kHeadroom = 11.f;          // P = 2^(x + 11) ...
 constexpr float kExceed = 15.f;            // ... stays below 2^15
@@ -74,94 +71,6 @@ template <typename T, int D_, int NT_> struct Attn {
     static_assert(D != 64 || NT * D * 4 <= STAGES * STAGE, "the epilogue's exchange fits the stages");
 };
 
-// What a CTA works on.
-struct Job {
-    int b, h, lo, n, len;       // request, kv head, first packed row, rows, tokens
-    int col0, ncols;            // first column of the tile, real columns
-    int ntiles, np, f0;         // tiles to visit: 0 .. np - 1, then f0, f0 + 1, ...
-};
-
-__device__ __forceinline__ int tile_of(const Job &w, int i) { return i < w.np ? i : w.f0 + i - w.np; }
-
-__device__ __forceinline__ int slot_position(const CacheView &c, const AttnParams &p, int b, int slot)
-{
-    if (!p.slot_pos) return slot;
-    const int page = page_of(c, b, slot);
-    return page < 0 ? 0 : __ldg(p.slot_pos + static_cast<int64_t>(page) * c.page_tokens + slot % c.page_tokens);
-}
-
-// Copy the 4 blocks of a tile into a stage; lanes 0..3 of one warp, a block
-// each.  nv: the tokens of each block that exist (0 for a bad page: its bytes
-// are not fetched, and what the stage holds there is masked).
-template <int D>
-__device__ __forceinline__ void load_tile(const CacheView &c, const Job &w, int tile, int page, uint8_t *stage,
-                                          uint64_t *full, int *nv, uint32_t *status)
-{
-    const int lane = threadIdx.x & 31;
-    const int slot0 = tile * kTile + lane * kTok;
-    int n = lane < 4 ? min(max(w.len - slot0, 0), kTok) : 0;
-    if (n > 0 && page < 0) {
-        set_status(status, SPEC_STATUS_BAD_PAGE);
-        n = 0;
-    }
-    const uint32_t have = __ballot_sync(0xFFFFFFFFu, n > 0);
-    if (lane < 4) nv[lane] = n;
-    __syncwarp();
-    if (lane == 0) mbar_arrive_expect_tx(full, __popc(have) * block_bytes(D));
-    __syncwarp();
-    if (n > 0)
-        bulk_g2s(stage + lane * block_bytes(D), block_at(c, page, w.h, slot0 % c.page_tokens / kTok), block_bytes(D), full);
-}
-
-__device__ __forceinline__ int tile_page(const CacheView &c, const Job &w, int tile)
-{
-    const int lane = threadIdx.x & 31, slot0 = tile * kTile + lane * kTok;
-    return lane < 4 && slot0 < w.len ? page_of(c, w.b, slot0) : -1;
-}
-
-__device__ __forceinline__ uint32_t h2_mul(uint32_t a, uint32_t b)
-{
-    uint32_t r;
-    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
-
-// 4 bytes of codes -> 4 f16x2
-__device__ __forceinline__ void decode4(uint32_t w, uint32_t *r)
-{
-    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\tmov.b32 {b0, b1, b2, b3}, %4;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %0, b0;\n\tcvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %2, b2;\n\tcvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-        : "r"(w));
-}
-
-// The keys of this thread's token (block = warp, token = lane) -> D/2 columns
-template <int D>
-__device__ __forceinline__ void decode_keys(const uint8_t *blk, uint32_t taddr)
-{
-    const int lane = threadIdx.x & 31;
-    constexpr int G = D / 16;
-    uint32_t sc[G / 4];
-#pragma unroll
-    for (int i = 0; i < G / 4; ++i)
-        sc[i] = *reinterpret_cast<const uint32_t *>(blk + k_scale_at(D) + lane * G + 4 * i);
-#pragma unroll
-    for (int ch = 0; ch < D / 32; ++ch) {
-        const uint4 v = *reinterpret_cast<const uint4 *>(blk + ch * 512 + lane * 16);
-        const uint32_t s2 = e4m3x2(sc[ch / 2] >> (ch % 2 * 16));
-        const uint32_t s_lo = __byte_perm(s2, 0, 0x1010), s_hi = __byte_perm(s2, 0, 0x3232);
-        uint32_t r[16];
-        decode4(v.x, r);
-        decode4(v.y, r + 4);
-        decode4(v.z, r + 8);
-        decode4(v.w, r + 12);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) r[i] = h2_mul(r[i], i < 8 ? s_lo : s_hi);
-        tmem_st16(taddr + ch * 16, r);
-    }
-}
-
 // The values of one channel over the 32 tokens of a block -> 16 columns.  Tokens
 // past nv get scale 0 (their bytes can be anything, NaN scales included).
 template <int D, bool WIDE>
@@ -191,78 +100,6 @@ __device__ __forceinline__ void decode_values(const uint8_t *blk, int d, int nv,
         if (WIDE) r[i] = (r[i] >> 3 & 0x0FFF0FFFu) | (r[i] & 0x80008000u);
     }
     tmem_st16(taddr, r);
-}
-
-__device__ __forceinline__ uint32_t pack_h2(float lo, float hi)
-{
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-
-// Query columns as the K-major B operand, scaled by the power of two 2^e (and
-// the sign of the softmax scale) that brings the tile's largest to 2^14; the
-// second f16 term behind the first for fp32.  Returns 2^-e.
-template <typename T, int D, int NT, int PIECES>
-__device__ float stage_queries(const AttnParams &p, const Job &w, int group, uint8_t *qs, float *red)
-{
-    const int tid = threadIdx.x;
-    constexpr int PER = D / 8;                        // 8-channel groups of a column
-    float big = 0.f;
-    for (int i = tid; i < w.ncols * PER; i += kAttnThreads) {
-        const int col = w.col0 + i / PER;
-        const T *src = static_cast<const T *>(p.q) + (w.lo + col / group) * p.q_row +
-                       (w.h * group + col % group) * p.q_head + i % PER * 8;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) big = fmaxf(big, fabsf(to_f32<T>(src[k])));
-    }
-    big = warp_max_f32(big);
-    if ((tid & 31) == 0) red[tid >> 5] = big;
-    __syncthreads();
-    big = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-    // exponent arithmetic on the bits; a tile of zeros (or subnormals) stays as it is
-    const int ex = static_cast<int>(__float_as_uint(big) >> 23) - 127;
-    const int e = ex > -127 ? min(max(13 - ex, -120), 100) : 0;
-    const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-    const float f = p.scale == 0.f ? 0.f : (p.scale < 0.f ? -up : up);
-    for (int i = tid; i < NT * PER; i += kAttnThreads) {
-        const int c = i / PER, k8 = i % PER, col = w.col0 + c;
-        float x[8] = {};
-        if (c < w.ncols) {
-            const T *src = static_cast<const T *>(p.q) + (w.lo + col / group) * p.q_row +
-                           (w.h * group + col % group) * p.q_head + k8 * 8;
-#pragma unroll
-            for (int k = 0; k < 8; ++k) x[k] = to_f32<T>(src[k]) * f;
-        }
-        uint8_t *dst = qs + k8 * (NT * 16) + c / 8 * 128 + c % 8 * 16;
-        uint32_t hi[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) hi[k] = pack_h2(x[2 * k], x[2 * k + 1]);
-        *reinterpret_cast<uint4 *>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        if (PIECES == 2) {
-            uint32_t l[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const float2 y = h2_float2(hi[k]);
-                l[k] = pack_h2(x[2 * k] - y.x, x[2 * k + 1] - y.y);
-            }
-            *reinterpret_cast<uint4 *>(dst + NT * D * 2) = make_uint4(l[0], l[1], l[2], l[3]);
-        }
-    }
-    return __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-}
-
-// S^T = K Q^T over all channels (one thread issues)
-template <int D, int NT, int PIECES>
-__device__ __forceinline__ void issue_scores(uint32_t s_addr, uint32_t a_addr, const uint8_t *qs)
-{
-    const uint32_t q = smem_addr(qs);
-#pragma unroll
-    for (int pc = 0; pc < PIECES; ++pc)
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k)
-            mma_f16(s_addr, a_addr + k * 8, smem_desc(q + pc * NT * D * 2 + k * 2 * NT * 16, NT * 16, 128),
-                    mma_f16_desc(NT, false), pc > 0 || k > 0);
 }
 
 // O^T += V^T P^T over the tile's tokens, `pieces` terms of P (one thread issues)
@@ -301,19 +138,6 @@ __device__ __forceinline__ uint32_t pack_bf2(float lo, float hi)
     uint32_t r;
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
-}
-
-// the score in log2 units of a raw product, with cap and distance bias
-__device__ __forceinline__ float option_score(float cap, float twice, float v, float mult, float slope2, int dist)
-{
-    float y = v * mult;
-    if (cap > 0.f) {
-        // cap tanh(s / cap) = cap - 2 cap / (1 + 2^(2 y / cap))  (y in log2 units)
-        const float c2 = cap * kLog2e;
-        const float t = 1.f + ex2(fminf(twice * y, 126.f));
-        y = c2 - __fdividef(2.f * c2, t);
-    }
-    return y - slope2 * static_cast<float>(dist);
 }
 
 // Sum over the 32 lanes of each of 16 values: lane l gets the sum of value l/2
@@ -365,16 +189,7 @@ attend_kernel(const CacheView c, const AttnParams p, const Split sp)
         if (tid == 0) set_status(p.status, SPEC_STATUS_BAD_LENGTH);
         w.len = 0;
     }
-    w.ntiles = (w.len + kTile - 1) / kTile;
-    w.np = 0;
-    w.f0 = 0;
-    if (p.window > 0 && !p.slot_pos) {
-        // the first row sees from slot len - n - window + 1 on, and the prefix
-        const int first = max(w.len - w.n - p.window + 1, 0) / kTile;
-        w.np = min((p.prefix + kTile - 1) / kTile, first);
-        w.f0 = first;
-        w.ntiles = w.np + max(w.ntiles - first, 0);
-    }
+    visible_tiles(p, w);
     const int nsplit = max((w.ntiles + sp.tiles - 1) / sp.tiles, 1);
     if (split >= nsplit) return;
     const int i0 = split * sp.tiles, i1 = min(i0 + sp.tiles, w.ntiles);
@@ -405,7 +220,7 @@ attend_kernel(const CacheView c, const AttnParams p, const Split sp)
 #pragma unroll
         for (int i = 0; i < A::STAGES; ++i) {
             if (i0 + i < i1)
-                load_tile<D>(c, w, tile_of(w, i0 + i), page, stages + i * A::STAGE, &full[i], nv[i], p.status);
+                load_tile<block_bytes(D)>(c, w, w.h, tile_of(w, i0 + i), page, stages + i * A::STAGE, &full[i], nv[i], p.status);
             page = i0 + i + 1 < i1 ? tile_page(c, w, tile_of(w, i0 + i + 1)) : -1;
         }
     }
@@ -592,7 +407,7 @@ attend_kernel(const CacheView c, const AttnParams p, const Split sp)
             }
         }
         if (warp == 3 && i + A::STAGES < i1) {
-            load_tile<D>(c, w, tile_of(w, i + A::STAGES), page, stage, &full[st], nv[st], p.status);
+            load_tile<block_bytes(D)>(c, w, w.h, tile_of(w, i + A::STAGES), page, stage, &full[st], nv[st], p.status);
             page = i + A::STAGES + 1 < i1 ? tile_page(c, w, tile_of(w, i + A::STAGES + 1)) : -1;
         }
     }
@@ -732,67 +547,6 @@ attend_kernel(const CacheView c, const AttnParams p, const Split sp)
     }
 }
 
-// One CTA per (tile of 128 tokens, request): a thread per token, every row and
-// query head in turn.
-template <typename T>
-__global__ void __launch_bounds__(kAttnThreads) weights_kernel(const CacheView c, const AttnParams p)
-{
-    const int b = blockIdx.y, tid = threadIdx.x, t = blockIdx.x * kAttnThreads + tid;
-    int lo, n;
-    if (!request_rows(p.cu_rows, b, p.R_cap, p.k_max + 1, p.status, lo, n)) return;
-    const int len = p.len[b], D = c.D;
-    if (len < 0 || len > p.max_len) {
-        if (tid == 0) set_status(p.status, SPEC_STATUS_BAD_LENGTH);
-        return;
-    }
-    __shared__ float q[256];
-    const int page = t < len ? page_of(c, b, t) : -1;
-    if (t < len && page < 0) set_status(p.status, SPEC_STATUS_BAD_PAGE);
-    const int tpos = page >= 0 ? slot_position(c, p, b, t) : 0;
-    float sum = 0.f;
-    bool seen = false;
-    for (int j = 0; j < n; ++j) {
-        const int own = len - n + j;
-        const int pos = own >= 0 ? slot_position(c, p, b, own) : 0;
-        for (int h = 0; h < p.Hq; ++h) {
-            const int hk = h / (p.Hq / c.H);
-            __syncthreads();
-            const T *qp = static_cast<const T *>(p.q) + (lo + j) * p.q_row + h * p.q_head;
-            for (int d = tid; d < D; d += kAttnThreads) q[d] = to_f32<T>(qp[d]);
-            __syncthreads();
-            const float lse = p.lse[static_cast<int64_t>(lo + j) * p.Hq + h];
-            const int dist = pos - tpos;
-            if (page >= 0 && t <= own && (p.window <= 0 || dist < p.window || t < p.prefix)) {
-                seen = true;
-                if (lse == -INFINITY) continue;
-                const uint8_t *blk = block_at(c, page, hk, t % c.page_tokens / kTok);
-                float a = 0.f;
-                for (int g = 0; g < D / 16; ++g) {
-                    float part = 0.f;
-                    for (int i = 0; i < 8; ++i) {
-                        const float2 x = h2_float2(e2m1x2(blk[g / 2 * 512 + t % kTok * 16 + g % 2 * 8 + i]));
-                        part += x.x * q[16 * g + 2 * i] + x.y * q[16 * g + 2 * i + 1];
-                    }
-                    a += part * e4m3_value(blk[k_scale_at(D) + t % kTok * (D / 16) + g]);
-                }
-                float s = a * p.scale * (c.k_scale ? c.k_scale[hk] : 1.f);
-                if (p.cap > 0.f) s = p.cap * tanhf(s / p.cap);
-                sum += __expf(s - (p.slopes ? p.slopes[h] : 0.f) * static_cast<float>(dist) - lse);
-            }
-        }
-    }
-    if (seen) p.score[static_cast<int64_t>(page) * c.page_tokens + t % c.page_tokens] += sum;
-}
-
-// Columns of a column tile: the fewest of 16, 32, 64 that hold a request's
-// rows; 64 only for bf16 heads of up to 128 channels (tensor and shared memory).
-int column_tile(int cols, int D, int dtype)
-{
-    if (cols <= 16) return 16;
-    if (cols <= 32 || D == 256 || dtype == SPEC_F32) return 32;
-    return 64;
-}
-
 // Tiles of a split: as many splits as two rounds of resident CTAs need, so that
 // ragged requests even out.
 Split split_of(int B, int k_max, int Hq, int H, int D, int max_len, int dtype)
@@ -867,14 +621,6 @@ size_t cache_attend_workspace(int B, int k_max, int Hq, int H, int D, int max_le
 cudaError_t launch_cache_attend(const CacheView &c, const AttnParams &p, int dtype, cudaStream_t s)
 {
     return dtype == SPEC_BF16 ? launch_attend<__nv_bfloat16>(c, p, dtype, s) : launch_attend<float>(c, p, dtype, s);
-}
-
-cudaError_t launch_cache_weights(const CacheView &c, const AttnParams &p, int dtype, cudaStream_t s)
-{
-    const dim3 grid((p.max_len + kAttnThreads - 1) / kAttnThreads, c.B);
-    if (dtype == SPEC_BF16) weights_kernel<__nv_bfloat16><<<grid, kAttnThreads, 0, s>>>(c, p);
-    else weights_kernel<float><<<grid, kAttnThreads, 0, s>>>(c, p);
-    return cudaGetLastError();
 }
 
 }  // namespace specv
