@@ -1,6 +1,10 @@
 // attend.cuh -- what the attention (cache_attend.cu) and the weights
 // (cache_weights.cu) share: the tiles a request's rows see, their way into
 // shared and tensor memory, the queries as an operand, the scores.
+//
+// A CTA has 8 warps.  Tensor memory is reached by quarter: warps w and w + 4
+// hold lanes 32 (w % 4) ..., so the two share a quarter's tokens (or channels)
+// and split the columns -- of K, of the scores, of the results -- in halves.
 #pragma once
 
 #include "cache.cuh"
@@ -8,8 +12,10 @@
 
 namespace specv {
 
-constexpr int kAttnThreads = 128;
+constexpr int kAttnThreads = 256;
 constexpr int kTile = 128;                 // tokens of a tile: 4 blocks
+constexpr int kLoadWarp = 7;               // the warp that fetches tiles
+
 // What a CTA works on.
 struct Job {
     int b, h, lo, n, len;       // request, kv head, first packed row, rows, tokens
@@ -26,24 +32,44 @@ __device__ __forceinline__ int slot_position(const CacheView &c, const AttnParam
     return page < 0 ? 0 : __ldg(p.slot_pos + static_cast<int64_t>(page) * c.page_tokens + slot % c.page_tokens);
 }
 
-// The tiles that some row of the request sees.
-__device__ __forceinline__ void visible_tiles(const AttnParams &p, Job &w)
+// The tiles that some row of the request sees.  With a window the first row
+// sees the prefix and what lies less than `window` positions before its own
+// slot; positions do not decrease over slots, so the hidden tiles in between
+// are counted by a 32-way search over the tiles' last slots (every warp does it
+// for itself).
+__device__ __forceinline__ void visible_tiles(const CacheView &c, const AttnParams &p, Job &w)
 {
     w.ntiles = (w.len + kTile - 1) / kTile;
     w.np = 0;
     w.f0 = 0;
-    if (p.window > 0 && !p.slot_pos) {
-        // the first row sees from slot len - n - window + 1 on, and the prefix
-        const int first = max(w.len - w.n - p.window + 1, 0) / kTile;
-        w.np = min((p.prefix + kTile - 1) / kTile, first);
-        w.f0 = first;
-        w.ntiles = w.np + max(w.ntiles - first, 0);
+    const int own = w.len - w.n;
+    if (p.window <= 0 || own <= 0) return;
+    int first = max(own - p.window + 1, 0) / kTile;
+    if (p.slot_pos) {
+        const int limit = slot_position(c, p, w.b, own) - p.window;
+        int lo = 0, hi = own / kTile;              // tiles below lo are hidden, tile hi is not
+        while (lo < hi) {
+            const int step = (hi - lo + 31) / 32, t = lo + static_cast<int>(threadIdx.x & 31) * step;
+            const int slot = t * kTile + kTile - 1;
+            // (a bad page has no positions: its tile counts as seen, its tokens are masked)
+            const bool hidden = t < hi && page_of(c, w.b, slot) >= 0 && slot_position(c, p, w.b, slot) <= limit;
+            const uint32_t seen = ~__ballot_sync(0xFFFFFFFFu, hidden);
+            const int k = seen ? __ffs(seen) - 1 : 32;           // probes 0 .. k - 1 are hidden, probe k is not
+            if (k == 0) break;
+            hi = min(hi, lo + k * step);
+            lo += (k - 1) * step + 1;
+        }
+        first = lo;
     }
+    w.np = min((p.prefix + kTile - 1) / kTile, first);
+    w.f0 = first;
+    w.ntiles = w.np + max(w.ntiles - first, 0);
 }
 
 // Copy the first BYTES of the 4 blocks of a tile into a stage (all of a block,
-// or its keys); lanes 0..3 of one warp, a block each.  nv: the tokens of each block that exist (0 for a bad page: its bytes
-// are not fetched, and what the stage holds there is masked).
+// or its keys); lanes 0..3 of one warp, a block each.  nv: the tokens of each
+// block that exist (0 for a bad page: its bytes are not fetched, and what the
+// stage holds there is masked).
 template <int BYTES>
 __device__ __forceinline__ void load_tile(const CacheView &c, const Job &w, int h, int tile, int page, uint8_t *stage,
                                           uint64_t *full, int *nv, uint32_t *status)
@@ -87,28 +113,32 @@ __device__ __forceinline__ void decode4(uint32_t w, uint32_t *r)
         : "r"(w));
 }
 
-// The keys of this thread's token (block = warp, token = lane) -> D/2 columns
+__device__ __forceinline__ void decode16(uint4 v, uint32_t (&r)[16])
+{
+    decode4(v.x, r);
+    decode4(v.y, r + 4);
+    decode4(v.z, r + 8);
+    decode4(v.w, r + 12);
+}
+
+// This warp's half of the keys of its lane's token, D/4 columns of tensor memory
+// (blk: the quarter's block)
 template <int D>
 __device__ __forceinline__ void decode_keys(const uint8_t *blk, uint32_t taddr)
 {
-    const int lane = threadIdx.x & 31;
-    constexpr int G = D / 16;
-    uint32_t sc[G / 4];
+    const int lane = threadIdx.x & 31, half = threadIdx.x / 128;
+    constexpr int G = D / 16, CH = D / 64;           // scales of a token, 32-channel chunks of a half
 #pragma unroll
-    for (int i = 0; i < G / 4; ++i)
-        sc[i] = *reinterpret_cast<const uint32_t *>(blk + k_scale_at(D) + lane * G + 4 * i);
-#pragma unroll
-    for (int ch = 0; ch < D / 32; ++ch) {
+    for (int i = 0; i < CH; ++i) {
+        const int ch = half * CH + i;
         const uint4 v = *reinterpret_cast<const uint4 *>(blk + ch * 512 + lane * 16);
-        const uint32_t s2 = e4m3x2(sc[ch / 2] >> (ch % 2 * 16));
+        const uint32_t s2 =
+            e4m3x2(*reinterpret_cast<const uint16_t *>(blk + k_scale_at(D) + lane * G + 2 * ch));
         const uint32_t s_lo = __byte_perm(s2, 0, 0x1010), s_hi = __byte_perm(s2, 0, 0x3232);
         uint32_t r[16];
-        decode4(v.x, r);
-        decode4(v.y, r + 4);
-        decode4(v.z, r + 8);
-        decode4(v.w, r + 12);
+        decode16(v, r);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) r[i] = h2_mul(r[i], i < 8 ? s_lo : s_hi);
+        for (int k = 0; k < 16; ++k) r[k] = h2_mul(r[k], k < 8 ? s_lo : s_hi);
         tmem_st16(taddr + ch * 16, r);
     }
 }
@@ -120,59 +150,78 @@ __device__ __forceinline__ uint32_t pack_h2(float lo, float hi)
     return r;
 }
 
-// Query columns as the K-major B operand, scaled by the power of two 2^e (and
-// the sign of the softmax scale) that brings the tile's largest to 2^14; the
-// second f16 term behind the first for fp32.  Returns 2^-e.
-template <typename T, int D, int NT, int PIECES>
-__device__ float stage_queries(const AttnParams &p, const Job &w, int group, uint8_t *qs, float *red)
+template <typename T>
+__device__ __forceinline__ void load8(const T *p, bool aligned, float (&x)[8])
 {
-    const int tid = threadIdx.x;
-    constexpr int PER = D / 8;                        // 8-channel groups of a column
-    float big = 0.f;
-    for (int i = tid; i < w.ncols * PER; i += kAttnThreads) {
-        const int col = w.col0 + i / PER;
-        const T *src = static_cast<const T *>(p.q) + (w.lo + col / group) * p.q_row +
-                       (w.h * group + col % group) * p.q_head + i % PER * 8;
+    if (aligned) {
+        constexpr int N = sizeof(T) / 2;
+        uint4 v[N];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) big = fmaxf(big, fabsf(to_f32<T>(src[k])));
+        for (int i = 0; i < N; ++i) v[i] = __ldg(reinterpret_cast<const uint4 *>(p) + i);
+        const T *e = reinterpret_cast<const T *>(v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = to_f32<T>(e[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = to_f32<T>(p[i]);
     }
-    big = warp_max_f32(big);
-    if ((tid & 31) == 0) red[tid >> 5] = big;
-    __syncthreads();
-    big = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-    // exponent arithmetic on the bits; a tile of zeros (or subnormals) stays as it is
-    const int ex = static_cast<int>(__float_as_uint(big) >> 23) - 127;
-    const int e = ex > -127 ? min(max(13 - ex, -120), 100) : 0;
-    const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-    const float f = p.scale == 0.f ? 0.f : (p.scale < 0.f ? -up : up);
-    for (int i = tid; i < NT * PER; i += kAttnThreads) {
-        const int c = i / PER, k8 = i % PER, col = w.col0 + c;
+}
+
+// The query columns of kv head w.h as the K-major B operand: each scaled by the
+// power of two that brings its largest channel to 2^13 (and by the sign of the
+// softmax scale), the second f16 term behind the first for fp32.  mult[col]
+// takes a raw product to its score in natural units; `unit` multiplies it (log2
+// e for log2 units).  A column belongs to D/8 lanes of one warp: no barrier.
+template <typename T, int D, int NT, int PIECES>
+__device__ __forceinline__ void stage_queries(const AttnParams &p, const Job &w, int group, float gk, double unit,
+                                              uint8_t *qs, float *mult)
+{
+    constexpr int PER = D / 8;                        // 8-channel groups of a column
+#pragma unroll 1
+    for (int i = threadIdx.x; i < NT * PER; i += kAttnThreads) {
+        const int cl = i / PER, k8 = i % PER, col = w.col0 + cl;
         float x[8] = {};
-        if (c < w.ncols) {
-            const T *src = static_cast<const T *>(p.q) + (w.lo + col / group) * p.q_row +
-                           (w.h * group + col % group) * p.q_head + k8 * 8;
+        if (cl < w.ncols)
+            load8<T>(static_cast<const T *>(p.q) + (w.lo + col / group) * p.q_row +
+                         (w.h * group + col % group) * p.q_head + k8 * 8,
+                     p.q_aligned, x);
+        float big = 0.f;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) x[k] = to_f32<T>(src[k]) * f;
-        }
-        uint8_t *dst = qs + k8 * (NT * 16) + c / 8 * 128 + c % 8 * 16;
+        for (int k = 0; k < 8; ++k) big = fmaxf(big, fabsf(x[k]));
+#pragma unroll
+        for (int o = PER / 2; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xFFFFFFFFu, big, o));
+        // exponent arithmetic on the bits; a column of zeros (or subnormals) stays as it is
+        const int ex = static_cast<int>(__float_as_uint(big) >> 23) - 127;
+        const int e = ex > -127 ? min(max(13 - ex, -120), 100) : 0;
+        const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+        const float f = p.scale == 0.f ? 0.f : (p.scale < 0.f ? -up : up);
+        // rounded to fp32 once; never 0, so that a hidden slot's -inf stays -inf
+        if (k8 == 0)
+            mult[cl] = p.scale == 0.f ? 1.f
+                                      : fmaxf(static_cast<float>(fabs(static_cast<double>(p.scale)) * gk * unit) *
+                                                  __uint_as_float(static_cast<uint32_t>(127 - e) << 23),
+                                              1e-37f);
+        uint8_t *dst = qs + k8 * (NT * 16) + cl / 8 * 128 + cl % 8 * 16;
         uint32_t hi[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) hi[k] = pack_h2(x[2 * k], x[2 * k + 1]);
+        for (int k = 0; k < 4; ++k) hi[k] = pack_h2(x[2 * k] * f, x[2 * k + 1] * f);
         *reinterpret_cast<uint4 *>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
         if (PIECES == 2) {
             uint32_t l[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 const float2 y = h2_float2(hi[k]);
-                l[k] = pack_h2(x[2 * k] - y.x, x[2 * k + 1] - y.y);
+                l[k] = pack_h2(x[2 * k] * f - y.x, x[2 * k + 1] * f - y.y);
             }
             *reinterpret_cast<uint4 *>(dst + NT * D * 2) = make_uint4(l[0], l[1], l[2], l[3]);
         }
     }
-    return __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
 }
 
-// S^T = K Q^T over all channels (one thread issues)
+// S^T = K Q^T over all channels (one thread issues).  The terms of fp32 queries
+// go to accumulators of their own, NT columns apart: the tensor cores truncate
+// a sum at its last place, and adding the small products of the second term to
+// the large sum would cost a bit or two in every step.
 template <int D, int NT, int PIECES>
 __device__ __forceinline__ void issue_scores(uint32_t s_addr, uint32_t a_addr, const uint8_t *qs)
 {
@@ -181,21 +230,35 @@ __device__ __forceinline__ void issue_scores(uint32_t s_addr, uint32_t a_addr, c
     for (int pc = 0; pc < PIECES; ++pc)
 #pragma unroll
         for (int k = 0; k < D / 16; ++k)
-            mma_f16(s_addr, a_addr + k * 8, smem_desc(q + pc * NT * D * 2 + k * 2 * NT * 16, NT * 16, 128),
-                    mma_f16_desc(NT, false), pc > 0 || k > 0);
+            mma_f16(s_addr + pc * NT, a_addr + k * 8, smem_desc(q + pc * NT * D * 2 + k * 2 * NT * 16, NT * 16, 128),
+                    mma_f16_desc(NT, false), k > 0);
 }
 
-// the score in log2 units of a raw product, with cap and distance bias
-__device__ __forceinline__ float option_score(float cap, float twice, float v, float mult, float slope2, int dist)
+// N raw products of this thread's token, from column `addr` on
+template <int N, int NT, int PIECES>
+__device__ __forceinline__ void load_products(uint32_t addr, float (&v)[N])
 {
-    float y = v * mult;
-    if (cap > 0.f) {
-        // cap tanh(s / cap) = cap - 2 cap / (1 + 2^(2 y / cap))  (y in log2 units)
-        const float c2 = cap * kLog2e;
-        const float t = 1.f + ex2(fminf(twice * y, 126.f));
-        y = c2 - __fdividef(2.f * c2, t);
+    tmem_ld<N>(addr, reinterpret_cast<uint32_t *>(v));
+    if constexpr (PIECES == 2) {
+        float t[N];
+        tmem_ld<N>(addr + NT, reinterpret_cast<uint32_t *>(t));
+        tmem_wait_ld();
+#pragma unroll
+        for (int q = 0; q < N; ++q) v[q] += t[q];
+    } else {
+        tmem_wait_ld();
     }
-    return y - slope2 * static_cast<float>(dist);
+}
+
+// cap * tanh(s / cap), s and the result in units of `unit` (1 or log2 e).  EXACT
+// (fp32 results): the library's tanh.  Else 1 - 2 / (1 + e^2z), within 2^-21 of
+// cap absolute.
+template <bool EXACT>
+__device__ __forceinline__ float cap_score(float y, float cap, float rcap)
+{
+    if (EXACT) return cap * tanhf(y * rcap);
+    const float t = 1.f + ex2(fminf(2.f * kLog2e * rcap * y, 126.f));
+    return cap - __fdividef(2.f * cap, t);
 }
 
 // Columns of a column tile: the fewest of 16, 32, 64 that hold a request's
@@ -206,5 +269,13 @@ inline int column_tile(int cols, int D, int dtype)
     if (cols <= 32 || D == 256 || dtype == SPEC_F32) return 32;
     return 64;
 }
+
+// CTAs an SM by tensor memory (`cols` columns each), and what a CTA may then use
+// of the SM's 227 KB, less `fixed` bytes of static shared memory.  No more CTAs
+// than that may fit either: one more would sit waiting for tensor memory.
+__host__ __device__ constexpr int tmem_cols(int used) { return used <= 128 ? 128 : (used <= 256 ? 256 : 512); }
+__host__ __device__ constexpr int smem_share(int ctas, int fixed) { return 232448 / ctas - 1024 - fixed; }
+__host__ __device__ constexpr int smem_least(int ctas) { return 232448 / (ctas + 1); }
+__host__ __device__ constexpr int clamp_stages(int fit) { return fit < 2 ? 2 : (fit > 4 ? 4 : fit); }
 
 }  // namespace specv

@@ -2,10 +2,12 @@
 // packed verify rows, added to its score (include/spec_cache.h).
 //
 // score_j += sum over rows and heads of exp(s_ij - lse_i): with S^T = K Q^T
-// (cache_attend.cu) a token is a lane and its sum over the columns and heads
-// stays in one thread, in a fixed order -- no atomics, one read and one write of
-// the score.  A CTA takes a few tiles of one request through every kv head, so
-// that a head's queries are staged once for them; the keys alone are read.
+// (cache_attend.cu) a token is a lane, and its sum over the columns and heads
+// stays in two threads (a half of the columns each), in a fixed order -- no
+// atomics, one read and one write of the score.  A CTA takes a few tiles of one
+// request through every kv head; the keys alone are read.  The product of a
+// step runs while the weights of the step before are summed and the next head's
+// queries are staged.
 #include "attend.cuh"
 
 namespace specv {
@@ -15,20 +17,25 @@ namespace {
 constexpr int kMaxTiles = 8;               // tiles of a CTA at most
 
 template <typename T, int D_, int NT_> struct Weights {
-    static constexpr int D = D_, NT = NT_;
+    static constexpr int D = D_, NT = NT_, NH = NT / 2;
     static constexpr int PIECES = sizeof(T) == 4 ? 2 : 1;
     static constexpr int K_BYTES = v_codes_at(D);              // a block's keys and their scales
-    static constexpr int A_COLS = D / 2;
-    static constexpr int COLS = A_COLS + 2 * NT <= 128 ? 128 : 256;
+    static constexpr int A_COLS = D / 2, S_COLS = PIECES * NT;
+    static constexpr int COLS = tmem_cols(A_COLS + 2 * S_COLS);
     static constexpr int CTAS = 512 / COLS;
-    static constexpr int SHARE = 232448 / CTAS - 1024 - 4096 - kMaxTiles * kTile * 4;
     static constexpr int Q_BYTES = PIECES * NT * D * 2;
     static constexpr int STAGE = 4 * K_BYTES;
-    static constexpr int FIT = (SHARE - Q_BYTES) / STAGE;
-    static constexpr int STAGES = FIT < 2 ? 2 : (FIT > 4 ? 4 : FIT);
-    static constexpr int NEED = Q_BYTES + STAGES * STAGE;
-    static constexpr int LEAST = 232448 / (CTAS + 1);          // no more CTAs than tensor memory holds
-    static constexpr int SMEM = NEED > LEAST ? NEED : LEAST;
+    static constexpr int FIXED = 128 + 60 * NT + 2 * kMaxTiles * kTile * 4;
+    static constexpr int STAGES = clamp_stages((smem_share(CTAS, FIXED) - 2 * Q_BYTES) / STAGE);
+    static constexpr int NEED = 2 * Q_BYTES + STAGES * STAGE;
+    static constexpr int SMEM = NEED > smem_least(CTAS) ? NEED : smem_least(CTAS);
+};
+
+// Column constants of a head (shared memory); three sets, as a slow warp may
+// still read the one before last.
+template <int NT> struct Heads {
+    float mult[NT], lse[NT], slope[NT];
+    int own[NT], pos[NT];
 };
 
 // Step of a CTA: tile `t` of its tiles, column tile `qt` of kv head `h`.
@@ -41,14 +48,16 @@ __global__ void __launch_bounds__(kAttnThreads, (Weights<T, D, NT>::CTAS))
 weights_kernel(const CacheView c, const AttnParams p, const int tiles)
 {
     using A = Weights<T, D, NT>;
+    constexpr int NH = A::NH;
     extern __shared__ __align__(128) uint8_t smem[];
-    uint8_t *qs = smem, *stages = qs + A::Q_BYTES;
+    uint8_t *qs = smem, *stages = qs + 2 * A::Q_BYTES;
+    __shared__ __align__(16) Heads<NT> sets[3];
     __shared__ __align__(8) uint64_t full[A::STAGES], s_bar;
     __shared__ uint32_t tmem_base;
-    __shared__ int nv[A::STAGES][4], own_s[3][NT], pos_s[3][NT];
-    __shared__ __align__(16) float lse_s[3][NT], slope_s[3][NT];
-    __shared__ float mult_s[3], red[4], acc[kMaxTiles][kTile];
+    __shared__ int nv[A::STAGES][4];
+    __shared__ float acc[kMaxTiles][2][kTile];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int quarter = warp & 3, half = warp >> 2, tok = tid & 127;
     const int group = p.Hq / c.H;
     Job w;
     w.b = blockIdx.y;
@@ -58,8 +67,10 @@ weights_kernel(const CacheView c, const AttnParams p, const int tiles)
         if (tid == 0) set_status(p.status, SPEC_STATUS_BAD_LENGTH);
         return;
     }
-    visible_tiles(p, w);
-    const int i0 = blockIdx.x * tiles, nt = min(tiles, w.ntiles - i0);
+    const int i0 = blockIdx.x * tiles;
+    if (i0 * kTile >= w.len) return;
+    visible_tiles(c, p, w);
+    const int nt = min(tiles, w.ntiles - i0);
     if (nt <= 0) return;
 
     const int cols = w.n * group, qt_used = (cols + NT - 1) / NT;
@@ -68,99 +79,108 @@ weights_kernel(const CacheView c, const AttnParams p, const int tiles)
         const int t = i % nt, hq = i / nt;
         return Step{hq / qt_used, hq % qt_used, t};
     };
-    if (tid == 0) {
-        for (int i = 0; i < A::STAGES; ++i) mbar_init(&full[i], 1);
-        mbar_init(&s_bar, 1);
-        fence_mbar_init();
-    }
-    if (warp == 0) tmem_alloc(&tmem_base, A::COLS);
-    for (int t = 0; t < nt; ++t) acc[t][tid] = 0.f;
-    __syncthreads();
-    const uint32_t a_t = tmem_base, s_t = a_t + A::A_COLS;
-    const uint32_t lane_off = static_cast<uint32_t>(warp * 32) << 16;
     const auto load = [&](int i) {
         const Step s = step_at(i);
         const int tile = tile_of(w, i0 + s.t);
         load_tile<A::K_BYTES>(c, w, s.h, tile, tile_page(c, w, tile), stages + i % A::STAGES * A::STAGE,
                               &full[i % A::STAGES], nv[i % A::STAGES], p.status);
     };
-    if (warp == 3)
+    if (warp == kLoadWarp) {
+        if (lane == 0) {
+            for (int i = 0; i < A::STAGES; ++i) mbar_init(&full[i], 1);
+            mbar_init(&s_bar, 1);
+            fence_mbar_init();
+        }
+        __syncwarp();
         for (int i = 0; i < A::STAGES && i < steps; ++i) load(i);
+    }
+    if (warp == 0) tmem_alloc(&tmem_base, A::COLS);
+    for (int t = 0; t < nt; ++t) acc[t][half][tok] = 0.f;
 
     const bool options = p.cap > 0.f || p.slopes || p.window > 0;
-    // weights of a finished product: column constants of set `cb`
-    const auto add_weights = [&](int i, int cb) {
+    // queries and column constants of the head that step i begins
+    const auto stage_head = [&](int i, Heads<NT> &set, uint8_t *q) {
         const Step s = step_at(i);
-        const int tile = tile_of(w, i0 + s.t), slot = tile * kTile + tid;
+        w.h = s.h;
+        w.col0 = s.qt * NT;
+        w.ncols = min(cols - w.col0, NT);
+        if (tid < NT) {
+            const int col = min(w.col0 + tid, cols - 1), j = col / group, own = w.len - w.n + j;
+            const int head = s.h * group + col % group;
+            set.own[tid] = own;
+            set.pos[tid] = own >= 0 ? slot_position(c, p, w.b, own) : 0;
+            set.slope[tid] = p.slopes ? p.slopes[head] : 0.f;
+            // padded columns, and rows that saw nothing: weight exp(-inf) = 0
+            const float lse = tid < w.ncols ? p.lse[static_cast<int64_t>(w.lo + j) * p.Hq + head] : INFINITY;
+            set.lse[tid] = lse == -INFINITY ? INFINITY : lse;
+        }
+        stage_queries<T, D, NT, A::PIECES>(p, w, group, c.k_scale ? c.k_scale[s.h] : 1.f, 1.0, q, set.mult);
+        fence_proxy_async_smem();
+    };
+    int cb = 0, qb = 0;
+    stage_head(0, sets[0], qs);
+    __syncthreads();
+    tmem_fence_after();
+    const uint32_t a_t = tmem_base, s_t = a_t + A::A_COLS;
+    const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
+
+    // weights of a finished product
+    const auto add_weights = [&](int i, const Heads<NT> &set) {
+        const Step s = step_at(i);
+        const int tile = tile_of(w, i0 + s.t), slot = tile * kTile + tok;
         const int valid = min(max(w.len - (slot - lane), 0), kTok);
-        float v[NT];
-#pragma unroll
-        for (int q = 0; q < NT; q += 16)
-            tmem_ld16(s_t + (i & 1) * NT + lane_off + q, reinterpret_cast<uint32_t *>(v) + q);
-        tmem_wait_ld();
-        const float mult = mult_s[cb];
-        const bool edge = (tile + 1) * kTile - 1 > own_s[cb][0] || valid < kTok;
+        float v[NH];
+        load_products<NH, NT, A::PIECES>(s_t + (i & 1) * A::S_COLS + lane_off + half * NH, v);
+        const bool edge = (tile + 1) * kTile - 1 > set.own[0] || valid < kTok;
         float sum = 0.f;
         if (edge || options) {
-            const int tpos = options && p.slot_pos && lane < valid ? slot_position(c, p, w.b, slot) : slot;
-            const float twice = p.cap > 0.f ? 2.f / p.cap : 0.f;
+            const bool live = lane < valid;
+            const int tpos = options && p.slot_pos && live ? slot_position(c, p, w.b, slot) : slot;
+            const bool always = live && (p.window <= 0 || slot < p.prefix);
+            const float rcap = p.cap > 0.f ? 1.f / p.cap : 0.f;
 #pragma unroll
-            for (int q = 0; q < NT; ++q) {
-                float y = v[q] * mult;
-                const int dist = pos_s[cb][q] - tpos;
-                if (options) y = option_score(p.cap, twice, v[q], mult * kLog2e, slope_s[cb][q], dist) * kLn2;
-                const bool see = slot <= own_s[cb][q] && (p.window <= 0 || dist < p.window || slot < p.prefix);
-                sum += see ? ex2((y - lse_s[cb][q]) * kLog2e) : 0.f;
+            for (int k = 0; k < NH; ++k) {
+                const int q = half * NH + k, dist = set.pos[q] - tpos;
+                float y = v[k] * set.mult[q];
+                if (p.cap > 0.f) y = cap_score<true>(y, p.cap, rcap);
+                y -= set.slope[q] * static_cast<float>(dist);
+                const bool see = slot <= set.own[q] && (always || (live && dist < p.window));
+                sum += see ? ex2((y - set.lse[q]) * kLog2e) : 0.f;
             }
         } else {
 #pragma unroll
-            for (int q = 0; q < NT; ++q) sum += ex2(fmaf(v[q], mult, -lse_s[cb][q]) * kLog2e);
+            for (int k = 0; k < NH; ++k)
+                sum += ex2(fmaf(v[k], set.mult[half * NH + k], -set.lse[half * NH + k]) * kLog2e);
         }
-        acc[s.t][tid] += sum;
+        acc[s.t][half][tok] += sum;
     };
 
     bool fail = false;
-    int cb = 2;
     for (int i = 0; i < steps; ++i) {
-        const Step s = step_at(i);
         const int st = i % A::STAGES;
         const int cb_last = cb;
         if (i > 0) {
-            fail |= !mbar_wait(&s_bar, (i - 1) & 1);       // the keys' columns and the queries are used up
+            fail |= !mbar_wait(&s_bar, (i - 1) & 1);       // the keys' columns are used up
             tmem_fence_after();
-        }
-        if (s.t == 0) {
-            cb = cb == 2 ? 0 : cb + 1;   // three sets: a slow warp may still read the one before last
-            w.h = s.h;
-            w.col0 = s.qt * NT;
-            w.ncols = min(cols - w.col0, NT);
-            if (tid < NT) {
-                const int col = min(w.col0 + tid, cols - 1), j = col / group, own = w.len - w.n + j;
-                const int head = s.h * group + col % group;
-                own_s[cb][tid] = own;
-                pos_s[cb][tid] = own >= 0 ? slot_position(c, p, w.b, own) : 0;
-                slope_s[cb][tid] = p.slopes ? p.slopes[head] * kLog2e : 0.f;
-                // padded columns, and rows that saw nothing: weight exp(-inf) = 0
-                const float lse = tid < w.ncols ? p.lse[static_cast<int64_t>(w.lo + j) * p.Hq + head] : INFINITY;
-                lse_s[cb][tid] = lse == -INFINITY ? INFINITY : lse;
+            if (i % nt == 0) {
+                cb = cb == 2 ? 0 : cb + 1;
+                qb ^= 1;
             }
-            const float down = stage_queries<T, D, NT, A::PIECES>(p, w, group, qs, red);
-            if (tid == 0)
-                mult_s[cb] = p.scale == 0.f ? 1.f : fabsf(p.scale) * (c.k_scale ? c.k_scale[s.h] : 1.f) * down;
         }
         fail |= !mbar_wait(&full[st], i / A::STAGES & 1);
-        decode_keys<D>(stages + st * A::STAGE + warp * A::K_BYTES, a_t + lane_off);
+        decode_keys<D>(stages + st * A::STAGE + quarter * A::K_BYTES, a_t + lane_off);
         tmem_wait_st();
         tmem_fence_before();
-        fence_proxy_async_smem();
         if (__syncthreads_or(fail)) break;
         if (tid == 0) {
             tmem_fence_after();
-            issue_scores<D, NT, A::PIECES>(s_t + (i & 1) * NT, a_t, qs);
+            issue_scores<D, NT, A::PIECES>(s_t + (i & 1) * A::S_COLS, a_t, qs + qb * A::Q_BYTES);
             mma_commit(&s_bar);
         }
-        if (warp == 3 && i + A::STAGES < steps) load(i + A::STAGES);
-        if (i > 0) add_weights(i - 1, cb_last);
+        if (warp == kLoadWarp && i + A::STAGES < steps) load(i + A::STAGES);
+        if (i + 1 < steps && (i + 1) % nt == 0)
+            stage_head(i + 1, sets[cb == 2 ? 0 : cb + 1], qs + (qb ^ 1) * A::Q_BYTES);
+        if (i > 0) add_weights(i - 1, sets[cb_last]);
     }
     if (!fail) fail = !mbar_wait(&s_bar, (steps - 1) & 1);
     tmem_fence_after();
@@ -171,11 +191,13 @@ weights_kernel(const CacheView c, const AttnParams p, const int tiles)
             set_status(p.status, SPEC_STATUS_TIMEOUT);
         }
     } else {
-        add_weights(steps - 1, cb);
-        for (int t = 0; t < nt; ++t) {
-            const int slot = tile_of(w, i0 + t) * kTile + tid;
+        add_weights(steps - 1, sets[cb]);
+        __syncthreads();
+        for (int t = half; t < nt; t += 2) {
+            const int slot = tile_of(w, i0 + t) * kTile + tok;
             const int page = slot < w.len ? page_of(c, w.b, slot) : -1;
-            if (page >= 0) p.score[static_cast<int64_t>(page) * c.page_tokens + slot % c.page_tokens] += acc[t][tid];
+            if (page >= 0)
+                p.score[static_cast<int64_t>(page) * c.page_tokens + slot % c.page_tokens] += acc[t][0][tok] + acc[t][1][tok];
         }
     }
     tmem_fence_before();

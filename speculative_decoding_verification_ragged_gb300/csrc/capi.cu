@@ -243,6 +243,7 @@ int check_attention(const spec_cache *cache, const spec_attention *a, CacheView 
     p.prefix = a->prefix;
     p.slot_pos = a->slot_pos;
     p.status = a->status;
+    p.q_aligned = rows_aligned(a->q, a->q_row, a->q_head, elt_bytes(a->dtype));
     return SPEC_OK;
 }
 

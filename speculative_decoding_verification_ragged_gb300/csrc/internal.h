@@ -126,6 +126,7 @@ struct AttnParams {
     float *lse;                  // attend: written; weights: read
     float *score;                // weights only
     void *ws;
+    bool q_aligned;              // every query starts on a 16-byte boundary
 };
 
 struct EvictParams {

@@ -28,7 +28,16 @@ __device__ __forceinline__ void tmem_fence_after() { asm volatile("tcgen05.fence
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// 16 columns of this warp's 32 lanes (lane = thread); addr names the warp's first lane
+// N columns (8, or a multiple of 16) of this warp's 32 lanes (lane = thread);
+// addr names the warp's first lane
+__device__ __forceinline__ void tmem_ld8(uint32_t addr, uint32_t *r)
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(addr)
+                 : "memory");
+}
+
 __device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t *r)
 {
     asm volatile(
@@ -40,6 +49,16 @@ __device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t *r)
         : "memory");
 }
 
+template <int N> __device__ __forceinline__ void tmem_ld(uint32_t addr, uint32_t *r)
+{
+    if constexpr (N == 8) {
+        tmem_ld8(addr, r);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; i += 16) tmem_ld16(addr + i, r + i);
+    }
+}
+
 __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t *r)
 {
     asm volatile(
@@ -48,6 +67,13 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t *r)
         "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
         "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
+}
+
+__device__ __forceinline__ void tmem_st8(uint32_t addr, const uint32_t *r)
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(addr),
+                 "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
 }
 
 // Shared-memory operand without swizzle: 8 x 16-byte core matrices of 128
