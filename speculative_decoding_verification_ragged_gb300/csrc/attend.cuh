@@ -13,17 +13,21 @@
 namespace specv {
 
 constexpr int kAttnThreads = 256;
-constexpr int kTile = 128;                 // tokens of a tile: 4 blocks
-constexpr int kLoadWarp = 7;               // the warp that fetches tiles
+constexpr int kTile = 128;                 // tokens of a tile: 4 blocks, the lanes of tensor memory
+constexpr int kLoadWarp = 7;               // the warp that fetches steps
 
 // What a CTA works on.
 struct Job {
     int b, h, lo, n, len;       // request, kv head, first packed row, rows, tokens
     int col0, ncols;            // first column of the tile, real columns
-    int ntiles, np, f0;         // tiles to visit: 0 .. np - 1, then f0, f0 + 1, ...
+    int nsteps, np, f0;         // steps to visit: 0 .. np - 1, then f0, f0 + 1, ...
 };
 
-__device__ __forceinline__ int tile_of(const Job &w, int i) { return i < w.np ? i : w.f0 + i - w.np; }
+// first slot of the i-th step visited, steps of STEP tokens
+template <int STEP> __device__ __forceinline__ int step_slot(const Job &w, int i)
+{
+    return (i < w.np ? i : w.f0 + i - w.np) * STEP;
+}
 
 __device__ __forceinline__ int slot_position(const CacheView &c, const AttnParams &p, int b, int slot)
 {
@@ -32,26 +36,27 @@ __device__ __forceinline__ int slot_position(const CacheView &c, const AttnParam
     return page < 0 ? 0 : __ldg(p.slot_pos + static_cast<int64_t>(page) * c.page_tokens + slot % c.page_tokens);
 }
 
-// The tiles that some row of the request sees.  With a window the first row
+// The steps that some row of the request sees.  With a window the first row
 // sees the prefix and what lies less than `window` positions before its own
-// slot; positions do not decrease over slots, so the hidden tiles in between
-// are counted by a 32-way search over the tiles' last slots (every warp does it
+// slot; positions do not decrease over slots, so the hidden steps in between
+// are counted by a 32-way search over the steps' last slots (every warp does it
 // for itself).
-__device__ __forceinline__ void visible_tiles(const CacheView &c, const AttnParams &p, Job &w)
+template <int STEP>
+__device__ __forceinline__ void visible_steps(const CacheView &c, const AttnParams &p, Job &w)
 {
-    w.ntiles = (w.len + kTile - 1) / kTile;
+    w.nsteps = (w.len + STEP - 1) / STEP;
     w.np = 0;
     w.f0 = 0;
     const int own = w.len - w.n;
     if (p.window <= 0 || own <= 0) return;
-    int first = max(own - p.window + 1, 0) / kTile;
+    int first = max(own - p.window + 1, 0) / STEP;
     if (p.slot_pos) {
         const int limit = slot_position(c, p, w.b, own) - p.window;
-        int lo = 0, hi = own / kTile;              // tiles below lo are hidden, tile hi is not
+        int lo = 0, hi = own / STEP;              // steps below lo are hidden, step hi is not
         while (lo < hi) {
             const int step = (hi - lo + 31) / 32, t = lo + static_cast<int>(threadIdx.x & 31) * step;
-            const int slot = t * kTile + kTile - 1;
-            // (a bad page has no positions: its tile counts as seen, its tokens are masked)
+            const int slot = t * STEP + STEP - 1;
+            // (a bad page has no positions: its step counts as seen, its tokens are masked)
             const bool hidden = t < hi && page_of(c, w.b, slot) >= 0 && slot_position(c, p, w.b, slot) <= limit;
             const uint32_t seen = ~__ballot_sync(0xFFFFFFFFu, hidden);
             const int k = seen ? __ffs(seen) - 1 : 32;           // probes 0 .. k - 1 are hidden, probe k is not
@@ -61,28 +66,28 @@ __device__ __forceinline__ void visible_tiles(const CacheView &c, const AttnPara
         }
         first = lo;
     }
-    w.np = min((p.prefix + kTile - 1) / kTile, first);
+    w.np = min((p.prefix + STEP - 1) / STEP, first);
     w.f0 = first;
-    w.ntiles = w.np + max(w.ntiles - first, 0);
+    w.nsteps = w.np + max(w.nsteps - first, 0);
 }
 
-// Copy the first BYTES of the 4 blocks of a tile into a stage (all of a block,
-// or its keys); lanes 0..3 of one warp, a block each.  nv: the tokens of each
-// block that exist (0 for a bad page: its bytes are not fetched, and what the
-// stage holds there is masked).
-template <int BYTES>
-__device__ __forceinline__ void load_tile(const CacheView &c, const Job &w, int h, int tile, int page, uint8_t *stage,
+// Copy the first BYTES of the BLOCKS blocks of a step into a stage (all of a
+// block, or its keys); a lane of one warp per block, `page` its page.  nv: the
+// tokens of each block that exist (0 for a bad page: its bytes are not fetched,
+// and what the stage holds there is masked).
+template <int BYTES, int BLOCKS>
+__device__ __forceinline__ void load_step(const CacheView &c, const Job &w, int h, int slot, int page, uint8_t *stage,
                                           uint64_t *full, int *nv, uint32_t *status)
 {
     const int lane = threadIdx.x & 31;
-    const int slot0 = tile * kTile + lane * kTok;
-    int n = lane < 4 ? min(max(w.len - slot0, 0), kTok) : 0;
+    const int slot0 = slot + lane * kTok;
+    int n = lane < BLOCKS ? min(max(w.len - slot0, 0), kTok) : 0;
     if (n > 0 && page < 0) {
         set_status(status, SPEC_STATUS_BAD_PAGE);
         n = 0;
     }
     const uint32_t have = __ballot_sync(0xFFFFFFFFu, n > 0);
-    if (lane < 4) nv[lane] = n;
+    if (lane < BLOCKS) nv[lane] = n;
     __syncwarp();
     if (lane == 0) mbar_arrive_expect_tx(full, __popc(have) * BYTES);
     __syncwarp();
@@ -90,10 +95,19 @@ __device__ __forceinline__ void load_tile(const CacheView &c, const Job &w, int 
         bulk_g2s(stage + lane * BYTES, block_at(c, page, h, slot0 % c.page_tokens / kTok), BYTES, full);
 }
 
-__device__ __forceinline__ int tile_page(const CacheView &c, const Job &w, int tile)
+// page of this lane's block of the step at `slot`
+template <int BLOCKS>
+__device__ __forceinline__ int step_page(const CacheView &c, const Job &w, int slot)
 {
-    const int lane = threadIdx.x & 31, slot0 = tile * kTile + lane * kTok;
-    return lane < 4 && slot0 < w.len ? page_of(c, w.b, slot0) : -1;
+    const int lane = threadIdx.x & 31, slot0 = slot + lane * kTok;
+    return lane < BLOCKS && slot0 < w.len ? page_of(c, w.b, slot0) : -1;
+}
+
+// A wait that has given up once does not wait again: the CTA runs to its end,
+// stores nothing and reports the timeout.
+__device__ __forceinline__ void wait_or_fail(uint64_t *bar, uint32_t parity, bool &fail)
+{
+    if (!fail) fail = !mbar_wait(bar, parity);
 }
 
 __device__ __forceinline__ uint32_t h2_mul(uint32_t a, uint32_t b)

@@ -43,7 +43,7 @@ template <typename T, int D_, int NT_> struct Attn {
     static constexpr int D = D_, NT = NT_;
     static constexpr int NH = NT / 2;                          // columns of a thread
     static constexpr int PIECES = sizeof(T) == 4 ? 2 : 1;      // f16 terms of a query and of a weight
-    static constexpr int WIDE = sizeof(T) == 4 ? 3 : 2;        // bf16 terms of a weight in a wide tile
+    static constexpr int WIDE = sizeof(T) == 4 ? 3 : 2;        // bf16 terms of a weight in a wide step
     // exponent of the smallest weight with its bits in f16: a normal number; for
     // two terms 15 bits above the last place, 2^-25
     static constexpr float LEAST_EXP = sizeof(T) == 4 ? -10.f : -14.f;
@@ -52,33 +52,39 @@ template <typename T, int D_, int NT_> struct Attn {
     static constexpr int HALVES = D == 64 ? 2 : 1;
     static constexpr int VM = D == 256 ? 2 : 1;
     static constexpr int VT = kTile / HALVES;                  // tokens of a V^T row
-    static constexpr int A_COLS = D == 256 ? 128 : D / 2;      // tensor memory of K, then of V^T
+    static constexpr int A_COLS = D == 256 ? 128 : D / 2;      // tensor memory of a tile's K, then of its V^T
+    static constexpr int S_COLS = PIECES * NT;
     static constexpr int O_COLS = NT * HALVES * VM;
-    static constexpr int COLS = tmem_cols(A_COLS + PIECES * NT + O_COLS);
-    static constexpr int CTAS = 512 / COLS;
+    // Tiles of a step, where 256 columns hold them: barriers, waits and column
+    // constants are paid once a step (32 x 5 rows x 4096 tokens: 115 us with one
+    // tile a step and 4 CTAs an SM).
+    static constexpr int SUB = 2 * (A_COLS + S_COLS) + O_COLS <= 256 ? 2 : 1;
+    static constexpr int STEP = SUB * kTile, BLOCKS = 4 * SUB;
+    static constexpr int COLS = tmem_cols(SUB * (A_COLS + S_COLS) + O_COLS);
+    static constexpr int CTAS = COLS <= 256 ? 2 : 1;
     static constexpr int Q_BYTES = NT * D * 2;
-    static constexpr int P_BYTES = kTile * NT * 2;
-    static constexpr int VS_BYTES = D / 16 * kTile * 2;        // scales of V as f16
-    static constexpr int STAGE = 4 * block_bytes(D);
-    static constexpr int OPERANDS = PIECES * (Q_BYTES + P_BYTES) + VS_BYTES;
-    static constexpr int STAGES = clamp_stages((smem_share(CTAS, 64 + 60 * NT) - OPERANDS) / STAGE);
+    static constexpr int P_BYTES = kTile * NT * 2;             // a term of a tile's weights
+    static constexpr int VS_BYTES = D / 16 * kTile * 2;        // a tile's scales of V as f16
+    static constexpr int STAGE = BLOCKS * block_bytes(D);
+    static constexpr int OPERANDS = PIECES * (Q_BYTES + SUB * P_BYTES) + SUB * VS_BYTES;
+    static constexpr int STAGES = clamp_stages((smem_share(CTAS, 128 + 60 * NT) - OPERANDS) / STAGE);
     static constexpr int NEED = OPERANDS + STAGES * STAGE;
     static constexpr int SMEM = NEED > smem_least(CTAS) ? NEED : smem_least(CTAS);
     static_assert(D != 64 || NT * D * 4 <= STAGES * STAGE, "the epilogue's exchange fits the stages");
 };
 
-// Scales of the tile's values as f16, tokens in pairs, [D/16][64]; the scale of
-// a slot that does not exist is 0 (its bytes can be anything, NaN included).
+// Scales of a tile's values as f16, tokens in pairs, [D/16][64]; the scale of a
+// slot that does not exist is 0 (its bytes can be anything, NaN included).
 template <int D>
-__device__ __forceinline__ void value_scales(const uint8_t *stage, const int *nv, uint32_t *vs)
+__device__ __forceinline__ void value_scales(const uint8_t *tile, const int *nv, bool whole, uint32_t *vs)
 {
+    const int pair = threadIdx.x & 15, blk = threadIdx.x >> 4 & 3, g0 = threadIdx.x >> 6;
+    const int n = whole ? kTok : nv[blk] - 2 * pair;
 #pragma unroll
-    for (int i = threadIdx.x; i < D / 16 * 64; i += kAttnThreads) {
-        const int g = i / 64, blk = i % 64 / 16, pair = i % 16;
-        uint32_t s = *reinterpret_cast<const uint16_t *>(stage + blk * block_bytes(D) + v_scale_at(D) + g * kTok + 2 * pair);
-        const int n = nv[blk] - 2 * pair;
+    for (int g = 0; g < D / 16; g += 4) {
+        uint32_t s = *reinterpret_cast<const uint16_t *>(tile + blk * block_bytes(D) + v_scale_at(D) + (g0 + g) * kTok + 2 * pair);
         if (n < 2) s = n == 1 ? s & 255u : 0u;
-        vs[i] = e4m3x2(s);
+        vs[(g0 + g) * 64 + blk * 16 + pair] = e4m3x2(s);
     }
 }
 
@@ -104,7 +110,7 @@ __device__ __forceinline__ void decode_values(const uint8_t *blk, int d, const u
     tmem_st16(taddr, r);
 }
 
-// This warp's half of the tile's values into tensor memory
+// This warp's half of a tile's values into tensor memory
 template <typename A, bool WIDE>
 __device__ __forceinline__ void decode_tile_values(const uint8_t *stage, const uint32_t *vs, uint32_t taddr)
 {
@@ -124,22 +130,25 @@ __device__ __forceinline__ void decode_tile_values(const uint8_t *stage, const u
     }
 }
 
-// O^T += V^T P^T over the tile's tokens (one thread issues); the smaller term of
+// O^T += V^T P^T over the step's tokens (one thread issues); the smaller term of
 // P first, as in issue_scores
 template <typename A, bool WIDE>
-__device__ __forceinline__ void issue_values(uint32_t o_addr, uint32_t a_addr, const uint8_t *ps, bool accumulate)
+__device__ __forceinline__ void issue_values(uint32_t o_addr, uint32_t a_addr, const uint8_t *ps, int subs, bool accumulate)
 {
-    const uint32_t pa = smem_addr(ps);
     constexpr int PC = WIDE ? 1 : A::PIECES;
+#pragma unroll 1
+    for (int sub = 0; sub < subs; ++sub) {
+        const uint32_t pa = smem_addr(ps) + sub * A::PIECES * A::P_BYTES;
 #pragma unroll
-    for (int m = 0; m < A::VM; ++m)
+        for (int m = 0; m < A::VM; ++m)
 #pragma unroll
-        for (int pc = PC - 1; pc >= 0; --pc)
+            for (int pc = PC - 1; pc >= 0; --pc)
 #pragma unroll
-            for (int q = 0; q < A::VT / 16; ++q)
-                mma_f16(o_addr + m * A::NT, a_addr + m * 64 + q * 8,
-                        smem_desc(pa + pc * A::P_BYTES + q * 256, 128, A::VT * 16),
-                        mma_f16_desc(A::NT * A::HALVES, true, WIDE), accumulate || pc < PC - 1 || q > 0);
+                for (int q = 0; q < A::VT / 16; ++q)
+                    mma_f16(o_addr + m * A::NT, a_addr + sub * A::A_COLS + m * 64 + q * 8,
+                            smem_desc(pa + pc * A::P_BYTES + q * 256, 128, A::VT * 16),
+                            mma_f16_desc(A::NT * A::HALVES, true, WIDE), accumulate || sub > 0 || pc < PC - 1 || q > 0);
+    }
 }
 
 __device__ __forceinline__ uint32_t pack_bf2(float lo, float hi)
@@ -181,13 +190,30 @@ template <int NT> struct Columns {
     float red[4][NT];
 };
 
-// Scores of this thread's token in log2 units for N columns from q0 on, hidden
-// ones -inf.
-template <typename A, int N>
-__device__ __forceinline__ void tile_scores(const AttnParams &p, const Job &w, const Columns<A::NT> &cs, uint32_t s_addr,
-                                            int q0, int slot, int tpos, bool live, bool edge, bool options, float (&v)[N])
+// What a thread's token of a tile is.
+struct Token {
+    int slot, pos;
+    bool live;                  // it exists
+    bool edge;                  // some row may not see some token of the quarter
+};
+
+// Scores of a token in log2 units for N columns from q0 on, hidden ones -inf;
+// with REF the column's reference added (x + headroom).
+template <typename A, int N, bool REF>
+__device__ __forceinline__ void token_scores(const AttnParams &p, const Job &w, const Columns<A::NT> &cs, uint32_t s_addr,
+                                             int q0, const Token &t, bool options, float (&v)[N])
 {
     load_products<N, A::NT, A::PIECES>(s_addr + q0, v);
+    if (!t.edge && !options) {
+        // two columns an instruction
+#pragma unroll
+        for (int q = 0; q < N; q += 2) {
+            const uint64_t m = *reinterpret_cast<const uint64_t *>(&cs.mult[q0 + q]);
+            const uint64_t r = REF ? *reinterpret_cast<const uint64_t *>(&cs.ref[q0 + q]) : 0ull;
+            f2_unpack(f2_fma(f2_pack(v[q], v[q + 1]), m, r), v[q], v[q + 1]);
+        }
+        return;
+    }
 #pragma unroll
     for (int q = 0; q < N; ++q) v[q] *= cs.mult[q0 + q];
     if (options) {
@@ -197,21 +223,75 @@ __device__ __forceinline__ void tile_scores(const AttnParams &p, const Job &w, c
             for (int q = 0; q < N; ++q) v[q] = cap_score<A::PIECES == 2>(v[q], cap, rcap);
         }
 #pragma unroll
-        for (int q = 0; q < N; ++q) v[q] -= cs.slope[q0 + q] * static_cast<float>(cs.pos[q0 + q] - tpos);
+        for (int q = 0; q < N; ++q) v[q] -= cs.slope[q0 + q] * static_cast<float>(cs.pos[q0 + q] - t.pos);
     }
-    if (edge || options) {
-        const bool always = live && (p.window <= 0 || slot < p.prefix);
+    const bool always = t.live && (p.window <= 0 || t.slot < p.prefix);
 #pragma unroll
-        for (int q = 0; q < N; ++q) {
-            const bool see = slot <= cs.own[q0 + q] && (always || (live && cs.pos[q0 + q] - tpos < p.window)) &&
-                             q0 + q < w.ncols;
-            v[q] = see ? v[q] : -INFINITY;
-        }
+    for (int q = 0; q < N; ++q) {
+        const bool see = t.slot <= cs.own[q0 + q] && (always || (t.live && cs.pos[q0 + q] - t.pos < p.window)) &&
+                         q0 + q < w.ncols;
+        v[q] = see ? v[q] + (REF ? cs.ref[q0 + q] : 0.f) : -INFINITY;
     }
 }
 
+// Move the references to the step's maxima where those are larger, and set the
+// factors that take the sums and results along.
+template <typename A>
+__device__ __forceinline__ void move_references(const AttnParams &p, const Job &w, Columns<A::NT> &cs, uint32_t s_addr,
+                                                const Token (&t)[A::SUB], int subs, bool options)
+{
+    const int tid = threadIdx.x, lane = tid & 31, quarter = tid >> 5 & 3, half = tid >> 7;
+#pragma unroll 1
+    for (int q0 = half * A::NH; q0 < (half + 1) * A::NH; q0 += 8) {
+        float most[8], x[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) most[q] = -INFINITY;
+#pragma unroll
+        for (int sub = 0; sub < A::SUB; ++sub) {
+            if (sub >= subs) break;
+            token_scores<A, 8, false>(p, w, cs, s_addr + sub * A::S_COLS, q0, t[sub], options, x);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) most[q] = fmaxf(most[q], x[q]);
+        }
+        float mine = 0.f;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            const float m = warp_max_f32(most[q]);
+            if (lane == q) mine = m;
+        }
+        if (lane < 8) cs.red[quarter][q0 + lane] = mine;
+    }
+    __syncthreads();
+    if (tid < w.ncols) {
+        const float old = kHeadroom - cs.ref[tid];
+        const float m = fmaxf(old, fmaxf(fmaxf(cs.red[0][tid], cs.red[1][tid]), fmaxf(cs.red[2][tid], cs.red[3][tid])));
+        cs.factor[tid] = ex2(old - m);
+        cs.ref[tid] = kHeadroom - m;
+    } else if (tid < A::NT) {
+        cs.factor[tid] = 1.f;
+    }
+    __syncthreads();
+}
+
+// Rescale this thread's columns of the results in tensor memory
+template <typename A>
+__device__ __forceinline__ void rescale_results(const Columns<A::NT> &cs, uint32_t o_addr)
+{
+    const int half = threadIdx.x >> 7;
+#pragma unroll 1
+    for (int q0 = half * A::O_COLS / 2; q0 < (half + 1) * A::O_COLS / 2; q0 += 8) {
+        uint32_t r[8];
+        tmem_ld<8>(o_addr + q0, r);
+        tmem_wait_ld();
+#pragma unroll
+        for (int q = 0; q < 8; ++q) r[q] = __float_as_uint(__uint_as_float(r[q]) * cs.factor[(q0 + q) % A::NT]);
+        tmem_st8(o_addr + q0, r);
+    }
+    tmem_wait_st();
+}
+
 struct Split {
-    int tiles, most;            // tiles of a split, splits of the longest request
+    int steps, most;            // steps of a split, splits of the longest request
     int qtiles, cols;           // column tiles, columns of a request at most
 };
 
@@ -225,12 +305,12 @@ attend_kernel(const CacheView c, const AttnParams p, const Split sp)
     constexpr int OR = kPromote ? NH * A::VM : 1;     // fp32: results kept in registers
     extern __shared__ __align__(128) uint8_t smem[];
     uint8_t *qs = smem, *ps = qs + A::PIECES * A::Q_BYTES;
-    uint32_t *vs = reinterpret_cast<uint32_t *>(ps + A::PIECES * A::P_BYTES);
-    uint8_t *stages = ps + A::PIECES * A::P_BYTES + A::VS_BYTES;
+    uint32_t *vs = reinterpret_cast<uint32_t *>(ps + A::SUB * A::PIECES * A::P_BYTES);
+    uint8_t *stages = ps + A::SUB * (A::PIECES * A::P_BYTES + A::VS_BYTES);
     __shared__ __align__(16) Columns<NT> cs;
     __shared__ __align__(8) uint64_t full[A::STAGES], s_bar, o_bar;
     __shared__ uint32_t tmem_base, arrived;
-    __shared__ int nv[A::STAGES][4];
+    __shared__ __align__(16) int nv[A::STAGES][A::BLOCKS];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int quarter = warp & 3, half = warp >> 2, tok = tid & 127;
 
@@ -248,11 +328,11 @@ attend_kernel(const CacheView c, const AttnParams p, const Split sp)
         if (tid == 0) set_status(p.status, SPEC_STATUS_BAD_LENGTH);
         w.len = 0;
     }
-    if (split > 0 && split * sp.tiles * kTile >= w.len) return;
-    visible_tiles(c, p, w);
-    const int nsplit = max((w.ntiles + sp.tiles - 1) / sp.tiles, 1);
+    if (split > 0 && split * sp.steps * A::STEP >= w.len) return;
+    visible_steps<A::STEP>(c, p, w);
+    const int nsplit = max((w.nsteps + sp.steps - 1) / sp.steps, 1);
     if (split >= nsplit) return;
-    const int i0 = split * sp.tiles, i1 = min(i0 + sp.tiles, w.ntiles);
+    const int i0 = split * sp.steps, i1 = min(i0 + sp.steps, w.nsteps);
 
     int page = -1;
     if (warp == kLoadWarp) {
@@ -263,12 +343,13 @@ attend_kernel(const CacheView c, const AttnParams p, const Split sp)
             fence_mbar_init();
         }
         __syncwarp();
-        // the first tiles' loads go out before anything else
+        // the first loads go out before anything else
         for (int i = 0; i < A::STAGES && i0 + i < i1; ++i) {
-            const int tile = tile_of(w, i0 + i);
-            load_tile<block_bytes(D)>(c, w, w.h, tile, tile_page(c, w, tile), stages + i * A::STAGE, &full[i], nv[i], p.status);
+            const int slot = step_slot<A::STEP>(w, i0 + i);
+            load_step<block_bytes(D), A::BLOCKS>(c, w, w.h, slot, step_page<A::BLOCKS>(c, w, slot), stages + i * A::STAGE,
+                                                 &full[i], nv[i], p.status);
         }
-        if (i0 + A::STAGES < i1) page = tile_page(c, w, tile_of(w, i0 + A::STAGES));
+        if (i0 + A::STAGES < i1) page = step_page<A::BLOCKS>(c, w, step_slot<A::STEP>(w, i0 + A::STAGES));
     }
     if (warp == 0) tmem_alloc(&tmem_base, A::COLS);
     if (tid < NT) {
@@ -285,7 +366,7 @@ attend_kernel(const CacheView c, const AttnParams p, const Split sp)
     __syncthreads();
     tmem_fence_after();
     const bool options = p.cap > 0.f || p.slopes || p.window > 0;
-    const uint32_t a_t = tmem_base, s_t = a_t + A::A_COLS, o_t = s_t + A::PIECES * NT;
+    const uint32_t a_t = tmem_base, s_t = a_t + A::SUB * A::A_COLS, o_t = s_t + A::SUB * A::S_COLS;
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
     // where this thread's columns of the result lie (D = 64: those of its tokens)
     const uint32_t o_mine = o_t + lane_off + half * NH + (D == 64 && quarter >= 2 ? NT : 0);
@@ -310,171 +391,173 @@ attend_kernel(const CacheView c, const AttnParams p, const Split sp)
     bool fail = false;
     int o_count = 0;                                                 // completed products with V^T
     const int own_first = cs.own[0];
+    constexpr int PN8 = A::VT * 16;
+    uint8_t *const p_mine = ps + (tok / A::VT * (NT / 8) + half * (NH / 8)) * PN8 + tok % A::VT * 16;
     for (int i = i0; i < i1; ++i) {
-        const int k = i - i0, st = k % A::STAGES, tile = tile_of(w, i);
-        uint8_t *stage = stages + st * A::STAGE;
-        const int slot = tile * kTile + tok;
-        int tpos = slot;
-        fail |= !mbar_wait(&full[st], k / A::STAGES & 1);
-        const bool live = lane < nv[st][quarter];
-        if (options && p.slot_pos && live) tpos = slot_position(c, p, w.b, slot);
-        value_scales<D>(stage, nv[st], vs + 0);
+        const int k = i - i0, st = k % A::STAGES, slot0 = step_slot<A::STEP>(w, i);
+        const uint8_t *stage = stages + st * A::STAGE;
+        const int subs = A::SUB == 1 || w.len - slot0 <= kTile ? 1 : 2;
+        wait_or_fail(&full[st], k / A::STAGES & 1, fail);
+        Token t[A::SUB];
+        bool whole = true;
+#pragma unroll
+        for (int sub = 0; sub < A::SUB; ++sub) {
+            const int4 n = *reinterpret_cast<const int4 *>(&nv[st][4 * sub]);
+            const bool w32 = (n.x & n.y & n.z & n.w) == kTok;        // (each at most 32)
+            whole = whole && w32;
+            t[sub].slot = t[sub].pos = slot0 + sub * kTile + tok;
+            t[sub].live = w32 || lane < nv[st][4 * sub + quarter];
+            t[sub].edge = !w32 || slot0 + sub * kTile + kTile - 1 > own_first;
+            if (options && p.slot_pos && t[sub].live) t[sub].pos = slot_position(c, p, w.b, t[sub].slot);
+        }
+#pragma unroll 1
+        for (int sub = 0; sub < subs; ++sub)
+            value_scales<D>(stage + sub * 4 * block_bytes(D), &nv[st][4 * sub], whole, vs + sub * (A::VS_BYTES / 4));
         if (k > 0) {
-            fail |= !mbar_wait(&o_bar, o_count++ & 1);               // V^T of the last tile is used up
+            wait_or_fail(&o_bar, o_count++ & 1, fail);               // V^T of the last step is used up
             tmem_fence_after();
             promote();
         }
-        decode_keys<D>(stage + quarter * block_bytes(D), a_t + lane_off);
+#pragma unroll 1
+        for (int sub = 0; sub < subs; ++sub)
+            decode_keys<D>(stage + (sub * 4 + quarter) * block_bytes(D), a_t + sub * A::A_COLS + lane_off);
         tmem_wait_st();
         tmem_fence_before();
-        if (__syncthreads_or(fail)) break;
+        __syncthreads();
         if (tid == 0) {
             tmem_fence_after();
-            issue_scores<D, NT, A::PIECES>(s_t, a_t, qs);
+#pragma unroll 1
+            for (int sub = 0; sub < subs; ++sub)
+                issue_scores<D, NT, A::PIECES>(s_t + sub * A::S_COLS, a_t + sub * A::A_COLS, qs);
             mma_commit(&s_bar);
         }
-        const bool edge = (tile + 1) * kTile - 1 > own_first || nv[st][quarter] < kTok;
-        fail |= !mbar_wait(&s_bar, k & 1);
+        wait_or_fail(&s_bar, k & 1, fail);
         tmem_fence_after();
-        float v[NH];
+        float v[A::SUB][NH];
         bool wide = false;
         for (;;) {
-            tile_scores<A, NH>(p, w, cs, s_t + lane_off, half * NH, slot, tpos, live, edge, options, v);
             float most = -INFINITY, least = INFINITY;
 #pragma unroll
-            for (int q = 0; q < NH; ++q) {
-                v[q] += cs.ref[half * NH + q];
-                most = fmaxf(most, v[q]);
-            }
-            if (edge || options) {
+            for (int sub = 0; sub < A::SUB; ++sub) {
+                if (sub >= subs) break;
+                token_scores<A, NH, true>(p, w, cs, s_t + sub * A::S_COLS + lane_off, half * NH, t[sub], options, v[sub]);
 #pragma unroll
-                for (int q = 0; q < NH; ++q) least = fminf(least, v[q] == -INFINITY ? INFINITY : v[q]);
-            } else {
+                for (int q = 0; q < NH; ++q) most = fmaxf(most, v[sub][q]);
+                if (t[sub].edge || options) {
 #pragma unroll
-                for (int q = 0; q < NH; ++q) least = fminf(least, v[q]);
+                    for (int q = 0; q < NH; ++q) least = fminf(least, v[sub][q] == -INFINITY ? INFINITY : v[sub][q]);
+                } else {
+#pragma unroll
+                    for (int q = 0; q < NH; ++q) least = fminf(least, v[sub][q]);
+                }
             }
             if (!__syncthreads_or(most > kExceed || least < A::LEAST_EXP)) break;
             if (!__syncthreads_or(most > kExceed)) {
                 wide = true;
                 break;
             }
-            // move the references to the tile's maxima
-#pragma unroll 1
-            for (int q0 = half * NH; q0 < half * NH + NH; q0 += 8) {
-                float x[8];
-                tile_scores<A, 8>(p, w, cs, s_t + lane_off, q0, slot, tpos, live, edge, options, x);
-                float mine = 0.f;
-#pragma unroll
-                for (int q = 0; q < 8; ++q) {
-                    const float m = warp_max_f32(x[q]);
-                    if (lane == q) mine = m;
-                }
-                if (lane < 8) cs.red[quarter][q0 + lane] = mine;
-            }
-            __syncthreads();
-            if (tid < w.ncols) {
-                const float old = kHeadroom - cs.ref[tid];
-                const float m = fmaxf(old, fmaxf(fmaxf(cs.red[0][tid], cs.red[1][tid]), fmaxf(cs.red[2][tid], cs.red[3][tid])));
-                cs.factor[tid] = ex2(old - m);
-                cs.ref[tid] = kHeadroom - m;
-            } else if (tid < NT) {
-                cs.factor[tid] = 1.f;
-            }
-            __syncthreads();
+            move_references<A>(p, w, cs, s_t + lane_off, t, subs, options);
 #pragma unroll
             for (int q = 0; q < NH; ++q) l[q] *= cs.factor[half * NH + q];
             if (kPromote) {
 #pragma unroll
                 for (int q = 0; q < OR; ++q) acc[q] *= cs.factor[half * NH + q % NH];
             } else if (k > 0) {
-#pragma unroll 1
-                for (int q0 = half * A::O_COLS / 2; q0 < (half + 1) * A::O_COLS / 2; q0 += 8) {
-                    uint32_t r[8];
-                    tmem_ld<8>(o_t + lane_off + q0, r);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int q = 0; q < 8; ++q) r[q] = __float_as_uint(__uint_as_float(r[q]) * cs.factor[(q0 + q) % NT]);
-                    tmem_st8(o_t + lane_off + q0, r);
-                }
-                tmem_wait_st();
+                rescale_results<A>(cs, o_t + lane_off);
             }
         }
         // weights: sums in fp32, the operand 8 columns of this token per store
-#pragma unroll
-        for (int q = 0; q < NH; ++q) {
-            v[q] = ex2(v[q]);
-            l[q] += v[q];
-        }
-        constexpr int PN8 = A::VT * 16;
-        uint8_t *dst = ps + (tok / A::VT * (NT / 8) + half * (NH / 8)) * PN8 + tok % A::VT * 16;
         const bool accumulate = !kPromote && k > 0;
-        if (!wide) {
+#pragma unroll
+        for (int sub = 0; sub < A::SUB; ++sub) {
+            if (sub >= subs) break;
+#pragma unroll
+            for (int q = 0; q < NH; q += 2) {
+                v[sub][q] = ex2(v[sub][q]);
+                v[sub][q + 1] = ex2(v[sub][q + 1]);
+                f2_unpack(f2_add(f2_pack(l[q], l[q + 1]), f2_pack(v[sub][q], v[sub][q + 1])), l[q], l[q + 1]);
+            }
+            if (wide) continue;
+            uint8_t *dst = p_mine + sub * A::PIECES * A::P_BYTES;
 #pragma unroll
             for (int q0 = 0; q0 < NH; q0 += 8) {
                 uint32_t hi[4];
 #pragma unroll
-                for (int q = 0; q < 4; ++q) hi[q] = pack_h2(v[q0 + 2 * q], v[q0 + 2 * q + 1]);
+                for (int q = 0; q < 4; ++q) hi[q] = pack_h2(v[sub][q0 + 2 * q], v[sub][q0 + 2 * q + 1]);
                 *reinterpret_cast<uint4 *>(dst + q0 / 8 * PN8) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
                 if (A::PIECES == 2) {
                     uint32_t lo[4];
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
                         const float2 y = h2_float2(hi[q]);
-                        lo[q] = pack_h2(v[q0 + 2 * q] - y.x, v[q0 + 2 * q + 1] - y.y);
+                        lo[q] = pack_h2(v[sub][q0 + 2 * q] - y.x, v[sub][q0 + 2 * q + 1] - y.y);
                     }
                     *reinterpret_cast<uint4 *>(dst + A::P_BYTES + q0 / 8 * PN8) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                 }
             }
+        }
+        if (!wide) {
             // values over the keys' columns (the product that read them is complete)
-            decode_tile_values<A, false>(stage, vs, a_t + lane_off);
+#pragma unroll 1
+            for (int sub = 0; sub < subs; ++sub)
+                decode_tile_values<A, false>(stage + sub * 4 * block_bytes(D), vs + sub * (A::VS_BYTES / 4),
+                                             a_t + sub * A::A_COLS + lane_off);
             tmem_wait_st();
             tmem_fence_before();
             fence_proxy_async_smem();
-            if (__syncthreads_or(fail)) break;
+            __syncthreads();
             if (tid == 0) {
                 tmem_fence_after();
-                issue_values<A, false>(o_t, a_t, ps, accumulate);
+                issue_values<A, false>(o_t, a_t, ps, subs, accumulate);
                 mma_commit(&o_bar);
             }
         } else {
-            decode_tile_values<A, true>(stage, vs, a_t + lane_off);
+#pragma unroll 1
+            for (int sub = 0; sub < subs; ++sub)
+                decode_tile_values<A, true>(stage + sub * 4 * block_bytes(D), vs + sub * (A::VS_BYTES / 4),
+                                            a_t + sub * A::A_COLS + lane_off);
             tmem_wait_st();
 #pragma unroll 1
             for (int pc = 0; pc < A::WIDE; ++pc) {
-                if (pc > 0) fail |= !mbar_wait(&o_bar, o_count++ & 1);
+                if (pc > 0) wait_or_fail(&o_bar, o_count++ & 1, fail);
 #pragma unroll
-                for (int q0 = 0; q0 < NH; q0 += 8) {
-                    uint32_t term[4];
+                for (int sub = 0; sub < A::SUB; ++sub) {
+                    if (sub >= subs) break;
+                    uint8_t *dst = p_mine + sub * A::PIECES * A::P_BYTES;
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        float &x = v[q0 + 2 * q], &y = v[q0 + 2 * q + 1];
-                        if (pc == 0) {
-                            x *= kWideScale;
-                            y *= kWideScale;
+                    for (int q0 = 0; q0 < NH; q0 += 8) {
+                        uint32_t term[4];
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            float &x = v[sub][q0 + 2 * q], &y = v[sub][q0 + 2 * q + 1];
+                            if (pc == 0) {
+                                x *= kWideScale;
+                                y *= kWideScale;
+                            }
+                            term[q] = pack_bf2(x, y);
+                            x -= bf_lo(term[q]);
+                            y -= bf_hi(term[q]);
                         }
-                        term[q] = pack_bf2(x, y);
-                        x -= bf_lo(term[q]);
-                        y -= bf_hi(term[q]);
+                        *reinterpret_cast<uint4 *>(dst + q0 / 8 * PN8) = make_uint4(term[0], term[1], term[2], term[3]);
                     }
-                    *reinterpret_cast<uint4 *>(dst + q0 / 8 * PN8) = make_uint4(term[0], term[1], term[2], term[3]);
                 }
                 tmem_fence_before();
                 fence_proxy_async_smem();
-                if (__syncthreads_or(fail)) break;
+                __syncthreads();
                 if (tid == 0) {
                     tmem_fence_after();
-                    issue_values<A, true>(o_t, a_t, ps, accumulate || pc > 0);
+                    issue_values<A, true>(o_t, a_t, ps, subs, accumulate || pc > 0);
                     mma_commit(&o_bar);
                 }
             }
-            if (__syncthreads_or(fail)) break;
         }
         if (warp == kLoadWarp && i + A::STAGES < i1) {
-            load_tile<block_bytes(D)>(c, w, w.h, tile_of(w, i + A::STAGES), page, stage, &full[st], nv[st], p.status);
-            page = i + A::STAGES + 1 < i1 ? tile_page(c, w, tile_of(w, i + A::STAGES + 1)) : -1;
+            load_step<block_bytes(D), A::BLOCKS>(c, w, w.h, step_slot<A::STEP>(w, i + A::STAGES), page,
+                                                 stages + st * A::STAGE, &full[st], nv[st], p.status);
+            page = i + A::STAGES + 1 < i1 ? step_page<A::BLOCKS>(c, w, step_slot<A::STEP>(w, i + A::STAGES + 1)) : -1;
         }
     }
-    if (i1 > i0 && !fail) fail = !mbar_wait(&o_bar, o_count & 1);
+    if (i1 > i0) wait_or_fail(&o_bar, o_count & 1, fail);
     if (__syncthreads_or(fail)) {
         // a wait gave up: let the copies in flight land (bounded), then leave
         if (tid == 0) {
@@ -595,7 +678,14 @@ attend_kernel(const CacheView c, const AttnParams p, const Split sp)
     }
 }
 
-// Tiles of a split: as many splits as a few rounds of resident CTAs need, so
+// tokens of a step of the kernel for these
+int step_tokens(int D, int nt, int dtype)
+{
+    const int pieces = dtype == SPEC_F32 ? 2 : 1, a = D == 256 ? 128 : D / 2, o = nt * (D == 128 ? 1 : 2);
+    return 2 * (a + pieces * nt) + o <= 256 ? 2 * kTile : kTile;
+}
+
+// Steps of a split: as many splits as a few rounds of resident CTAs need, so
 // that ragged requests even out.
 Split split_of(int B, int k_max, int Hq, int H, int D, int max_len, int dtype)
 {
@@ -603,12 +693,13 @@ Split split_of(int B, int k_max, int Hq, int H, int D, int max_len, int dtype)
     s.cols = (k_max + 1) * (Hq / H);
     const int nt = column_tile(s.cols, D, dtype);
     s.qtiles = (s.cols + nt - 1) / nt;
-    const int tiles = (max_len + kTile - 1) / kTile;
-    const int64_t all = static_cast<int64_t>(B) * H * s.qtiles * tiles;
-    const int64_t slots = 152 * 4 * 2;
+    const int step = step_tokens(D, nt, dtype);
+    const int steps = (max_len + step - 1) / step;
+    const int64_t all = static_cast<int64_t>(B) * H * s.qtiles * steps;
+    const int64_t slots = 152 * 2 * 4;
     const int64_t t = (all + slots - 1) / slots;
-    s.tiles = static_cast<int>(t < 1 ? 1 : (t > tiles ? tiles : t));
-    s.most = (tiles + s.tiles - 1) / s.tiles;
+    s.steps = static_cast<int>(t < 1 ? 1 : (t > steps ? steps : t));
+    s.most = (steps + s.steps - 1) / s.steps;
     return s;
 }
 
@@ -616,6 +707,7 @@ template <typename T, int D, int NT>
 cudaError_t launch_one(const CacheView &c, const AttnParams &p, const Split &sp, cudaStream_t s)
 {
     using A = Attn<T, D, NT>;
+    if (step_tokens(D, NT, sizeof(T) == 4 ? SPEC_F32 : SPEC_BF16) != A::STEP) return cudaErrorInvalidValue;
     static bool done[64] = {false};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);

@@ -69,8 +69,8 @@ weights_kernel(const CacheView c, const AttnParams p, const int tiles)
     }
     const int i0 = blockIdx.x * tiles;
     if (i0 * kTile >= w.len) return;
-    visible_tiles(c, p, w);
-    const int nt = min(tiles, w.ntiles - i0);
+    visible_steps<kTile>(c, p, w);
+    const int nt = min(tiles, w.nsteps - i0);
     if (nt <= 0) return;
 
     const int cols = w.n * group, qt_used = (cols + NT - 1) / NT;
@@ -81,8 +81,8 @@ weights_kernel(const CacheView c, const AttnParams p, const int tiles)
     };
     const auto load = [&](int i) {
         const Step s = step_at(i);
-        const int tile = tile_of(w, i0 + s.t);
-        load_tile<A::K_BYTES>(c, w, s.h, tile, tile_page(c, w, tile), stages + i % A::STAGES * A::STAGE,
+        const int slot = step_slot<kTile>(w, i0 + s.t);
+        load_step<A::K_BYTES, 4>(c, w, s.h, slot, step_page<4>(c, w, slot), stages + i % A::STAGES * A::STAGE,
                               &full[i % A::STAGES], nv[i % A::STAGES], p.status);
     };
     if (warp == kLoadWarp) {
@@ -127,11 +127,11 @@ weights_kernel(const CacheView c, const AttnParams p, const int tiles)
     // weights of a finished product
     const auto add_weights = [&](int i, const Heads<NT> &set) {
         const Step s = step_at(i);
-        const int tile = tile_of(w, i0 + s.t), slot = tile * kTile + tok;
+        const int slot0 = step_slot<kTile>(w, i0 + s.t), slot = slot0 + tok;
         const int valid = min(max(w.len - (slot - lane), 0), kTok);
         float v[NH];
         load_products<NH, NT, A::PIECES>(s_t + (i & 1) * A::S_COLS + lane_off + half * NH, v);
-        const bool edge = (tile + 1) * kTile - 1 > set.own[0] || valid < kTok;
+        const bool edge = slot0 + kTile - 1 > set.own[0] || valid < kTok;
         float sum = 0.f;
         if (edge || options) {
             const bool live = lane < valid;
@@ -160,18 +160,18 @@ weights_kernel(const CacheView c, const AttnParams p, const int tiles)
         const int st = i % A::STAGES;
         const int cb_last = cb;
         if (i > 0) {
-            fail |= !mbar_wait(&s_bar, (i - 1) & 1);       // the keys' columns are used up
+            wait_or_fail(&s_bar, (i - 1) & 1, fail);       // the keys' columns are used up
             tmem_fence_after();
             if (i % nt == 0) {
                 cb = cb == 2 ? 0 : cb + 1;
                 qb ^= 1;
             }
         }
-        fail |= !mbar_wait(&full[st], i / A::STAGES & 1);
+        wait_or_fail(&full[st], i / A::STAGES & 1, fail);
         decode_keys<D>(stages + st * A::STAGE + quarter * A::K_BYTES, a_t + lane_off);
         tmem_wait_st();
         tmem_fence_before();
-        if (__syncthreads_or(fail)) break;
+        __syncthreads();
         if (tid == 0) {
             tmem_fence_after();
             issue_scores<D, NT, A::PIECES>(s_t + (i & 1) * A::S_COLS, a_t, qs + qb * A::Q_BYTES);
@@ -182,7 +182,7 @@ weights_kernel(const CacheView c, const AttnParams p, const int tiles)
             stage_head(i + 1, sets[cb == 2 ? 0 : cb + 1], qs + (qb ^ 1) * A::Q_BYTES);
         if (i > 0) add_weights(i - 1, sets[cb_last]);
     }
-    if (!fail) fail = !mbar_wait(&s_bar, (steps - 1) & 1);
+    wait_or_fail(&s_bar, (steps - 1) & 1, fail);
     tmem_fence_after();
     if (__syncthreads_or(fail)) {
         if (tid == 0) {
@@ -194,7 +194,7 @@ weights_kernel(const CacheView c, const AttnParams p, const int tiles)
         add_weights(steps - 1, sets[cb]);
         __syncthreads();
         for (int t = half; t < nt; t += 2) {
-            const int slot = tile_of(w, i0 + t) * kTile + tok;
+            const int slot = step_slot<kTile>(w, i0 + t) + tok;
             const int page = slot < w.len ? page_of(c, w.b, slot) : -1;
             if (page >= 0)
                 p.score[static_cast<int64_t>(page) * c.page_tokens + slot % c.page_tokens] += acc[t][0][tok] + acc[t][1][tok];
