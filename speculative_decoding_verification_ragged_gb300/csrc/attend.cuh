@@ -14,7 +14,7 @@ namespace specv {
 
 constexpr int kAttnThreads = 256;
 constexpr int kTile = 128;                 // tokens of a tile: 4 blocks, the lanes of tensor memory
-constexpr int kLoadWarp = 7;               // the warp that fetches steps
+constexpr int kLoadWarp = 7;               // the warp that fetches tiles (weights)
 
 // What a CTA works on.
 struct Job {
@@ -237,9 +237,8 @@ __device__ __forceinline__ void stage_queries(const AttnParams &p, const Job &w,
 // a sum at its last place, and adding the small products of the second term to
 // the large sum would cost a bit or two in every step.
 template <int D, int NT, int PIECES>
-__device__ __forceinline__ void issue_scores(uint32_t s_addr, uint32_t a_addr, const uint8_t *qs)
+__device__ __forceinline__ void issue_scores(uint32_t s_addr, uint32_t a_addr, uint32_t q)
 {
-    const uint32_t q = smem_addr(qs);
 #pragma unroll
     for (int pc = 0; pc < PIECES; ++pc)
 #pragma unroll

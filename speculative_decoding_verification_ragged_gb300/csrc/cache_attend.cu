@@ -43,7 +43,7 @@ template <typename T, int D_, int NT_> struct Attn {
     static constexpr int D = D_, NT = NT_;
     static constexpr int NH = NT / 2;                          // columns of a thread
     static constexpr int PIECES = sizeof(T) == 4 ? 2 : 1;      // f16 terms of a query and of a weight
-    static constexpr int WIDE = sizeof(T) == 4 ? 3 : 2;        // bf16 terms of a weight in a wide step
+    static constexpr int WIDE = sizeof(T) == 4 ? 3 : 2;        // bf16 terms of a weight in a wide tile
     // exponent of the smallest weight with its bits in f16: a normal number; for
     // two terms 15 bits above the last place, 2^-25
     static constexpr float LEAST_EXP = sizeof(T) == 4 ? -10.f : -14.f;
@@ -52,21 +52,17 @@ template <typename T, int D_, int NT_> struct Attn {
     static constexpr int HALVES = D == 64 ? 2 : 1;
     static constexpr int VM = D == 256 ? 2 : 1;
     static constexpr int VT = kTile / HALVES;                  // tokens of a V^T row
-    static constexpr int A_COLS = D == 256 ? 128 : D / 2;      // tensor memory of a tile's K, then of its V^T
+    static constexpr int A_COLS = D / 2;                       // tensor memory of a tile's K
     static constexpr int S_COLS = PIECES * NT;
     static constexpr int O_COLS = NT * HALVES * VM;
-    // Tiles of a step, where 256 columns hold them: barriers, waits and column
-    // constants are paid once a step (32 x 5 rows x 4096 tokens: 115 us with one
-    // tile a step and 4 CTAs an SM).
-    static constexpr int SUB = 2 * (A_COLS + S_COLS) + O_COLS <= 256 ? 2 : 1;
-    static constexpr int STEP = SUB * kTile, BLOCKS = 4 * SUB;
-    static constexpr int COLS = tmem_cols(SUB * (A_COLS + S_COLS) + O_COLS);
+    static constexpr int V_COLS = D == 64 ? 32 : 64 * VM;      // tensor memory of a tile's V^T
+    static constexpr int COLS = tmem_cols(A_COLS + V_COLS + S_COLS + O_COLS);
     static constexpr int CTAS = COLS <= 256 ? 2 : 1;
     static constexpr int Q_BYTES = NT * D * 2;
     static constexpr int P_BYTES = kTile * NT * 2;             // a term of a tile's weights
     static constexpr int VS_BYTES = D / 16 * kTile * 2;        // a tile's scales of V as f16
-    static constexpr int STAGE = BLOCKS * block_bytes(D);
-    static constexpr int OPERANDS = PIECES * (Q_BYTES + SUB * P_BYTES) + SUB * VS_BYTES;
+    static constexpr int STAGE = 4 * block_bytes(D);
+    static constexpr int OPERANDS = PIECES * (Q_BYTES + P_BYTES) + 2 * VS_BYTES;
     static constexpr int STAGES = clamp_stages((smem_share(CTAS, 128 + 60 * NT) - OPERANDS) / STAGE);
     static constexpr int NEED = OPERANDS + STAGES * STAGE;
     static constexpr int SMEM = NEED > smem_least(CTAS) ? NEED : smem_least(CTAS);
@@ -130,25 +126,21 @@ __device__ __forceinline__ void decode_tile_values(const uint8_t *stage, const u
     }
 }
 
-// O^T += V^T P^T over the step's tokens (one thread issues); the smaller term of
+// O^T += V^T P^T over the tile's tokens (one thread issues); the smaller term of
 // P first, as in issue_scores
 template <typename A, bool WIDE>
-__device__ __forceinline__ void issue_values(uint32_t o_addr, uint32_t a_addr, const uint8_t *ps, int subs, bool accumulate)
+__device__ __forceinline__ void issue_values(uint32_t o_addr, uint32_t v_addr, uint32_t ps, bool accumulate)
 {
     constexpr int PC = WIDE ? 1 : A::PIECES;
-#pragma unroll 1
-    for (int sub = 0; sub < subs; ++sub) {
-        const uint32_t pa = smem_addr(ps) + sub * A::PIECES * A::P_BYTES;
 #pragma unroll
-        for (int m = 0; m < A::VM; ++m)
+    for (int m = 0; m < A::VM; ++m)
 #pragma unroll
-            for (int pc = PC - 1; pc >= 0; --pc)
+        for (int pc = PC - 1; pc >= 0; --pc)
 #pragma unroll
-                for (int q = 0; q < A::VT / 16; ++q)
-                    mma_f16(o_addr + m * A::NT, a_addr + sub * A::A_COLS + m * 64 + q * 8,
-                            smem_desc(pa + pc * A::P_BYTES + q * 256, 128, A::VT * 16),
-                            mma_f16_desc(A::NT * A::HALVES, true, WIDE), accumulate || sub > 0 || pc < PC - 1 || q > 0);
-    }
+            for (int q = 0; q < A::VT / 16; ++q)
+                mma_f16(o_addr + m * A::NT, v_addr + m * 64 + q * 8,
+                        smem_desc(ps + pc * A::P_BYTES + q * 256, 128, A::VT * 16),
+                        mma_f16_desc(A::NT * A::HALVES, true, WIDE), accumulate || pc < PC - 1 || q > 0);
 }
 
 __device__ __forceinline__ uint32_t pack_bf2(float lo, float hi)
@@ -234,34 +226,26 @@ __device__ __forceinline__ void token_scores(const AttnParams &p, const Job &w, 
     }
 }
 
-// Move the references to the step's maxima where those are larger, and set the
+// Move the references to the tile's maxima where those are larger, and set the
 // factors that take the sums and results along.
 template <typename A>
 __device__ __forceinline__ void move_references(const AttnParams &p, const Job &w, Columns<A::NT> &cs, uint32_t s_addr,
-                                                const Token (&t)[A::SUB], int subs, bool options)
+                                                const Token &t, bool options)
 {
     const int tid = threadIdx.x, lane = tid & 31, quarter = tid >> 5 & 3, half = tid >> 7;
 #pragma unroll 1
     for (int q0 = half * A::NH; q0 < (half + 1) * A::NH; q0 += 8) {
-        float most[8], x[8];
-#pragma unroll
-        for (int q = 0; q < 8; ++q) most[q] = -INFINITY;
-#pragma unroll
-        for (int sub = 0; sub < A::SUB; ++sub) {
-            if (sub >= subs) break;
-            token_scores<A, 8, false>(p, w, cs, s_addr + sub * A::S_COLS, q0, t[sub], options, x);
-#pragma unroll
-            for (int q = 0; q < 8; ++q) most[q] = fmaxf(most[q], x[q]);
-        }
+        float x[8];
+        token_scores<A, 8, false>(p, w, cs, s_addr, q0, t, options, x);
         float mine = 0.f;
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
-            const float m = warp_max_f32(most[q]);
+            const float m = warp_max_f32(x[q]);
             if (lane == q) mine = m;
         }
         if (lane < 8) cs.red[quarter][q0 + lane] = mine;
     }
-    __syncthreads();
+    csync();
     if (tid < w.ncols) {
         const float old = kHeadroom - cs.ref[tid];
         const float m = fmaxf(old, fmaxf(fmaxf(cs.red[0][tid], cs.red[1][tid]), fmaxf(cs.red[2][tid], cs.red[3][tid])));
@@ -270,7 +254,7 @@ __device__ __forceinline__ void move_references(const AttnParams &p, const Job &
     } else if (tid < A::NT) {
         cs.factor[tid] = 1.f;
     }
-    __syncthreads();
+    csync();
 }
 
 // Rescale this thread's columns of the results in tensor memory
@@ -295,8 +279,13 @@ struct Split {
     int qtiles, cols;           // column tiles, columns of a request at most
 };
 
+// Warps 0..7 decode, weigh and store; warp 8 fetches tiles and issues the
+// products.  Per tile the eight warps wait for S^T, turn it into weights (one
+// barrier: do the references hold?), decode the next tile's keys, then this
+// tile's values; each product runs while they decode the other operand, and they
+// meet the ninth warp at mbarriers only.
 template <typename T, int D, int NT>
-__global__ void __launch_bounds__(kAttnThreads, (Attn<T, D, NT>::CTAS))
+__global__ void __launch_bounds__(kAttnThreads + 32, (Attn<T, D, NT>::CTAS))
 attend_kernel(const CacheView c, const AttnParams p, const Split sp)
 {
     using A = Attn<T, D, NT>;
@@ -305,14 +294,14 @@ attend_kernel(const CacheView c, const AttnParams p, const Split sp)
     constexpr int OR = kPromote ? NH * A::VM : 1;     // fp32: results kept in registers
     extern __shared__ __align__(128) uint8_t smem[];
     uint8_t *qs = smem, *ps = qs + A::PIECES * A::Q_BYTES;
-    uint32_t *vs = reinterpret_cast<uint32_t *>(ps + A::SUB * A::PIECES * A::P_BYTES);
-    uint8_t *stages = ps + A::SUB * (A::PIECES * A::P_BYTES + A::VS_BYTES);
+    uint32_t *vs = reinterpret_cast<uint32_t *>(ps + A::PIECES * A::P_BYTES);
+    uint8_t *stages = ps + A::PIECES * A::P_BYTES + 2 * A::VS_BYTES;
     __shared__ __align__(16) Columns<NT> cs;
-    __shared__ __align__(8) uint64_t full[A::STAGES], s_bar, o_bar;
+    __shared__ __align__(8) uint64_t full[A::STAGES], k_bar, p_bar, s_bar, o_bar;
     __shared__ uint32_t tmem_base, arrived;
-    __shared__ __align__(16) int nv[A::STAGES][A::BLOCKS];
+    __shared__ int more;                              // wide tile: terms to come after this one, +1
+    __shared__ __align__(16) int nv[A::STAGES][4];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int quarter = warp & 3, half = warp >> 2, tok = tid & 127;
 
     const int group = p.Hq / c.H;
     Job w;
@@ -328,45 +317,91 @@ attend_kernel(const CacheView c, const AttnParams p, const Split sp)
         if (tid == 0) set_status(p.status, SPEC_STATUS_BAD_LENGTH);
         w.len = 0;
     }
-    if (split > 0 && split * sp.steps * A::STEP >= w.len) return;
-    visible_steps<A::STEP>(c, p, w);
+    if (split > 0 && split * sp.steps * kTile >= w.len) return;
+    visible_steps<kTile>(c, p, w);
     const int nsplit = max((w.nsteps + sp.steps - 1) / sp.steps, 1);
     if (split >= nsplit) return;
-    const int i0 = split * sp.steps, i1 = min(i0 + sp.steps, w.nsteps);
+    const int i0 = split * sp.steps, n = min(i0 + sp.steps, w.nsteps) - i0;
 
-    int page = -1;
-    if (warp == kLoadWarp) {
+    if (warp == 8) {
         if (lane == 0) {
             for (int i = 0; i < A::STAGES; ++i) mbar_init(&full[i], 1);
+            mbar_init(&k_bar, 8);
+            mbar_init(&p_bar, 8);
             mbar_init(&s_bar, 1);
             mbar_init(&o_bar, 1);
             fence_mbar_init();
         }
         __syncwarp();
         // the first loads go out before anything else
-        for (int i = 0; i < A::STAGES && i0 + i < i1; ++i) {
-            const int slot = step_slot<A::STEP>(w, i0 + i);
-            load_step<block_bytes(D), A::BLOCKS>(c, w, w.h, slot, step_page<A::BLOCKS>(c, w, slot), stages + i * A::STAGE,
-                                                 &full[i], nv[i], p.status);
+        for (int i = 0; i < A::STAGES && i < n; ++i) {
+            const int slot = step_slot<kTile>(w, i0 + i);
+            load_step<block_bytes(D), 4>(c, w, w.h, slot, step_page<4>(c, w, slot), stages + i * A::STAGE, &full[i], nv[i],
+                                         p.status);
         }
-        if (i0 + A::STAGES < i1) page = step_page<A::BLOCKS>(c, w, step_slot<A::STEP>(w, i0 + A::STAGES));
+    } else {
+        if (warp == 0) tmem_alloc(&tmem_base, A::COLS);
+        if (tid < NT) {
+            const int col = w.col0 + tid, j = min(col / group, w.n - 1);
+            const int own = w.len > 0 ? w.len - w.n + j : -1;
+            cs.own[tid] = own;
+            cs.pos[tid] = own >= 0 ? slot_position(c, p, w.b, own) : 0;
+            cs.slope[tid] = p.slopes && tid < w.ncols ? p.slopes[w.h * group + col % group] * kLog2e : 0.f;
+            cs.ref[tid] = tid < w.ncols ? kHeadroom - kUnset : 0.f;      // (a padded column's results are unused)
+        }
+        stage_queries<T, D, NT, A::PIECES>(p, w, group, c.k_scale ? c.k_scale[w.h] : 1.f, 1.4426950408889634, qs, cs.mult);
+        fence_proxy_async_smem();
     }
-    if (warp == 0) tmem_alloc(&tmem_base, A::COLS);
-    if (tid < NT) {
-        const int col = w.col0 + tid, j = min(col / group, w.n - 1);
-        const int own = w.len > 0 ? w.len - w.n + j : -1;
-        cs.own[tid] = own;
-        cs.pos[tid] = own >= 0 ? slot_position(c, p, w.b, own) : 0;
-        cs.slope[tid] = p.slopes && tid < w.ncols ? p.slopes[w.h * group + col % group] * kLog2e : 0.f;
-        cs.ref[tid] = tid < w.ncols ? kHeadroom - kUnset : 0.f;      // (a padded column's results are unused)
-    }
-    const float gk = c.k_scale ? c.k_scale[w.h] : 1.f, gv = c.v_scale ? c.v_scale[w.h] : 1.f;
-    stage_queries<T, D, NT, A::PIECES>(p, w, group, gk, 1.4426950408889634, qs, cs.mult);
-    fence_proxy_async_smem();
     __syncthreads();
     tmem_fence_after();
+    const uint32_t a_t = tmem_base, v_t = a_t + A::A_COLS, s_t = v_t + A::V_COLS, o_t = s_t + A::S_COLS;
+    bool fail = false;
+
+    if (warp == 8) {
+        // the ninth warp: products in the order their operands come, and the
+        // stage of a finished tile filled again
+        const bool leader = elect_one();
+        const uint32_t q_addr = smem_addr(qs), p_addr = smem_addr(ps);
+        int p_count = 0;
+        int page = A::STAGES < n ? step_page<4>(c, w, step_slot<kTile>(w, i0 + A::STAGES)) : -1;
+        for (int k = -1; k < n; ++k) {
+            if (k + 1 < n) {
+                wait_or_fail(&k_bar, (k + 1) & 1, fail);
+                tmem_fence_after();
+                if (leader) {
+                    issue_scores<D, NT, A::PIECES>(s_t, a_t, q_addr);
+                    mma_commit(&s_bar);
+                }
+                __syncwarp();
+            }
+            if (k < 0) continue;
+            bool again = false;
+            do {
+                wait_or_fail(&p_bar, p_count++ & 1, fail);
+                tmem_fence_after();
+                const int left = *reinterpret_cast<volatile int *>(&more);
+                if (leader) {
+                    const bool first = !again && (kPromote || k == 0);
+                    if (left == 0) issue_values<A, false>(o_t, v_t, p_addr, !first);
+                    else issue_values<A, true>(o_t, v_t, p_addr, !first);
+                    mma_commit(&o_bar);
+                }
+                __syncwarp();
+                again = left > 1;
+            } while (again && !fail);
+            if (k + A::STAGES < n) {
+                const int st = k % A::STAGES;
+                load_step<block_bytes(D), 4>(c, w, w.h, step_slot<kTile>(w, i0 + k + A::STAGES), page, stages + st * A::STAGE,
+                                             &full[st], nv[st], p.status);
+                page = k + A::STAGES + 1 < n ? step_page<4>(c, w, step_slot<kTile>(w, i0 + k + A::STAGES + 1)) : -1;
+            }
+        }
+        return;
+    }
+
+    const int quarter = warp & 3, half = warp >> 2, tok = tid & 127;
+    const float gv = c.v_scale ? c.v_scale[w.h] : 1.f;
     const bool options = p.cap > 0.f || p.slopes || p.window > 0;
-    const uint32_t a_t = tmem_base, s_t = a_t + A::SUB * A::A_COLS, o_t = s_t + A::SUB * A::S_COLS;
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
     // where this thread's columns of the result lie (D = 64: those of its tokens)
     const uint32_t o_mine = o_t + lane_off + half * NH + (D == 64 && quarter >= 2 ? NT : 0);
@@ -376,7 +411,13 @@ attend_kernel(const CacheView c, const AttnParams p, const Split sp)
     for (int i = 0; i < NH; ++i) l[i] = 0.f;
 #pragma unroll
     for (int i = 0; i < OR; ++i) acc[i] = 0.f;
-    const auto promote = [&] {
+    int o_count = 0;                                  // products with V^T waited for
+    bool pending = false;                             // one is under way
+    // wait for the product with V^T under way; fp32: add its result up
+    const auto finish_values = [&] {
+        pending = false;
+        wait_or_fail(&o_bar, o_count++ & 1, fail);
+        tmem_fence_after();
         if constexpr (kPromote) {
 #pragma unroll
             for (int m = 0; m < A::VM; ++m) {
@@ -388,75 +429,54 @@ attend_kernel(const CacheView c, const AttnParams p, const Split sp)
             }
         }
     };
-    bool fail = false;
-    int o_count = 0;                                                 // completed products with V^T
+    const auto keys = [&](int k) {
+        const int st = k % A::STAGES;
+        wait_or_fail(&full[st], k / A::STAGES & 1, fail);
+        decode_keys<D>(stages + st * A::STAGE + quarter * block_bytes(D), a_t + lane_off);
+        tmem_wait_st();
+        tmem_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&k_bar);
+    };
     const int own_first = cs.own[0];
     constexpr int PN8 = A::VT * 16;
     uint8_t *const p_mine = ps + (tok / A::VT * (NT / 8) + half * (NH / 8)) * PN8 + tok % A::VT * 16;
-    for (int i = i0; i < i1; ++i) {
-        const int k = i - i0, st = k % A::STAGES, slot0 = step_slot<A::STEP>(w, i);
+    if (n > 0) keys(0);
+    for (int k = 0; k < n; ++k) {
+        const int st = k % A::STAGES, slot0 = step_slot<kTile>(w, i0 + k);
         const uint8_t *stage = stages + st * A::STAGE;
-        const int subs = A::SUB == 1 || w.len - slot0 <= kTile ? 1 : 2;
-        wait_or_fail(&full[st], k / A::STAGES & 1, fail);
-        Token t[A::SUB];
-        bool whole = true;
-#pragma unroll
-        for (int sub = 0; sub < A::SUB; ++sub) {
-            const int4 n = *reinterpret_cast<const int4 *>(&nv[st][4 * sub]);
-            const bool w32 = (n.x & n.y & n.z & n.w) == kTok;        // (each at most 32)
-            whole = whole && w32;
-            t[sub].slot = t[sub].pos = slot0 + sub * kTile + tok;
-            t[sub].live = w32 || lane < nv[st][4 * sub + quarter];
-            t[sub].edge = !w32 || slot0 + sub * kTile + kTile - 1 > own_first;
-            if (options && p.slot_pos && t[sub].live) t[sub].pos = slot_position(c, p, w.b, t[sub].slot);
-        }
-#pragma unroll 1
-        for (int sub = 0; sub < subs; ++sub)
-            value_scales<D>(stage + sub * 4 * block_bytes(D), &nv[st][4 * sub], whole, vs + sub * (A::VS_BYTES / 4));
-        if (k > 0) {
-            wait_or_fail(&o_bar, o_count++ & 1, fail);               // V^T of the last step is used up
-            tmem_fence_after();
-            promote();
-        }
-#pragma unroll 1
-        for (int sub = 0; sub < subs; ++sub)
-            decode_keys<D>(stage + (sub * 4 + quarter) * block_bytes(D), a_t + sub * A::A_COLS + lane_off);
-        tmem_wait_st();
-        tmem_fence_before();
-        __syncthreads();
-        if (tid == 0) {
-            tmem_fence_after();
-#pragma unroll 1
-            for (int sub = 0; sub < subs; ++sub)
-                issue_scores<D, NT, A::PIECES>(s_t + sub * A::S_COLS, a_t + sub * A::A_COLS, qs);
-            mma_commit(&s_bar);
-        }
+        uint32_t *vsk = vs + (k & 1) * (A::VS_BYTES / 4);
+        Token t;
+        const int4 n4 = *reinterpret_cast<const int4 *>(nv[st]);
+        const bool whole = (n4.x & n4.y & n4.z & n4.w) == kTok;      // (each at most 32)
+        t.slot = t.pos = slot0 + tok;
+        t.live = whole || lane < nv[st][quarter];
+        t.edge = !whole || slot0 + kTile - 1 > own_first;
+        if (options && p.slot_pos && t.live) t.pos = slot_position(c, p, w.b, t.slot);
+        value_scales<D>(stage, nv[st], whole, vsk);
         wait_or_fail(&s_bar, k & 1, fail);
         tmem_fence_after();
-        float v[A::SUB][NH];
+        float v[NH];
         bool wide = false;
         for (;;) {
+            token_scores<A, NH, true>(p, w, cs, s_t + lane_off, half * NH, t, options, v);
             float most = -INFINITY, least = INFINITY;
 #pragma unroll
-            for (int sub = 0; sub < A::SUB; ++sub) {
-                if (sub >= subs) break;
-                token_scores<A, NH, true>(p, w, cs, s_t + sub * A::S_COLS + lane_off, half * NH, t[sub], options, v[sub]);
+            for (int q = 0; q < NH; ++q) most = fmaxf(most, v[q]);
+            if (t.edge || options) {
 #pragma unroll
-                for (int q = 0; q < NH; ++q) most = fmaxf(most, v[sub][q]);
-                if (t[sub].edge || options) {
+                for (int q = 0; q < NH; ++q) least = fminf(least, v[q] == -INFINITY ? INFINITY : v[q]);
+            } else {
 #pragma unroll
-                    for (int q = 0; q < NH; ++q) least = fminf(least, v[sub][q] == -INFINITY ? INFINITY : v[sub][q]);
-                } else {
-#pragma unroll
-                    for (int q = 0; q < NH; ++q) least = fminf(least, v[sub][q]);
-                }
+                for (int q = 0; q < NH; ++q) least = fminf(least, v[q]);
             }
-            if (!__syncthreads_or(most > kExceed || least < A::LEAST_EXP)) break;
-            if (!__syncthreads_or(most > kExceed)) {
+            if (!csync_count(most > kExceed || least < A::LEAST_EXP)) break;
+            if (!csync_count(most > kExceed)) {
                 wide = true;
                 break;
             }
-            move_references<A>(p, w, cs, s_t + lane_off, t, subs, options);
+            move_references<A>(p, w, cs, s_t + lane_off, t, options);
+            if (pending) finish_values();
 #pragma unroll
             for (int q = 0; q < NH; ++q) l[q] *= cs.factor[half * NH + q];
             if (kPromote) {
@@ -466,121 +486,93 @@ attend_kernel(const CacheView c, const AttnParams p, const Split sp)
                 rescale_results<A>(cs, o_t + lane_off);
             }
         }
+        // S^T is read, the keys' columns are free: on to the next tile's keys
+        if (k + 1 < n) keys(k + 1);
+        if (pending) finish_values();                 // V^T's columns and P are free
         // weights: sums in fp32, the operand 8 columns of this token per store
-        const bool accumulate = !kPromote && k > 0;
 #pragma unroll
-        for (int sub = 0; sub < A::SUB; ++sub) {
-            if (sub >= subs) break;
-#pragma unroll
-            for (int q = 0; q < NH; q += 2) {
-                v[sub][q] = ex2(v[sub][q]);
-                v[sub][q + 1] = ex2(v[sub][q + 1]);
-                f2_unpack(f2_add(f2_pack(l[q], l[q + 1]), f2_pack(v[sub][q], v[sub][q + 1])), l[q], l[q + 1]);
-            }
-            if (wide) continue;
-            uint8_t *dst = p_mine + sub * A::PIECES * A::P_BYTES;
+        for (int q = 0; q < NH; q += 2) {
+            v[q] = ex2(v[q]);
+            v[q + 1] = ex2(v[q + 1]);
+            f2_unpack(f2_add(f2_pack(l[q], l[q + 1]), f2_pack(v[q], v[q + 1])), l[q], l[q + 1]);
+        }
+        if (!wide) {
 #pragma unroll
             for (int q0 = 0; q0 < NH; q0 += 8) {
                 uint32_t hi[4];
 #pragma unroll
-                for (int q = 0; q < 4; ++q) hi[q] = pack_h2(v[sub][q0 + 2 * q], v[sub][q0 + 2 * q + 1]);
-                *reinterpret_cast<uint4 *>(dst + q0 / 8 * PN8) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                for (int q = 0; q < 4; ++q) hi[q] = pack_h2(v[q0 + 2 * q], v[q0 + 2 * q + 1]);
+                *reinterpret_cast<uint4 *>(p_mine + q0 / 8 * PN8) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
                 if (A::PIECES == 2) {
                     uint32_t lo[4];
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
                         const float2 y = h2_float2(hi[q]);
-                        lo[q] = pack_h2(v[sub][q0 + 2 * q] - y.x, v[sub][q0 + 2 * q + 1] - y.y);
+                        lo[q] = pack_h2(v[q0 + 2 * q] - y.x, v[q0 + 2 * q + 1] - y.y);
                     }
-                    *reinterpret_cast<uint4 *>(dst + A::P_BYTES + q0 / 8 * PN8) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                    *reinterpret_cast<uint4 *>(p_mine + A::P_BYTES + q0 / 8 * PN8) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                 }
             }
-        }
-        if (!wide) {
-            // values over the keys' columns (the product that read them is complete)
-#pragma unroll 1
-            for (int sub = 0; sub < subs; ++sub)
-                decode_tile_values<A, false>(stage + sub * 4 * block_bytes(D), vs + sub * (A::VS_BYTES / 4),
-                                             a_t + sub * A::A_COLS + lane_off);
+            decode_tile_values<A, false>(stage, vsk, v_t + lane_off);
+            if (tid == 0) more = 0;
             tmem_wait_st();
             tmem_fence_before();
             fence_proxy_async_smem();
-            __syncthreads();
-            if (tid == 0) {
-                tmem_fence_after();
-                issue_values<A, false>(o_t, a_t, ps, subs, accumulate);
-                mma_commit(&o_bar);
-            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&p_bar);
         } else {
-#pragma unroll 1
-            for (int sub = 0; sub < subs; ++sub)
-                decode_tile_values<A, true>(stage + sub * 4 * block_bytes(D), vs + sub * (A::VS_BYTES / 4),
-                                            a_t + sub * A::A_COLS + lane_off);
+            decode_tile_values<A, true>(stage, vsk, v_t + lane_off);
             tmem_wait_st();
 #pragma unroll 1
             for (int pc = 0; pc < A::WIDE; ++pc) {
                 if (pc > 0) wait_or_fail(&o_bar, o_count++ & 1, fail);
 #pragma unroll
-                for (int sub = 0; sub < A::SUB; ++sub) {
-                    if (sub >= subs) break;
-                    uint8_t *dst = p_mine + sub * A::PIECES * A::P_BYTES;
+                for (int q0 = 0; q0 < NH; q0 += 8) {
+                    uint32_t term[4];
 #pragma unroll
-                    for (int q0 = 0; q0 < NH; q0 += 8) {
-                        uint32_t term[4];
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            float &x = v[sub][q0 + 2 * q], &y = v[sub][q0 + 2 * q + 1];
-                            if (pc == 0) {
-                                x *= kWideScale;
-                                y *= kWideScale;
-                            }
-                            term[q] = pack_bf2(x, y);
-                            x -= bf_lo(term[q]);
-                            y -= bf_hi(term[q]);
+                    for (int q = 0; q < 4; ++q) {
+                        float &x = v[q0 + 2 * q], &y = v[q0 + 2 * q + 1];
+                        if (pc == 0) {
+                            x *= kWideScale;
+                            y *= kWideScale;
                         }
-                        *reinterpret_cast<uint4 *>(dst + q0 / 8 * PN8) = make_uint4(term[0], term[1], term[2], term[3]);
+                        term[q] = pack_bf2(x, y);
+                        x -= bf_lo(term[q]);
+                        y -= bf_hi(term[q]);
                     }
+                    *reinterpret_cast<uint4 *>(p_mine + q0 / 8 * PN8) = make_uint4(term[0], term[1], term[2], term[3]);
                 }
+                if (tid == 0) more = A::WIDE - pc;
                 tmem_fence_before();
                 fence_proxy_async_smem();
-                __syncthreads();
-                if (tid == 0) {
-                    tmem_fence_after();
-                    issue_values<A, true>(o_t, a_t, ps, subs, accumulate || pc > 0);
-                    mma_commit(&o_bar);
-                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_bar);
             }
         }
-        if (warp == kLoadWarp && i + A::STAGES < i1) {
-            load_step<block_bytes(D), A::BLOCKS>(c, w, w.h, step_slot<A::STEP>(w, i + A::STAGES), page,
-                                                 stages + st * A::STAGE, &full[st], nv[st], p.status);
-            page = i + A::STAGES + 1 < i1 ? step_page<A::BLOCKS>(c, w, step_slot<A::STEP>(w, i + A::STAGES + 1)) : -1;
-        }
+        pending = true;
     }
-    if (i1 > i0) wait_or_fail(&o_bar, o_count & 1, fail);
-    if (__syncthreads_or(fail)) {
+    if (pending) finish_values();
+    if (csync_count(fail)) {
         // a wait gave up: let the copies in flight land (bounded), then leave
         if (tid == 0) {
             for (int s = 0; s < A::STAGES; ++s)
                 for (int ph = 0; ph < 2; ++ph) mbar_wait(&full[s], ph);
             set_status(p.status, SPEC_STATUS_TIMEOUT);
         }
-        __syncthreads();
+        csync();
         if (warp == 0) tmem_free(a_t, A::COLS);
         return;
     }
-    tmem_fence_after();
-    const bool seen = i1 > i0;
-    if (seen) promote();
+    const bool seen = n > 0;
 
     // sums over the tile's tokens (= lanes and quarters)
     {
         const float s = lane_sums<NH>(l);
         if (lane % (32 / NH) == 0) cs.red[quarter][half * NH + lane / (32 / NH)] = s;
     }
-    __syncthreads();
+    csync();
     if (tid < NT) cs.sum[tid] = (cs.red[0][tid] + cs.red[1][tid]) + (cs.red[2][tid] + cs.red[3][tid]);
-    __syncthreads();
+    csync();
 
     const int64_t task = (static_cast<int64_t>(w.b) * c.H + w.h) * sp.qtiles + blockIdx.x % sp.qtiles;
     // partials of a task: [split][NT][D] fp32, then [split][NT] (reference, sum)
@@ -608,7 +600,7 @@ attend_kernel(const CacheView c, const AttnParams p, const Split sp)
             if (quarter >= 2)
 #pragma unroll
                 for (int q = 0; q < NH; ++q) xch[(half * NH + q) * 64 + tok - 64] = r[q];
-            __syncthreads();
+            csync();
             if (quarter >= 2) continue;
 #pragma unroll
             for (int q = 0; q < NH; ++q) r[q] += xch[(half * NH + q) * 64 + tok];
@@ -632,7 +624,7 @@ attend_kernel(const CacheView c, const AttnParams p, const Split sp)
         else if (p.lse) p.lse[out_row(tid)] = ls > 0.f ? (m - kHeadroom + log2f(ls)) * kLn2 : -INFINITY;
     }
     tmem_fence_before();
-    __syncthreads();
+    csync();
     if (warp == 0) tmem_free(a_t, A::COLS);
     if (nsplit == 1) return;
 
@@ -643,7 +635,7 @@ attend_kernel(const CacheView c, const AttnParams p, const Split sp)
         arrived = atomicAdd(ticket, 1u);
         fence_acq_rel_gpu();
     }
-    __syncthreads();
+    csync();
     if (arrived != static_cast<uint32_t>(nsplit - 1)) return;
     if (tid == 0) *ticket = 0u;
     for (int col = warp; col < w.ncols; col += kAttnThreads / 32) {
@@ -678,13 +670,6 @@ attend_kernel(const CacheView c, const AttnParams p, const Split sp)
     }
 }
 
-// tokens of a step of the kernel for these
-int step_tokens(int D, int nt, int dtype)
-{
-    const int pieces = dtype == SPEC_F32 ? 2 : 1, a = D == 256 ? 128 : D / 2, o = nt * (D == 128 ? 1 : 2);
-    return 2 * (a + pieces * nt) + o <= 256 ? 2 * kTile : kTile;
-}
-
 // Steps of a split: as many splits as a few rounds of resident CTAs need, so
 // that ragged requests even out.
 Split split_of(int B, int k_max, int Hq, int H, int D, int max_len, int dtype)
@@ -693,8 +678,7 @@ Split split_of(int B, int k_max, int Hq, int H, int D, int max_len, int dtype)
     s.cols = (k_max + 1) * (Hq / H);
     const int nt = column_tile(s.cols, D, dtype);
     s.qtiles = (s.cols + nt - 1) / nt;
-    const int step = step_tokens(D, nt, dtype);
-    const int steps = (max_len + step - 1) / step;
+    const int steps = (max_len + kTile - 1) / kTile;
     const int64_t all = static_cast<int64_t>(B) * H * s.qtiles * steps;
     const int64_t slots = 152 * 2 * 4;
     const int64_t t = (all + slots - 1) / slots;
@@ -707,7 +691,6 @@ template <typename T, int D, int NT>
 cudaError_t launch_one(const CacheView &c, const AttnParams &p, const Split &sp, cudaStream_t s)
 {
     using A = Attn<T, D, NT>;
-    if (step_tokens(D, NT, sizeof(T) == 4 ? SPEC_F32 : SPEC_BF16) != A::STEP) return cudaErrorInvalidValue;
     static bool done[64] = {false};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -719,7 +702,7 @@ cudaError_t launch_one(const CacheView &c, const AttnParams &p, const Split &sp,
         done[dev] = true;
     }
     const dim3 grid(c.H * sp.qtiles, sp.most, c.B);
-    attend_kernel<T, D, NT><<<grid, kAttnThreads, A::SMEM, s>>>(c, p, sp);
+    attend_kernel<T, D, NT><<<grid, kAttnThreads + 32, A::SMEM, s>>>(c, p, sp);
     return cudaGetLastError();
 }
 

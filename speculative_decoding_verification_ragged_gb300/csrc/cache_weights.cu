@@ -174,7 +174,7 @@ weights_kernel(const CacheView c, const AttnParams p, const int tiles)
         __syncthreads();
         if (tid == 0) {
             tmem_fence_after();
-            issue_scores<D, NT, A::PIECES>(s_t + (i & 1) * A::S_COLS, a_t, qs + qb * A::Q_BYTES);
+            issue_scores<D, NT, A::PIECES>(s_t + (i & 1) * A::S_COLS, a_t, smem_addr(qs) + qb * A::Q_BYTES);
             mma_commit(&s_bar);
         }
         if (warp == kLoadWarp && i + A::STAGES < steps) load(i + A::STAGES);

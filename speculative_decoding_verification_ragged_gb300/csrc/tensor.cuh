@@ -8,6 +8,19 @@
 
 namespace specv {
 
+// one lane of the warp (the same one each time)
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
+
+__device__ __forceinline__ void mbar_arrive(uint64_t *bar)
+{
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+
 // Tensor memory: `cols` 32-bit columns (a power of two, 32..512) of 128 lanes.
 // The warp that allocates frees; the address lands in shared memory.
 __device__ __forceinline__ void tmem_alloc(uint32_t *dst, uint32_t cols)
