@@ -1,6 +1,7 @@
 // cache.cu -- the 4-bit paged cache itself: append (quantise and write), read,
 // and eviction by accumulated attention weight (include/spec_cache.h).
 #include <climits>
+#include <cooperative_groups.h>
 
 #include "cache.cuh"
 
@@ -35,52 +36,60 @@ __device__ __forceinline__ bool block_rows(const CacheView &c, const CacheRows &
     return true;
 }
 
-// Quantise 16 channels (spec_cache.h: s = e4m3(amax / (6 g)), code =
-// e2m1(x / (s g)); IEEE divisions and round-to-nearest-even conversions, so
-// the codes are those of the formula bit for bit).  Returns the scale byte;
-// codes[i] holds channels 2i (low nibble) and 2i + 1.
-__device__ __forceinline__ uint32_t quantise16(const float (&x)[16], float g, uint32_t (&codes)[8])
+// A thread's share of a row: 16 bytes of values (4 of fp32, 8 of bf16), so that
+// a warp's loads are whole lines; LPG lanes share a group of 16 channels.
+template <typename T> struct Share {
+    static constexpr int N = 16 / sizeof(T), LPG = 16 / N;
+};
+
+template <typename T>
+__device__ __forceinline__ void load_share(const T *p, bool aligned, float (&x)[Share<T>::N])
+{
+    __align__(16) T e[Share<T>::N];
+    if (aligned) {
+        *reinterpret_cast<uint4 *>(e) = __ldg(reinterpret_cast<const uint4 *>(p));
+    } else {
+#pragma unroll
+        for (int i = 0; i < Share<T>::N; ++i) e[i] = p[i];
+    }
+#pragma unroll
+    for (int i = 0; i < Share<T>::N; ++i) x[i] = to_f32<T>(e[i]);
+}
+
+// Quantise a share (spec_cache.h: s = e4m3(amax / (6 g)), code = e2m1(x / (s g));
+// IEEE divisions and round-to-nearest-even conversions, so the codes are those of
+// the formula bit for bit).  Returns the group's scale byte; the share's codes
+// come packed, the first in the lowest nibble.
+template <int N, int LPG>
+__device__ __forceinline__ uint32_t quantise(const float (&x)[N], float g, uint32_t &codes)
 {
     float amax = 0.f;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(x[i]));
+    for (int i = 0; i < N; ++i) amax = fmaxf(amax, fabsf(x[i]));
+#pragma unroll
+    for (int o = 1; o < LPG; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
     const float t = fminf(__fdiv_rn(amax, 6.0f * g), 448.0f);
     uint16_t s8;
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(s8) : "f"(0.f), "f"(t));
     const float den = e4m3_value(s8) * g;
+    codes = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float a = den > 0.f ? __fdiv_rn(x[2 * i], den) : 0.f;
-        const float b = den > 0.f ? __fdiv_rn(x[2 * i + 1], den) : 0.f;
-        asm("{\n\t.reg .b8 c;\n\tcvt.rn.satfinite.e2m1x2.f32 c, %1, %2;\n\t"
-            "mov.b32 %0, {c, c, c, c};\n\t}"
-            : "=r"(codes[i])
+    for (int i = 0; i < N; i += 2) {
+        const float a = den > 0.f ? __fdiv_rn(x[i], den) : 0.f;
+        const float b = den > 0.f ? __fdiv_rn(x[i + 1], den) : 0.f;
+        uint32_t c;
+        asm("{\n\t.reg .b8 c;\n\tcvt.rn.satfinite.e2m1x2.f32 c, %1, %2;\n\tmov.b32 %0, {c, c, c, c};\n\t}"
+            : "=r"(c)
             : "f"(b), "f"(a));
-        codes[i] &= 255u;
+        codes |= (c & 255u) << (4 * i);
     }
     return s8 & 255u;
 }
 
-template <typename T>
-__device__ __forceinline__ void load16(const T *p, bool aligned, float (&x)[16])
-{
-    if (aligned) {
-        constexpr int N = 16 * sizeof(T) / 16;
-        uint4 v[N];
-#pragma unroll
-        for (int i = 0; i < N; ++i) v[i] = __ldg(reinterpret_cast<const uint4 *>(p) + i);
-        const T *e = reinterpret_cast<const T *>(v);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) x[i] = to_f32<T>(e[i]);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) x[i] = to_f32<T>(p[i]);
-    }
-}
-
 // One CTA per (block of 32 slots, kv head, request).  A block belongs to one
 // CTA, so the value codes, two tokens to a byte, are read, merged and written
-// back without atomics.
+// back without atomics.  Bound by the rows' bytes: a warp reads 512 of them per
+// load.
 template <typename T, int D>
 __global__ void __launch_bounds__(kRowThreads) append_kernel(const CacheView c, const CacheRows r)
 {
@@ -92,33 +101,40 @@ __global__ void __launch_bounds__(kRowThreads) append_kernel(const CacheView c, 
         if (tid == 0) set_status(r.status, SPEC_STATUS_BAD_PAGE);
         return;
     }
-    constexpr int G = D / 16;
-    __shared__ uint8_t vcode[kTok][D];
+    constexpr int G = D / 16, N = Share<T>::N, LPG = Share<T>::LPG, PER = D / N;
+    // value codes, a channel's 8 tokens to a word once transposed; a row of words
+    // is padded so that the lanes of a column lie in different banks
+    __shared__ uint32_t vcode[kTok][D / 8 + 1];
     uint8_t *blk = block_at(c, page, h, o.slot0 % c.page_tokens / kTok);
     const float gk = c.k_scale ? c.k_scale[h] : 1.f, gv = c.v_scale ? c.v_scale[h] : 1.f;
     const int n = o.last - o.first;
-    for (int i = tid; i < n * G * 2; i += kRowThreads) {
-        const int g = i % G, t = o.first + i / G % n;
-        const bool val = i >= n * G;
-        const int64_t row = o.lo + (o.slot0 + t - o.start);
-        const T *src = val ? static_cast<const T *>(r.v) + row * r.v_row + h * r.v_head
-                           : static_cast<const T *>(r.k) + row * r.k_row + h * r.k_head;
-        float x[16];
-        uint32_t q[8];
-        load16<T>(src + 16 * g, val ? r.v_aligned : r.k_aligned, x);
-        const uint32_t s = quantise16(x, val ? gv : gk, q);
-        const uint2 w = make_uint2(q[0] | q[1] << 8 | q[2] << 16 | q[3] << 24,
-                                   q[4] | q[5] << 8 | q[6] << 16 | q[7] << 24);
-        if (!val) {
-            *reinterpret_cast<uint2 *>(blk + g / 2 * 512 + t * 16 + g % 2 * 8) = w;
-            blk[k_scale_at(D) + t * G + g] = static_cast<uint8_t>(s);
-        } else {
+    // keys, then values: whole groups of lanes take part (PER divides the warp or
+    // is a multiple of it), so the shuffles of quantise() are complete
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                vcode[t][16 * g + 2 * j] = q[j] & 15u;
-                vcode[t][16 * g + 2 * j + 1] = q[j] >> 4;
+    for (int val = 0; val < 2; ++val) {
+        const T *base = val ? static_cast<const T *>(r.v) + h * r.v_head : static_cast<const T *>(r.k) + h * r.k_head;
+        const int64_t stride = val ? r.v_row : r.k_row;
+        const bool aligned = val ? r.v_aligned : r.k_aligned;
+        for (int i0 = 0; i0 < n * PER; i0 += kRowThreads) {
+            const int i = i0 + tid, t = o.first + i / PER, d = i % PER * N;
+            const bool in = i < n * PER;
+            float x[N] = {};
+            uint32_t codes;
+            if (in) load_share<T>(base + (o.lo + (o.slot0 + t - o.start)) * stride + d, aligned, x);
+            const uint32_t s = quantise<N, LPG>(x, val ? gv : gk, codes);
+            if (!in) continue;
+            const bool lead = d % 16 == 0;
+            if (!val) {
+                uint8_t *at = blk + d / 32 * 512 + t * 16 + d % 32 / 2;
+                if (N == 8) *reinterpret_cast<uint32_t *>(at) = codes;
+                else *reinterpret_cast<uint16_t *>(at) = static_cast<uint16_t>(codes);
+                if (lead) blk[k_scale_at(D) + t * G + d / 16] = static_cast<uint8_t>(s);
+            } else {
+                uint8_t *at = reinterpret_cast<uint8_t *>(vcode[t]) + d / 2;
+                if (N == 8) *reinterpret_cast<uint32_t *>(at) = codes;
+                else *reinterpret_cast<uint16_t *>(at) = static_cast<uint16_t>(codes);
+                if (lead) blk[v_scale_at(D) + d / 16 * kTok + t] = static_cast<uint8_t>(s);
             }
-            blk[v_scale_at(D) + g * kTok + t] = static_cast<uint8_t>(s);
         }
     }
     if (h == 0 && (r.score || r.slot_pos) && tid >= o.first && tid < o.last) {
@@ -130,19 +146,22 @@ __global__ void __launch_bounds__(kRowThreads) append_kernel(const CacheView c, 
     __syncthreads();
     // 8 tokens of one channel per 32-bit word
     for (int i = tid; i < D * 4; i += kRowThreads) {
-        const int d = i % D, t0 = i / D * 8;
+        const int d = i / 4, t0 = i % 4 * 8;
         if (t0 + 8 <= o.first || t0 >= o.last) continue;
         uint32_t *p = reinterpret_cast<uint32_t *>(blk + v_codes_at(D) + d * 16 + t0 / 2);
         const bool whole = t0 >= o.first && t0 + 8 <= o.last;
         uint32_t w = whole ? 0u : *p;
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-            if (t0 + j >= o.first && t0 + j < o.last)
-                w = (w & ~(15u << 4 * j)) | static_cast<uint32_t>(vcode[t0 + j][d]) << 4 * j;
+            if (whole || (t0 + j >= o.first && t0 + j < o.last))
+                w = (w & ~(15u << 4 * j)) | (vcode[t0 + j][d / 8] >> (d % 8 * 4) & 15u) << 4 * j;
         *p = w;
     }
 }
 
+// One CTA per (block, kv head, request): a thread takes 8 channels of a token's
+// key, then a channel (or two, of bf16) of every token's value, so that both
+// sides move whole words.
 template <typename T, int D>
 __global__ void __launch_bounds__(kRowThreads) read_kernel(const CacheView c, const CacheRows r)
 {
@@ -151,40 +170,81 @@ __global__ void __launch_bounds__(kRowThreads) read_kernel(const CacheView c, co
     if (!block_rows(c, r, b, idx, o)) return;
     const int page = page_of(c, b, o.slot0);
     if (page < 0 && tid == 0) set_status(r.status, SPEC_STATUS_BAD_PAGE);
-    constexpr int G = D / 16;
+    constexpr int G = D / 16, N = Share<T>::N, PER = D / N, CH = 4 / sizeof(T);
     const uint8_t *blk = page < 0 ? nullptr : block_at(c, page, h, o.slot0 % c.page_tokens / kTok);
     const float gk = c.k_scale ? c.k_scale[h] : 1.f, gv = c.v_scale ? c.v_scale[h] : 1.f;
     const int n = o.last - o.first;
-    for (int i = tid; i < n * D * 2; i += kRowThreads) {
-        const int d = i % D, t = o.first + i / D % n;
-        const bool val = i >= n * D;
-        const int64_t row = o.lo + (o.slot0 + t - o.start);
-        float x = 0.f;
+    const int64_t row0 = o.lo + (o.slot0 + o.first - o.start);
+    T *kp = static_cast<T *>(r.k) + row0 * r.k_row + h * r.k_head, *vp = static_cast<T *>(r.v) + row0 * r.v_row + h * r.v_head;
+    for (int i = tid; i < n * PER; i += kRowThreads) {
+        const int t = o.first + i / PER, d = i % PER * N;
+        uint32_t w = 0;
+        float s = 0.f;
         if (blk) {
-            const uint32_t code = val ? blk[v_codes_at(D) + d * 16 + t / 2] >> (t % 2 * 4)
-                                      : blk[d / 32 * 512 + t * 16 + d % 32 / 2] >> (d % 2 * 4);
-            const uint32_t s = val ? blk[v_scale_at(D) + d / 16 * kTok + t]
-                                   : blk[k_scale_at(D) + t * G + d / 16];
-            x = e2m1_value(code) * e4m3_value(s) * (val ? gv : gk);
+            const uint8_t *at = blk + d / 32 * 512 + t * 16 + d % 32 / 2;
+            w = N == 8 ? *reinterpret_cast<const uint32_t *>(at) : *reinterpret_cast<const uint16_t *>(at);
+            s = e4m3_value(blk[k_scale_at(D) + t * G + d / 16]);
         }
-        T *dst = val ? static_cast<T *>(r.v) + row * r.v_row + h * r.v_head
-                     : static_cast<T *>(r.k) + row * r.k_row + h * r.k_head;
-        dst[d] = from_f32<T>(x);
+        __align__(16) T e[N];
+#pragma unroll
+        for (int j = 0; j < N; j += 2) {
+            const float2 x = h2_float2(e2m1x2(w >> (4 * j)));
+            e[j] = from_f32<T>(x.x * s * gk);
+            e[j + 1] = from_f32<T>(x.y * s * gk);
+        }
+        T *to = kp + (t - o.first) * r.k_row + d;
+        if (r.k_aligned) {
+            *reinterpret_cast<uint4 *>(to) = *reinterpret_cast<const uint4 *>(e);
+        } else {
+#pragma unroll
+            for (int j = 0; j < N; ++j) to[j] = e[j];
+        }
+    }
+    for (int d = tid * CH; d < D; d += kRowThreads * CH) {
+        uint4 v[CH], s[2];
+#pragma unroll
+        for (int k = 0; k < CH; ++k)
+            v[k] = blk ? *reinterpret_cast<const uint4 *>(blk + v_codes_at(D) + (d + k) * 16) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+            s[k] = blk ? *reinterpret_cast<const uint4 *>(blk + v_scale_at(D) + d / 16 * kTok + 16 * k) : make_uint4(0, 0, 0, 0);
+        const uint32_t sw[8] = {s[0].x, s[0].y, s[0].z, s[0].w, s[1].x, s[1].y, s[1].z, s[1].w};
+#pragma unroll
+        for (int t = 0; t < kTok; t += 2) {
+            const float2 sc = h2_float2(e4m3x2(sw[t / 4] >> (t % 4 * 8)));
+            __align__(4) T e[2][CH];
+#pragma unroll
+            for (int k = 0; k < CH; ++k) {
+                const uint32_t w = t < 16 ? (t < 8 ? v[k].x : v[k].y) : (t < 24 ? v[k].z : v[k].w);
+                const float2 x = h2_float2(e2m1x2(w >> (t % 8 * 4)));
+                e[0][k] = from_f32<T>(x.x * sc.x * gv);
+                e[1][k] = from_f32<T>(x.y * sc.y * gv);
+            }
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+                if (t + u >= o.first && t + u < o.last) {
+                    T *to = vp + (t + u - o.first) * r.v_row + d;
+                    if (CH == 1 || r.v_aligned) {
+                        *reinterpret_cast<uint32_t *>(to) = *reinterpret_cast<const uint32_t *>(e[u]);
+                    } else {
+                        to[0] = e[u][0];
+                        to[CH - 1] = e[u][CH - 1];
+                    }
+                }
+        }
     }
 }
 
 // ------------------------------------------------------------- eviction ---
 
 constexpr int kSelThreads = 1024;
+constexpr int kSelCtas = 8;                // cluster of a request
+constexpr int kBins = 2048;                // a radix digit: 11 bits (the last: 10)
+constexpr int kSelStaged = 40 * 1024;      // scores a CTA keeps in shared memory
+constexpr int kSelSmem = (kSelStaged + kSelStaged / 16) * 4;
 
 // Order-preserving key of a score: NaN below everything, -0 equal to +0.
 __device__ __forceinline__ uint32_t score_key(float x) { return x != x ? 0u : fkey(x); }
-
-__device__ __forceinline__ float *score_at(const CacheView &c, const EvictParams &p, int b, int slot)
-{
-    const int64_t page = c.page_table[static_cast<int64_t>(b) * c.max_pages + slot / c.page_tokens];
-    return p.score + page * c.page_tokens + slot % c.page_tokens;
-}
 
 // exclusive scan of one value per thread over the CTA, and the total
 __device__ __forceinline__ int cta_scan(int v, int *warp_sum, int &total)
@@ -199,7 +259,7 @@ __device__ __forceinline__ int cta_scan(int v, int *warp_sum, int &total)
     __syncthreads();
     if (lane == 31) warp_sum[warp] = incl;
     __syncthreads();
-    int s = lane < kSelThreads / 32 ? warp_sum[lane] : 0;
+    int s = warp_sum[lane];
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const int y = __shfl_up_sync(0xFFFFFFFFu, s, o);
@@ -210,13 +270,22 @@ __device__ __forceinline__ int cta_scan(int v, int *warp_sum, int &total)
     return (warp ? before : 0) + incl - v;
 }
 
-// Selection: one CTA per request.  A radix search over the score keys (8 bits
-// a pass) finds the key of the last score kept, then an ordered scan lists the
-// kept slots: those above the key, the first few at it, and the newest.
-__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const CacheView c, const EvictParams p)
+// Selection: a cluster of 8 CTAs per request, each with a contiguous eighth of
+// the slots, its keys in shared memory (read again from the cache's scores where
+// they do not fit).  A radix search, 11 bits a pass over the cluster's summed
+// histograms, finds the key of the last score kept; then a thread lists the kept
+// slots of a contiguous run of its own: those above the key, the first few at
+// it, and the newest.  2 x 131072 scores: one CTA a request took 370 us of the
+// call's 415.
+__global__ void __cluster_dims__(kSelCtas, 1, 1) __launch_bounds__(kSelThreads)
+evict_select_kernel(const CacheView c, const EvictParams p)
 {
-    const int b = blockIdx.x, tid = threadIdx.x;
-    __shared__ int hist[256], warp_sum[kSelThreads / 32], pick[2];
+    namespace cg = cooperative_groups;
+    cg::cluster_group cluster = cg::this_cluster();
+    extern __shared__ __align__(16) uint8_t smem_raw[];
+    uint32_t *keys = reinterpret_cast<uint32_t *>(smem_raw);
+    __shared__ int hist[kBins], warp_sum[kSelThreads / 32], pick[2], count[2];
+    const int b = blockIdx.x / kSelCtas, rank = blockIdx.x % kSelCtas, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int len = p.len[b];
     int32_t *kept = p.kept + static_cast<int64_t>(b) * p.budget;
     const int64_t room = static_cast<int64_t>(c.max_pages) * c.page_tokens;
@@ -232,81 +301,147 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const CacheVi
         }
         if (__syncthreads_or(bad_page)) bad = SPEC_STATUS_BAD_PAGE;
     }
+    // (the same in every CTA of the cluster: none is left waiting)
+    const int all = kSelCtas * kSelThreads, me = rank * kSelThreads + tid;
     if (bad) {
-        if (tid == 0) {
+        if (me == 0) {
             set_status(p.status, bad);
             p.new_len[b] = -1;
         }
-        for (int i = tid; i < p.budget; i += kSelThreads) kept[i] = -1;
+        for (int i = me; i < p.budget; i += all) kept[i] = -1;
         return;
     }
-    if (tid == 0) p.new_len[b] = keep;
-    for (int i = keep + tid; i < p.budget; i += kSelThreads) kept[i] = -1;
+    if (me == 0) p.new_len[b] = keep;
+    for (int i = keep + me; i < p.budget; i += all) kept[i] = -1;
     if (len <= p.budget) {
-        for (int i = tid; i < len; i += kSelThreads) kept[i] = i;
+        for (int i = me; i < len; i += all) kept[i] = i;
         return;
     }
+
     const int old = len - p.recent;          // slots that compete for `want` places
     int want = p.budget - p.recent;
+    // this CTA's slots: a run of `run` (a multiple of 16) per thread
+    const int run = ((len + all - 1) / all + 15) / 16 * 16, slice = run * kSelThreads;
+    const int64_t first = static_cast<int64_t>(rank) * slice;
+    const bool staged = slice <= kSelStaged;
+    // keys are padded by one in 16, so that runs of 16 start in different banks;
+    // slots that do not compete have key 0
+    const auto place = [](int i) { return i + i / 16; };
+    const auto fetch = [&](int i) {
+        const int64_t slot = first + i;
+        if (slot >= old) return 0u;
+        const int s = static_cast<int>(slot);
+        const int64_t page = __ldg(c.page_table + static_cast<int64_t>(b) * c.max_pages + s / c.page_tokens);
+        return score_key(p.score[page * c.page_tokens + s % c.page_tokens]);
+    };
+    const int mine = first >= old ? 0 : static_cast<int>(min(static_cast<int64_t>(slice), old - first));
+    if (staged) {
+        // a warp reads 4 x 32 consecutive scores at a time, each 32 of one page
+        for (int i0 = warp * 128; i0 < slice; i0 += kSelThreads / 32 * 128) {
+            uint32_t k[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) k[u] = i0 + u * 32 + lane < mine ? fetch(i0 + u * 32 + lane) : 0u;
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                if (i0 + u * 32 + lane < slice) keys[place(i0 + u * 32 + lane)] = k[u];
+        }
+    }
+    const auto key_at = [&](int i) { return staged ? keys[place(i)] : fetch(i); };
     uint32_t key = 0u;
-    for (int shift = 24; shift >= 0 && want > 0; shift -= 8) {
-        for (int i = tid; i < 256; i += kSelThreads) hist[i] = 0;
+    const bool any = want > 0;
+    for (int pass = 0; pass < 3 && any; ++pass) {
+        const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0), bins = pass == 2 ? 1024 : kBins;
+        for (int i = tid; i < kBins; i += kSelThreads) hist[i] = 0;
         __syncthreads();
-        for (int i = tid; i < old; i += kSelThreads) {
-            const uint32_t k = score_key(*score_at(c, p, b, i));
-            if (shift == 24 || (k >> (shift + 8)) == (key >> (shift + 8)))
-                atomicAdd(&hist[(k >> shift) & 255u], 1);
+        for (int i = tid; i < mine; i += kSelThreads) {
+            const uint32_t k = key_at(i);
+            if (pass == 0 || (k >> (pass == 1 ? 21 : 10)) == (key >> (pass == 1 ? 21 : 10)))
+                atomicAdd(&hist[(k >> shift) & (bins - 1)], 1);
         }
-        __syncthreads();
-        // the digit where the count from the top reaches `want`
+        cluster.sync();
+        // bins from the top, two a thread, summed over the cluster
+        int two[2] = {0, 0};
+#pragma unroll
+        for (int r = 0; r < kSelCtas; ++r) {
+            const int *h = cluster.map_shared_rank(hist, r);
+            const int at = bins - 2 - 2 * tid;
+            if (at >= 0) {
+                const int2 x = *reinterpret_cast<const int2 *>(h + at);
+                two[0] += x.y;
+                two[1] += x.x;
+            }
+        }
         int total;
-        const int mine = tid < 256 ? hist[255 - tid] : 0;
-        const int above = cta_scan(mine, warp_sum, total);
-        if (above < want && above + mine >= want) {
-            pick[0] = 255 - tid;
-            pick[1] = want - above;
+        int above = cta_scan(two[0] + two[1], warp_sum, total);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            if (above < want && above + two[u] >= want) {
+                pick[0] = bins - 1 - 2 * tid - u;
+                pick[1] = want - above;
+            }
+            above += two[u];
         }
-        __syncthreads();
+        cluster.sync();                       // (also the CTA's barrier for `pick`)
         key |= static_cast<uint32_t>(pick[0]) << shift;
         want = pick[1];
         __syncthreads();
     }
-    // `want` of the slots whose key equals `key` are kept, the lowest ones
-    int out = 0, ties = 0;
-    const bool any = p.budget > p.recent;
-    for (int base = 0; base < len; base += kSelThreads) {
-        const int i = base + tid;
-        uint32_t k = 0u;
-        if (i < old) k = score_key(*score_at(c, p, b, i));
-        const int tie = any && i < old && k == key;
-        int n_tie, n_out;
-        const int t = ties + cta_scan(tie, warp_sum, n_tie);
-        const int take = i < len && (i >= old || (any && (k > key || (tie && t < want))));
-        const int at = out + cta_scan(take, warp_sum, n_out);
-        if (take) kept[at] = i;
-        ties += n_tie;
-        out += n_out;
+    // `want` of the slots whose key equals `key` are kept, the lowest ones: count
+    // ties and slots above the key in this thread's run, then in the CTAs before
+    const int r0 = tid * run;
+    int ties = 0, over = 0;
+    if (any)
+        for (int i = r0; i < min(r0 + run, mine); ++i) {
+            const uint32_t k = key_at(i);
+            ties += k == key;
+            over += k > key;
+        }
+    int n_ties, n_over;
+    int tie_rank = cta_scan(ties, warp_sum, n_ties);
+    int over_rank = cta_scan(over, warp_sum, n_over);
+    if (tid == 0) {
+        count[0] = n_ties;
+        count[1] = n_over;
     }
+    cluster.sync();
+    for (int r = 0; r < rank; ++r) {
+        const int *cnt = cluster.map_shared_rank(count, r);
+        tie_rank += cnt[0];
+        over_rank += cnt[1];
+    }
+    cluster.sync();                           // no CTA leaves while its counts are read
+    int at = over_rank + min(tie_rank, want);
+    if (any)
+        for (int i = r0; i < min(r0 + run, mine); ++i) {
+            const uint32_t k = key_at(i);
+            const bool tie = k == key;
+            if (k > key || (tie && tie_rank < want)) kept[at++] = static_cast<int>(first) + i;
+            tie_rank += tie;
+        }
+    for (int i = me; i < p.recent; i += all) kept[keep - p.recent + i] = old + i;
 }
 
 constexpr int kMoveThreads = 128;
 
-// Move: one CTA per (destination block, kv head, request).
+// Move: one CTA per (destination block, kv head, request).  Keys go 16 bytes (32
+// channels) a thread.  A thread takes the values of a channel: 16 bytes of a
+// source block hold its 32 tokens there, read once for all the kept ones.
+template <int D>
 __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const CacheView c, const EvictParams p)
 {
     const int blk = blockIdx.x, h = blockIdx.y, b = blockIdx.z, tid = threadIdx.x;
     const int keep = p.new_len[b];
     if (blk * kTok >= keep) return;          // also a skipped request (-1)
-    const int D = c.D, G = D / 16;
+    constexpr int G = D / 16;
     __shared__ const uint8_t *src[kTok];     // source block of each token
-    __shared__ int tok[kTok];
+    __shared__ int tok[kTok];                // its place there, -1: none
     const int32_t *kept = p.kept + static_cast<int64_t>(b) * p.budget;
     const int dpage = p.dst_table[static_cast<int64_t>(b) * p.dst_pages + blk * kTok / c.page_tokens];
     uint8_t *dst = block_at(c, dpage, h, blk * kTok % c.page_tokens / kTok);
     if (tid < kTok) {
         const int i = blk * kTok + tid;
         src[tid] = nullptr;
-        tok[tid] = 0;
+        tok[tid] = -1;
         float sc = 0.f;
         int pos = 0;
         if (i < keep) {
@@ -327,29 +462,45 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const CacheVie
         }
     }
     __syncthreads();
+    const uint4 none = make_uint4(0, 0, 0, 0);
+#pragma unroll
     for (int i = tid; i < D; i += kMoveThreads) {          // 16 bytes of K codes each
         const int ch = i / kTok, t = i % kTok;
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (src[t]) v = *reinterpret_cast<const uint4 *>(src[t] + ch * 512 + tok[t] * 16);
+        const uint4 v = tok[t] >= 0 ? __ldg(reinterpret_cast<const uint4 *>(src[t] + ch * 512 + tok[t] * 16)) : none;
         *reinterpret_cast<uint4 *>(dst + ch * 512 + t * 16) = v;
     }
-    for (int i = tid; i < kTok * G; i += kMoveThreads) {
-        const int t = i / G, g = i % G;
-        dst[k_scale_at(D) + i] = src[t] ? src[t][k_scale_at(D) + tok[t] * G + g] : 0;
-        const int u = i % kTok, w = i / kTok;
-        dst[v_scale_at(D) + i] = src[u] ? src[u][v_scale_at(D) + w * kTok + tok[u]] : 0;
-    }
-    for (int i = tid; i < D * 4; i += kMoveThreads) {      // 8 tokens of a channel
-        const int d = i % D, t0 = i / D * 8;
-        uint32_t w = 0;
+    if (tid < kTok) {                                      // a token's K scales
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int t = t0 + j;
-            if (src[t])
-                w |= static_cast<uint32_t>(src[t][v_codes_at(D) + d * 16 + tok[t] / 2] >> (tok[t] % 2 * 4) & 15)
-                     << 4 * j;
+        for (int g = 0; g < G; g += 4)
+            *reinterpret_cast<uint32_t *>(dst + k_scale_at(D) + tid * G + g) =
+                tok[tid] >= 0 ? __ldg(reinterpret_cast<const uint32_t *>(src[tid] + k_scale_at(D) + tok[tid] * G + g)) : 0u;
+    }
+#pragma unroll
+    for (int i = tid; i < kTok * G; i += kMoveThreads) {   // V scales
+        const int u = i % kTok, w = i / kTok;
+        dst[v_scale_at(D) + i] = tok[u] >= 0 ? __ldg(src[u] + v_scale_at(D) + w * kTok + tok[u]) : 0;
+    }
+    for (int d = tid; d < D; d += kMoveThreads) {
+        uint32_t out[4];
+        const uint8_t *cur = nullptr;
+        uint4 v = none;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            uint32_t w = 0;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int t = tok[8 * q + j];
+                if (t < 0) continue;                       // (uniform, as all of this)
+                if (src[8 * q + j] != cur) {
+                    cur = src[8 * q + j];
+                    v = __ldg(reinterpret_cast<const uint4 *>(cur + v_codes_at(D) + d * 16));
+                }
+                const uint32_t word = t < 16 ? (t < 8 ? v.x : v.y) : (t < 24 ? v.z : v.w);
+                w |= (word >> (t % 8 * 4) & 15u) << (4 * j);
+            }
+            out[q] = w;
         }
-        *reinterpret_cast<uint32_t *>(dst + v_codes_at(D) + d * 16 + t0 / 2) = w;
+        *reinterpret_cast<uint4 *>(dst + v_codes_at(D) + d * 16) = make_uint4(out[0], out[1], out[2], out[3]);
     }
 }
 
@@ -383,13 +534,25 @@ cudaError_t launch_cache_rows(const CacheView &c, const CacheRows &r, int dtype,
 
 cudaError_t launch_cache_evict(const CacheView &c, const EvictParams &p, cudaStream_t s)
 {
-    evict_select_kernel<<<c.B, kSelThreads, 0, s>>>(c, p);
-    cudaError_t e = cudaGetLastError();
+    static bool done[64] = {false};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (!done[dev]) {
+        e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelSmem);
+        if (e != cudaSuccess) return e;
+        done[dev] = true;
+    }
+    evict_select_kernel<<<c.B * kSelCtas, kSelThreads, kSelSmem, s>>>(c, p);
+    e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     const int64_t most = static_cast<int64_t>(c.max_pages) * c.page_tokens;
     const int64_t keep = most < p.budget ? most : p.budget;
     const dim3 grid(static_cast<unsigned>((keep + kTok - 1) / kTok), c.H, c.B);
-    evict_move_kernel<<<grid, kMoveThreads, 0, s>>>(c, p);
+    if (c.D == 64) evict_move_kernel<64><<<grid, kMoveThreads, 0, s>>>(c, p);
+    else if (c.D == 128) evict_move_kernel<128><<<grid, kMoveThreads, 0, s>>>(c, p);
+    else evict_move_kernel<256><<<grid, kMoveThreads, 0, s>>>(c, p);
     return cudaGetLastError();
 }
 

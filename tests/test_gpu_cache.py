@@ -210,6 +210,31 @@ def test_append_strided_rows_scores_and_positions():
     np.testing.assert_array_equal(pos.cpu().numpy(), want_p)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_read_into_strided_unaligned_rows(dtype):
+    """The C call with strides and bases that allow no wide stores: the values
+    of the aligned call, and nothing between the rows touched."""
+    import ctypes as C
+    from speculative_decoding_verification_ragged_gb300.cache import _Rows
+    sv = need_gpu()
+    rng = np.random.default_rng(8)
+    c = quick_pool(rng, B=1, H=2, D=64, page=32, lens=[45])
+    cache, tab = gpu_cache(sv, c), dev(c.table)
+    cu, start = dev(np.array([0, 40], np.int32)), dev(np.array([5], np.int32))
+    want = sv.cache_read(cache, cu, start, tab, B=1, max_rows=40, dtype=DT[dtype])
+    wide = [torch.full((40, 2 * 67 + 1), 7.0, device="cuda", dtype=DT[dtype]) for _ in range(2)]
+    view = cache._view(tab, 1)
+    at = [w.data_ptr() + w.element_size() for w in wide]
+    rows = _Rows(at[0], at[1], 1 if dtype == "bf16" else 0, 135, 67, 135, 67, 40, 40, cu.data_ptr(), start.data_ptr())
+    assert sv.load_library().spec_cache_read(C.byref(view), C.byref(rows), None) == 0
+    torch.cuda.synchronize()
+    for w, x in zip(wide, (want["k"], want["v"])):
+        for h in range(2):
+            assert torch.equal(w[:, 1 + 67 * h:65 + 67 * h], x[:, h])
+            w[:, 1 + 67 * h:65 + 67 * h] = 7.0
+        assert (w == 7.0).all()
+
+
 def test_append_and_read_skip_bad_requests():
     sv = need_gpu()
     rng = np.random.default_rng(7)
