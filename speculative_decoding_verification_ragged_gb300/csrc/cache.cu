@@ -238,10 +238,17 @@ __global__ void __launch_bounds__(kRowThreads) read_kernel(const CacheView c, co
 // ------------------------------------------------------------- eviction ---
 
 constexpr int kSelThreads = 1024;
-constexpr int kSelCtas = 8;                // cluster of a request
+constexpr int kSelCtas = 8;                // CTAs of a request's cluster at most
 constexpr int kBins = 2048;                // a radix digit: 11 bits (the last: 10)
 constexpr int kSelStaged = 40 * 1024;      // scores a CTA keeps in shared memory
-constexpr int kSelSmem = (kSelStaged + kSelStaged / 16) * 4;
+constexpr int kRun = 16;                   // a thread's slots are a multiple of this
+
+// slots of a CTA's slice where a cluster of `ctas` shares `len`
+__host__ __device__ inline int64_t sel_slice(int64_t len, int ctas)
+{
+    const int64_t per = static_cast<int64_t>(ctas) * kSelThreads;
+    return ((len + per - 1) / per + kRun - 1) / kRun * kRun * kSelThreads;
+}
 
 // Order-preserving key of a score: NaN below everything, -0 equal to +0.
 __device__ __forceinline__ uint32_t score_key(float x) { return x != x ? 0u : fkey(x); }
@@ -270,22 +277,23 @@ __device__ __forceinline__ int cta_scan(int v, int *warp_sum, int &total)
     return (warp ? before : 0) + incl - v;
 }
 
-// Selection: a cluster of 8 CTAs per request, each with a contiguous eighth of
-// the slots, its keys in shared memory (read again from the cache's scores where
-// they do not fit).  A radix search, 11 bits a pass over the cluster's summed
+// Selection: a cluster of 1, 2, 4 or 8 CTAs per request (one for every 16384
+// slots: a pass costs a cluster 2 barriers and the reading of its histograms, 4 us
+// in all), each with a contiguous part of the slots, its keys in shared memory
+// (read again from the cache's scores where they do not fit).  A radix search, 11 bits a pass over the cluster's summed
 // histograms, finds the key of the last score kept; then a thread lists the kept
 // slots of a contiguous run of its own: those above the key, the first few at
 // it, and the newest.  2 x 131072 scores: one CTA a request took 370 us of the
 // call's 415.
-__global__ void __cluster_dims__(kSelCtas, 1, 1) __launch_bounds__(kSelThreads)
-evict_select_kernel(const CacheView c, const EvictParams p)
+__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const CacheView c, const EvictParams p)
 {
     namespace cg = cooperative_groups;
     cg::cluster_group cluster = cg::this_cluster();
     extern __shared__ __align__(16) uint8_t smem_raw[];
     uint32_t *keys = reinterpret_cast<uint32_t *>(smem_raw);
     __shared__ int hist[kBins], warp_sum[kSelThreads / 32], pick[2], count[2];
-    const int b = blockIdx.x / kSelCtas, rank = blockIdx.x % kSelCtas, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int ctas = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
+    const int b = blockIdx.x / ctas, tid = threadIdx.x;
     const int len = p.len[b];
     int32_t *kept = p.kept + static_cast<int64_t>(b) * p.budget;
     const int64_t room = static_cast<int64_t>(c.max_pages) * c.page_tokens;
@@ -302,7 +310,7 @@ evict_select_kernel(const CacheView c, const EvictParams p)
         if (__syncthreads_or(bad_page)) bad = SPEC_STATUS_BAD_PAGE;
     }
     // (the same in every CTA of the cluster: none is left waiting)
-    const int all = kSelCtas * kSelThreads, me = rank * kSelThreads + tid;
+    const int all = ctas * kSelThreads, me = rank * kSelThreads + tid;
     if (bad) {
         if (me == 0) {
             set_status(p.status, bad);
@@ -320,13 +328,12 @@ evict_select_kernel(const CacheView c, const EvictParams p)
 
     const int old = len - p.recent;          // slots that compete for `want` places
     int want = p.budget - p.recent;
-    // this CTA's slots: a run of `run` (a multiple of 16) per thread
-    const int run = ((len + all - 1) / all + 15) / 16 * 16, slice = run * kSelThreads;
+    const int slice = static_cast<int>(sel_slice(len, ctas)), run = slice / kSelThreads;   // a run per thread
     const int64_t first = static_cast<int64_t>(rank) * slice;
     const bool staged = slice <= kSelStaged;
     // keys are padded by one in 16, so that runs of 16 start in different banks;
     // slots that do not compete have key 0
-    const auto place = [](int i) { return i + i / 16; };
+    const auto place = [](int i) { return i + i / kRun; };
     const auto fetch = [&](int i) {
         const int64_t slot = first + i;
         if (slot >= old) return 0u;
@@ -336,14 +343,14 @@ evict_select_kernel(const CacheView c, const EvictParams p)
     };
     const int mine = first >= old ? 0 : static_cast<int>(min(static_cast<int64_t>(slice), old - first));
     if (staged) {
-        // a warp reads 4 x 32 consecutive scores at a time, each 32 of one page
-        for (int i0 = warp * 128; i0 < slice; i0 += kSelThreads / 32 * 128) {
-            uint32_t k[4];
+        // 16 loads of a thread in flight
+        for (int i0 = tid; i0 < mine; i0 += kSelThreads * kRun) {
+            uint32_t k[kRun];
 #pragma unroll
-            for (int u = 0; u < 4; ++u) k[u] = i0 + u * 32 + lane < mine ? fetch(i0 + u * 32 + lane) : 0u;
+            for (int u = 0; u < kRun; ++u) k[u] = i0 + u * kSelThreads < mine ? fetch(i0 + u * kSelThreads) : 0u;
 #pragma unroll
-            for (int u = 0; u < 4; ++u)
-                if (i0 + u * 32 + lane < slice) keys[place(i0 + u * 32 + lane)] = k[u];
+            for (int u = 0; u < kRun; ++u)
+                if (i0 + u * kSelThreads < mine) keys[place(i0 + u * kSelThreads)] = k[u];
         }
     }
     const auto key_at = [&](int i) { return staged ? keys[place(i)] : fetch(i); };
@@ -361,8 +368,7 @@ evict_select_kernel(const CacheView c, const EvictParams p)
         cluster.sync();
         // bins from the top, two a thread, summed over the cluster
         int two[2] = {0, 0};
-#pragma unroll
-        for (int r = 0; r < kSelCtas; ++r) {
+        for (int r = 0; r < ctas; ++r) {
             const int *h = cluster.map_shared_rank(hist, r);
             const int at = bins - 2 - 2 * tid;
             if (at >= 0) {
@@ -540,12 +546,29 @@ cudaError_t launch_cache_evict(const CacheView &c, const EvictParams &p, cudaStr
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     if (!done[dev]) {
-        e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelSmem);
+        e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (kSelStaged + kSelStaged / kRun) * 4);
         if (e != cudaSuccess) return e;
         done[dev] = true;
     }
-    evict_select_kernel<<<c.B * kSelCtas, kSelThreads, kSelSmem, s>>>(c, p);
-    e = cudaGetLastError();
+    const int64_t room = static_cast<int64_t>(c.max_pages) * c.page_tokens;
+    int ctas = 1;
+    while (ctas < kSelCtas && sel_slice(room, ctas) > kRun * kSelThreads) ctas *= 2;
+    int64_t slice = sel_slice(room, ctas);
+    if (slice > kSelStaged) slice = kSelStaged;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = ctas;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(c.B * ctas, 1, 1);
+    cfg.blockDim = dim3(kSelThreads, 1, 1);
+    cfg.dynamicSmemBytes = static_cast<size_t>(slice + slice / kRun) * 4;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, evict_select_kernel, c, p);
     if (e != cudaSuccess) return e;
     const int64_t most = static_cast<int64_t>(c.max_pages) * c.page_tokens;
     const int64_t keep = most < p.budget ? most : p.budget;
