@@ -39,8 +39,8 @@ __device__ __forceinline__ int slot_position(const CacheView &c, const AttnParam
 // The steps that some row of the request sees.  With a window the first row
 // sees the prefix and what lies less than `window` positions before its own
 // slot; positions do not decrease over slots, so the hidden steps in between
-// are counted by a 32-way search over the steps' last slots (every warp does it
-// for itself).
+// are counted by an 8-way search over the steps' last slots.  A thread does it
+// alone, and always by the same probes: whoever asks gets the same answer.
 template <int STEP>
 __device__ __forceinline__ void visible_steps(const CacheView &c, const AttnParams &p, Job &w)
 {
@@ -52,23 +52,41 @@ __device__ __forceinline__ void visible_steps(const CacheView &c, const AttnPara
     int first = max(own - p.window + 1, 0) / STEP;
     if (p.slot_pos) {
         const int limit = slot_position(c, p, w.b, own) - p.window;
-        int lo = 0, hi = own / STEP;              // steps below lo are hidden, step hi is not
+        int lo = 0, hi = own / STEP;               // steps below lo are hidden, step hi is not
         while (lo < hi) {
-            const int step = (hi - lo + 31) / 32, t = lo + static_cast<int>(threadIdx.x & 31) * step;
-            const int slot = t * STEP + STEP - 1;
-            // (a bad page has no positions: its step counts as seen, its tokens are masked)
-            const bool hidden = t < hi && page_of(c, w.b, slot) >= 0 && slot_position(c, p, w.b, slot) <= limit;
-            const uint32_t seen = ~__ballot_sync(0xFFFFFFFFu, hidden);
-            const int k = seen ? __ffs(seen) - 1 : 32;           // probes 0 .. k - 1 are hidden, probe k is not
+            const int by = (hi - lo + 6) / 7;
+            uint32_t hidden = 0;
+#pragma unroll
+            for (int u = 0; u < 7; ++u) {
+                const int t = lo + u * by, slot = t * STEP + STEP - 1;
+                // (a bad page has no positions: its step counts as seen, its tokens are masked)
+                if (t < hi && page_of(c, w.b, slot) >= 0 && slot_position(c, p, w.b, slot) <= limit) hidden |= 1u << u;
+            }
+            const int k = __ffs(~hidden) - 1;      // probes 0 .. k - 1 are hidden, probe k is not
             if (k == 0) break;
-            hi = min(hi, lo + k * step);
-            lo += (k - 1) * step + 1;
+            if (k < 7) hi = min(hi, lo + k * by);
+            lo += (k - 1) * by + 1;
         }
         first = lo;
     }
     w.np = min((p.prefix + STEP - 1) / STEP, first);
     w.f0 = first;
     w.nsteps = w.np + max(w.nsteps - first, 0);
+}
+
+// Rows and length of request w.b: false where it has no rows to attend with.
+// `status`: where to report what is wrong with it, or null.
+template <int STEP>
+__device__ __forceinline__ bool load_job(const CacheView &c, const AttnParams &p, Job &w, uint32_t *status)
+{
+    if (!request_rows(p.cu_rows, w.b, p.R_cap, p.k_max + 1, status, w.lo, w.n) || w.n == 0) return false;
+    w.len = p.len[w.b];
+    if (w.len < 0 || w.len > p.max_len) {
+        set_status(status, SPEC_STATUS_BAD_LENGTH);
+        w.len = 0;
+    }
+    visible_steps<STEP>(c, p, w);
+    return true;
 }
 
 // Copy the first BYTES of the BLOCKS blocks of a step into a stage (all of a

@@ -22,7 +22,8 @@ struct BlockRows {
 __device__ __forceinline__ bool block_rows(const CacheView &c, const CacheRows &r, int b, int idx,
                                            BlockRows &o)
 {
-    if (!request_rows(r.cu_rows, b, r.R_cap, r.max_rows, r.status, o.lo, o.n) || o.n == 0) return false;
+    if (!request_rows(r.cu_rows, b, r.R_cap, r.max_rows, threadIdx.x == 0 ? r.status : nullptr, o.lo, o.n) || o.n == 0)
+        return false;
     o.start = r.start[b];
     const int64_t room = static_cast<int64_t>(c.max_pages) * c.page_tokens;
     if (o.start < 0 || o.start + static_cast<int64_t>(o.n) > room) {

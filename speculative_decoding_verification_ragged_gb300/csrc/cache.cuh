@@ -44,7 +44,7 @@ __device__ __forceinline__ bool request_rows(const int32_t *cu_rows, int b, int 
     const int64_t d = static_cast<int64_t>(hi) - lo;
     n = static_cast<int>(d);
     if (lo < 0 || hi > R_cap || d < 0 || d > max_rows) {
-        if (threadIdx.x == 0) set_status(status, SPEC_STATUS_BAD_ROWS);
+        set_status(status, SPEC_STATUS_BAD_ROWS);
         n = 0;
         return false;
     }

@@ -40,6 +40,7 @@ constexpr float kExceed = 15.f;            // ... stays below 2^15
 constexpr float kWideScale = 5.192296858534828e33f;
 
 template <typename T, int D_, int NT_> struct Attn {
+    using Type = T;
     static constexpr int D = D_, NT = NT_;
     static constexpr int NH = NT / 2;                          // columns of a thread
     static constexpr int PIECES = sizeof(T) == 4 ? 2 : 1;      // f16 terms of a query and of a weight
@@ -63,10 +64,10 @@ template <typename T, int D_, int NT_> struct Attn {
     static constexpr int VS_BYTES = D / 16 * kTile * 2;        // a tile's scales of V as f16
     static constexpr int STAGE = 4 * block_bytes(D);
     static constexpr int OPERANDS = PIECES * (Q_BYTES + P_BYTES) + 2 * VS_BYTES;
-    static constexpr int STAGES = clamp_stages((smem_share(CTAS, 128 + 60 * NT) - OPERANDS) / STAGE);
+    static constexpr int STAGES = clamp_stages((smem_share(CTAS, 512 + 60 * NT) - OPERANDS) / STAGE);
     static constexpr int NEED = OPERANDS + STAGES * STAGE;
     static constexpr int SMEM = NEED > smem_least(CTAS) ? NEED : smem_least(CTAS);
-    static_assert(D != 64 || NT * D * 4 <= STAGES * STAGE, "the epilogue's exchange fits the stages");
+    static_assert(D != 64 || NT * D * 4 <= PIECES * P_BYTES, "the epilogue's exchange fits the weights' place");
 };
 
 // Scales of a tile's values as f16, tokens in pairs, [D/16][64]; the scale of a
@@ -274,19 +275,138 @@ __device__ __forceinline__ void rescale_results(const Columns<A::NT> &cs, uint32
     tmem_wait_st();
 }
 
-struct Split {
-    int steps, most;            // steps of a split, splits of the longest request
-    int qtiles, cols;           // column tiles, columns of a request at most
+// The work of a call, laid out in one line: request by request, kv head by kv
+// head, column tile by column tile ("tasks"), the visible tiles of each.  A task
+// without tiles counts one (its rows are written as zeros).  CTA i of `grid` (no
+// more than there are units: none is empty) takes [i * total / grid, (i + 1) *
+// total / grid): whatever the lengths, the CTAs end together, and a task is split
+// at most where two CTAs meet.
+struct Layout {
+    int grid;                   // CTAs at most, all resident at once
+    int qtiles;                 // column tiles of a request at most
 };
 
-// Warps 0..7 decode, weigh and store; warp 8 fetches tiles and issues the
-// products.  Per tile the eight warps wait for S^T, turn it into weights (one
-// barrier: do the references hold?), decode the next tile's keys, then this
-// tile's values; each product runs while they decode the other operand, and they
-// meet the ninth warp at mbarriers only.
+__device__ __forceinline__ int64_t range_start(int64_t total, int grid, int i) { return total * i / grid; }
+// the CTA whose range holds unit t
+__device__ __forceinline__ int range_of(int64_t total, int grid, int64_t t)
+{
+    return static_cast<int>(((t + 1) * grid - 1) / total);
+}
+
+// A place in the line: task `task` (head * column tiles + column tile) of
+// request w.b, unit `unit` of it.
+template <int NT> struct Cursor {
+    Job w;
+    int64_t left;               // units to go in this CTA's range
+    int qt, tasks, task, unit;
+
+    __device__ __forceinline__ bool load(const CacheView &c, const AttnParams &p, int group)
+    {
+        if (!load_job<kTile>(c, p, w, nullptr)) return false;
+        qt = (w.n * group + NT - 1) / NT;
+        tasks = c.H * qt;
+        return true;
+    }
+    __device__ __forceinline__ int units() const { return max(w.nsteps, 1); }
+    // units of this task in the range, and the job's head and columns
+    __device__ __forceinline__ int segment(int group)
+    {
+        w.h = task / qt;
+        w.col0 = task % qt * NT;
+        w.ncols = min(w.n * group - w.col0, NT);
+        return static_cast<int>(min(static_cast<int64_t>(units() - unit), left));
+    }
+    __device__ __forceinline__ void next(const CacheView &c, const AttnParams &p, int group, int done)
+    {
+        left -= done;
+        unit = 0;
+        if (left > 0 && ++task == tasks) {
+            task = 0;
+            do {
+                if (++w.b >= c.B) {                   // (the line ends with the last request)
+                    left = 0;
+                    return;
+                }
+            } while (!load(c, p, group));
+        }
+    }
+};
+
+// Where this CTA's range begins: every thread takes a request at a time, a scan
+// of their units places them.
+template <int NT>
+__device__ __forceinline__ int64_t find_range(const CacheView &c, const AttnParams &p, const Layout &lay, int group,
+                                              int &grid, int64_t &t0, int &b0, int64_t &off)
+{
+    constexpr int N = kAttnThreads + 32;
+    __shared__ int64_t sums[N / 32 + 1], place[2];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const auto weight = [&](int b, bool report) {
+        Job w;
+        w.b = b;
+        if (b >= c.B || !load_job<kTile>(c, p, w, report && blockIdx.x == 0 ? p.status : nullptr)) return static_cast<int64_t>(0);
+        return static_cast<int64_t>(c.H) * ((w.n * group + NT - 1) / NT) * max(w.nsteps, 1);
+    };
+    // inclusive scan over the CTA; `all`: its total
+    const auto scan = [&](int64_t v, int64_t &all) {
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t y = __shfl_up_sync(0xFFFFFFFFu, v, o);
+            if (lane >= o) v += y;
+        }
+        __syncthreads();
+        if (lane == 31) sums[warp] = v;
+        __syncthreads();
+        int64_t before = 0;
+        all = 0;
+#pragma unroll
+        for (int i = 0; i < N / 32; ++i) {
+            before += i < warp ? sums[i] : 0;
+            all += sums[i];
+        }
+        return before + v;
+    };
+    int64_t total, mine = weight(tid, true), at = scan(mine, total);
+    int64_t part = total;                         // of the N requests at hand
+    for (int b = N; b < c.B; b += N) {
+        int64_t v = weight(b + tid, true);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+        __syncthreads();
+        if (lane == 0) sums[warp] = v;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < N / 32; ++i) total += sums[i];
+    }
+    grid = static_cast<int>(min(static_cast<int64_t>(lay.grid), total));
+    if (static_cast<int>(blockIdx.x) >= grid) return total;
+    t0 = range_start(total, grid, blockIdx.x);
+    int64_t base = 0;
+    for (int b = 0;; ) {
+        if (at - mine + base <= t0 && t0 < at + base) {
+            place[0] = b + tid;
+            place[1] = t0 - (at - mine + base);
+        }
+        base += part;
+        b += N;
+        if (b >= c.B || base > t0) break;
+        mine = weight(b + tid, false);
+        at = scan(mine, part);
+    }
+    __syncthreads();
+    b0 = static_cast<int>(place[0]);
+    off = place[1];
+    return total;
+}
+
+// Warps 0..7 decode, weigh and store; warp 8 fetches tiles, ahead over the whole
+// range, and issues the products.  Per tile the eight warps wait for S^T, turn it
+// into weights (one barrier: do the references hold?), decode the next tile's
+// keys, then this tile's values; each product runs while they decode the other
+// operand, and they meet the ninth warp at mbarriers only.
 template <typename T, int D, int NT>
 __global__ void __launch_bounds__(kAttnThreads + 32, (Attn<T, D, NT>::CTAS))
-attend_kernel(const CacheView c, const AttnParams p, const Split sp)
+attend_kernel(const CacheView c, const AttnParams p, const Layout lay)
 {
     using A = Attn<T, D, NT>;
     constexpr int NH = A::NH;
@@ -299,124 +419,123 @@ attend_kernel(const CacheView c, const AttnParams p, const Split sp)
     __shared__ __align__(16) Columns<NT> cs;
     __shared__ __align__(8) uint64_t full[A::STAGES], k_bar, p_bar, s_bar, o_bar;
     __shared__ uint32_t tmem_base, arrived;
-    __shared__ int more;                              // wide tile: terms to come after this one, +1
+    // what the eight warps tell the ninth: with keys, kFirst / kLast of a segment
+    // or kEnd; with weights, 0 or the bf16 terms to come, this one included
+    constexpr int kFirst = 1, kLast = 2, kEnd = 4;
+    __shared__ int keys_are, terms;
     __shared__ __align__(16) int nv[A::STAGES][4];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-
     const int group = p.Hq / c.H;
-    Job w;
-    const int split = blockIdx.y;
-    w.h = blockIdx.x / sp.qtiles;
-    w.b = blockIdx.z;
-    w.col0 = static_cast<int>(blockIdx.x) % sp.qtiles * NT;
-    if (!request_rows(p.cu_rows, w.b, p.R_cap, p.k_max + 1, p.status, w.lo, w.n)) return;
-    w.ncols = min(w.n * group - w.col0, NT);
-    if (w.ncols <= 0) return;
-    w.len = p.len[w.b];
-    if (w.len < 0 || w.len > p.max_len) {
-        if (tid == 0) set_status(p.status, SPEC_STATUS_BAD_LENGTH);
-        w.len = 0;
-    }
-    if (split > 0 && split * sp.steps * kTile >= w.len) return;
-    visible_steps<kTile>(c, p, w);
-    const int nsplit = max((w.nsteps + sp.steps - 1) / sp.steps, 1);
-    if (split >= nsplit) return;
-    const int i0 = split * sp.steps, n = min(i0 + sp.steps, w.nsteps) - i0;
 
-    if (warp == 8) {
-        if (lane == 0) {
-            for (int i = 0; i < A::STAGES; ++i) mbar_init(&full[i], 1);
-            mbar_init(&k_bar, 8);
-            mbar_init(&p_bar, 8);
-            mbar_init(&s_bar, 1);
-            mbar_init(&o_bar, 1);
-            fence_mbar_init();
-        }
-        __syncwarp();
-        // the first loads go out before anything else
-        for (int i = 0; i < A::STAGES && i < n; ++i) {
-            const int slot = step_slot<kTile>(w, i0 + i);
-            load_step<block_bytes(D), 4>(c, w, w.h, slot, step_page<4>(c, w, slot), stages + i * A::STAGE, &full[i], nv[i],
-                                         p.status);
-        }
-    } else {
-        if (warp == 0) tmem_alloc(&tmem_base, A::COLS);
-        if (tid < NT) {
-            const int col = w.col0 + tid, j = min(col / group, w.n - 1);
-            const int own = w.len > 0 ? w.len - w.n + j : -1;
-            cs.own[tid] = own;
-            cs.pos[tid] = own >= 0 ? slot_position(c, p, w.b, own) : 0;
-            cs.slope[tid] = p.slopes && tid < w.ncols ? p.slopes[w.h * group + col % group] * kLog2e : 0.f;
-            cs.ref[tid] = tid < w.ncols ? kHeadroom - kUnset : 0.f;      // (a padded column's results are unused)
-        }
-        stage_queries<T, D, NT, A::PIECES>(p, w, group, c.k_scale ? c.k_scale[w.h] : 1.f, 1.4426950408889634, qs, cs.mult);
-        fence_proxy_async_smem();
+    if (warp == 8 && lane == 0) {
+        for (int i = 0; i < A::STAGES; ++i) mbar_init(&full[i], 1);
+        mbar_init(&k_bar, 8);
+        mbar_init(&p_bar, 8);
+        mbar_init(&s_bar, 1);
+        mbar_init(&o_bar, 1);
+        fence_mbar_init();
     }
+    // the place of the eight warps in the line (they move it one thread at a time,
+    // and read it where they need it: registers are short), its unit and the total
+    __shared__ Cursor<NT> cur_s;
+    __shared__ int64_t t0_s, total_s;
+    __shared__ int grid_s;
+    Cursor<NT> cur;
+    {
+        int64_t t0, off;
+        int grid;
+        const int64_t total = find_range<NT>(c, p, lay, group, grid, t0, cur.w.b, off);
+        if (static_cast<int>(blockIdx.x) >= grid) return;
+        cur.left = range_start(total, grid, blockIdx.x + 1) - t0;
+        cur.load(c, p, group);
+        cur.task = static_cast<int>(off / cur.units());
+        cur.unit = static_cast<int>(off % cur.units());
+        if (tid == 0) {
+            cur.segment(group);
+            cur_s = cur;
+            t0_s = t0;
+            total_s = total;
+            grid_s = grid;
+        }
+    }
+    if (warp == 0) tmem_alloc(&tmem_base, A::COLS);
     __syncthreads();
     tmem_fence_after();
     const uint32_t a_t = tmem_base, v_t = a_t + A::A_COLS, s_t = v_t + A::V_COLS, o_t = s_t + A::S_COLS;
     bool fail = false;
 
     if (warp == 8) {
-        // the ninth warp: products in the order their operands come, and the
-        // stage of a finished tile filled again
         const bool leader = elect_one();
         const uint32_t q_addr = smem_addr(qs), p_addr = smem_addr(ps);
-        int p_count = 0;
-        int page = A::STAGES < n ? step_page<4>(c, w, step_slot<kTile>(w, i0 + A::STAGES)) : -1;
-        for (int k = -1; k < n; ++k) {
-            if (k + 1 < n) {
-                wait_or_fail(&k_bar, (k + 1) & 1, fail);
-                tmem_fence_after();
-                if (leader) {
-                    issue_scores<D, NT, A::PIECES>(s_t, a_t, q_addr);
-                    mma_commit(&s_bar);
-                }
-                __syncwarp();
+        // the next tile of the range into the ring
+        int ring = 0, seg = cur.segment(group), k_ld = 0;
+        const auto load_next = [&] {
+            while (cur.left > 0 && (k_ld == seg || cur.w.nsteps == 0)) {
+                cur.next(c, p, group, seg);
+                if (cur.left > 0) seg = cur.segment(group);
+                k_ld = 0;
             }
-            if (k < 0) continue;
+            if (cur.left <= 0) return;
+            const int slot = step_slot<kTile>(cur.w, cur.unit + k_ld++);
+            load_step<block_bytes(D), 4>(c, cur.w, cur.w.h, slot, step_page<4>(c, cur.w, slot), stages + ring * A::STAGE,
+                                         &full[ring], nv[ring], p.status);
+            ring = ring + 1 == A::STAGES ? 0 : ring + 1;
+        };
+        for (int i = 0; i < A::STAGES; ++i) load_next();
+        // products in the order their operands come
+        int g = 0, p_count = 0, now = 0;
+        const auto scores = [&] {
+            wait_or_fail(&k_bar, g++ & 1, fail);
+            tmem_fence_after();
+            now = fail ? kEnd : *reinterpret_cast<volatile int *>(&keys_are);
+            if (now == kEnd) return;
+            if (leader) {
+                issue_scores<D, NT, A::PIECES>(s_t, a_t, q_addr);
+                mma_commit(&s_bar);
+            }
+            __syncwarp();
+        };
+        scores();
+        while (now != kEnd) {
+            const int here = now;
+            if (!(here & kLast)) scores();
             bool again = false;
             do {
                 wait_or_fail(&p_bar, p_count++ & 1, fail);
                 tmem_fence_after();
-                const int left = *reinterpret_cast<volatile int *>(&more);
+                const int left = *reinterpret_cast<volatile int *>(&terms);
                 if (leader) {
-                    const bool first = !again && (kPromote || k == 0);
-                    if (left == 0) issue_values<A, false>(o_t, v_t, p_addr, !first);
-                    else issue_values<A, true>(o_t, v_t, p_addr, !first);
+                    const bool accumulate = again || !(kPromote || (here & kFirst));
+                    if (left == 0) issue_values<A, false>(o_t, v_t, p_addr, accumulate);
+                    else issue_values<A, true>(o_t, v_t, p_addr, accumulate);
                     mma_commit(&o_bar);
                 }
                 __syncwarp();
                 again = left > 1;
             } while (again && !fail);
-            if (k + A::STAGES < n) {
-                const int st = k % A::STAGES;
-                load_step<block_bytes(D), 4>(c, w, w.h, step_slot<kTile>(w, i0 + k + A::STAGES), page, stages + st * A::STAGE,
-                                             &full[st], nv[st], p.status);
-                page = k + A::STAGES + 1 < n ? step_page<4>(c, w, step_slot<kTile>(w, i0 + k + A::STAGES + 1)) : -1;
-            }
+            load_next();
+            if (here & kLast) scores();
         }
         return;
     }
 
     const int quarter = warp & 3, half = warp >> 2, tok = tid & 127;
-    const float gv = c.v_scale ? c.v_scale[w.h] : 1.f;
     const bool options = p.cap > 0.f || p.slopes || p.window > 0;
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
     // where this thread's columns of the result lie (D = 64: those of its tokens)
     const uint32_t o_mine = o_t + lane_off + half * NH + (D == 64 && quarter >= 2 ? NT : 0);
+    constexpr int PN8 = A::VT * 16;
+    uint8_t *const p_mine = ps + (tok / A::VT * (NT / 8) + half * (NH / 8)) * PN8 + tok % A::VT * 16;
 
     float l[NH], acc[OR];
-#pragma unroll
-    for (int i = 0; i < NH; ++i) l[i] = 0.f;
-#pragma unroll
-    for (int i = 0; i < OR; ++i) acc[i] = 0.f;
-    int o_count = 0;                                  // products with V^T waited for
-    bool pending = false;                             // one is under way
+    bool pending = false;                             // a product with V^T is under way
+    uint32_t s_phase = 0, o_phase = 0, ring_phase = 0;
+    int ring = 0, vbuf = 0;                           // stage of the tile whose values come next
     // wait for the product with V^T under way; fp32: add its result up
     const auto finish_values = [&] {
         pending = false;
-        wait_or_fail(&o_bar, o_count++ & 1, fail);
+        wait_or_fail(&o_bar, o_phase, fail);
+        o_phase ^= 1;
         tmem_fence_after();
         if constexpr (kPromote) {
 #pragma unroll
@@ -429,266 +548,310 @@ attend_kernel(const CacheView c, const AttnParams p, const Split sp)
             }
         }
     };
-    const auto keys = [&](int k) {
-        const int st = k % A::STAGES;
-        wait_or_fail(&full[st], k / A::STAGES & 1, fail);
+    // the keys of the tile in stage `st` (in phase `phase` of the ring)
+    const auto keys = [&](int st, uint32_t phase, int what) {
+        wait_or_fail(&full[st], phase, fail);
         decode_keys<D>(stages + st * A::STAGE + quarter * block_bytes(D), a_t + lane_off);
+        if (tid == 0) keys_are = what;
         tmem_wait_st();
         tmem_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&k_bar);
     };
-    const int own_first = cs.own[0];
-    constexpr int PN8 = A::VT * 16;
-    uint8_t *const p_mine = ps + (tok / A::VT * (NT / 8) + half * (NH / 8)) * PN8 + tok % A::VT * 16;
-    if (n > 0) keys(0);
-    for (int k = 0; k < n; ++k) {
-        const int st = k % A::STAGES, slot0 = step_slot<kTile>(w, i0 + k);
-        const uint8_t *stage = stages + st * A::STAGE;
-        uint32_t *vsk = vs + (k & 1) * (A::VS_BYTES / 4);
-        Token t;
-        const int4 n4 = *reinterpret_cast<const int4 *>(nv[st]);
-        const bool whole = (n4.x & n4.y & n4.z & n4.w) == kTok;      // (each at most 32)
-        t.slot = t.pos = slot0 + tok;
-        t.live = whole || lane < nv[st][quarter];
-        t.edge = !whole || slot0 + kTile - 1 > own_first;
-        if (options && p.slot_pos && t.live) t.pos = slot_position(c, p, w.b, t.slot);
-        value_scales<D>(stage, nv[st], whole, vsk);
-        wait_or_fail(&s_bar, k & 1, fail);
-        tmem_fence_after();
-        float v[NH];
-        bool wide = false;
-        for (;;) {
-            token_scores<A, NH, true>(p, w, cs, s_t + lane_off, half * NH, t, options, v);
-            float most = -INFINITY, least = INFINITY;
-#pragma unroll
-            for (int q = 0; q < NH; ++q) most = fmaxf(most, v[q]);
-            if (t.edge || options) {
-#pragma unroll
-                for (int q = 0; q < NH; ++q) least = fminf(least, v[q] == -INFINITY ? INFINITY : v[q]);
-            } else {
-#pragma unroll
-                for (int q = 0; q < NH; ++q) least = fminf(least, v[q]);
-            }
-            if (!csync_count(most > kExceed || least < A::LEAST_EXP)) break;
-            if (!csync_count(most > kExceed)) {
-                wide = true;
-                break;
-            }
-            move_references<A>(p, w, cs, s_t + lane_off, t, options);
-            if (pending) finish_values();
-#pragma unroll
-            for (int q = 0; q < NH; ++q) l[q] *= cs.factor[half * NH + q];
-            if (kPromote) {
-#pragma unroll
-                for (int q = 0; q < OR; ++q) acc[q] *= cs.factor[half * NH + q % NH];
-            } else if (k > 0) {
-                rescale_results<A>(cs, o_t + lane_off);
-            }
+
+    const Job &w = cur_s.w;
+    while (cur_s.left > 0) {
+        const int seg = static_cast<int>(min(static_cast<int64_t>(cur_s.units() - cur_s.unit), cur_s.left));
+        const int n = w.nsteps > 0 ? seg : 0;         // tiles here
+        const float gk = c.k_scale ? c.k_scale[w.h] : 1.f, gv = c.v_scale ? c.v_scale[w.h] : 1.f;
+        if (tid < NT) {
+            const int col = w.col0 + tid, j = min(col / group, w.n - 1);
+            const int own = w.len > 0 ? w.len - w.n + j : -1;
+            cs.own[tid] = own;
+            cs.pos[tid] = own >= 0 ? slot_position(c, p, w.b, own) : 0;
+            cs.slope[tid] = p.slopes && tid < w.ncols ? p.slopes[w.h * group + col % group] * kLog2e : 0.f;
+            cs.ref[tid] = tid < w.ncols ? kHeadroom - kUnset : 0.f;      // (a padded column's results are unused)
         }
-        // S^T is read, the keys' columns are free: on to the next tile's keys
-        if (k + 1 < n) keys(k + 1);
-        if (pending) finish_values();                 // V^T's columns and P are free
-        // weights: sums in fp32, the operand 8 columns of this token per store
+        stage_queries<T, D, NT, A::PIECES>(p, w, group, gk, 1.4426950408889634, qs, cs.mult);
+        fence_proxy_async_smem();
+        csync();
 #pragma unroll
-        for (int q = 0; q < NH; q += 2) {
-            v[q] = ex2(v[q]);
-            v[q + 1] = ex2(v[q + 1]);
-            f2_unpack(f2_add(f2_pack(l[q], l[q + 1]), f2_pack(v[q], v[q + 1])), l[q], l[q + 1]);
-        }
-        if (!wide) {
+        for (int i = 0; i < NH; ++i) l[i] = 0.f;
 #pragma unroll
-            for (int q0 = 0; q0 < NH; q0 += 8) {
-                uint32_t hi[4];
+        for (int i = 0; i < OR; ++i) acc[i] = 0.f;
+        const int own_first = cs.own[0];
+        if (n > 0) keys(ring, ring_phase, kFirst | (n == 1 ? kLast : 0));
+        for (int k = 0; k < n; ++k) {
+            const uint8_t *stage = stages + ring * A::STAGE;
+            uint32_t *vsk = vs + vbuf * (A::VS_BYTES / 4);
+            const int slot0 = step_slot<kTile>(w, cur_s.unit + k);
+            Token t;
+            const int4 n4 = *reinterpret_cast<const int4 *>(nv[ring]);
+            const bool whole = (n4.x & n4.y & n4.z & n4.w) == kTok;      // (each at most 32)
+            t.slot = t.pos = slot0 + tok;
+            t.live = whole || lane < nv[ring][quarter];
+            t.edge = !whole || slot0 + kTile - 1 > own_first;
+            if (options && p.slot_pos && t.live) t.pos = slot_position(c, p, w.b, t.slot);
+            value_scales<D>(stage, nv[ring], whole, vsk);
+            vbuf ^= 1;
+            if (++ring == A::STAGES) {
+                ring = 0;
+                ring_phase ^= 1;
+            }
+            wait_or_fail(&s_bar, s_phase, fail);
+            s_phase ^= 1;
+            tmem_fence_after();
+            float v[NH];
+            bool wide = false;
+            for (;;) {
+                token_scores<A, NH, true>(p, w, cs, s_t + lane_off, half * NH, t, options, v);
+                float most = -INFINITY, least = INFINITY;
 #pragma unroll
-                for (int q = 0; q < 4; ++q) hi[q] = pack_h2(v[q0 + 2 * q], v[q0 + 2 * q + 1]);
-                *reinterpret_cast<uint4 *>(p_mine + q0 / 8 * PN8) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                if (A::PIECES == 2) {
-                    uint32_t lo[4];
+                for (int q = 0; q < NH; ++q) most = fmaxf(most, v[q]);
+                if (t.edge || options) {
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const float2 y = h2_float2(hi[q]);
-                        lo[q] = pack_h2(v[q0 + 2 * q] - y.x, v[q0 + 2 * q + 1] - y.y);
-                    }
-                    *reinterpret_cast<uint4 *>(p_mine + A::P_BYTES + q0 / 8 * PN8) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                    for (int q = 0; q < NH; ++q) least = fminf(least, v[q] == -INFINITY ? INFINITY : v[q]);
+                } else {
+#pragma unroll
+                    for (int q = 0; q < NH; ++q) least = fminf(least, v[q]);
+                }
+                if (!csync_count(most > kExceed || least < A::LEAST_EXP)) break;
+                if (!csync_count(most > kExceed)) {
+                    wide = true;
+                    break;
+                }
+                move_references<A>(p, w, cs, s_t + lane_off, t, options);
+                if (pending) finish_values();
+#pragma unroll
+                for (int q = 0; q < NH; ++q) l[q] *= cs.factor[half * NH + q];
+                if (kPromote) {
+#pragma unroll
+                    for (int q = 0; q < OR; ++q) acc[q] *= cs.factor[half * NH + q % NH];
+                } else if (k > 0) {
+                    rescale_results<A>(cs, o_t + lane_off);
                 }
             }
-            decode_tile_values<A, false>(stage, vsk, v_t + lane_off);
-            if (tid == 0) more = 0;
-            tmem_wait_st();
-            tmem_fence_before();
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&p_bar);
-        } else {
-            decode_tile_values<A, true>(stage, vsk, v_t + lane_off);
-            tmem_wait_st();
-#pragma unroll 1
-            for (int pc = 0; pc < A::WIDE; ++pc) {
-                if (pc > 0) wait_or_fail(&o_bar, o_count++ & 1, fail);
+            // S^T is read, the keys' columns are free: on to the next tile's keys
+            if (k + 1 < n) keys(ring, ring_phase, k + 2 == n ? kLast : 0);
+            if (pending) finish_values();             // V^T's columns and P are free
+            // weights: sums in fp32, the operand 8 columns of this token per store
+#pragma unroll
+            for (int q = 0; q < NH; q += 2) {
+                v[q] = ex2(v[q]);
+                v[q + 1] = ex2(v[q + 1]);
+                f2_unpack(f2_add(f2_pack(l[q], l[q + 1]), f2_pack(v[q], v[q + 1])), l[q], l[q + 1]);
+            }
+            if (!wide) {
 #pragma unroll
                 for (int q0 = 0; q0 < NH; q0 += 8) {
-                    uint32_t term[4];
+                    uint32_t hi[4];
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        float &x = v[q0 + 2 * q], &y = v[q0 + 2 * q + 1];
-                        if (pc == 0) {
-                            x *= kWideScale;
-                            y *= kWideScale;
+                    for (int q = 0; q < 4; ++q) hi[q] = pack_h2(v[q0 + 2 * q], v[q0 + 2 * q + 1]);
+                    *reinterpret_cast<uint4 *>(p_mine + q0 / 8 * PN8) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    if (A::PIECES == 2) {
+                        uint32_t lo[4];
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const float2 y = h2_float2(hi[q]);
+                            lo[q] = pack_h2(v[q0 + 2 * q] - y.x, v[q0 + 2 * q + 1] - y.y);
                         }
-                        term[q] = pack_bf2(x, y);
-                        x -= bf_lo(term[q]);
-                        y -= bf_hi(term[q]);
+                        *reinterpret_cast<uint4 *>(p_mine + A::P_BYTES + q0 / 8 * PN8) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                     }
-                    *reinterpret_cast<uint4 *>(p_mine + q0 / 8 * PN8) = make_uint4(term[0], term[1], term[2], term[3]);
                 }
-                if (tid == 0) more = A::WIDE - pc;
+                decode_tile_values<A, false>(stage, vsk, v_t + lane_off);
+                if (tid == 0) terms = 0;
+                tmem_wait_st();
                 tmem_fence_before();
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&p_bar);
+            } else {
+                decode_tile_values<A, true>(stage, vsk, v_t + lane_off);
+                tmem_wait_st();
+#pragma unroll 1
+                for (int pc = 0; pc < A::WIDE; ++pc) {
+                    if (pc > 0) {
+                        wait_or_fail(&o_bar, o_phase, fail);
+                        o_phase ^= 1;
+                    }
+#pragma unroll
+                    for (int q0 = 0; q0 < NH; q0 += 8) {
+                        uint32_t term[4];
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            float &x = v[q0 + 2 * q], &y = v[q0 + 2 * q + 1];
+                            if (pc == 0) {
+                                x *= kWideScale;
+                                y *= kWideScale;
+                            }
+                            term[q] = pack_bf2(x, y);
+                            x -= bf_lo(term[q]);
+                            y -= bf_hi(term[q]);
+                        }
+                        *reinterpret_cast<uint4 *>(p_mine + q0 / 8 * PN8) = make_uint4(term[0], term[1], term[2], term[3]);
+                    }
+                    if (tid == 0) terms = A::WIDE - pc;
+                    tmem_fence_before();
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&p_bar);
+                }
+            }
+            pending = true;
+        }
+        if (pending) finish_values();
+
+        // sums over the tiles' tokens (= lanes and quarters)
+        {
+            const float s = lane_sums<NH>(l);
+            if (lane % (32 / NH) == 0) cs.red[quarter][half * NH + lane / (32 / NH)] = s;
+        }
+        if (csync_count(fail)) break;
+        if (tid < NT) cs.sum[tid] = (cs.red[0][tid] + cs.red[1][tid]) + (cs.red[2][tid] + cs.red[3][tid]);
+        csync();
+
+        // A task that this CTA has only a part of leaves a partial result, [NT][D]
+        // fp32 and [NT] (reference, sum), in slot 2 i (it began before the range) or
+        // 2 i + 1 (it goes on after it).
+        const bool head = cur_s.unit > 0, tail = cur_s.unit + seg < cur_s.units();
+        const bool split = head || tail;
+        uint8_t *parts = static_cast<uint8_t *>(p.ws) + (static_cast<int64_t>(c.B) * c.H * lay.qtiles * 4 + 255) / 256 * 256;
+        float *const part_all = reinterpret_cast<float *>(parts);
+        float2 *const ml_all = reinterpret_cast<float2 *>(part_all + static_cast<int64_t>(lay.grid) * 2 * NT * D);
+        const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (head ? 0 : 1);
+        const auto out_row = [&](int q) {
+            const int col = w.col0 + q;
+            return static_cast<int64_t>(w.lo + col / group) * p.Hq + w.h * group + col % group;
+        };
+        float *xch = reinterpret_cast<float *>(ps);
+#pragma unroll
+        for (int m = 0; m < A::VM; ++m) {
+            float r[NH] = {};
+            if constexpr (kPromote) {
+#pragma unroll
+                for (int q = 0; q < NH; ++q) r[q] = acc[m * NH + q];
+            } else if (n > 0) {
+                tmem_ld<NH>(o_mine + m * NT, reinterpret_cast<uint32_t *>(r));
+                tmem_wait_ld();
+            }
+            if constexpr (D == 64) {
+                // the upper lanes hold the second half of the tokens
+                if (quarter >= 2)
+#pragma unroll
+                    for (int q = 0; q < NH; ++q) xch[(half * NH + q) * 64 + tok - 64] = r[q];
+                csync();
+                if (quarter >= 2) continue;
+#pragma unroll
+                for (int q = 0; q < NH; ++q) r[q] += xch[(half * NH + q) * 64 + tok];
+            }
+            const int d = m * 128 + tok;
+#pragma unroll
+            for (int q = 0; q < NH; ++q) {
+                const int col = half * NH + q;
+                if (col >= w.ncols) continue;
+                if (split) {
+                    part_all[(slot * NT + col) * D + d] = r[q];
+                } else {
+                    const float ls = cs.sum[col];
+                    static_cast<T *>(p.out)[out_row(col) * D + d] = from_f32<T>(ls > 0.f ? r[q] * (gv / ls) : 0.f);
+                }
             }
         }
-        pending = true;
-    }
-    if (pending) finish_values();
-    if (csync_count(fail)) {
-        // a wait gave up: let the copies in flight land (bounded), then leave
+        if (tid < w.ncols) {
+            const float m = kHeadroom - cs.ref[tid], ls = cs.sum[tid];
+            if (split) ml_all[slot * NT + tid] = make_float2(m, ls);
+            else if (p.lse) p.lse[out_row(tid)] = ls > 0.f ? (m - kHeadroom + log2f(ls)) * kLn2 : -INFINITY;
+        }
+        if (split) {
+            // the CTA that arrives last joins the parts, in the line's order
+            const int64_t begin = t0_s - cur_s.unit, end = begin + cur_s.units();
+            const int c0 = range_of(total_s, grid_s, begin), c1 = range_of(total_s, grid_s, end - 1);
+            uint32_t *ticket = static_cast<uint32_t *>(p.ws) + (static_cast<int64_t>(w.b) * c.H + w.h) * lay.qtiles + w.col0 / NT;
+            csync();
+            if (tid == 0) {
+                fence_acq_rel_gpu();
+                arrived = atomicAdd(ticket, 1u);
+                fence_acq_rel_gpu();
+            }
+            csync();
+            if (arrived == static_cast<uint32_t>(c1 - c0)) {
+                if (tid == 0) *ticket = 0u;
+                const int parts_n = c1 - c0 + 1;
+                const auto slot_of = [&](int s) { return 2 * static_cast<int64_t>(c0 + s) + (s == 0 ? 1 : 0); };
+                for (int col = warp; col < w.ncols; col += 8) {
+                    float M = kUnset;
+                    for (int s = lane; s < parts_n; s += 32) {
+                        const float2 x = __ldcg(ml_all + slot_of(s) * NT + col);
+                        if (x.y > 0.f) M = fmaxf(M, x.x);
+                    }
+                    M = warp_max_f32(M);
+                    float L = 0.f;
+                    float o[D / 32] = {};
+                    for (int s0 = 0; s0 < parts_n; s0 += 32) {
+                        float2 x = make_float2(0.f, 0.f);
+                        if (s0 + lane < parts_n) x = __ldcg(ml_all + slot_of(s0 + lane) * NT + col);
+                        const float f = x.y > 0.f ? ex2(x.x - M) : 0.f;
+                        const float lf = f * x.y;
+                        const int m = min(32, parts_n - s0);
+#pragma unroll 4
+                        for (int s = 0; s < m; ++s) {
+                            const float fs = __shfl_sync(0xFFFFFFFFu, f, s);
+                            L += __shfl_sync(0xFFFFFFFFu, lf, s);
+                            const float *src = part_all + (slot_of(s0 + s) * NT + col) * D;
+#pragma unroll
+                            for (int q = 0; q < D / 32; ++q) o[q] += fs * __ldcg(src + q * 32 + lane);
+                        }
+                    }
+                    const int64_t at = out_row(col);
+#pragma unroll
+                    for (int q = 0; q < D / 32; ++q)
+                        static_cast<T *>(p.out)[at * D + q * 32 + lane] = from_f32<T>(L > 0.f ? o[q] * (gv / L) : 0.f);
+                    if (p.lse && lane == 0) p.lse[at] = L > 0.f ? (M - kHeadroom + log2f(L)) * kLn2 : -INFINITY;
+                }
+            }
+        }
+        tmem_fence_before();
+        csync();                                      // the column constants, P and the place are free
         if (tid == 0) {
-            for (int s = 0; s < A::STAGES; ++s)
-                for (int ph = 0; ph < 2; ++ph) mbar_wait(&full[s], ph);
-            set_status(p.status, SPEC_STATUS_TIMEOUT);
+            t0_s += seg;
+            cur_s.next(c, p, group, seg);
+            if (cur_s.left > 0) cur_s.segment(group);
         }
         csync();
-        if (warp == 0) tmem_free(a_t, A::COLS);
-        return;
     }
-    const bool seen = n > 0;
-
-    // sums over the tile's tokens (= lanes and quarters)
-    {
-        const float s = lane_sums<NH>(l);
-        if (lane % (32 / NH) == 0) cs.red[quarter][half * NH + lane / (32 / NH)] = s;
+    // tell the ninth warp, and leave
+    if (tid == 0) keys_are = kEnd;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&k_bar);
+    if (csync_count(fail) && tid == 0) {
+        // a wait gave up: let the copies in flight land (bounded), then leave
+        for (int s = 0; s < A::STAGES; ++s)
+            for (int ph = 0; ph < 2; ++ph) mbar_wait(&full[s], ph);
+        set_status(p.status, SPEC_STATUS_TIMEOUT);
     }
-    csync();
-    if (tid < NT) cs.sum[tid] = (cs.red[0][tid] + cs.red[1][tid]) + (cs.red[2][tid] + cs.red[3][tid]);
-    csync();
-
-    const int64_t task = (static_cast<int64_t>(w.b) * c.H + w.h) * sp.qtiles + blockIdx.x % sp.qtiles;
-    // partials of a task: [split][NT][D] fp32, then [split][NT] (reference, sum)
-    float *part = reinterpret_cast<float *>(static_cast<uint8_t *>(p.ws) +
-                                            (static_cast<int64_t>(c.B) * c.H * sp.qtiles * 4 + 255) / 256 * 256) +
-                  task * sp.most * NT * (D + 2);
-    float2 *ml = reinterpret_cast<float2 *>(part + static_cast<int64_t>(sp.most) * NT * D);
-    const auto out_row = [&](int q) {
-        const int col = w.col0 + q;
-        return static_cast<int64_t>(w.lo + col / group) * p.Hq + w.h * group + col % group;
-    };
-    float *xch = reinterpret_cast<float *>(stages);
-#pragma unroll
-    for (int m = 0; m < A::VM; ++m) {
-        float r[NH] = {};
-        if constexpr (kPromote) {
-#pragma unroll
-            for (int q = 0; q < NH; ++q) r[q] = acc[m * NH + q];
-        } else if (seen) {
-            tmem_ld<NH>(o_mine + m * NT, reinterpret_cast<uint32_t *>(r));
-            tmem_wait_ld();
-        }
-        if constexpr (D == 64) {
-            // the upper lanes hold the second half of the tokens
-            if (quarter >= 2)
-#pragma unroll
-                for (int q = 0; q < NH; ++q) xch[(half * NH + q) * 64 + tok - 64] = r[q];
-            csync();
-            if (quarter >= 2) continue;
-#pragma unroll
-            for (int q = 0; q < NH; ++q) r[q] += xch[(half * NH + q) * 64 + tok];
-        }
-        const int d = m * 128 + tok;
-#pragma unroll
-        for (int q = 0; q < NH; ++q) {
-            const int col = half * NH + q;
-            if (col >= w.ncols) continue;
-            if (nsplit > 1) {
-                part[(static_cast<int64_t>(split) * NT + col) * D + d] = r[q];
-            } else {
-                const float ls = cs.sum[col];
-                static_cast<T *>(p.out)[out_row(col) * D + d] = from_f32<T>(ls > 0.f ? r[q] * (gv / ls) : 0.f);
-            }
-        }
-    }
-    if (tid < w.ncols) {
-        const float m = kHeadroom - cs.ref[tid], ls = cs.sum[tid];
-        if (nsplit > 1) ml[split * NT + tid] = make_float2(m, ls);
-        else if (p.lse) p.lse[out_row(tid)] = ls > 0.f ? (m - kHeadroom + log2f(ls)) * kLn2 : -INFINITY;
-    }
-    tmem_fence_before();
     csync();
     if (warp == 0) tmem_free(a_t, A::COLS);
-    if (nsplit == 1) return;
-
-    // the split that arrives last joins them, in split order
-    uint32_t *ticket = static_cast<uint32_t *>(p.ws) + task;
-    if (tid == 0) {
-        fence_acq_rel_gpu();
-        arrived = atomicAdd(ticket, 1u);
-        fence_acq_rel_gpu();
-    }
-    csync();
-    if (arrived != static_cast<uint32_t>(nsplit - 1)) return;
-    if (tid == 0) *ticket = 0u;
-    for (int col = warp; col < w.ncols; col += kAttnThreads / 32) {
-        float M = kUnset;
-        for (int s = lane; s < nsplit; s += 32) {
-            const float2 x = __ldcg(ml + s * NT + col);
-            if (x.y > 0.f) M = fmaxf(M, x.x);
-        }
-        M = warp_max_f32(M);
-        float L = 0.f;
-        float o[D / 32] = {};
-        for (int s0 = 0; s0 < nsplit; s0 += 32) {
-            float2 x = make_float2(0.f, 0.f);
-            if (s0 + lane < nsplit) x = __ldcg(ml + (s0 + lane) * NT + col);
-            const float f = x.y > 0.f ? ex2(x.x - M) : 0.f;
-            const float lf = f * x.y;
-            const int n = min(32, nsplit - s0);
-#pragma unroll 4
-            for (int s = 0; s < n; ++s) {
-                const float fs = __shfl_sync(0xFFFFFFFFu, f, s);
-                L += __shfl_sync(0xFFFFFFFFu, lf, s);
-                const float *src = part + (static_cast<int64_t>(s0 + s) * NT + col) * D;
-#pragma unroll
-                for (int q = 0; q < D / 32; ++q) o[q] += fs * __ldcg(src + q * 32 + lane);
-            }
-        }
-        const int64_t at = out_row(col);
-#pragma unroll
-        for (int q = 0; q < D / 32; ++q)
-            static_cast<T *>(p.out)[at * D + q * 32 + lane] = from_f32<T>(L > 0.f ? o[q] * (gv / L) : 0.f);
-        if (p.lse && lane == 0) p.lse[at] = L > 0.f ? (M - kHeadroom + log2f(L)) * kLn2 : -INFINITY;
-    }
 }
 
-// Steps of a split: as many splits as a few rounds of resident CTAs need, so
-// that ragged requests even out.
-Split split_of(int B, int k_max, int Hq, int H, int D, int max_len, int dtype)
+// CTAs for a call: as many as are resident, no more than there can be units.
+template <typename A> Layout layout_of(int B, int k_max, int Hq, int H, int max_len)
 {
-    Split s;
-    s.cols = (k_max + 1) * (Hq / H);
-    const int nt = column_tile(s.cols, D, dtype);
-    s.qtiles = (s.cols + nt - 1) / nt;
-    const int steps = (max_len + kTile - 1) / kTile;
-    const int64_t all = static_cast<int64_t>(B) * H * s.qtiles * steps;
-    const int64_t slots = 152 * 2 * 4;
-    const int64_t t = (all + slots - 1) / slots;
-    s.steps = static_cast<int>(t < 1 ? 1 : (t > steps ? steps : t));
-    s.most = (steps + s.steps - 1) / s.steps;
-    return s;
+    Layout l;
+    l.qtiles = ((k_max + 1) * (Hq / H) + A::NT - 1) / A::NT;
+    const int64_t units = static_cast<int64_t>(B) * H * l.qtiles * ((max_len + kTile - 1) / kTile);
+    l.grid = static_cast<int>(units < 152 * A::CTAS ? units : 152 * A::CTAS);
+    return l;
+}
+
+template <typename A> size_t workspace_of(int B, int k_max, int Hq, int H, int max_len)
+{
+    const Layout l = layout_of<A>(B, k_max, Hq, H, max_len);
+    const size_t tickets = static_cast<size_t>(B) * H * l.qtiles * 4;
+    return (tickets + 255) / 256 * 256 + static_cast<size_t>(l.grid) * 2 * A::NT * (A::D + 2) * 4;
 }
 
 template <typename T, int D, int NT>
-cudaError_t launch_one(const CacheView &c, const AttnParams &p, const Split &sp, cudaStream_t s)
+cudaError_t launch_one(const CacheView &c, const AttnParams &p, cudaStream_t s)
 {
     using A = Attn<T, D, NT>;
     static bool done[64] = {false};
@@ -701,28 +864,24 @@ cudaError_t launch_one(const CacheView &c, const AttnParams &p, const Split &sp,
         if (e != cudaSuccess) return e;
         done[dev] = true;
     }
-    const dim3 grid(c.H * sp.qtiles, sp.most, c.B);
-    attend_kernel<T, D, NT><<<grid, kAttnThreads + 32, A::SMEM, s>>>(c, p, sp);
+    const Layout l = layout_of<A>(c.B, p.k_max, p.Hq, c.H, p.max_len);
+    attend_kernel<T, D, NT><<<l.grid, kAttnThreads + 32, A::SMEM, s>>>(c, p, l);
     return cudaGetLastError();
 }
 
-template <typename T, int D>
-cudaError_t launch_width(const CacheView &c, const AttnParams &p, const Split &sp, int nt, cudaStream_t s)
+// What to do with the kernel for a call's type, channels and columns
+template <typename F> auto with_kernel(int dtype, int D, int cols, F f)
 {
-    if (nt == 16) return launch_one<T, D, 16>(c, p, sp, s);
-    if constexpr (sizeof(T) == 2 && D != 256)
-        if (nt == 64) return launch_one<T, D, 64>(c, p, sp, s);
-    return launch_one<T, D, 32>(c, p, sp, s);
-}
-
-template <typename T>
-cudaError_t launch_attend(const CacheView &c, const AttnParams &p, int dtype, cudaStream_t s)
-{
-    const Split sp = split_of(c.B, p.k_max, p.Hq, c.H, c.D, p.max_len, dtype);
-    const int nt = column_tile(sp.cols, c.D, dtype);
-    if (c.D == 64) return launch_width<T, 64>(c, p, sp, nt, s);
-    if (c.D == 128) return launch_width<T, 128>(c, p, sp, nt, s);
-    return launch_width<T, 256>(c, p, sp, nt, s);
+    const int nt = column_tile(cols, D, dtype);
+    if (dtype == SPEC_F32) {
+        if (D == 64) return nt == 16 ? f(Attn<float, 64, 16>()) : f(Attn<float, 64, 32>());
+        if (D == 128) return nt == 16 ? f(Attn<float, 128, 16>()) : f(Attn<float, 128, 32>());
+        return nt == 16 ? f(Attn<float, 256, 16>()) : f(Attn<float, 256, 32>());
+    }
+    using B = __nv_bfloat16;
+    if (D == 64) return nt == 16 ? f(Attn<B, 64, 16>()) : (nt == 32 ? f(Attn<B, 64, 32>()) : f(Attn<B, 64, 64>()));
+    if (D == 128) return nt == 16 ? f(Attn<B, 128, 16>()) : (nt == 32 ? f(Attn<B, 128, 32>()) : f(Attn<B, 128, 64>()));
+    return nt == 16 ? f(Attn<B, 256, 16>()) : f(Attn<B, 256, 32>());
 }
 
 }  // namespace
@@ -732,10 +891,9 @@ size_t cache_attend_workspace(int B, int k_max, int Hq, int H, int D, int max_le
 {
     size_t most = 0;
     for (int dtype : {SPEC_F32, SPEC_BF16}) {
-        const Split s = split_of(B, k_max, Hq, H, D, max_len, dtype);
-        const size_t tasks = static_cast<size_t>(B) * H * s.qtiles;
-        size_t n = (tasks * 4 + 255) / 256 * 256;
-        n += tasks * s.most * column_tile(s.cols, D, dtype) * (D + 2) * 4;
+        const size_t n = with_kernel(dtype, D, (k_max + 1) * (Hq / H), [&](auto a) {
+            return workspace_of<decltype(a)>(B, k_max, Hq, H, max_len);
+        });
         most = n > most ? n : most;
     }
     return most;
@@ -743,7 +901,10 @@ size_t cache_attend_workspace(int B, int k_max, int Hq, int H, int D, int max_le
 
 cudaError_t launch_cache_attend(const CacheView &c, const AttnParams &p, int dtype, cudaStream_t s)
 {
-    return dtype == SPEC_BF16 ? launch_attend<__nv_bfloat16>(c, p, dtype, s) : launch_attend<float>(c, p, dtype, s);
+    return with_kernel(dtype, c.D, (p.k_max + 1) * (p.Hq / c.H), [&](auto a) {
+        using A = decltype(a);
+        return launch_one<typename A::Type, A::D, A::NT>(c, p, s);
+    });
 }
 
 }  // namespace specv

@@ -61,15 +61,8 @@ weights_kernel(const CacheView c, const AttnParams p, const int tiles)
     const int group = p.Hq / c.H;
     Job w;
     w.b = blockIdx.y;
-    if (!request_rows(p.cu_rows, w.b, p.R_cap, p.k_max + 1, p.status, w.lo, w.n) || w.n == 0) return;
-    w.len = p.len[w.b];
-    if (w.len < 0 || w.len > p.max_len) {
-        if (tid == 0) set_status(p.status, SPEC_STATUS_BAD_LENGTH);
-        return;
-    }
+    if (!load_job<kTile>(c, p, w, tid == 0 ? p.status : nullptr)) return;
     const int i0 = blockIdx.x * tiles;
-    if (i0 * kTile >= w.len) return;
-    visible_steps<kTile>(c, p, w);
     const int nt = min(tiles, w.nsteps - i0);
     if (nt <= 0) return;
 
