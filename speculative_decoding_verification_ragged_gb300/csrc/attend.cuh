@@ -122,10 +122,11 @@ __device__ __forceinline__ int step_page(const CacheView &c, const Job &w, int s
 }
 
 // A wait that has given up once does not wait again: the CTA runs to its end,
-// stores nothing and reports the timeout.
+// stores nothing and reports the timeout.  (Most waits find their phase complete:
+// one try, one branch.)
 __device__ __forceinline__ void wait_or_fail(uint64_t *bar, uint32_t parity, bool &fail)
 {
-    if (!fail) fail = !mbar_wait(bar, parity);
+    if (!mbar_try(bar, parity) && !fail) fail = !mbar_wait(bar, parity);
 }
 
 __device__ __forceinline__ uint32_t h2_mul(uint32_t a, uint32_t b)

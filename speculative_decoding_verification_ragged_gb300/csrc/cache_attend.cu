@@ -34,7 +34,7 @@ namespace {
 
 constexpr float kUnset = -1e30f;           // reference of a column that has seen nothing yet
 constexpr float kHeadroom = 11.f;          // P = 2^(x + 11) ...
-constexpr float kExceed = 15.f;            // ... stays below 2^15
+constexpr uint32_t kMostBits = 0x7800u;    // ... stays below 2^15 (f16 bits)
 // V decoded to bf16 keeps f16's exponent bits, which stand for 2^-112 of the
 // value there; the weights carry the 2^112
 constexpr float kWideScale = 5.192296858534828e33f;
@@ -48,6 +48,7 @@ template <typename T, int D_, int NT_> struct Attn {
     // exponent of the smallest weight with its bits in f16: a normal number; for
     // two terms 15 bits above the last place, 2^-25
     static constexpr float LEAST_EXP = sizeof(T) == 4 ? -10.f : -14.f;
+    static constexpr uint32_t LEAST_BITS = sizeof(T) == 4 ? 0x1400u : 0x0400u;     // as f16 bits
     // D = 64 fills the 128 lanes of V^T with two halves of the tile's tokens,
     // each with its own columns of P^T; D = 256 takes two products of 128 channels
     static constexpr int HALVES = D == 64 ? 2 : 1;
@@ -63,11 +64,11 @@ template <typename T, int D_, int NT_> struct Attn {
     static constexpr int P_BYTES = kTile * NT * 2;             // a term of a tile's weights
     static constexpr int VS_BYTES = D / 16 * kTile * 2;        // a tile's scales of V as f16
     static constexpr int STAGE = 4 * block_bytes(D);
-    static constexpr int OPERANDS = PIECES * (Q_BYTES + P_BYTES) + 2 * VS_BYTES;
+    static constexpr int OPERANDS = PIECES * Q_BYTES + WIDE * P_BYTES + 2 * VS_BYTES;
     static constexpr int STAGES = clamp_stages((smem_share(CTAS, 512 + 60 * NT) - OPERANDS) / STAGE);
     static constexpr int NEED = OPERANDS + STAGES * STAGE;
     static constexpr int SMEM = NEED > smem_least(CTAS) ? NEED : smem_least(CTAS);
-    static_assert(D != 64 || NT * D * 4 <= PIECES * P_BYTES, "the epilogue's exchange fits the weights' place");
+    static_assert(D != 64 || NT * D * 4 <= WIDE * P_BYTES, "the epilogue's exchange fits the weights' place");
 };
 
 // Scales of a tile's values as f16, tokens in pairs, [D/16][64]; the scale of a
@@ -75,13 +76,17 @@ template <typename T, int D_, int NT_> struct Attn {
 template <int D>
 __device__ __forceinline__ void value_scales(const uint8_t *tile, const int *nv, bool whole, uint32_t *vs)
 {
-    const int pair = threadIdx.x & 15, blk = threadIdx.x >> 4 & 3, g0 = threadIdx.x >> 6;
-    const int n = whole ? kTok : nv[blk] - 2 * pair;
+    // 4 tokens a thread and group: 32 threads to a group
+    const int word = threadIdx.x & 7, blk = threadIdx.x >> 3 & 3, g0 = threadIdx.x >> 5;
+    if (D == 64 && g0 >= 4) return;
 #pragma unroll
-    for (int g = 0; g < D / 16; g += 4) {
-        uint32_t s = *reinterpret_cast<const uint16_t *>(tile + blk * block_bytes(D) + v_scale_at(D) + (g0 + g) * kTok + 2 * pair);
-        if (n < 2) s = n == 1 ? s & 255u : 0u;
-        vs[(g0 + g) * 64 + blk * 16 + pair] = e4m3x2(s);
+    for (int g = 0; g < D / 16; g += 8) {
+        uint32_t s = *reinterpret_cast<const uint32_t *>(tile + blk * block_bytes(D) + v_scale_at(D) + (g0 + g) * kTok + 4 * word);
+        if (!whole) {
+            const int n = nv[blk] - 4 * word;
+            s = n >= 4 ? s : (n <= 0 ? 0u : s & ((1u << 8 * n) - 1u));
+        }
+        *reinterpret_cast<uint2 *>(vs + (g0 + g) * 64 + blk * 16 + 2 * word) = make_uint2(e4m3x2(s), e4m3x2(s >> 16));
     }
 }
 
@@ -127,12 +132,12 @@ __device__ __forceinline__ void decode_tile_values(const uint8_t *stage, const u
     }
 }
 
-// O^T += V^T P^T over the tile's tokens (one thread issues); the smaller term of
+// O^T += V^T P^T over the tile's tokens (one thread issues); the smaller terms of
 // P first, as in issue_scores
 template <typename A, bool WIDE>
 __device__ __forceinline__ void issue_values(uint32_t o_addr, uint32_t v_addr, uint32_t ps, bool accumulate)
 {
-    constexpr int PC = WIDE ? 1 : A::PIECES;
+    constexpr int PC = WIDE ? A::WIDE : A::PIECES;
 #pragma unroll
     for (int m = 0; m < A::VM; ++m)
 #pragma unroll
@@ -142,6 +147,20 @@ __device__ __forceinline__ void issue_values(uint32_t o_addr, uint32_t v_addr, u
                 mma_f16(o_addr + m * A::NT, v_addr + m * 64 + q * 8,
                         smem_desc(ps + pc * A::P_BYTES + q * 256, 128, A::VT * 16),
                         mma_f16_desc(A::NT * A::HALVES, true, WIDE), accumulate || pc < PC - 1 || q > 0);
+}
+
+__device__ __forceinline__ uint32_t h2_max(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t h2_min(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    asm("min.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
 }
 
 __device__ __forceinline__ uint32_t pack_bf2(float lo, float hi)
@@ -198,12 +217,14 @@ __device__ __forceinline__ void token_scores(const AttnParams &p, const Job &w, 
 {
     load_products<N, A::NT, A::PIECES>(s_addr + q0, v);
     if (!t.edge && !options) {
-        // two columns an instruction
 #pragma unroll
-        for (int q = 0; q < N; q += 2) {
-            const uint64_t m = *reinterpret_cast<const uint64_t *>(&cs.mult[q0 + q]);
-            const uint64_t r = REF ? *reinterpret_cast<const uint64_t *>(&cs.ref[q0 + q]) : 0ull;
-            f2_unpack(f2_fma(f2_pack(v[q], v[q + 1]), m, r), v[q], v[q + 1]);
+        for (int q = 0; q < N; q += 4) {
+            const float4 m = *reinterpret_cast<const float4 *>(&cs.mult[q0 + q]);
+            const float4 r = REF ? *reinterpret_cast<const float4 *>(&cs.ref[q0 + q]) : make_float4(0.f, 0.f, 0.f, 0.f);
+            v[q] = fmaf(v[q], m.x, r.x);
+            v[q + 1] = fmaf(v[q + 1], m.y, r.y);
+            v[q + 2] = fmaf(v[q + 2], m.z, r.z);
+            v[q + 3] = fmaf(v[q + 3], m.w, r.w);
         }
         return;
     }
@@ -414,15 +435,15 @@ attend_kernel(const CacheView c, const AttnParams p, const Layout lay)
     constexpr int OR = kPromote ? NH * A::VM : 1;     // fp32: results kept in registers
     extern __shared__ __align__(128) uint8_t smem[];
     uint8_t *qs = smem, *ps = qs + A::PIECES * A::Q_BYTES;
-    uint32_t *vs = reinterpret_cast<uint32_t *>(ps + A::PIECES * A::P_BYTES);
-    uint8_t *stages = ps + A::PIECES * A::P_BYTES + 2 * A::VS_BYTES;
+    uint32_t *vs = reinterpret_cast<uint32_t *>(ps + A::WIDE * A::P_BYTES);
+    uint8_t *stages = ps + A::WIDE * A::P_BYTES + 2 * A::VS_BYTES;
     __shared__ __align__(16) Columns<NT> cs;
     __shared__ __align__(8) uint64_t full[A::STAGES], k_bar, p_bar, s_bar, o_bar;
     __shared__ uint32_t tmem_base, arrived;
     // what the eight warps tell the ninth: with keys, kFirst / kLast of a segment
-    // or kEnd; with weights, 0 or the bf16 terms to come, this one included
+    // or kEnd; with weights, whether they are those of a wide tile
     constexpr int kFirst = 1, kLast = 2, kEnd = 4;
-    __shared__ int keys_are, terms;
+    __shared__ int keys_are, weights_wide;
     __shared__ __align__(16) int nv[A::STAGES][4];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int group = p.Hq / c.H;
@@ -499,20 +520,16 @@ attend_kernel(const CacheView c, const AttnParams p, const Layout lay)
         while (now != kEnd) {
             const int here = now;
             if (!(here & kLast)) scores();
-            bool again = false;
-            do {
-                wait_or_fail(&p_bar, p_count++ & 1, fail);
-                tmem_fence_after();
-                const int left = *reinterpret_cast<volatile int *>(&terms);
-                if (leader) {
-                    const bool accumulate = again || !(kPromote || (here & kFirst));
-                    if (left == 0) issue_values<A, false>(o_t, v_t, p_addr, accumulate);
-                    else issue_values<A, true>(o_t, v_t, p_addr, accumulate);
-                    mma_commit(&o_bar);
-                }
-                __syncwarp();
-                again = left > 1;
-            } while (again && !fail);
+            wait_or_fail(&p_bar, p_count++ & 1, fail);
+            tmem_fence_after();
+            const bool wide = *reinterpret_cast<volatile int *>(&weights_wide);
+            if (leader) {
+                const bool accumulate = !(kPromote || (here & kFirst));
+                if (wide) issue_values<A, true>(o_t, v_t, p_addr, accumulate);
+                else issue_values<A, false>(o_t, v_t, p_addr, accumulate);
+                mma_commit(&o_bar);
+            }
+            __syncwarp();
             load_next();
             if (here & kLast) scores();
         }
@@ -530,7 +547,7 @@ attend_kernel(const CacheView c, const AttnParams p, const Layout lay)
     float l[NH], acc[OR];
     bool pending = false;                             // a product with V^T is under way
     uint32_t s_phase = 0, o_phase = 0, ring_phase = 0;
-    int ring = 0, vbuf = 0;                           // stage of the tile whose values come next
+    int ring = 0, buf = 0;                            // stage, and scales' place, of the tile whose values come next
     // wait for the product with V^T under way; fp32: add its result up
     const auto finish_values = [&] {
         pending = false;
@@ -583,7 +600,7 @@ attend_kernel(const CacheView c, const AttnParams p, const Layout lay)
         if (n > 0) keys(ring, ring_phase, kFirst | (n == 1 ? kLast : 0));
         for (int k = 0; k < n; ++k) {
             const uint8_t *stage = stages + ring * A::STAGE;
-            uint32_t *vsk = vs + vbuf * (A::VS_BYTES / 4);
+            uint32_t *vsk = vs + buf * (A::VS_BYTES / 4);
             const int slot0 = step_slot<kTile>(w, cur_s.unit + k);
             Token t;
             const int4 n4 = *reinterpret_cast<const int4 *>(nv[ring]);
@@ -593,7 +610,6 @@ attend_kernel(const CacheView c, const AttnParams p, const Layout lay)
             t.edge = !whole || slot0 + kTile - 1 > own_first;
             if (options && p.slot_pos && t.live) t.pos = slot_position(c, p, w.b, t.slot);
             value_scales<D>(stage, nv[ring], whole, vsk);
-            vbuf ^= 1;
             if (++ring == A::STAGES) {
                 ring = 0;
                 ring_phase ^= 1;
@@ -601,102 +617,102 @@ attend_kernel(const CacheView c, const AttnParams p, const Layout lay)
             wait_or_fail(&s_bar, s_phase, fail);
             s_phase ^= 1;
             tmem_fence_after();
-            float v[NH];
-            bool wide = false;
-            for (;;) {
-                token_scores<A, NH, true>(p, w, cs, s_t + lane_off, half * NH, t, options, v);
-                float most = -INFINITY, least = INFINITY;
+            float v[NH], x[NH];
+            uint32_t hi[NH / 2];
+            // weights, and whether they are fit for f16: none beyond 2^15 (the reference
+            // has to move) and no visible one without its bits (1: too large, 2: too small)
+            const auto weigh = [&] {
+                token_scores<A, NH, true>(p, w, cs, s_t + lane_off, half * NH, t, options, x);
 #pragma unroll
-                for (int q = 0; q < NH; ++q) most = fmaxf(most, v[q]);
+                for (int q = 0; q < NH; ++q) v[q] = ex2(x[q]);
+#pragma unroll
+                for (int q = 0; q < NH / 2; ++q) hi[q] = pack_h2(v[2 * q], v[2 * q + 1]);
+                uint32_t most = hi[0], least = hi[0];
+#pragma unroll
+                for (int q = 1; q < NH / 2; ++q) {
+                    most = h2_max(most, hi[q]);
+                    least = h2_min(least, hi[q]);
+                }
+                // (weights are positive: their bits compare as they do)
+                int unfit = max(most >> 16, most & 0xFFFFu) > kMostBits ? 1 : 0;
                 if (t.edge || options) {
+                    float low = INFINITY;
 #pragma unroll
-                    for (int q = 0; q < NH; ++q) least = fminf(least, v[q] == -INFINITY ? INFINITY : v[q]);
+                    for (int q = 0; q < NH; ++q) low = fminf(low, x[q] == -INFINITY ? INFINITY : x[q]);
+                    unfit |= low < A::LEAST_EXP ? 2 : 0;
                 } else {
-#pragma unroll
-                    for (int q = 0; q < NH; ++q) least = fminf(least, v[q]);
+                    unfit |= min(least >> 16, least & 0xFFFFu) < A::LEAST_BITS ? 2 : 0;
                 }
-                if (!csync_count(most > kExceed || least < A::LEAST_EXP)) break;
-                if (!csync_count(most > kExceed)) {
-                    wide = true;
-                    break;
-                }
-                move_references<A>(p, w, cs, s_t + lane_off, t, options);
-                if (pending) finish_values();
+                return unfit;
+            };
+            bool wide = false;
+            int unfit = weigh();
+            if (csync_count(unfit)) {
+                while (csync_count(unfit & 1)) {
+                    move_references<A>(p, w, cs, s_t + lane_off, t, options);
+                    if (pending) finish_values();
 #pragma unroll
-                for (int q = 0; q < NH; ++q) l[q] *= cs.factor[half * NH + q];
-                if (kPromote) {
+                    for (int q = 0; q < NH; ++q) l[q] *= cs.factor[half * NH + q];
+                    if (kPromote) {
 #pragma unroll
-                    for (int q = 0; q < OR; ++q) acc[q] *= cs.factor[half * NH + q % NH];
-                } else if (k > 0) {
-                    rescale_results<A>(cs, o_t + lane_off);
+                        for (int q = 0; q < OR; ++q) acc[q] *= cs.factor[half * NH + q % NH];
+                    } else if (k > 0) {
+                        rescale_results<A>(cs, o_t + lane_off);
+                    }
+                    unfit = weigh();
                 }
+                wide = csync_count(unfit);
             }
             // S^T is read, the keys' columns are free: on to the next tile's keys
             if (k + 1 < n) keys(ring, ring_phase, k + 2 == n ? kLast : 0);
             if (pending) finish_values();             // V^T's columns and P are free
             // weights: sums in fp32, the operand 8 columns of this token per store
 #pragma unroll
-            for (int q = 0; q < NH; q += 2) {
-                v[q] = ex2(v[q]);
-                v[q + 1] = ex2(v[q + 1]);
-                f2_unpack(f2_add(f2_pack(l[q], l[q + 1]), f2_pack(v[q], v[q + 1])), l[q], l[q + 1]);
-            }
+            for (int q = 0; q < NH; ++q) l[q] += v[q];
             if (!wide) {
 #pragma unroll
                 for (int q0 = 0; q0 < NH; q0 += 8) {
-                    uint32_t hi[4];
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) hi[q] = pack_h2(v[q0 + 2 * q], v[q0 + 2 * q + 1]);
-                    *reinterpret_cast<uint4 *>(p_mine + q0 / 8 * PN8) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    const uint32_t *h = hi + q0 / 2;
+                    *reinterpret_cast<uint4 *>(p_mine + q0 / 8 * PN8) = make_uint4(h[0], h[1], h[2], h[3]);
                     if (A::PIECES == 2) {
                         uint32_t lo[4];
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
-                            const float2 y = h2_float2(hi[q]);
+                            const float2 y = h2_float2(h[q]);
                             lo[q] = pack_h2(v[q0 + 2 * q] - y.x, v[q0 + 2 * q + 1] - y.y);
                         }
                         *reinterpret_cast<uint4 *>(p_mine + A::P_BYTES + q0 / 8 * PN8) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                     }
                 }
-                decode_tile_values<A, false>(stage, vsk, v_t + lane_off);
-                if (tid == 0) terms = 0;
-                tmem_wait_st();
-                tmem_fence_before();
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&p_bar);
             } else {
-                decode_tile_values<A, true>(stage, vsk, v_t + lane_off);
-                tmem_wait_st();
+#pragma unroll
+                for (int q = 0; q < NH; ++q) v[q] *= kWideScale;
 #pragma unroll 1
                 for (int pc = 0; pc < A::WIDE; ++pc) {
-                    if (pc > 0) {
-                        wait_or_fail(&o_bar, o_phase, fail);
-                        o_phase ^= 1;
-                    }
 #pragma unroll
                     for (int q0 = 0; q0 < NH; q0 += 8) {
                         uint32_t term[4];
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
-                            float &x = v[q0 + 2 * q], &y = v[q0 + 2 * q + 1];
-                            if (pc == 0) {
-                                x *= kWideScale;
-                                y *= kWideScale;
-                            }
-                            term[q] = pack_bf2(x, y);
-                            x -= bf_lo(term[q]);
-                            y -= bf_hi(term[q]);
+                            float &a = v[q0 + 2 * q], &b = v[q0 + 2 * q + 1];
+                            term[q] = pack_bf2(a, b);
+                            a -= bf_lo(term[q]);
+                            b -= bf_hi(term[q]);
                         }
-                        *reinterpret_cast<uint4 *>(p_mine + q0 / 8 * PN8) = make_uint4(term[0], term[1], term[2], term[3]);
+                        *reinterpret_cast<uint4 *>(p_mine + pc * A::P_BYTES + q0 / 8 * PN8) =
+                            make_uint4(term[0], term[1], term[2], term[3]);
                     }
-                    if (tid == 0) terms = A::WIDE - pc;
-                    tmem_fence_before();
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&p_bar);
                 }
             }
+            if (!wide) decode_tile_values<A, false>(stage, vsk, v_t + lane_off);
+            else decode_tile_values<A, true>(stage, vsk, v_t + lane_off);
+            if (tid == 0) weights_wide = wide;
+            tmem_wait_st();
+            tmem_fence_before();
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&p_bar);
+            buf ^= 1;
             pending = true;
         }
         if (pending) finish_values();
