@@ -89,36 +89,43 @@ __device__ __forceinline__ bool load_job(const CacheView &c, const AttnParams &p
     return true;
 }
 
-// Copy the first BYTES of the BLOCKS blocks of a step into a stage (all of a
-// block, or its keys); a lane of one warp per block, `page` its page.  nv: the
-// tokens of each block that exist (0 for a bad page: its bytes are not fetched,
-// and what the stage holds there is masked).
-template <int BYTES, int BLOCKS>
-__device__ __forceinline__ void load_step(const CacheView &c, const Job &w, int h, int slot, int page, uint8_t *stage,
-                                          uint64_t *full, int *nv, uint32_t *status)
+// The next tile to fetch, its page ids asked for ahead: a fetch does not wait for
+// the page table (the ids are looked at only when the copies are issued).
+struct Fetch {
+    int h, slot, len, page;     // page: of this lane's block, as the table has it
+};
+
+__device__ __forceinline__ Fetch ask_pages(const CacheView &c, const Job &w, int h, int slot)
+{
+    const int lane = threadIdx.x & 31, slot0 = slot + lane * kTok;
+    Fetch f = {h, slot, w.len, -1};
+    if (lane < 4 && slot0 < w.len)
+        f.page = __ldg(c.page_table + static_cast<int64_t>(w.b) * c.max_pages + slot0 / c.page_tokens);
+    return f;
+}
+
+// Copy the first BYTES of a tile's 4 blocks into a stage (all of a block, or its
+// keys); a lane of one warp per block.  nv: the tokens of each block that exist (0
+// for a bad page: its bytes are not fetched, and what the stage holds there is
+// masked).
+template <int BYTES>
+__device__ __forceinline__ void load_tile(const CacheView &c, const Fetch &f, uint8_t *stage, uint64_t *full, int *nv,
+                                          uint32_t *status)
 {
     const int lane = threadIdx.x & 31;
-    const int slot0 = slot + lane * kTok;
-    int n = lane < BLOCKS ? min(max(w.len - slot0, 0), kTok) : 0;
-    if (n > 0 && page < 0) {
+    const int slot0 = f.slot + lane * kTok;
+    int n = lane < 4 ? min(max(f.len - slot0, 0), kTok) : 0;
+    if (n > 0 && (f.page < 0 || f.page >= c.n_pages)) {
         set_status(status, SPEC_STATUS_BAD_PAGE);
         n = 0;
     }
     const uint32_t have = __ballot_sync(0xFFFFFFFFu, n > 0);
-    if (lane < BLOCKS) nv[lane] = n;
+    if (lane < 4) nv[lane] = n;
     __syncwarp();
     if (lane == 0) mbar_arrive_expect_tx(full, __popc(have) * BYTES);
     __syncwarp();
     if (n > 0)
-        bulk_g2s(stage + lane * BYTES, block_at(c, page, h, slot0 % c.page_tokens / kTok), BYTES, full);
-}
-
-// page of this lane's block of the step at `slot`
-template <int BLOCKS>
-__device__ __forceinline__ int step_page(const CacheView &c, const Job &w, int slot)
-{
-    const int lane = threadIdx.x & 31, slot0 = slot + lane * kTok;
-    return lane < BLOCKS && slot0 < w.len ? page_of(c, w.b, slot0) : -1;
+        bulk_g2s(stage + lane * BYTES, block_at(c, f.page, f.h, slot0 % c.page_tokens / kTok), BYTES, full);
 }
 
 // A wait that has given up once does not wait again: the CTA runs to its end,
@@ -200,56 +207,68 @@ __device__ __forceinline__ void load8(const T *p, bool aligned, float (&x)[8])
     }
 }
 
-// The query columns of kv head w.h as the K-major B operand: each scaled by the
+// The query columns of a kv head as the K-major B operand: each scaled by the
 // power of two that brings its largest channel to 2^13 (and by the sign of the
-// softmax scale), the second f16 term behind the first for fp32.  mult[col]
-// takes a raw product to its score in natural units; `unit` multiplies it (log2
-// e for log2 units).  A column belongs to D/8 lanes of one warp: no barrier.
-template <typename T, int D, int NT, int PIECES>
-__device__ __forceinline__ void stage_queries(const AttnParams &p, const Job &w, int group, float gk, double unit,
-                                              uint8_t *qs, float *mult)
-{
-    constexpr int PER = D / 8;                        // 8-channel groups of a column
-#pragma unroll 1
-    for (int i = threadIdx.x; i < NT * PER; i += kAttnThreads) {
-        const int cl = i / PER, k8 = i % PER, col = w.col0 + cl;
-        float x[8] = {};
-        if (cl < w.ncols)
-            load8<T>(static_cast<const T *>(p.q) + (w.lo + col / group) * p.q_row +
-                         (w.h * group + col % group) * p.q_head + k8 * 8,
-                     p.q_aligned, x);
-        float big = 0.f;
+// softmax scale), the second f16 term behind the first for fp32.  A thread's
+// share, the same for every head, is placed once; a column belongs to D/8 lanes of
+// one warp, so staging has no barrier.
+template <typename T, int D, int NT, int PIECES> struct QueryStage {
+    static constexpr int PER = D / 8;                 // 8-channel groups of a column
+    static constexpr int SHARES = (NT * PER + kAttnThreads - 1) / kAttnThreads;
+    const T *src[SHARES];                             // in kv head 0; null: no such column
+
+    __device__ __forceinline__ void place(const AttnParams &p, const Job &w, int group)
+    {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) big = fmaxf(big, fabsf(x[k]));
-#pragma unroll
-        for (int o = PER / 2; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xFFFFFFFFu, big, o));
-        // exponent arithmetic on the bits; a column of zeros (or subnormals) stays as it is
-        const int ex = static_cast<int>(__float_as_uint(big) >> 23) - 127;
-        const int e = ex > -127 ? min(max(13 - ex, -120), 100) : 0;
-        const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-        const float f = p.scale == 0.f ? 0.f : (p.scale < 0.f ? -up : up);
-        // rounded to fp32 once; never 0, so that a hidden slot's -inf stays -inf
-        if (k8 == 0)
-            mult[cl] = p.scale == 0.f ? 1.f
-                                      : fmaxf(static_cast<float>(fabs(static_cast<double>(p.scale)) * gk * unit) *
-                                                  __uint_as_float(static_cast<uint32_t>(127 - e) << 23),
-                                              1e-37f);
-        uint8_t *dst = qs + k8 * (NT * 16) + cl / 8 * 128 + cl % 8 * 16;
-        uint32_t hi[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) hi[k] = pack_h2(x[2 * k] * f, x[2 * k + 1] * f);
-        *reinterpret_cast<uint4 *>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        if (PIECES == 2) {
-            uint32_t l[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const float2 y = h2_float2(hi[k]);
-                l[k] = pack_h2(x[2 * k] * f - y.x, x[2 * k + 1] * f - y.y);
-            }
-            *reinterpret_cast<uint4 *>(dst + NT * D * 2) = make_uint4(l[0], l[1], l[2], l[3]);
+        for (int s = 0; s < SHARES; ++s) {
+            const int i = s * kAttnThreads + threadIdx.x, col = w.col0 + i / PER;
+            src[s] = i / PER < w.ncols ? static_cast<const T *>(p.q) + (w.lo + col / group) * p.q_row +
+                                             col % group * p.q_head + i % PER * 8
+                                       : nullptr;
         }
     }
-}
+
+    // kv head h; mult[col] takes a raw product to its score: unit * gk, by the
+    // power of two (unit: the softmax scale's magnitude in the units wanted)
+    __device__ __forceinline__ void stage(const AttnParams &p, int64_t head, float unit, uint8_t *qs, float *mult) const
+    {
+#pragma unroll
+        for (int s = 0; s < SHARES; ++s) {
+            const int i = s * kAttnThreads + threadIdx.x, cl = i / PER, k8 = i % PER;
+            if (NT * PER < kAttnThreads && i >= NT * PER) break;         // (whole warps)
+            float x[8] = {};
+            if (src[s]) load8<T>(src[s] + head, p.q_aligned, x);
+            float big = 0.f;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) big = fmaxf(big, fabsf(x[k]));
+#pragma unroll
+            for (int o = PER / 2; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xFFFFFFFFu, big, o));
+            // exponent arithmetic on the bits; a column of zeros (or subnormals) stays as it is
+            const int ex = static_cast<int>(__float_as_uint(big) >> 23) - 127;
+            const int e = ex > -127 ? min(max(13 - ex, -120), 100) : 0;
+            const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+            const float f = p.scale == 0.f ? 0.f : (p.scale < 0.f ? -up : up);
+            // never 0, so that a hidden slot's -inf stays -inf
+            if (k8 == 0)
+                mult[cl] = p.scale == 0.f ? 1.f
+                                          : fmaxf(unit * __uint_as_float(static_cast<uint32_t>(127 - e) << 23), 1e-37f);
+            uint8_t *dst = qs + k8 * (NT * 16) + cl / 8 * 128 + cl % 8 * 16;
+            uint32_t hi[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) hi[k] = pack_h2(x[2 * k] * f, x[2 * k + 1] * f);
+            *reinterpret_cast<uint4 *>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            if (PIECES == 2) {
+                uint32_t l[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float2 y = h2_float2(hi[k]);
+                    l[k] = pack_h2(x[2 * k] * f - y.x, x[2 * k + 1] * f - y.y);
+                }
+                *reinterpret_cast<uint4 *>(dst + NT * D * 2) = make_uint4(l[0], l[1], l[2], l[3]);
+            }
+        }
+    }
+};
 
 // S^T = K Q^T over all channels (one thread issues).  The terms of fp32 queries
 // go to accumulators of their own, NT columns apart: the tensor cores truncate

@@ -324,9 +324,13 @@ template <int NT> struct Cursor {
     __device__ __forceinline__ bool load(const CacheView &c, const AttnParams &p, int group)
     {
         if (!load_job<kTile>(c, p, w, nullptr)) return false;
+        start(c, group);
+        return true;
+    }
+    __device__ __forceinline__ void start(const CacheView &c, int group)
+    {
         qt = (w.n * group + NT - 1) / NT;
         tasks = c.H * qt;
-        return true;
     }
     __device__ __forceinline__ int units() const { return max(w.nsteps, 1); }
     // units of this task in the range, and the job's head and columns
@@ -357,13 +361,14 @@ template <int NT> struct Cursor {
 // of their units places them.
 template <int NT>
 __device__ __forceinline__ int64_t find_range(const CacheView &c, const AttnParams &p, const Layout &lay, int group,
-                                              int &grid, int64_t &t0, int &b0, int64_t &off)
+                                              int &grid, int64_t &t0, Job &job, int64_t &off)
 {
     constexpr int N = kAttnThreads + 32;
-    __shared__ int64_t sums[N / 32 + 1], place[2];
+    __shared__ int64_t sums[N / 32 + 1], offset;
+    __shared__ Job found;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    Job w;
     const auto weight = [&](int b, bool report) {
-        Job w;
         w.b = b;
         if (b >= c.B || !load_job<kTile>(c, p, w, report && blockIdx.x == 0 ? p.status : nullptr)) return static_cast<int64_t>(0);
         return static_cast<int64_t>(c.H) * ((w.n * group + NT - 1) / NT) * max(w.nsteps, 1);
@@ -389,6 +394,7 @@ __device__ __forceinline__ int64_t find_range(const CacheView &c, const AttnPara
     };
     int64_t total, mine = weight(tid, true), at = scan(mine, total);
     int64_t part = total;                         // of the N requests at hand
+    const Job own = w;                            // of the first N requests
     for (int b = N; b < c.B; b += N) {
         int64_t v = weight(b + tid, true);
 #pragma unroll
@@ -403,10 +409,11 @@ __device__ __forceinline__ int64_t find_range(const CacheView &c, const AttnPara
     if (static_cast<int>(blockIdx.x) >= grid) return total;
     t0 = range_start(total, grid, blockIdx.x);
     int64_t base = 0;
+    w = own;
     for (int b = 0;; ) {
         if (at - mine + base <= t0 && t0 < at + base) {
-            place[0] = b + tid;
-            place[1] = t0 - (at - mine + base);
+            found = w;
+            offset = t0 - (at - mine + base);
         }
         base += part;
         b += N;
@@ -415,8 +422,8 @@ __device__ __forceinline__ int64_t find_range(const CacheView &c, const AttnPara
         at = scan(mine, part);
     }
     __syncthreads();
-    b0 = static_cast<int>(place[0]);
-    off = place[1];
+    job = found;
+    off = offset;
     return total;
 }
 
@@ -465,10 +472,10 @@ attend_kernel(const CacheView c, const AttnParams p, const Layout lay)
     {
         int64_t t0, off;
         int grid;
-        const int64_t total = find_range<NT>(c, p, lay, group, grid, t0, cur.w.b, off);
+        const int64_t total = find_range<NT>(c, p, lay, group, grid, t0, cur.w, off);
         if (static_cast<int>(blockIdx.x) >= grid) return;
         cur.left = range_start(total, grid, blockIdx.x + 1) - t0;
-        cur.load(c, p, group);
+        cur.start(c, group);
         cur.task = static_cast<int>(off / cur.units());
         cur.unit = static_cast<int>(off % cur.units());
         if (tid == 0) {
@@ -488,20 +495,26 @@ attend_kernel(const CacheView c, const AttnParams p, const Layout lay)
     if (warp == 8) {
         const bool leader = elect_one();
         const uint32_t q_addr = smem_addr(qs), p_addr = smem_addr(ps);
-        // the next tile of the range into the ring
+        // tiles of the range into the ring, the page ids of the one after asked for
         int ring = 0, seg = cur.segment(group), k_ld = 0;
-        const auto load_next = [&] {
+        bool any = true;
+        Fetch next;
+        const auto ask_next = [&] {
             while (cur.left > 0 && (k_ld == seg || cur.w.nsteps == 0)) {
                 cur.next(c, p, group, seg);
                 if (cur.left > 0) seg = cur.segment(group);
                 k_ld = 0;
             }
-            if (cur.left <= 0) return;
-            const int slot = step_slot<kTile>(cur.w, cur.unit + k_ld++);
-            load_step<block_bytes(D), 4>(c, cur.w, cur.w.h, slot, step_page<4>(c, cur.w, slot), stages + ring * A::STAGE,
-                                         &full[ring], nv[ring], p.status);
-            ring = ring + 1 == A::STAGES ? 0 : ring + 1;
+            any = cur.left > 0;
+            if (any) next = ask_pages(c, cur.w, cur.w.h, step_slot<kTile>(cur.w, cur.unit + k_ld++));
         };
+        const auto load_next = [&] {
+            if (!any) return;
+            load_tile<block_bytes(D)>(c, next, stages + ring * A::STAGE, &full[ring], nv[ring], p.status);
+            ring = ring + 1 == A::STAGES ? 0 : ring + 1;
+            ask_next();
+        };
+        ask_next();
         for (int i = 0; i < A::STAGES; ++i) load_next();
         // products in the order their operands come
         int g = 0, p_count = 0, now = 0;
@@ -589,7 +602,9 @@ attend_kernel(const CacheView c, const AttnParams p, const Layout lay)
             cs.slope[tid] = p.slopes && tid < w.ncols ? p.slopes[w.h * group + col % group] * kLog2e : 0.f;
             cs.ref[tid] = tid < w.ncols ? kHeadroom - kUnset : 0.f;      // (a padded column's results are unused)
         }
-        stage_queries<T, D, NT, A::PIECES>(p, w, group, gk, 1.4426950408889634, qs, cs.mult);
+        QueryStage<T, D, NT, A::PIECES> queries;
+        queries.place(p, w, group);
+        queries.stage(p, static_cast<int64_t>(w.h) * group * p.q_head, p.scale_log2 * gk, qs, cs.mult);
         fence_proxy_async_smem();
         csync();
 #pragma unroll

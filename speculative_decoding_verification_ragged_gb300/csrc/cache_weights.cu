@@ -72,11 +72,15 @@ weights_kernel(const CacheView c, const AttnParams p, const int tiles)
         const int t = i % nt, hq = i / nt;
         return Step{hq / qt_used, hq % qt_used, t};
     };
-    const auto load = [&](int i) {
+    Fetch next;
+    const auto ask = [&](int i) {
         const Step s = step_at(i);
-        const int slot = step_slot<kTile>(w, i0 + s.t);
-        load_step<A::K_BYTES, 4>(c, w, s.h, slot, step_page<4>(c, w, slot), stages + i % A::STAGES * A::STAGE,
-                              &full[i % A::STAGES], nv[i % A::STAGES], p.status);
+        if (i < steps) next = ask_pages(c, w, s.h, step_slot<kTile>(w, i0 + s.t));
+    };
+    const auto load = [&](int i) {
+        const int st = i % A::STAGES;
+        load_tile<A::K_BYTES>(c, next, stages + st * A::STAGE, &full[st], nv[st], p.status);
+        ask(i + 1);
     };
     if (warp == kLoadWarp) {
         if (lane == 0) {
@@ -85,12 +89,14 @@ weights_kernel(const CacheView c, const AttnParams p, const int tiles)
             fence_mbar_init();
         }
         __syncwarp();
+        ask(0);
         for (int i = 0; i < A::STAGES && i < steps; ++i) load(i);
     }
     if (warp == 0) tmem_alloc(&tmem_base, A::COLS);
     for (int t = 0; t < nt; ++t) acc[t][half][tok] = 0.f;
 
     const bool options = p.cap > 0.f || p.slopes || p.window > 0;
+    QueryStage<T, D, NT, A::PIECES> queries;
     // queries and column constants of the head that step i begins
     const auto stage_head = [&](int i, Heads<NT> &set, uint8_t *q) {
         const Step s = step_at(i);
@@ -107,7 +113,8 @@ weights_kernel(const CacheView c, const AttnParams p, const int tiles)
             const float lse = tid < w.ncols ? p.lse[static_cast<int64_t>(w.lo + j) * p.Hq + head] : INFINITY;
             set.lse[tid] = lse == -INFINITY ? INFINITY : lse;
         }
-        stage_queries<T, D, NT, A::PIECES>(p, w, group, c.k_scale ? c.k_scale[s.h] : 1.f, 1.0, q, set.mult);
+        if (i == 0 || qt_used > 1) queries.place(p, w, group);
+        queries.stage(p, static_cast<int64_t>(s.h) * group * p.q_head, fabsf(p.scale) * (c.k_scale ? c.k_scale[s.h] : 1.f), q, set.mult);
         fence_proxy_async_smem();
     };
     int cb = 0, qb = 0;

@@ -1,6 +1,7 @@
 // capi.cu -- the extern "C" entry points of libspecverify: host-side argument
 // checks (nothing is launched when they fail), workspace layout, dispatch.
 #include <climits>
+#include <cmath>
 #include <cstdint>
 #include <cstdio>
 #include <cstring>
@@ -237,6 +238,7 @@ int check_attention(const spec_cache *cache, const spec_attention *a, CacheView 
     p.len = a->len;
     p.max_len = a->max_len ? a->max_len : static_cast<int32_t>(room);
     p.scale = a->scale;
+    p.scale_log2 = static_cast<float>(std::fabs(static_cast<double>(a->scale)) * 1.4426950408889634);
     p.cap = a->cap;
     p.slopes = a->slopes;
     p.window = a->window;

@@ -118,6 +118,7 @@ struct AttnParams {
     const int32_t *cu_rows, *len;
     int32_t max_len;
     float scale, cap;
+    float scale_log2;            // |scale| log2 e, rounded once
     const float *slopes;
     int32_t window, prefix;
     const int32_t *slot_pos;
