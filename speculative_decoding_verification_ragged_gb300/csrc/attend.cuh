@@ -212,6 +212,12 @@ __device__ __forceinline__ void load8(const T *p, bool aligned, float (&x)[8])
 // softmax scale), the second f16 term behind the first for fp32.  A thread's
 // share, the same for every head, is placed once; a column belongs to D/8 lanes of
 // one warp, so staging has no barrier.
+//
+// A core matrix (8 columns x 8 channels) starts kCore bytes after the one of the
+// channels before: the lanes of a column store to different banks.
+constexpr int kCore = 144;
+__host__ __device__ constexpr int query_bytes(int D, int NT) { return NT / 8 * (D / 8) * kCore; }
+
 template <typename T, int D, int NT, int PIECES> struct QueryStage {
     static constexpr int PER = D / 8;                 // 8-channel groups of a column
     static constexpr int SHARES = (NT * PER + kAttnThreads - 1) / kAttnThreads;
@@ -252,7 +258,7 @@ template <typename T, int D, int NT, int PIECES> struct QueryStage {
             if (k8 == 0)
                 mult[cl] = p.scale == 0.f ? 1.f
                                           : fmaxf(unit * __uint_as_float(static_cast<uint32_t>(127 - e) << 23), 1e-37f);
-            uint8_t *dst = qs + k8 * (NT * 16) + cl / 8 * 128 + cl % 8 * 16;
+            uint8_t *dst = qs + (cl / 8 * PER + k8) * kCore + cl % 8 * 16;
             uint32_t hi[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) hi[k] = pack_h2(x[2 * k] * f, x[2 * k + 1] * f);
@@ -264,7 +270,7 @@ template <typename T, int D, int NT, int PIECES> struct QueryStage {
                     const float2 y = h2_float2(hi[k]);
                     l[k] = pack_h2(x[2 * k] * f - y.x, x[2 * k + 1] * f - y.y);
                 }
-                *reinterpret_cast<uint4 *>(dst + NT * D * 2) = make_uint4(l[0], l[1], l[2], l[3]);
+                *reinterpret_cast<uint4 *>(dst + query_bytes(D, NT)) = make_uint4(l[0], l[1], l[2], l[3]);
             }
         }
     }
@@ -281,7 +287,8 @@ __device__ __forceinline__ void issue_scores(uint32_t s_addr, uint32_t a_addr, u
     for (int pc = 0; pc < PIECES; ++pc)
 #pragma unroll
         for (int k = 0; k < D / 16; ++k)
-            mma_f16(s_addr + pc * NT, a_addr + k * 8, smem_desc(q + pc * NT * D * 2 + k * 2 * NT * 16, NT * 16, 128),
+            mma_f16(s_addr + pc * NT, a_addr + k * 8,
+                    smem_desc(q + pc * query_bytes(D, NT) + k * 2 * kCore, kCore, D / 8 * kCore),
                     mma_f16_desc(NT, false), k > 0);
 }
 

@@ -60,7 +60,7 @@ template <typename T, int D_, int NT_> struct Attn {
     static constexpr int V_COLS = D == 64 ? 32 : 64 * VM;      // tensor memory of a tile's V^T
     static constexpr int COLS = tmem_cols(A_COLS + V_COLS + S_COLS + O_COLS);
     static constexpr int CTAS = COLS <= 256 ? 2 : 1;
-    static constexpr int Q_BYTES = NT * D * 2;
+    static constexpr int Q_BYTES = query_bytes(D, NT);
     static constexpr int P_BYTES = kTile * NT * 2;             // a term of a tile's weights
     static constexpr int VS_BYTES = D / 16 * kTile * 2;        // a tile's scales of V as f16
     static constexpr int STAGE = 4 * block_bytes(D);

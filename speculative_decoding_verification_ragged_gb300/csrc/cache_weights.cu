@@ -23,7 +23,7 @@ template <typename T, int D_, int NT_> struct Weights {
     static constexpr int A_COLS = D / 2, S_COLS = PIECES * NT;
     static constexpr int COLS = tmem_cols(A_COLS + 2 * S_COLS);
     static constexpr int CTAS = 512 / COLS;
-    static constexpr int Q_BYTES = PIECES * NT * D * 2;
+    static constexpr int Q_BYTES = PIECES * query_bytes(D, NT);
     static constexpr int STAGE = 4 * K_BYTES;
     static constexpr int FIXED = 128 + 60 * NT + 2 * kMaxTiles * kTile * 4;
     static constexpr int STAGES = clamp_stages((smem_share(CTAS, FIXED) - 2 * Q_BYTES) / STAGE);
@@ -41,6 +41,15 @@ template <int NT> struct Heads {
 // Step of a CTA: tile `t` of its tiles, column tile `qt` of kv head `h`.
 struct Step {
     int h, qt, t;
+
+    __device__ __forceinline__ void next(int tiles, int qtiles)
+    {
+        if (++t < tiles) return;
+        t = 0;
+        if (++qt < qtiles) return;
+        qt = 0;
+        ++h;
+    }
 };
 
 template <typename T, int D, int NT>
@@ -68,19 +77,19 @@ weights_kernel(const CacheView c, const AttnParams p, const int tiles)
 
     const int cols = w.n * group, qt_used = (cols + NT - 1) / NT;
     const int steps = c.H * qt_used * nt;
-    const auto step_at = [&](int i) {
-        const int t = i % nt, hq = i / nt;
-        return Step{hq / qt_used, hq % qt_used, t};
-    };
+    // the loading warp: its next step, the page ids of it asked for ahead
+    Step to_load = {0, 0, 0};
+    int load_ring = 0;
     Fetch next;
-    const auto ask = [&](int i) {
-        const Step s = step_at(i);
-        if (i < steps) next = ask_pages(c, w, s.h, step_slot<kTile>(w, i0 + s.t));
+    const auto ask = [&] {
+        if (to_load.h < c.H) next = ask_pages(c, w, to_load.h, step_slot<kTile>(w, i0 + to_load.t));
     };
-    const auto load = [&](int i) {
-        const int st = i % A::STAGES;
-        load_tile<A::K_BYTES>(c, next, stages + st * A::STAGE, &full[st], nv[st], p.status);
-        ask(i + 1);
+    const auto load = [&] {
+        if (to_load.h >= c.H) return;
+        load_tile<A::K_BYTES>(c, next, stages + load_ring * A::STAGE, &full[load_ring], nv[load_ring], p.status);
+        load_ring = load_ring + 1 == A::STAGES ? 0 : load_ring + 1;
+        to_load.next(nt, qt_used);
+        ask();
     };
     if (warp == kLoadWarp) {
         if (lane == 0) {
@@ -89,17 +98,16 @@ weights_kernel(const CacheView c, const AttnParams p, const int tiles)
             fence_mbar_init();
         }
         __syncwarp();
-        ask(0);
-        for (int i = 0; i < A::STAGES && i < steps; ++i) load(i);
+        ask();
+        for (int i = 0; i < A::STAGES; ++i) load();
     }
     if (warp == 0) tmem_alloc(&tmem_base, A::COLS);
     for (int t = 0; t < nt; ++t) acc[t][half][tok] = 0.f;
 
     const bool options = p.cap > 0.f || p.slopes || p.window > 0;
     QueryStage<T, D, NT, A::PIECES> queries;
-    // queries and column constants of the head that step i begins
-    const auto stage_head = [&](int i, Heads<NT> &set, uint8_t *q) {
-        const Step s = step_at(i);
+    // queries and column constants of the head that step s begins
+    const auto stage_head = [&](const Step &s, Heads<NT> &set, uint8_t *q) {
         w.h = s.h;
         w.col0 = s.qt * NT;
         w.ncols = min(cols - w.col0, NT);
@@ -113,20 +121,20 @@ weights_kernel(const CacheView c, const AttnParams p, const int tiles)
             const float lse = tid < w.ncols ? p.lse[static_cast<int64_t>(w.lo + j) * p.Hq + head] : INFINITY;
             set.lse[tid] = lse == -INFINITY ? INFINITY : lse;
         }
-        if (i == 0 || qt_used > 1) queries.place(p, w, group);
+        if ((s.h == 0 && s.qt == 0) || qt_used > 1) queries.place(p, w, group);
         queries.stage(p, static_cast<int64_t>(s.h) * group * p.q_head, fabsf(p.scale) * (c.k_scale ? c.k_scale[s.h] : 1.f), q, set.mult);
         fence_proxy_async_smem();
     };
     int cb = 0, qb = 0;
-    stage_head(0, sets[0], qs);
+    Step now = {0, 0, 0}, last = now;
+    stage_head(now, sets[0], qs);
     __syncthreads();
     tmem_fence_after();
     const uint32_t a_t = tmem_base, s_t = a_t + A::A_COLS;
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
 
     // weights of a finished product
-    const auto add_weights = [&](int i, const Heads<NT> &set) {
-        const Step s = step_at(i);
+    const auto add_weights = [&](int i, const Step &s, const Heads<NT> &set) {
         const int slot0 = step_slot<kTile>(w, i0 + s.t), slot = slot0 + tok;
         const int valid = min(max(w.len - (slot - lane), 0), kTok);
         float v[NH];
@@ -156,18 +164,19 @@ weights_kernel(const CacheView c, const AttnParams p, const int tiles)
     };
 
     bool fail = false;
+    int st = 0;
+    uint32_t phase = 0;
     for (int i = 0; i < steps; ++i) {
-        const int st = i % A::STAGES;
         const int cb_last = cb;
         if (i > 0) {
             wait_or_fail(&s_bar, (i - 1) & 1, fail);       // the keys' columns are used up
             tmem_fence_after();
-            if (i % nt == 0) {
+            if (now.t == 0) {
                 cb = cb == 2 ? 0 : cb + 1;
                 qb ^= 1;
             }
         }
-        wait_or_fail(&full[st], i / A::STAGES & 1, fail);
+        wait_or_fail(&full[st], phase, fail);
         decode_keys<D>(stages + st * A::STAGE + quarter * A::K_BYTES, a_t + lane_off);
         tmem_wait_st();
         tmem_fence_before();
@@ -177,10 +186,17 @@ weights_kernel(const CacheView c, const AttnParams p, const int tiles)
             issue_scores<D, NT, A::PIECES>(s_t + (i & 1) * A::S_COLS, a_t, smem_addr(qs) + qb * A::Q_BYTES);
             mma_commit(&s_bar);
         }
-        if (warp == kLoadWarp && i + A::STAGES < steps) load(i + A::STAGES);
-        if (i + 1 < steps && (i + 1) % nt == 0)
-            stage_head(i + 1, sets[cb == 2 ? 0 : cb + 1], qs + (qb ^ 1) * A::Q_BYTES);
-        if (i > 0) add_weights(i - 1, sets[cb_last]);
+        if (++st == A::STAGES) {
+            st = 0;
+            phase ^= 1;
+        }
+        if (warp == kLoadWarp) load();
+        Step after = now;
+        after.next(nt, qt_used);
+        if (after.h < c.H && after.t == 0) stage_head(after, sets[cb == 2 ? 0 : cb + 1], qs + (qb ^ 1) * A::Q_BYTES);
+        if (i > 0) add_weights(i - 1, last, sets[cb_last]);
+        last = now;
+        now = after;
     }
     wait_or_fail(&s_bar, (steps - 1) & 1, fail);
     tmem_fence_after();
@@ -191,7 +207,7 @@ weights_kernel(const CacheView c, const AttnParams p, const int tiles)
             set_status(p.status, SPEC_STATUS_TIMEOUT);
         }
     } else {
-        add_weights(steps - 1, sets[cb]);
+        add_weights(steps - 1, last, sets[cb]);
         __syncthreads();
         for (int t = half; t < nt; t += 2) {
             const int slot = step_slot<kTile>(w, i0 + t) + tok;
