@@ -34,7 +34,7 @@ template <typename T, int D_, int NT_> struct Weights {
 // Column constants of a head (shared memory); three sets, as a slow warp may
 // still read the one before last.
 template <int NT> struct Heads {
-    float mult[NT], lse[NT], slope[NT];
+    float mult[NT], lse[NT], slope[NT];           // (lse negated)
     int own[NT], pos[NT];
 };
 
@@ -118,8 +118,8 @@ weights_kernel(const CacheView c, const AttnParams p, const int tiles)
             set.pos[tid] = own >= 0 ? slot_position(c, p, w.b, own) : 0;
             set.slope[tid] = p.slopes ? p.slopes[head] : 0.f;
             // padded columns, and rows that saw nothing: weight exp(-inf) = 0
-            const float lse = tid < w.ncols ? p.lse[static_cast<int64_t>(w.lo + j) * p.Hq + head] : INFINITY;
-            set.lse[tid] = lse == -INFINITY ? INFINITY : lse;
+            const float lse = tid < w.ncols ? p.lse[static_cast<int64_t>(w.lo + j) * p.Hq + head] : -INFINITY;
+            set.lse[tid] = lse == -INFINITY ? -INFINITY : -lse;
         }
         if ((s.h == 0 && s.qt == 0) || qt_used > 1) queries.place(p, w, group);
         queries.stage(p, static_cast<int64_t>(s.h) * group * p.q_head, fabsf(p.scale) * (c.k_scale ? c.k_scale[s.h] : 1.f), q, set.mult);
@@ -153,12 +153,23 @@ weights_kernel(const CacheView c, const AttnParams p, const int tiles)
                 if (p.cap > 0.f) y = cap_score<true>(y, p.cap, rcap);
                 y -= set.slope[q] * static_cast<float>(dist);
                 const bool see = slot <= set.own[q] && (always || (live && dist < p.window));
-                sum += see ? ex2((y - set.lse[q]) * kLog2e) : 0.f;
+                sum += see ? ex2((y + set.lse[q]) * kLog2e) : 0.f;
             }
         } else {
+            // two columns an instruction (lse is held negated)
+            uint64_t two = 0ull;
+            const uint64_t log2e2 = f2_pack(kLog2e, kLog2e);
 #pragma unroll
-            for (int k = 0; k < NH; ++k)
-                sum += ex2(fmaf(v[k], set.mult[half * NH + k], -set.lse[half * NH + k]) * kLog2e);
+            for (int k = 0; k < NH; k += 2) {
+                const uint64_t m = *reinterpret_cast<const uint64_t *>(&set.mult[half * NH + k]);
+                const uint64_t ls = *reinterpret_cast<const uint64_t *>(&set.lse[half * NH + k]);
+                float a, b;
+                f2_unpack(f2_fma(f2_fma(f2_pack(v[k], v[k + 1]), m, ls), log2e2, 0ull), a, b);
+                two = f2_add(two, f2_pack(ex2(a), ex2(b)));
+            }
+            float a, b;
+            f2_unpack(two, a, b);
+            sum = a + b;
         }
         acc[s.t][half][tok] += sum;
     };
@@ -235,9 +246,10 @@ cudaError_t launch_one(const CacheView &c, const AttnParams &p, cudaStream_t s)
         if (e != cudaSuccess) return e;
         done[dev] = true;
     }
-    // as many tiles a CTA as leave two rounds of resident CTAs
+    // tiles a CTA: one round of resident CTAs, so that a head's queries are staged
+    // for as many tiles as the call allows
     const int tiles = (p.max_len + kTile - 1) / kTile;
-    const int64_t per = static_cast<int64_t>(c.B) * tiles / (152 * A::CTAS * 2);
+    const int64_t per = (static_cast<int64_t>(c.B) * tiles + 152 * A::CTAS - 1) / (152 * A::CTAS);
     const int t = static_cast<int>(per < 1 ? 1 : (per > kMaxTiles ? kMaxTiles : per));
     weights_kernel<T, D, NT><<<dim3((tiles + t - 1) / t, c.B), kAttnThreads, A::SMEM, s>>>(c, p, t);
     return cudaGetLastError();
