@@ -276,7 +276,7 @@ template <typename T, int D, int NT, int PIECES> struct QueryStage {
     }
 };
 
-// S^T = K Q^T over all channels (one thread issues).  The terms of fp32 queries
+// S^T = K Q^T over all channels (one warp issues).  The terms of fp32 queries
 // go to accumulators of their own, NT columns apart: the tensor cores truncate
 // a sum at its last place, and adding the small products of the second term to
 // the large sum would cost a bit or two in every step.

@@ -132,7 +132,7 @@ __device__ __forceinline__ void decode_tile_values(const uint8_t *stage, const u
     }
 }
 
-// O^T += V^T P^T over the tile's tokens (one thread issues); the smaller terms of
+// O^T += V^T P^T over the tile's tokens (one warp issues); the smaller terms of
 // P first, as in issue_scores
 template <typename A, bool WIDE>
 __device__ __forceinline__ void issue_values(uint32_t o_addr, uint32_t v_addr, uint32_t ps, bool accumulate)
@@ -452,7 +452,7 @@ attend_kernel(const CacheView c, const AttnParams p, const Layout lay)
     constexpr int kFirst = 1, kLast = 2, kEnd = 4;
     __shared__ int keys_are, weights_wide;
     __shared__ __align__(16) int nv[A::STAGES][4];
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = warp_index(), lane = tid & 31;
     const int group = p.Hq / c.H;
 
     if (warp == 8 && lane == 0) {
@@ -489,11 +489,10 @@ attend_kernel(const CacheView c, const AttnParams p, const Layout lay)
     if (warp == 0) tmem_alloc(&tmem_base, A::COLS);
     __syncthreads();
     tmem_fence_after();
-    const uint32_t a_t = tmem_base, v_t = a_t + A::A_COLS, s_t = v_t + A::V_COLS, o_t = s_t + A::S_COLS;
+    const uint32_t a_t = __shfl_sync(0xFFFFFFFFu, tmem_base, 0), v_t = a_t + A::A_COLS, s_t = v_t + A::V_COLS, o_t = s_t + A::S_COLS;
     bool fail = false;
 
     if (warp == 8) {
-        const bool leader = elect_one();
         const uint32_t q_addr = smem_addr(qs), p_addr = smem_addr(ps);
         // tiles of the range into the ring, the page ids of the one after asked for
         int ring = 0, seg = cur.segment(group), k_ld = 0;
@@ -521,13 +520,10 @@ attend_kernel(const CacheView c, const AttnParams p, const Layout lay)
         const auto scores = [&] {
             wait_or_fail(&k_bar, g++ & 1, fail);
             tmem_fence_after();
-            now = fail ? kEnd : *reinterpret_cast<volatile int *>(&keys_are);
+            now = __shfl_sync(0xFFFFFFFFu, fail ? kEnd : *reinterpret_cast<volatile int *>(&keys_are), 0);
             if (now == kEnd) return;
-            if (leader) {
-                issue_scores<D, NT, A::PIECES>(s_t, a_t, q_addr);
-                mma_commit(&s_bar);
-            }
-            __syncwarp();
+            issue_scores<D, NT, A::PIECES>(s_t, a_t, q_addr);
+            mma_commit(&s_bar);
         };
         scores();
         while (now != kEnd) {
@@ -535,14 +531,11 @@ attend_kernel(const CacheView c, const AttnParams p, const Layout lay)
             if (!(here & kLast)) scores();
             wait_or_fail(&p_bar, p_count++ & 1, fail);
             tmem_fence_after();
-            const bool wide = *reinterpret_cast<volatile int *>(&weights_wide);
-            if (leader) {
-                const bool accumulate = !(kPromote || (here & kFirst));
-                if (wide) issue_values<A, true>(o_t, v_t, p_addr, accumulate);
-                else issue_values<A, false>(o_t, v_t, p_addr, accumulate);
-                mma_commit(&o_bar);
-            }
-            __syncwarp();
+            const bool wide = __shfl_sync(0xFFFFFFFFu, *reinterpret_cast<volatile int *>(&weights_wide), 0);
+            const bool accumulate = !(kPromote || (here & kFirst));
+            if (wide) issue_values<A, true>(o_t, v_t, p_addr, accumulate);
+            else issue_values<A, false>(o_t, v_t, p_addr, accumulate);
+            mma_commit(&o_bar);
             load_next();
             if (here & kLast) scores();
         }

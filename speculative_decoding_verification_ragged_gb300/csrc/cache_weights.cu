@@ -65,7 +65,7 @@ weights_kernel(const CacheView c, const AttnParams p, const int tiles)
     __shared__ uint32_t tmem_base;
     __shared__ int nv[A::STAGES][4];
     __shared__ float acc[kMaxTiles][2][kTile];
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = warp_index(), lane = tid & 31;
     const int quarter = warp & 3, half = warp >> 2, tok = tid & 127;
     const int group = p.Hq / c.H;
     Job w;
@@ -130,7 +130,7 @@ weights_kernel(const CacheView c, const AttnParams p, const int tiles)
     stage_head(now, sets[0], qs);
     __syncthreads();
     tmem_fence_after();
-    const uint32_t a_t = tmem_base, s_t = a_t + A::A_COLS;
+    const uint32_t a_t = __shfl_sync(0xFFFFFFFFu, tmem_base, 0), s_t = a_t + A::A_COLS;
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
 
     // weights of a finished product
@@ -192,7 +192,7 @@ weights_kernel(const CacheView c, const AttnParams p, const int tiles)
         tmem_wait_st();
         tmem_fence_before();
         __syncthreads();
-        if (tid == 0) {
+        if (warp == 0) {
             tmem_fence_after();
             issue_scores<D, NT, A::PIECES>(s_t + (i & 1) * A::S_COLS, a_t, smem_addr(qs) + qb * A::Q_BYTES);
             mma_commit(&s_bar);

@@ -8,13 +8,8 @@
 
 namespace specv {
 
-// one lane of the warp (the same one each time)
-__device__ __forceinline__ bool elect_one()
-{
-    uint32_t r;
-    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
-    return r != 0;
-}
+// the warp's index, known to be the same in all its lanes
+__device__ __forceinline__ int warp_index() { return __shfl_sync(0xFFFFFFFFu, static_cast<int>(threadIdx.x >> 5), 0); }
 
 __device__ __forceinline__ void mbar_arrive(uint64_t *bar)
 {
@@ -117,21 +112,26 @@ __host__ __device__ constexpr uint32_t mma_f16_desc(int n, bool b_n_major, bool 
     return 1u << 4 | (bf16 ? 1u << 7 | 1u << 10 : 0u) | (b_n_major ? 1u << 16 : 0u) | static_cast<uint32_t>(n >> 3) << 17 | (128u >> 4) << 24;
 }
 
-// D[128 x n] (+)= A[128 x 16] B[16 x n]; one thread issues
+// D[128 x n] (+)= A[128 x 16] B[16 x n].  A whole warp calls it, converged, with
+// the same operands, and one lane issues: the election is inside, so that the
+// operands stay in uniform registers (a branch around the call made each issue cost
+// about 120 cycles).
 __device__ __forceinline__ void mma_f16(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool accumulate)
 {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc),
+        "{\n\t.reg .pred p, q;\n\telect.sync _|q, 0xffffffff;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc),
         "r"(static_cast<uint32_t>(accumulate))
         : "memory");
 }
 
-// arrive on `bar` when every product issued so far by this thread is complete
+// arrive on `bar` when every product issued so far by this warp is complete
 __device__ __forceinline__ void mma_commit(uint64_t *bar)
 {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
-                 : "memory");
+    asm volatile(
+        "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_addr(bar))
+        : "memory");
 }
 
 }  // namespace specv
