@@ -363,7 +363,7 @@ template <int NT>
 __device__ __forceinline__ int64_t find_range(const CacheView &c, const AttnParams &p, const Layout &lay, int group,
                                               int &grid, int64_t &t0, Job &job, int64_t &off)
 {
-    constexpr int N = kAttnThreads + 32;
+    constexpr int N = kAttnThreads + 64;
     __shared__ int64_t sums[N / 32 + 1], offset;
     __shared__ Job found;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -427,17 +427,17 @@ __device__ __forceinline__ int64_t find_range(const CacheView &c, const AttnPara
     return total;
 }
 
-// Warps 0..7 decode, weigh and store; warp 8 fetches tiles, ahead over the whole
-// range, and issues the products.  Per tile the eight warps wait for S^T, turn it
+// Warps 0..7 decode, weigh and store; warp 8 issues the products, warp 9 fetches
+// tiles, ahead over the whole range.  Per tile the eight warps wait for S^T, turn it
 // into weights (one barrier: do the references hold?), decode the next tile's
 // keys, then this tile's values; each product runs while they decode the other
-// operand, and they meet the ninth warp at mbarriers only.
+// operand, and they meet the other two at mbarriers only.
 template <typename T, int D, int NT>
-__global__ void __launch_bounds__(kAttnThreads + 32, (Attn<T, D, NT>::CTAS))
+__global__ void __launch_bounds__(kAttnThreads + 64, (Attn<T, D, NT>::CTAS))
 attend_kernel(const CacheView c, const AttnParams p, const Layout lay)
 {
     using A = Attn<T, D, NT>;
-    constexpr int NH = A::NH;
+    constexpr int NH = A::NH, kIssuer = 8, kLoader = 9;
     constexpr bool kPromote = A::PIECES == 2;
     constexpr int OR = kPromote ? NH * A::VM : 1;     // fp32: results kept in registers
     extern __shared__ __align__(128) uint8_t smem[];
@@ -445,9 +445,9 @@ attend_kernel(const CacheView c, const AttnParams p, const Layout lay)
     uint32_t *vs = reinterpret_cast<uint32_t *>(ps + A::WIDE * A::P_BYTES);
     uint8_t *stages = ps + A::WIDE * A::P_BYTES + 2 * A::VS_BYTES;
     __shared__ __align__(16) Columns<NT> cs;
-    __shared__ __align__(8) uint64_t full[A::STAGES], k_bar, p_bar, s_bar, o_bar;
+    __shared__ __align__(8) uint64_t full[A::STAGES], empty[A::STAGES], k_bar, p_bar, s_bar, o_bar;
     __shared__ uint32_t tmem_base, arrived;
-    // what the eight warps tell the ninth: with keys, kFirst / kLast of a segment
+    // what the eight warps tell the issuer: with keys, kFirst / kLast of a segment
     // or kEnd; with weights, whether they are those of a wide tile
     constexpr int kFirst = 1, kLast = 2, kEnd = 4;
     __shared__ int keys_are, weights_wide;
@@ -455,8 +455,11 @@ attend_kernel(const CacheView c, const AttnParams p, const Layout lay)
     const int tid = threadIdx.x, warp = warp_index(), lane = tid & 31;
     const int group = p.Hq / c.H;
 
-    if (warp == 8 && lane == 0) {
-        for (int i = 0; i < A::STAGES; ++i) mbar_init(&full[i], 1);
+    if (warp == kIssuer && lane == 0) {
+        for (int i = 0; i < A::STAGES; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 8);
+        }
         mbar_init(&k_bar, 8);
         mbar_init(&p_bar, 8);
         mbar_init(&s_bar, 1);
@@ -492,10 +495,10 @@ attend_kernel(const CacheView c, const AttnParams p, const Layout lay)
     const uint32_t a_t = __shfl_sync(0xFFFFFFFFu, tmem_base, 0), v_t = a_t + A::A_COLS, s_t = v_t + A::V_COLS, o_t = s_t + A::S_COLS;
     bool fail = false;
 
-    if (warp == 8) {
-        const uint32_t q_addr = smem_addr(qs), p_addr = smem_addr(ps);
+    if (warp == kLoader) {
         // tiles of the range into the ring, the page ids of the one after asked for
         int ring = 0, seg = cur.segment(group), k_ld = 0;
+        uint32_t phase = 1;                           // (a stage is empty at first)
         bool any = true;
         Fetch next;
         const auto ask_next = [&] {
@@ -507,15 +510,21 @@ attend_kernel(const CacheView c, const AttnParams p, const Layout lay)
             any = cur.left > 0;
             if (any) next = ask_pages(c, cur.w, cur.w.h, step_slot<kTile>(cur.w, cur.unit + k_ld++));
         };
-        const auto load_next = [&] {
-            if (!any) return;
-            load_tile<block_bytes(D)>(c, next, stages + ring * A::STAGE, &full[ring], nv[ring], p.status);
-            ring = ring + 1 == A::STAGES ? 0 : ring + 1;
-            ask_next();
-        };
         ask_next();
-        for (int i = 0; i < A::STAGES; ++i) load_next();
+        while (any && !fail) {
+            wait_or_fail(&empty[ring], phase, fail);
+            load_tile<block_bytes(D)>(c, next, stages + ring * A::STAGE, &full[ring], nv[ring], p.status);
+            if (++ring == A::STAGES) {
+                ring = 0;
+                phase ^= 1;
+            }
+            ask_next();
+        }
+        return;
+    }
+    if (warp == kIssuer) {
         // products in the order their operands come
+        const uint32_t q_addr = smem_addr(qs), p_addr = smem_addr(ps);
         int g = 0, p_count = 0, now = 0;
         const auto scores = [&] {
             wait_or_fail(&k_bar, g++ & 1, fail);
@@ -536,7 +545,6 @@ attend_kernel(const CacheView c, const AttnParams p, const Layout lay)
             if (wide) issue_values<A, true>(o_t, v_t, p_addr, accumulate);
             else issue_values<A, false>(o_t, v_t, p_addr, accumulate);
             mma_commit(&o_bar);
-            load_next();
             if (here & kLast) scores();
         }
         return;
@@ -618,6 +626,7 @@ attend_kernel(const CacheView c, const AttnParams p, const Layout lay)
             t.edge = !whole || slot0 + kTile - 1 > own_first;
             if (options && p.slot_pos && t.live) t.pos = slot_position(c, p, w.b, t.slot);
             value_scales<D>(stage, nv[ring], whole, vsk);
+            uint64_t *const done = &empty[ring];
             if (++ring == A::STAGES) {
                 ring = 0;
                 ring_phase ^= 1;
@@ -715,6 +724,8 @@ attend_kernel(const CacheView c, const AttnParams p, const Layout lay)
             if (!wide) decode_tile_values<A, false>(stage, vsk, v_t + lane_off);
             else decode_tile_values<A, true>(stage, vsk, v_t + lane_off);
             if (tid == 0) weights_wide = wide;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(done);         // the stage is read
             tmem_wait_st();
             tmem_fence_before();
             fence_proxy_async_smem();
@@ -843,7 +854,7 @@ attend_kernel(const CacheView c, const AttnParams p, const Layout lay)
         }
         csync();
     }
-    // tell the ninth warp, and leave
+    // tell the issuer, and leave
     if (tid == 0) keys_are = kEnd;
     __syncwarp();
     if (lane == 0) mbar_arrive(&k_bar);
@@ -889,7 +900,7 @@ cudaError_t launch_one(const CacheView &c, const AttnParams &p, cudaStream_t s)
         done[dev] = true;
     }
     const Layout l = layout_of<A>(c.B, p.k_max, p.Hq, c.H, p.max_len);
-    attend_kernel<T, D, NT><<<l.grid, kAttnThreads + 32, A::SMEM, s>>>(c, p, l);
+    attend_kernel<T, D, NT><<<l.grid, kAttnThreads + 64, A::SMEM, s>>>(c, p, l);
     return cudaGetLastError();
 }
 
