@@ -111,12 +111,14 @@ typedef struct {
     const float *slopes;       /* [Hq] or NULL: s -= slope * (pos_row - pos_slot)             */
     int32_t window;            /* > 0: only slots with pos_row - pos_slot < window ...        */
     int32_t prefix;            /* ... or slot < prefix                                        */
-    const int32_t *slot_pos;   /* [n_pages, page_tokens] or NULL: position of a slot; NULL: its index */
+    const int32_t *slot_pos;   /* [n_pages, page_tokens] or NULL: position of a slot, not
+                                  decreasing over a request's slots; NULL: its index          */
     uint32_t *status;          /* [1] or NULL                                                 */
 } spec_attention;
 
-/* Workspace of spec_cache_attend (zero-filled once before its first use, like
- * the verify workspace); 0 for invalid sizes. */
+/* Workspace of spec_cache_attend, zero-filled once before its first use; any
+ * number of stream-ordered calls, of any shapes that it is large enough for, can
+ * then share it.  0 for invalid sizes. */
 SPEC_API size_t spec_cache_workspace_bytes(int32_t B, int32_t k_max, int32_t Hq, int32_t H,
                                            int32_t D, int32_t max_len);
 
@@ -129,7 +131,9 @@ SPEC_API size_t spec_cache_workspace_bytes(int32_t B, int32_t k_max, int32_t Hq,
  * a bad length) gets out = 0 and lse = -inf.  Slots that no row of the
  * request sees are not read, whatever their bytes.  out [R_cap, Hq, D], lse
  * [R_cap, Hq] or NULL, both contiguous; rows >= cu_rows[B] are not written.
- * Results do not depend on the order in which blocks run.
+ * Results do not depend on the order in which blocks run.  One launch.  bf16
+ * outputs come from weights rounded to 11 bits, fp32 ones from 22 bits; sums of
+ * weights, and so lse, are fp32.
  */
 SPEC_API int spec_cache_attend(const spec_cache *cache, const spec_attention *attn, void *out,
                                float *lse, void *workspace, size_t workspace_bytes,

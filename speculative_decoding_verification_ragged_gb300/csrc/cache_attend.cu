@@ -304,8 +304,13 @@ __device__ __forceinline__ void rescale_results(const Columns<A::NT> &cs, uint32
 // at most where two CTAs meet.
 struct Layout {
     int grid;                   // CTAs at most, all resident at once
-    int qtiles;                 // column tiles of a request at most
 };
+
+// The workspace: arrivals at each split task, by the CTA where it begins, then the
+// parts.  The arrivals have one place for calls of all shapes, so that calls of
+// different shapes can share a workspace.
+constexpr int kSms = 152, kTicketBytes = 2 * kSms * 4 + 64;
+static_assert(kTicketBytes % 16 == 0, "the parts are read by vectors");
 
 __device__ __forceinline__ int64_t range_start(int64_t total, int grid, int i) { return total * i / grid; }
 // the CTA whose range holds unit t
@@ -750,8 +755,7 @@ attend_kernel(const CacheView c, const AttnParams p, const Layout lay)
         // 2 i + 1 (it goes on after it).
         const bool head = cur_s.unit > 0, tail = cur_s.unit + seg < cur_s.units();
         const bool split = head || tail;
-        uint8_t *parts = static_cast<uint8_t *>(p.ws) + (static_cast<int64_t>(c.B) * c.H * lay.qtiles * 4 + 255) / 256 * 256;
-        float *const part_all = reinterpret_cast<float *>(parts);
+        float *const part_all = reinterpret_cast<float *>(static_cast<uint8_t *>(p.ws) + kTicketBytes);
         float2 *const ml_all = reinterpret_cast<float2 *>(part_all + static_cast<int64_t>(lay.grid) * 2 * NT * D);
         const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (head ? 0 : 1);
         const auto out_row = [&](int q) {
@@ -801,7 +805,7 @@ attend_kernel(const CacheView c, const AttnParams p, const Layout lay)
             // the CTA that arrives last joins the parts, in the line's order
             const int64_t begin = t0_s - cur_s.unit, end = begin + cur_s.units();
             const int c0 = range_of(total_s, grid_s, begin), c1 = range_of(total_s, grid_s, end - 1);
-            uint32_t *ticket = static_cast<uint32_t *>(p.ws) + (static_cast<int64_t>(w.b) * c.H + w.h) * lay.qtiles + w.col0 / NT;
+            uint32_t *ticket = static_cast<uint32_t *>(p.ws) + c0;     // (one task at most goes on after a range)
             csync();
             if (tid == 0) {
                 fence_acq_rel_gpu();
@@ -871,18 +875,17 @@ attend_kernel(const CacheView c, const AttnParams p, const Layout lay)
 // CTAs for a call: as many as are resident, no more than there can be units.
 template <typename A> Layout layout_of(int B, int k_max, int Hq, int H, int max_len)
 {
+    const int qtiles = ((k_max + 1) * (Hq / H) + A::NT - 1) / A::NT;
+    const int64_t units = static_cast<int64_t>(B) * H * qtiles * ((max_len + kTile - 1) / kTile);
     Layout l;
-    l.qtiles = ((k_max + 1) * (Hq / H) + A::NT - 1) / A::NT;
-    const int64_t units = static_cast<int64_t>(B) * H * l.qtiles * ((max_len + kTile - 1) / kTile);
-    l.grid = static_cast<int>(units < 152 * A::CTAS ? units : 152 * A::CTAS);
+    l.grid = static_cast<int>(units < kSms * A::CTAS ? units : kSms * A::CTAS);
     return l;
 }
 
 template <typename A> size_t workspace_of(int B, int k_max, int Hq, int H, int max_len)
 {
     const Layout l = layout_of<A>(B, k_max, Hq, H, max_len);
-    const size_t tickets = static_cast<size_t>(B) * H * l.qtiles * 4;
-    return (tickets + 255) / 256 * 256 + static_cast<size_t>(l.grid) * 2 * A::NT * (A::D + 2) * 4;
+    return kTicketBytes + static_cast<size_t>(l.grid) * 2 * A::NT * (A::D + 2) * 4;
 }
 
 template <typename T, int D, int NT>

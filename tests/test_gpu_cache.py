@@ -324,6 +324,78 @@ def test_attention_long_caches(D, dtype, rows, group):
     check_attention(sv, c, q, cu, lens, rows - 1)
 
 
+@pytest.mark.parametrize("D,group,rows,dtype", [(64, 8, 8, "bf16"), (128, 8, 8, "bf16"), (128, 12, 32, "bf16"), (64, 16, 32, "f32")])
+def test_attention_many_columns(D, group, rows, dtype):
+    """64 columns of one kv head, and several column tiles of them."""
+    sv = need_gpu()
+    rng = np.random.default_rng(D + group)
+    lens = [700, 40, 129, 33]
+    cu = np.concatenate([[0], np.cumsum([rows, rows, 1, rows])])
+    c = quick_pool(rng, B=4, H=1, D=D, page=64, lens=lens)
+    check_attention(sv, c, queries(rng, int(cu[-1]), group, D, dtype, 0.5), cu, lens, rows - 1)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_attention_over_many_requests(dtype):
+    """More requests than a block has threads, empty ones, ones without rows and
+    malformed ones among them."""
+    sv = need_gpu()
+    rng = np.random.default_rng(15)
+    B = 1100
+    lens = rng.integers(0, 90, B)
+    lens[5], lens[901] = 3000, 1500
+    n = rng.integers(0, 4, B)
+    n[::7] = 0
+    cu = np.concatenate([[0], np.cumsum(n)])
+    c = quick_pool(rng, B=B, H=1, D=64, page=32, lens=list(lens))
+    q = queries(rng, int(cu[-1]), 2, 64, dtype)
+    check_attention(sv, c, q, cu, [int(x) for x in lens], 3)
+    # with k_max = 0 the requests of several rows are malformed, and skipped
+    res, _, status = run_attention(sv, c, q, cu, [int(x) for x in lens], int(n.max()) - 1)
+    wide, _, status_w = run_attention(sv, c, q, cu, [int(x) for x in lens], 0)
+    assert status == 0 and status_w == 0x10
+    one = np.nonzero(n == 1)[0]
+    for b in one[::9]:
+        assert torch.equal(res["out"][cu[b]], wide["out"][cu[b]])
+
+
+def test_a_workspace_serves_calls_of_different_shapes():
+    sv = need_gpu()
+    rng = np.random.default_rng(16)
+    lens = [5000, 900, 3100, 70]
+    c = quick_pool(rng, B=4, H=2, D=128, page=64, lens=lens)
+    cache, tab, ln = gpu_cache(sv, c), dev(c.table), dev(np.asarray(lens, np.int32))
+    shapes = [(4, 5, 10), (1, 1, 2), (3, 2, 8), (4, 1, 32), (2, 8, 16)]
+    ws = torch.zeros(max(sv.cache_workspace_bytes(b, r - 1, hq, 2, 128, tab.shape[1] * 64) for b, r, hq in shapes),
+                     dtype=torch.uint8, device="cuda")
+    for _ in range(2):
+        for b, r, hq in shapes:
+            q = queries(rng, b * r, hq, 128, "bf16")
+            cu = dev(np.arange(0, b * r + 1, r).astype(np.int32))
+            got = sv.cache_attend(cache, q, cu, ln, tab, B=b, k_max=r - 1, workspace=ws)
+            want = sv.cache_attend(cache, q, cu, ln, tab, B=b, k_max=r - 1)
+            assert torch.equal(got["out"], want["out"]) and torch.equal(got["lse"], want["lse"])
+
+
+@pytest.mark.parametrize("n,budget,recent", [(30000, 10000, 100), (70000, 69999, 0), (131072, 5, 2), (400001, 100000, 1000)])
+def test_evict_from_long_caches(n, budget, recent):
+    """Clusters of every size, and more scores than stay on chip."""
+    sv = need_gpu()
+    rng = np.random.default_rng(n)
+    per = -(-n // 128)
+    pages = torch.randint(0, 120, (per + -(-budget // 128), 1, 4, 36 * 64), dtype=torch.uint8, device="cuda")
+    score = rng.exponential(1, (len(pages), 128)).astype(np.float32).round(3)
+    table = rng.permutation(per).astype(np.int32)[None]
+    dst = np.arange(per, len(pages), dtype=np.int32)[None]
+    s = dev(score)
+    got = sv.cache_evict(sv.PagedCache(pages), s, dev(np.array([n], np.int32)), dev(table), dev(dst), B=1, budget=budget,
+                         recent=recent)
+    i = np.arange(n)
+    keep = ref.evict(score[table[0, i // 128], i % 128], n, budget, recent)
+    np.testing.assert_array_equal(got["kept"].cpu().numpy()[0], keep)
+    np.testing.assert_array_equal(s.cpu().numpy()[dst[0]].reshape(-1)[:budget], score[table[0, keep // 128], keep % 128])
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_attention_rows_that_see_nothing(dtype):
     """len 0, len < rows, rows of zero length, a bad length, bad rows, a bad page."""
