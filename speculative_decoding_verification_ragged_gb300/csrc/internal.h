@@ -145,6 +145,9 @@ cudaError_t launch_cache_rows(const CacheView &c, const CacheRows &r, int dtype,
                               cudaStream_t stream);
 cudaError_t launch_cache_attend(const CacheView &c, const AttnParams &p, int dtype,
                                 cudaStream_t stream);
+// the same with a cap, distance biases or a window (called by launch_cache_attend)
+cudaError_t launch_cache_attend_options(const CacheView &c, const AttnParams &p, int dtype,
+                                        cudaStream_t stream);
 cudaError_t launch_cache_weights(const CacheView &c, const AttnParams &p, int dtype,
                                  cudaStream_t stream);
 // workspace bytes of the attention (for queries of either type)
