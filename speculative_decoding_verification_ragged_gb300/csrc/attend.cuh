@@ -14,7 +14,6 @@ namespace specv {
 
 constexpr int kAttnThreads = 256;
 constexpr int kTile = 128;                 // tokens of a tile: 4 blocks, the lanes of tensor memory
-constexpr int kLoadWarp = 7;               // the warp that fetches tiles (weights)
 
 // What a CTA works on.
 struct Job {

@@ -2,12 +2,13 @@
 // packed verify rows, added to its score (include/spec_cache.h).
 //
 // score_j += sum over rows and heads of exp(s_ij - lse_i): with S^T = K Q^T
-// (cache_attend.cu) a token is a lane, and its sum over the columns and heads
+// (cache_attend.cuh) a token is a lane, and its sum over the columns and heads
 // stays in two threads (a half of the columns each), in a fixed order -- no
 // atomics, one read and one write of the score.  A CTA takes a few tiles of one
-// request through every kv head; the keys alone are read.  The product of a
-// step runs while the weights of the step before are summed and the next head's
-// queries are staged.
+// request through every kv head; the keys alone are read.  The product of a step
+// runs while the weights of the step before are summed and the next head's queries
+// are staged; warp 8 issues the products, warp 9 fetches, and the eight warps that
+// decode and sum meet them, and each other, at mbarriers only.
 #include "attend.cuh"
 
 namespace specv {
@@ -22,21 +23,23 @@ template <typename T, int D_, int NT_> struct Weights {
     static constexpr int K_BYTES = v_codes_at(D);              // a block's keys and their scales
     static constexpr int A_COLS = D / 2, S_COLS = PIECES * NT;
     static constexpr int COLS = tmem_cols(A_COLS + 2 * S_COLS);
-    static constexpr int CTAS = 512 / COLS;
+    static constexpr int CTAS = COLS == 128 ? 3 : 2;           // 64 registers a thread, or 96
     static constexpr int Q_BYTES = PIECES * query_bytes(D, NT);
     static constexpr int STAGE = 4 * K_BYTES;
-    static constexpr int FIXED = 128 + 60 * NT + 2 * kMaxTiles * kTile * 4;
+    static constexpr int FIXED = 1024 + 80 * NT + 2 * kMaxTiles * kTile * 4;
     static constexpr int STAGES = clamp_stages((smem_share(CTAS, FIXED) - 2 * Q_BYTES) / STAGE);
     static constexpr int NEED = 2 * Q_BYTES + STAGES * STAGE;
-    static constexpr int SMEM = NEED > smem_least(CTAS) ? NEED : smem_least(CTAS);
+    static constexpr int SMEM = NEED > smem_least(CTAS) - FIXED ? NEED : smem_least(CTAS) - FIXED;
 };
 
-// Column constants of a head (shared memory); three sets, as a slow warp may
-// still read the one before last.
-template <int NT> struct Heads {
+// Column constants of a head (shared memory).  Four sets: a warp may still read
+// the one of three steps ago while the next is written.
+template <int NT> struct alignas(16) Heads {          // (read by pairs)
     float mult[NT], lse[NT], slope[NT];           // (lse negated)
     int own[NT], pos[NT];
+    int ncols;
 };
+constexpr int kSets = 4;
 
 // Step of a CTA: tile `t` of its tiles, column tile `qt` of kv head `h`.
 struct Step {
@@ -53,58 +56,79 @@ struct Step {
 };
 
 template <typename T, int D, int NT>
-__global__ void __launch_bounds__(kAttnThreads, (Weights<T, D, NT>::CTAS))
+__global__ void __launch_bounds__(kAttnThreads + 64, (Weights<T, D, NT>::CTAS))
 weights_kernel(const CacheView c, const AttnParams p, const int tiles)
 {
     using A = Weights<T, D, NT>;
-    constexpr int NH = A::NH;
+    constexpr int NH = A::NH, kIssuer = 8, kLoader = 9;
     extern __shared__ __align__(128) uint8_t smem[];
     uint8_t *qs = smem, *stages = qs + 2 * A::Q_BYTES;
-    __shared__ __align__(16) Heads<NT> sets[3];
-    __shared__ __align__(8) uint64_t full[A::STAGES], s_bar;
+    __shared__ __align__(16) Heads<NT> sets[kSets];
+    __shared__ __align__(8) uint64_t full[A::STAGES], empty[A::STAGES], k_bar, s_bar;
     __shared__ uint32_t tmem_base;
     __shared__ int nv[A::STAGES][4];
     __shared__ float acc[kMaxTiles][2][kTile];
     const int tid = threadIdx.x, warp = warp_index(), lane = tid & 31;
-    const int quarter = warp & 3, half = warp >> 2, tok = tid & 127;
     const int group = p.Hq / c.H;
     Job w;
     w.b = blockIdx.y;
     if (!load_job<kTile>(c, p, w, tid == 0 ? p.status : nullptr)) return;
-    const int i0 = blockIdx.x * tiles;
-    const int nt = min(tiles, w.nsteps - i0);
+    const int i0 = blockIdx.x * tiles, nt = min(tiles, w.nsteps - i0);
     if (nt <= 0) return;
-
     const int cols = w.n * group, qt_used = (cols + NT - 1) / NT;
     const int steps = c.H * qt_used * nt;
-    // the loading warp: its next step, the page ids of it asked for ahead
-    Step to_load = {0, 0, 0};
-    int load_ring = 0;
-    Fetch next;
-    const auto ask = [&] {
-        if (to_load.h < c.H) next = ask_pages(c, w, to_load.h, step_slot<kTile>(w, i0 + to_load.t));
-    };
-    const auto load = [&] {
-        if (to_load.h >= c.H) return;
-        load_tile<A::K_BYTES>(c, next, stages + load_ring * A::STAGE, &full[load_ring], nv[load_ring], p.status);
-        load_ring = load_ring + 1 == A::STAGES ? 0 : load_ring + 1;
-        to_load.next(nt, qt_used);
-        ask();
-    };
-    if (warp == kLoadWarp) {
-        if (lane == 0) {
-            for (int i = 0; i < A::STAGES; ++i) mbar_init(&full[i], 1);
-            mbar_init(&s_bar, 1);
-            fence_mbar_init();
+
+    if (warp == kIssuer && lane == 0) {
+        for (int i = 0; i < A::STAGES; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 8);
         }
-        __syncwarp();
-        ask();
-        for (int i = 0; i < A::STAGES; ++i) load();
+        mbar_init(&k_bar, 8);
+        mbar_init(&s_bar, 1);
+        fence_mbar_init();
     }
     if (warp == 0) tmem_alloc(&tmem_base, A::COLS);
-    for (int t = 0; t < nt; ++t) acc[t][half][tok] = 0.f;
+    __syncthreads();
+    tmem_fence_after();
+    const uint32_t a_t = __shfl_sync(0xFFFFFFFFu, tmem_base, 0), s_t = a_t + A::A_COLS;
+    bool fail = false;
 
+    if (warp == kLoader) {
+        // the keys of each step into the ring, the page ids of the step after asked for
+        Step at = {0, 0, 0};
+        int ring = 0;
+        uint32_t phase = 1;                               // (a stage is empty at first)
+        Fetch next = ask_pages(c, w, 0, step_slot<kTile>(w, i0));
+        for (int i = 0; i < steps && !fail; ++i) {
+            wait_or_fail(&empty[ring], phase, fail);
+            load_tile<A::K_BYTES>(c, next, stages + ring * A::STAGE, &full[ring], nv[ring], p.status);
+            if (++ring == A::STAGES) {
+                ring = 0;
+                phase ^= 1;
+            }
+            at.next(nt, qt_used);
+            if (i + 1 < steps) next = ask_pages(c, w, at.h, step_slot<kTile>(w, i0 + at.t));
+        }
+        return;
+    }
+    if (warp == kIssuer) {
+        Step at = {0, 0, 0};
+        int qb = 0;
+        for (int i = 0; i < steps && !fail; ++i) {
+            wait_or_fail(&k_bar, i & 1, fail);
+            tmem_fence_after();
+            issue_scores<D, NT, A::PIECES>(s_t + (i & 1) * A::S_COLS, a_t, smem_addr(qs) + qb * A::Q_BYTES);
+            mma_commit(&s_bar);
+            at.next(nt, qt_used);
+            if (at.t == 0) qb ^= 1;
+        }
+        return;
+    }
+
+    const int quarter = warp & 3, half = warp >> 2, tok = tid & 127;
+    const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
     const bool options = p.cap > 0.f || p.slopes || p.window > 0;
+    for (int t = 0; t < nt; ++t) acc[t][half][tok] = 0.f;
     QueryStage<T, D, NT, A::PIECES> queries;
     // queries and column constants of the head that step s begins
     const auto stage_head = [&](const Step &s, Heads<NT> &set, uint8_t *q) {
@@ -120,21 +144,17 @@ weights_kernel(const CacheView c, const AttnParams p, const int tiles)
             // padded columns, and rows that saw nothing: weight exp(-inf) = 0
             const float lse = tid < w.ncols ? p.lse[static_cast<int64_t>(w.lo + j) * p.Hq + head] : -INFINITY;
             set.lse[tid] = lse == -INFINITY ? -INFINITY : -lse;
+            if (tid == 0) set.ncols = w.ncols;
         }
         if ((s.h == 0 && s.qt == 0) || qt_used > 1) queries.place(p, w, group);
-        queries.stage(p, static_cast<int64_t>(s.h) * group * p.q_head, fabsf(p.scale) * (c.k_scale ? c.k_scale[s.h] : 1.f), q, set.mult);
+        queries.stage(p, static_cast<int64_t>(s.h) * group * p.q_head, fabsf(p.scale) * (c.k_scale ? c.k_scale[s.h] : 1.f), q,
+                      set.mult);
         fence_proxy_async_smem();
     };
-    int cb = 0, qb = 0;
-    Step now = {0, 0, 0}, last = now;
-    stage_head(now, sets[0], qs);
-    __syncthreads();
-    tmem_fence_after();
-    const uint32_t a_t = __shfl_sync(0xFFFFFFFFu, tmem_base, 0), s_t = a_t + A::A_COLS;
-    const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
-
     // weights of a finished product
     const auto add_weights = [&](int i, const Step &s, const Heads<NT> &set) {
+        const int real = set.ncols - half * NH;           // of this thread's columns
+        if (real <= 0) return;
         const int slot0 = step_slot<kTile>(w, i0 + s.t), slot = slot0 + tok;
         const int valid = min(max(w.len - (slot - lane), 0), kTok);
         float v[NH];
@@ -148,6 +168,7 @@ weights_kernel(const CacheView c, const AttnParams p, const int tiles)
             const float rcap = p.cap > 0.f ? 1.f / p.cap : 0.f;
 #pragma unroll
             for (int k = 0; k < NH; ++k) {
+                if (k >= real) break;
                 const int q = half * NH + k, dist = set.pos[q] - tpos;
                 float y = v[k] * set.mult[q];
                 if (p.cap > 0.f) y = cap_score<true>(y, p.cap, rcap);
@@ -156,7 +177,7 @@ weights_kernel(const CacheView c, const AttnParams p, const int tiles)
                 sum += see ? ex2((y + set.lse[q]) * kLog2e) : 0.f;
             }
         } else {
-            // two columns an instruction (lse is held negated)
+            // two columns an instruction
             uint64_t two = 0ull;
             const uint64_t log2e2 = f2_pack(kLog2e, kLog2e);
 #pragma unroll
@@ -174,44 +195,42 @@ weights_kernel(const CacheView c, const AttnParams p, const int tiles)
         acc[s.t][half][tok] += sum;
     };
 
-    bool fail = false;
-    int st = 0;
+    Step now = {0, 0, 0}, last = now;
+    int cb = 0, qb = 0, ring = 0;
     uint32_t phase = 0;
+    stage_head(now, sets[0], qs);
     for (int i = 0; i < steps; ++i) {
         const int cb_last = cb;
         if (i > 0) {
             wait_or_fail(&s_bar, (i - 1) & 1, fail);       // the keys' columns are used up
             tmem_fence_after();
             if (now.t == 0) {
-                cb = cb == 2 ? 0 : cb + 1;
+                cb = (cb + 1) % kSets;
                 qb ^= 1;
             }
         }
-        wait_or_fail(&full[st], phase, fail);
-        decode_keys<D>(stages + st * A::STAGE + quarter * A::K_BYTES, a_t + lane_off);
+        wait_or_fail(&full[ring], phase, fail);
+        decode_keys<D>(stages + ring * A::STAGE + quarter * A::K_BYTES, a_t + lane_off);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&empty[ring]);
         tmem_wait_st();
         tmem_fence_before();
-        __syncthreads();
-        if (warp == 0) {
-            tmem_fence_after();
-            issue_scores<D, NT, A::PIECES>(s_t + (i & 1) * A::S_COLS, a_t, smem_addr(qs) + qb * A::Q_BYTES);
-            mma_commit(&s_bar);
-        }
-        if (++st == A::STAGES) {
-            st = 0;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&k_bar);
+        if (++ring == A::STAGES) {
+            ring = 0;
             phase ^= 1;
         }
-        if (warp == kLoadWarp) load();
         Step after = now;
         after.next(nt, qt_used);
-        if (after.h < c.H && after.t == 0) stage_head(after, sets[cb == 2 ? 0 : cb + 1], qs + (qb ^ 1) * A::Q_BYTES);
+        if (i + 1 < steps && after.t == 0) stage_head(after, sets[(cb + 1) % kSets], qs + (qb ^ 1) * A::Q_BYTES);
         if (i > 0) add_weights(i - 1, last, sets[cb_last]);
         last = now;
         now = after;
     }
     wait_or_fail(&s_bar, (steps - 1) & 1, fail);
     tmem_fence_after();
-    if (__syncthreads_or(fail)) {
+    if (csync_count(fail)) {
         if (tid == 0) {
             for (int s = 0; s < A::STAGES; ++s)
                 for (int ph = 0; ph < 2; ++ph) mbar_wait(&full[s], ph);
@@ -219,7 +238,7 @@ weights_kernel(const CacheView c, const AttnParams p, const int tiles)
         }
     } else {
         add_weights(steps - 1, last, sets[cb]);
-        __syncthreads();
+        csync();
         for (int t = half; t < nt; t += 2) {
             const int slot = step_slot<kTile>(w, i0 + t) + tok;
             const int page = slot < w.len ? page_of(c, w.b, slot) : -1;
@@ -228,7 +247,7 @@ weights_kernel(const CacheView c, const AttnParams p, const int tiles)
         }
     }
     tmem_fence_before();
-    __syncthreads();
+    csync();
     if (warp == 0) tmem_free(a_t, A::COLS);
 }
 
@@ -251,7 +270,7 @@ cudaError_t launch_one(const CacheView &c, const AttnParams &p, cudaStream_t s)
     const int tiles = (p.max_len + kTile - 1) / kTile;
     const int64_t per = (static_cast<int64_t>(c.B) * tiles + 152 * A::CTAS - 1) / (152 * A::CTAS);
     const int t = static_cast<int>(per < 1 ? 1 : (per > kMaxTiles ? kMaxTiles : per));
-    weights_kernel<T, D, NT><<<dim3((tiles + t - 1) / t, c.B), kAttnThreads, A::SMEM, s>>>(c, p, t);
+    weights_kernel<T, D, NT><<<dim3((tiles + t - 1) / t, c.B), kAttnThreads + 64, A::SMEM, s>>>(c, p, t);
     return cudaGetLastError();
 }
 
