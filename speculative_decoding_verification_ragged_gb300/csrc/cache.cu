@@ -429,10 +429,12 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const CacheVi
 }
 
 constexpr int kMoveThreads = 128;
+constexpr int kWord = 1 << 16, kBlock = 1 << 17, kNone = 1 << 18;
 
 // Move: one CTA per (destination block, kv head, request).  Keys go 16 bytes (32
 // channels) a thread.  A thread takes the values of a channel: 16 bytes of a
-// source block hold its 32 tokens there, read once for all the kept ones.
+// source block hold its 32 tokens there, read once for all the kept ones, which
+// are shifted out one by one.
 template <int D>
 __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const CacheView c, const EvictParams p)
 {
@@ -442,6 +444,7 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const CacheVie
     constexpr int G = D / 16;
     __shared__ const uint8_t *src[kTok];     // source block of each token
     __shared__ int tok[kTok];                // its place there, -1: none
+    __shared__ int step[kTok];               // how the values get to it (below)
     const int32_t *kept = p.kept + static_cast<int64_t>(b) * p.budget;
     const int dpage = p.dst_table[static_cast<int64_t>(b) * p.dst_pages + blk * kTok / c.page_tokens];
     uint8_t *dst = block_at(c, dpage, h, blk * kTok % c.page_tokens / kTok);
@@ -462,6 +465,13 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const CacheVie
                 pos = p.slot_pos ? p.slot_pos[at] : 0;
             }
         }
+        // shift of the token's code in its word, the word, and whether the word or
+        // the block is another than the token's before
+        __syncwarp();
+        const int t = tok[tid], last = tid ? tok[tid - 1] : -1;
+        const bool block = t >= 0 && (last < 0 || src[tid] != src[tid - 1]);
+        const bool word = block || (t >= 0 && t / 8 != last / 8);
+        step[tid] = t < 0 ? kNone : t % 8 * 4 | t / 8 << 8 | (word ? kWord : 0) | (block ? kBlock : 0);
         if (h == 0) {
             const int64_t at = static_cast<int64_t>(dpage) * c.page_tokens + i % c.page_tokens;
             p.score[at] = sc;
@@ -488,22 +498,20 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const CacheVie
         dst[v_scale_at(D) + i] = tok[u] >= 0 ? __ldg(src[u] + v_scale_at(D) + w * kTok + tok[u]) : 0;
     }
     for (int d = tid; d < D; d += kMoveThreads) {
-        uint32_t out[4];
-        const uint8_t *cur = nullptr;
+        uint32_t out[4], word = 0;
         uint4 v = none;
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
             uint32_t w = 0;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const int t = tok[8 * q + j];
-                if (t < 0) continue;                       // (uniform, as all of this)
-                if (src[8 * q + j] != cur) {
-                    cur = src[8 * q + j];
-                    v = __ldg(reinterpret_cast<const uint4 *>(cur + v_codes_at(D) + d * 16));
-                }
-                const uint32_t word = t < 16 ? (t < 8 ? v.x : v.y) : (t < 24 ? v.z : v.w);
-                w |= (word >> (t % 8 * 4) & 15u) << (4 * j);
+                const int st = step[8 * q + j];            // (uniform, as the branches)
+                if (st & kBlock)
+                    v = __ldg(reinterpret_cast<const uint4 *>(src[8 * q + j] + v_codes_at(D) + d * 16));
+                if (st & kWord) word = (st & 0x200) ? ((st & 0x100) ? v.w : v.z) : ((st & 0x100) ? v.y : v.x);
+                if (st & kNone) word = 0;
+                // the code enters at the top while the ones before move down
+                w = __funnelshift_r(w, word >> (st & 31), 4);
             }
             out[q] = w;
         }

@@ -183,6 +183,51 @@ def test_append_extremes_and_ties():
     np.testing.assert_array_equal(cache.pages.cpu().numpy(), c.pages)
 
 
+@pytest.mark.parametrize("exponent", [-42, -20, 0, 17, 40])
+def test_append_rounds_every_quotient_as_ieee(exponent):
+    """Two million values of one magnitude range, some a last place away from where
+    the code changes, with head scales over the whole range of fp32."""
+    sv = need_gpu()
+    rng = np.random.default_rng(exponent + 100)
+    n, H = 4096, 4
+    c = ref.Cache(np.zeros((n // 32, H, 1, 36 * 64), np.uint8), np.arange(n // 32, dtype=np.int32)[None],
+                  *[(rng.uniform(0.5, 2, H) * 10.0 ** np.array([0, -30, 25, -44])).astype(np.float32) for _ in range(2)])
+    xs = []
+    for g in c.g:
+        x = rng.standard_normal((n, H, 64)) * 2.0 ** rng.integers(-3, 4, (n, H, 64)) * 2.0 ** exponent
+        x = (x * g[:, None]).astype(np.float32)
+        # near the places where a code changes, for the scale that the block will have
+        s = quantised_scale(x, g)
+        edge = rng.choice(np.array([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0], np.float32), x.shape)
+        near = np.nextafter((edge * s).astype(np.float32), np.float32(rng.choice([-np.inf, np.inf])))
+        pick = (rng.random(x.shape) < 0.5) & (np.abs(near) < np.abs(x).reshape(n, H, 4, 16).max(-1).repeat(16, -1))
+        xs.append(np.where(pick, near, x).astype(np.float32))
+    cache = gpu_cache(sv, c)
+    sv.cache_append(cache, dev(xs[0]), dev(xs[1]), dev(np.array([0, n], np.int32)), dev(np.zeros(1, np.int32)), dev(c.table),
+                    B=1, max_rows=n)
+    got = cache.pages.cpu().numpy()
+    for h in range(H):
+        kc, ks = ref.quantise(xs[0][:, h], c.g[0][h])
+        vc, vs = ref.quantise(xs[1][:, h], c.g[1][h])
+        blk = got[:, h, 0]                                              # [blocks, 36 * 64]
+        k = blk[:, :1024].reshape(-1, 2, 32, 16).transpose(0, 2, 1, 3).reshape(n, 32)
+        np.testing.assert_array_equal(k, kc[:, 0::2] | kc[:, 1::2] << 4)
+        np.testing.assert_array_equal(blk[:, 1024:1152].reshape(n, 4), ks)
+        v = blk[:, 1152:2176].reshape(-1, 64, 16).transpose(0, 2, 1)
+        want = vc.reshape(-1, 32, 64)
+        np.testing.assert_array_equal(v, want[:, 0::2] | want[:, 1::2] << 4)
+        np.testing.assert_array_equal(blk[:, 2176:].reshape(-1, 4, 32).transpose(0, 2, 1).reshape(n, 4), vs)
+
+
+def quantised_scale(x, g):
+    """code scale * head scale of every value's block, as the definition takes it"""
+    out = np.zeros_like(x)
+    for h in range(x.shape[1]):
+        _, s = ref.quantise(x[:, h], g[h])
+        out[:, h] = (ref.E4M3[s].astype(np.float32) * g[h]).repeat(16, -1)
+    return out
+
+
 def test_append_strided_rows_scores_and_positions():
     """k and v as slices of one projection (unaligned heads), scores zeroed and positions written."""
     sv = need_gpu()
