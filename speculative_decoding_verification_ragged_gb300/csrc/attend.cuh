@@ -106,10 +106,10 @@ __device__ __forceinline__ Fetch ask_pages(const CacheView &c, const Job &w, int
 // Copy the first BYTES of a tile's 4 blocks into a stage (all of a block, or its
 // keys); a lane of one warp per block.  nv: the tokens of each block that exist (0
 // for a bad page: its bytes are not fetched, and what the stage holds there is
-// masked).
+// masked); pages, where it is asked for: their page ids.
 template <int BYTES>
 __device__ __forceinline__ void load_tile(const CacheView &c, const Fetch &f, uint8_t *stage, uint64_t *full, int *nv,
-                                          uint32_t *status)
+                                          uint32_t *status, int *pages = nullptr)
 {
     const int lane = threadIdx.x & 31;
     const int slot0 = f.slot + lane * kTok;
@@ -120,6 +120,7 @@ __device__ __forceinline__ void load_tile(const CacheView &c, const Fetch &f, ui
     }
     const uint32_t have = __ballot_sync(0xFFFFFFFFu, n > 0);
     if (lane < 4) nv[lane] = n;
+    if (pages && lane < 4) pages[lane] = f.page;
     __syncwarp();
     if (lane == 0) mbar_arrive_expect_tx(full, __popc(have) * BYTES);
     __syncwarp();

@@ -493,7 +493,7 @@ attend_kernel(const CacheView c, const AttnParams p, const Layout lay)
     // or kEnd; with weights, whether they are those of a wide tile
     constexpr int kFirst = 1, kLast = 2, kEnd = 4;
     __shared__ int keys_are, weights_wide;
-    __shared__ __align__(16) int nv[A::STAGES][4];
+    __shared__ __align__(16) int nv[A::STAGES][4], pages[A::STAGES][4];
     const int tid = threadIdx.x, warp = warp_index(), lane = tid & 31;
     const int group = p.Hq / c.H;
 
@@ -556,7 +556,8 @@ attend_kernel(const CacheView c, const AttnParams p, const Layout lay)
         ask_next();
         while (any && !fail) {
             wait_or_fail(&empty[ring], phase, fail);
-            load_tile<block_bytes(D)>(c, next, stages + ring * A::STAGE, &full[ring], nv[ring], p.status);
+            load_tile<block_bytes(D)>(c, next, stages + ring * A::STAGE, &full[ring], nv[ring], p.status,
+                                      OPT ? pages[ring] : nullptr);
             if (++ring == A::STAGES) {
                 ring = 0;
                 phase ^= 1;
@@ -621,9 +622,16 @@ attend_kernel(const CacheView c, const AttnParams p, const Layout lay)
             }
         }
     };
-    // the keys of the tile in stage `st` (in phase `phase` of the ring)
-    const auto keys = [&](int st, uint32_t phase, int what) {
+    int pos = 0;                                      // of this thread's token of the tile whose keys came last
+    // the keys of the tile in stage `st` (in phase `phase` of the ring), first slot `slot0`
+    const auto keys = [&](int st, uint32_t phase, int slot0, int what) {
         wait_or_fail(&full[st], phase, fail);
+        if (OPT) {
+            pos = slot0 + tok;
+            // (asked for here, a tile ahead of its use)
+            if (p.slot_pos && lane < nv[st][quarter])
+                pos = __ldg(p.slot_pos + static_cast<int64_t>(pages[st][quarter]) * c.page_tokens + pos % c.page_tokens);
+        }
         decode_keys<D>(stages + st * A::STAGE + quarter * block_bytes(D), a_t + lane_off);
         if (tid == 0) keys_are = what;
         tmem_wait_st();
@@ -660,7 +668,7 @@ attend_kernel(const CacheView c, const AttnParams p, const Layout lay)
 #pragma unroll
         for (int i = 0; i < OR; ++i) acc[i] = 0.f;
         const int own_first = cs.own[0];
-        if (n > 0) keys(ring, ring_phase, kFirst | (n == 1 ? kLast : 0));
+        if (n > 0) keys(ring, ring_phase, step_slot<kTile>(w, seg.first), kFirst | (n == 1 ? kLast : 0));
         for (int k = 0; k < n; ++k) {
             const uint8_t *stage = stages + ring * A::STAGE;
             uint32_t *vsk = vs + buf * (A::VS_BYTES / 4);
@@ -668,10 +676,10 @@ attend_kernel(const CacheView c, const AttnParams p, const Layout lay)
             Token t;
             const int4 n4 = *reinterpret_cast<const int4 *>(nv[ring]);
             const bool whole = (n4.x & n4.y & n4.z & n4.w) == kTok;      // (each at most 32)
-            t.slot = t.pos = slot0 + tok;
+            t.slot = slot0 + tok;
+            t.pos = pos;
             t.live = whole || lane < nv[ring][quarter];
             t.edge = !whole || slot0 + kTile - 1 > own_first;
-            if (OPT && p.slot_pos && t.live) t.pos = slot_position(c, p, w.b, t.slot);
             value_scales<D>(stage, nv[ring], whole, vsk);
             uint64_t *const done = &empty[ring];
             if (++ring == A::STAGES) {
@@ -731,7 +739,7 @@ attend_kernel(const CacheView c, const AttnParams p, const Layout lay)
                 }
             }
             // S^T is read, the keys' columns are free: on to the next tile's keys
-            if (k + 1 < n) keys(ring, ring_phase, k + 2 == n ? kLast : 0);
+            if (k + 1 < n) keys(ring, ring_phase, step_slot<kTile>(w, seg.first + k + 1), k + 2 == n ? kLast : 0);
             if (pending) finish_values();             // V^T's columns and P are free
             // weights: sums in fp32, the operand 8 columns of this token per store
 #pragma unroll

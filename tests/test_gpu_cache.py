@@ -621,6 +621,16 @@ def test_evict_skips_bad_requests():
 
 # ---------------------------------------------------------------- together ---
 
+def test_the_example_runs_and_repeats_itself():
+    """examples/cached_step.py: the same tokens twice, and caches within budget."""
+    need_gpu()
+    from examples import cached_step
+    out, lens = cached_step.run(steps=30)
+    again, lens2 = cached_step.run(steps=30)
+    assert out == again and lens == lens2
+    assert all(n <= 320 + 5 for n in lens) and any(len(t) > 320 for t in out)
+
+
 def test_a_serving_loop():
     """Prompt, verify steps with rejected rows, weights, eviction, more steps:
     the cache's values and the last step's attention against the definition."""
