@@ -2,7 +2,7 @@
 // (cache_weights.cu) share: the tiles a request's rows see, their way into
 // shared and tensor memory, the queries as an operand, the scores.
 //
-// A CTA has 8 warps.  Tensor memory is reached by quarter: warps w and w + 4
+// 8 warps of a CTA decode.  Tensor memory is reached by quarter: warps w and w + 4
 // hold lanes 32 (w % 4) ..., so the two share a quarter's tokens (or channels)
 // and split the columns -- of K, of the scores, of the results -- in halves.
 #pragma once

@@ -9,6 +9,11 @@
 // runs while the weights of the step before are summed and the next head's queries
 // are staged; warp 8 issues the products, warp 9 fetches, and the eight warps that
 // decode and sum meet them, and each other, at mbarriers only.
+//
+// Bound by the latency of a step: 64 requests of 2 to 5 rows and 40 query heads over
+// up to 4096 tokens, ragged, take 66 us (1.2 TB/s of keys and scores), 128 x 5 rows x
+// 4096 tokens 147 us (2.1 TB/s).  With a barrier a step and fetches and products by
+// the decoding warps those were 109 and 237 us.
 #include "attend.cuh"
 
 namespace specv {
