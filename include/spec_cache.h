@@ -118,7 +118,8 @@ typedef struct {
 
 /* Workspace of spec_cache_attend, zero-filled once before its first use; any
  * number of stream-ordered calls, of any shapes that it is large enough for, can
- * then share it.  0 for invalid sizes. */
+ * then share it (after SPEC_STATUS_TIMEOUT it has to be zeroed again).  0 for
+ * invalid sizes. */
 SPEC_API size_t spec_cache_workspace_bytes(int32_t B, int32_t k_max, int32_t Hq, int32_t H,
                                            int32_t D, int32_t max_len);
 
@@ -131,7 +132,9 @@ SPEC_API size_t spec_cache_workspace_bytes(int32_t B, int32_t k_max, int32_t Hq,
  * a bad length) gets out = 0 and lse = -inf.  Slots that no row of the
  * request sees are not read, whatever their bytes.  out [R_cap, Hq, D], lse
  * [R_cap, Hq] or NULL, both contiguous; rows >= cu_rows[B] are not written.
- * Results do not depend on the order in which blocks run.  One launch.  bf16
+ * Results do not depend on the order in which blocks run.  A query row with a
+ * NaN or infinite value gets unspecified results, as can the request's other rows
+ * of the same kv head; every other row its own.  One launch.  bf16
  * outputs come from weights rounded to 11 bits, fp32 ones from 22 bits; sums of
  * weights, and so lse, are fp32.
  */

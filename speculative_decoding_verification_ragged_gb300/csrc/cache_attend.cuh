@@ -45,6 +45,7 @@ namespace {
 
 constexpr float kUnset = -1e30f;           // reference of a column that has seen nothing yet
 constexpr float kHeadroom = 11.f;          // P = 2^(x + 11) ...
+constexpr int kMostMoves = 4;              // of the references for one tile
 constexpr uint32_t kMostBits = 0x7800u;    // ... stays below 2^15 (f16 bits)
 // V decoded to bf16 keeps f16's exponent bits, which stand for 2^-112 of the
 // value there; the weights carry the 2^112
@@ -735,10 +736,12 @@ attend_kernel(const CacheView c, const AttnParams p, const Layout lay)
                 }
                 return unfit;
             };
-            // (a segment's first tile sets the references, whatever it holds)
+            // (a segment's first tile sets the references, whatever it holds; three moves
+            // are the most that numbers need, so that NaN or infinite ones end as well)
             bool wide = false, move = k == 0;
-            for (;;) {
+            for (int turn = 0;; ++turn) {
                 const int unfit = weigh();
+                if (turn == kMostMoves) break;
                 if (!move) {
                     if (!csync_count(unfit)) break;
                     wide = !csync_count(unfit & 1);

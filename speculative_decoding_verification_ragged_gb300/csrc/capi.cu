@@ -227,6 +227,9 @@ int check_attention(const spec_cache *cache, const spec_attention *a, CacheView 
     const int64_t room = static_cast<int64_t>(c.max_pages) * c.page_tokens;
     if (a->max_len < 0 || a->max_len > room) return SPEC_ERR_INVALID_ARG;
     if (reinterpret_cast<uintptr_t>(a->q) % elt_bytes(a->dtype)) return SPEC_ERR_INVALID_ARG;
+    // the work's units and their multiples stay far below 2^63
+    const double units = static_cast<double>(c.B) * a->Hq * (a->k_max + 1) * (room / 128 + 16);
+    if (units > 1e15) return SPEC_ERR_UNSUPPORTED;
     std::memset(&p, 0, sizeof p);
     p.q = a->q;
     p.q_row = a->q_row;

@@ -503,6 +503,27 @@ def test_attention_is_deterministic_and_reuses_its_workspace():
     assert all(torch.equal(first[k], got[k]) for k in first)
 
 
+@pytest.mark.parametrize("kw", [dict(), dict(cap=20.0, window=300, prefix=2)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_attention_with_nan_and_infinite_queries_ends(dtype, kw):
+    """The call returns, without a timeout, and the other requests keep their results."""
+    sv = need_gpu()
+    rng = np.random.default_rng(17)
+    lens, cu = [700, 300, 129, 2000], np.array([0, 2, 4, 6, 8])
+    c = quick_pool(rng, B=4, H=2, D=128, page=64, lens=lens)
+    q = queries(rng, 8, 8, 128, dtype)
+    clean, _, status = run_attention(sv, c, q, cu, lens, 1, **kw)
+    assert status == 0
+    for poison in (float("nan"), float("inf"), -float("inf")):
+        bad = q.clone()
+        bad[2, 1, 5] = poison
+        bad[7] = poison
+        got, _, status = run_attention(sv, c, bad, cu, lens, 1, **kw)
+        assert status == 0
+        for r in (0, 1, 4, 5):
+            assert torch.equal(got["out"][r], clean["out"][r]) and torch.equal(got["lse"][r], clean["lse"][r])
+
+
 def test_attention_strided_queries():
     """q as a slice of a fused projection, at an odd element offset."""
     sv = need_gpu()
