@@ -75,8 +75,7 @@ __device__ __forceinline__ float2 h2_float2(uint32_t h2)
     return __half22float2(*reinterpret_cast<const __half2 *>(&h2));
 }
 
-// one code (low nibble of c) and one scale byte as floats
-__device__ __forceinline__ float e2m1_value(uint32_t c) { return h2_float2(e2m1x2(c & 15u)).x; }
+// one scale byte as a float
 __device__ __forceinline__ float e4m3_value(uint32_t s) { return h2_float2(e4m3x2(s & 255u)).x; }
 
 template <typename T> __device__ __forceinline__ float to_f32(T x);

@@ -34,7 +34,8 @@
 // requests of 2 to 5 rows over up to 4096 tokens, ragged, 136 us (2.3 TB/s).  Two CTAs
 // an SM are what tensor memory holds (256 columns each); three operands of a tile in
 // columns of their own (K, V^T, S) let each product run while the other operand is
-// decoded (one buffer for K and V^T: 109 us against 78 over 32 x 5 rows x 4096).
+// decoded (128 x 5 rows x 4096: 298 us, and 335 with one buffer for K and V^T, at
+// the step that parted them).
 #pragma once
 
 #include "attend.cuh"

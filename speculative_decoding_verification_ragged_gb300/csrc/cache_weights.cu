@@ -13,7 +13,8 @@
 // Bound by the latency of a step: 64 requests of 2 to 5 rows and 40 query heads over
 // up to 4096 tokens, ragged, take 66 us (1.2 TB/s of keys and scores), 128 x 5 rows x
 // 4096 tokens 147 us (2.1 TB/s).  With a barrier a step and fetches and products by
-// the decoding warps those were 109 and 237 us.
+// the decoding warps those were 109 and 237 us (84 and 174 without, all CTAs in one
+// round; two rounds, which even out ragged requests, made the rest).
 #include "attend.cuh"
 
 namespace specv {
