@@ -30,8 +30,8 @@
 // Bound by instruction issue and the latency of a tile's chain (scores, weights,
 // values), not by HBM: a tile's 32 Ki codes are converted and stored to tensor
 // memory against 18 KB fetched.  Four single tokens over 131071 tokens each (32 / 8
-// heads of 128) take 162 us, 3.7 TB/s of cache, 55 % of the measured copy rate; 128
-// requests of 2 to 5 rows over up to 4096 tokens, ragged, 136 us (2.3 TB/s).  Two CTAs
+// heads of 128) take 163 us, 3.7 TB/s of cache, 55 % of the measured copy rate; 128
+// requests of 2 to 5 rows over up to 4096 tokens, ragged, 139 us (2.2 TB/s).  Two CTAs
 // an SM are what tensor memory holds (256 columns each); three operands of a tile in
 // columns of their own (K, V^T, S) let each product run while the other operand is
 // decoded (128 x 5 rows x 4096: 298 us, and 335 with one buffer for K and V^T, at
@@ -740,14 +740,14 @@ attend_kernel(const CacheView c, const AttnParams p, const Layout lay)
             // (a segment's first tile sets the references, whatever it holds; three moves
             // are the most that numbers need, so that NaN or infinite ones end as well)
             bool wide = false, move = k == 0;
-            for (int turn = 0;; ++turn) {
+            for (int moves = 0;; ++moves) {
                 const int unfit = weigh();
-                if (turn == kMostMoves) break;
                 if (!move) {
                     if (!csync_count(unfit)) break;
                     wide = !csync_count(unfit & 1);
                     if (wide) break;
                 }
+                if (moves == kMostMoves) break;
                 move = move_references<A>(w, cs, x);
                 if (k == 0) continue;
                 if (pending) finish_values();
