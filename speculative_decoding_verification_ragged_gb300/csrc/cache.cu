@@ -243,7 +243,7 @@ constexpr int kSelThreads = 1024;
 constexpr int kSelCtas = 8;                // CTAs of a request's cluster at most
 constexpr int kBins = 2048;                // a radix digit: 11 bits (the last: 10)
 constexpr int kSelStaged = 40 * 1024;      // scores a CTA keeps in shared memory
-constexpr int kRun = 16;                   // a thread's slots are a multiple of this
+constexpr int kRun = 16;                   // a warp's blocks of 32 slots are a multiple of this
 
 // slots of a CTA's slice where a cluster of `ctas` shares `len`
 __host__ __device__ inline int64_t sel_slice(int64_t len, int ctas)
@@ -284,18 +284,18 @@ __device__ __forceinline__ int cta_scan(int v, int *warp_sum, int &total)
 // in all), each with a contiguous part of the slots, its keys in shared memory
 // (read again from the cache's scores where they do not fit).  A radix search, 11
 // bits a pass over the cluster's summed histograms, finds the key of the last score
-// kept; then a thread lists the kept slots of a contiguous run of its own: those
-// above the key, the first few at it, and the newest.  2 x 131072 scores: 39 us; 32 x
-// 4096: 19 us (a cluster of 8 for each: 41).
+// kept; then a warp lists the kept slots of a contiguous run of its own by ballots:
+// those above the key, the first few at it, and the newest.  2 x 131072 scores: 39 us;
+// 32 x 4096: 19 us (a cluster of 8 for each: 41).
 __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const CacheView c, const EvictParams p)
 {
     namespace cg = cooperative_groups;
     cg::cluster_group cluster = cg::this_cluster();
     extern __shared__ __align__(16) uint8_t smem_raw[];
     uint32_t *keys = reinterpret_cast<uint32_t *>(smem_raw);
-    __shared__ int hist[kBins], warp_sum[kSelThreads / 32], pick[2], count[2];
+    __shared__ int hist[kBins], warp_sum[kSelThreads / 32], warp_over[kSelThreads / 32], pick[2], count[2];
     const int ctas = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
-    const int b = blockIdx.x / ctas, tid = threadIdx.x;
+    const int b = blockIdx.x / ctas, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int len = p.len[b];
     int32_t *kept = p.kept + static_cast<int64_t>(b) * p.budget;
     const int64_t room = static_cast<int64_t>(c.max_pages) * c.page_tokens;
@@ -330,102 +330,131 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const CacheVi
 
     const int old = len - p.recent;          // slots that compete for `want` places
     int want = p.budget - p.recent;
-    const int slice = static_cast<int>(sel_slice(len, ctas)), run = slice / kSelThreads;   // a run per thread
+    const int slice = static_cast<int>(sel_slice(len, ctas)), run = slice / kSelThreads * 32;   // a run per warp
     const int64_t first = static_cast<int64_t>(rank) * slice;
     const bool staged = slice <= kSelStaged;
-    // keys are padded by one in 16, so that runs of 16 start in different banks;
-    // slots that do not compete have key 0
-    const auto place = [](int i) { return i + i / kRun; };
-    const auto fetch = [&](int i) {
-        const int64_t slot = first + i;
-        if (slot >= old) return 0u;
-        const int s = static_cast<int>(slot);
-        const int64_t page = __ldg(c.page_table + static_cast<int64_t>(b) * c.max_pages + s / c.page_tokens);
-        return score_key(p.score[page * c.page_tokens + s % c.page_tokens]);
+    // where the scores of a slot of this slice lie (one that competes)
+    const auto score_at = [&](int i) {
+        const int s = static_cast<int>(first) + i, page = s / c.page_tokens;
+        const int64_t id = __ldg(c.page_table + static_cast<int64_t>(b) * c.max_pages + page);
+        return id * c.page_tokens + (s - page * c.page_tokens);
     };
     const int mine = first >= old ? 0 : static_cast<int>(min(static_cast<int64_t>(slice), old - first));
     if (staged) {
-        // 16 loads of a thread in flight
-        for (int i0 = tid; i0 < mine; i0 += kSelThreads * kRun) {
-            uint32_t k[kRun];
+        // a warp's loads are blocks of 32 slots, 16 in flight: lane u looks up the
+        // page of the u-th (a block lies within a page; for one past the end, the
+        // first block of the cache is loaded and not looked at)
+        for (int i0 = 0; i0 < mine; i0 += kSelThreads * kRun) {
+            const int i = i0 + warp * 32, look = i + lane % kRun * kSelThreads;
+            const int64_t at = look < mine ? score_at(look) : 0;
+            float x[kRun];            // (no condition: a warp does not wait for one load at a time)
 #pragma unroll
-            for (int u = 0; u < kRun; ++u) k[u] = i0 + u * kSelThreads < mine ? fetch(i0 + u * kSelThreads) : 0u;
+            for (int u = 0; u < kRun; ++u) x[u] = p.score[__shfl_sync(0xFFFFFFFFu, at, u) + lane];
 #pragma unroll
             for (int u = 0; u < kRun; ++u)
-                if (i0 + u * kSelThreads < mine) keys[place(i0 + u * kSelThreads)] = k[u];
+                if (i + u * kSelThreads + lane < mine) keys[i + u * kSelThreads + lane] = score_key(x[u]);
         }
     }
-    const auto key_at = [&](int i) { return staged ? keys[place(i)] : fetch(i); };
-    uint32_t key = 0u;
-    const bool any = want > 0;
-    for (int pass = 0; pass < 3 && any; ++pass) {
-        const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0), bins = pass == 2 ? 1024 : kBins;
-        for (int i = tid; i < kBins; i += kSelThreads) hist[i] = 0;
+    // (a body for each of the two, so that no look-up is in the loops over keys[])
+    const auto select = [&](auto key_at) {
+        uint32_t key = 0u;
+        const bool any = want > 0;
+        for (int pass = 0; pass < 3 && any; ++pass) {
+            const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0), bins = pass == 2 ? 1024 : kBins;
+            for (int i = tid; i < kBins; i += kSelThreads) hist[i] = 0;
+            __syncthreads();
+            for (int i = tid; i < mine; i += kSelThreads) {
+                const uint32_t k = key_at(i);
+                if (pass == 0 || (k >> (pass == 1 ? 21 : 10)) == (key >> (pass == 1 ? 21 : 10)))
+                    atomicAdd(&hist[(k >> shift) & (bins - 1)], 1);
+            }
+            cluster.sync();
+            // bins from the top, two a thread, summed over the cluster
+            int two[2] = {0, 0};
+            const int at = bins - 2 - 2 * tid;
+    #pragma unroll
+            for (int r = 0; r < kSelCtas; ++r) {
+                if (r < ctas && at >= 0) {
+                    const int *h = cluster.map_shared_rank(hist, r);
+                    const int2 x = *reinterpret_cast<const int2 *>(h + at);
+                    two[0] += x.y;
+                    two[1] += x.x;
+                }
+            }
+            int total;
+            int above = cta_scan(two[0] + two[1], warp_sum, total);
+    #pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                if (above < want && above + two[u] >= want) {
+                    pick[0] = bins - 1 - 2 * tid - u;
+                    pick[1] = want - above;
+                }
+                above += two[u];
+            }
+            cluster.sync();                       // (also the CTA's barrier for `pick`)
+            key |= static_cast<uint32_t>(pick[0]) << shift;
+            want = pick[1];
+            __syncthreads();
+        }
+        // `want` of the slots whose key equals `key` are kept, the lowest ones: count
+        // ties and slots above the key in this warp's run, then in the warps and the
+        // CTAs before
+        const int r0 = min(warp * run, mine), r1 = any ? min(r0 + run, mine) : r0;
+        int ties = 0, over = 0;
+    #pragma unroll 4
+        for (int i = r0; i < r1; i += 32) {
+            const bool real = i + lane < r1;
+            const uint32_t k = real ? key_at(i + lane) : 0u;
+            ties += __popc(__ballot_sync(0xFFFFFFFFu, real && k == key));
+            over += __popc(__ballot_sync(0xFFFFFFFFu, k > key));
+        }
+        if (lane == 0) {
+            warp_sum[warp] = ties;
+            warp_over[warp] = over;
+        }
         __syncthreads();
-        for (int i = tid; i < mine; i += kSelThreads) {
-            const uint32_t k = key_at(i);
-            if (pass == 0 || (k >> (pass == 1 ? 21 : 10)) == (key >> (pass == 1 ? 21 : 10)))
-                atomicAdd(&hist[(k >> shift) & (bins - 1)], 1);
+        int n_ties = warp_sum[lane], n_over = warp_over[lane];
+    #pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int t = __shfl_up_sync(0xFFFFFFFFu, n_ties, o), v = __shfl_up_sync(0xFFFFFFFFu, n_over, o);
+            if (lane >= o) {
+                n_ties += t;
+                n_over += v;
+            }
+        }
+        int tie_rank = __shfl_sync(0xFFFFFFFFu, n_ties, warp) - ties;
+        int over_rank = __shfl_sync(0xFFFFFFFFu, n_over, warp) - over;
+        n_ties = __shfl_sync(0xFFFFFFFFu, n_ties, 31);
+        n_over = __shfl_sync(0xFFFFFFFFu, n_over, 31);
+        if (tid == 0) {
+            count[0] = n_ties;
+            count[1] = n_over;
         }
         cluster.sync();
-        // bins from the top, two a thread, summed over the cluster
-        int two[2] = {0, 0};
-        for (int r = 0; r < ctas; ++r) {
-            const int *h = cluster.map_shared_rank(hist, r);
-            const int at = bins - 2 - 2 * tid;
-            if (at >= 0) {
-                const int2 x = *reinterpret_cast<const int2 *>(h + at);
-                two[0] += x.y;
-                two[1] += x.x;
-            }
+        for (int r = 0; r < rank; ++r) {
+            const int *cnt = cluster.map_shared_rank(count, r);
+            tie_rank += cnt[0];
+            over_rank += cnt[1];
         }
-        int total;
-        int above = cta_scan(two[0] + two[1], warp_sum, total);
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            if (above < want && above + two[u] >= want) {
-                pick[0] = bins - 1 - 2 * tid - u;
-                pick[1] = want - above;
-            }
-            above += two[u];
+        cluster.sync();                           // no CTA leaves while its counts are read
+        int at = over_rank + min(tie_rank, want);
+        const uint32_t below = (1u << lane) - 1u;
+    #pragma unroll 4
+        for (int i = r0; i < r1; i += 32) {
+            const bool real = i + lane < r1;
+            const uint32_t k = real ? key_at(i + lane) : 0u;
+            const uint32_t tie = __ballot_sync(0xFFFFFFFFu, real && k == key);
+            const bool stays = k > key || ((tie >> lane & 1u) && tie_rank + __popc(tie & below) < want);
+            const uint32_t stay = __ballot_sync(0xFFFFFFFFu, stays);
+            if (stays) kept[at + __popc(stay & below)] = static_cast<int>(first) + i + lane;
+            at += __popc(stay);
+            tie_rank += __popc(tie);
         }
-        cluster.sync();                       // (also the CTA's barrier for `pick`)
-        key |= static_cast<uint32_t>(pick[0]) << shift;
-        want = pick[1];
-        __syncthreads();
-    }
-    // `want` of the slots whose key equals `key` are kept, the lowest ones: count
-    // ties and slots above the key in this thread's run, then in the CTAs before
-    const int r0 = tid * run;
-    int ties = 0, over = 0;
-    if (any)
-        for (int i = r0; i < min(r0 + run, mine); ++i) {
-            const uint32_t k = key_at(i);
-            ties += k == key;
-            over += k > key;
-        }
-    int n_ties, n_over;
-    int tie_rank = cta_scan(ties, warp_sum, n_ties);
-    int over_rank = cta_scan(over, warp_sum, n_over);
-    if (tid == 0) {
-        count[0] = n_ties;
-        count[1] = n_over;
-    }
-    cluster.sync();
-    for (int r = 0; r < rank; ++r) {
-        const int *cnt = cluster.map_shared_rank(count, r);
-        tie_rank += cnt[0];
-        over_rank += cnt[1];
-    }
-    cluster.sync();                           // no CTA leaves while its counts are read
-    int at = over_rank + min(tie_rank, want);
-    if (any)
-        for (int i = r0; i < min(r0 + run, mine); ++i) {
-            const uint32_t k = key_at(i);
-            const bool tie = k == key;
-            if (k > key || (tie && tie_rank < want)) kept[at++] = static_cast<int>(first) + i;
-            tie_rank += tie;
-        }
+    };
+    if (staged)
+        select([&](int i) { return keys[i]; });
+    else
+        select([&](int i) { return score_key(p.score[score_at(i)]); });
     for (int i = me; i < p.recent; i += all) kept[keep - p.recent + i] = old + i;
 }
 
@@ -558,7 +587,7 @@ cudaError_t launch_cache_evict(const CacheView &c, const EvictParams &p, cudaStr
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     if (!done[dev]) {
         e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (kSelStaged + kSelStaged / kRun) * 4);
+                                 kSelStaged * 4);
         if (e != cudaSuccess) return e;
         done[dev] = true;
     }
@@ -575,7 +604,7 @@ cudaError_t launch_cache_evict(const CacheView &c, const EvictParams &p, cudaStr
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(c.B * ctas, 1, 1);
     cfg.blockDim = dim3(kSelThreads, 1, 1);
-    cfg.dynamicSmemBytes = static_cast<size_t>(slice + slice / kRun) * 4;
+    cfg.dynamicSmemBytes = static_cast<size_t>(slice) * 4;
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
