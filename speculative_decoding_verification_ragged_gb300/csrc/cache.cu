@@ -285,8 +285,9 @@ __device__ __forceinline__ int cta_scan(int v, int *warp_sum, int &total)
 // (read again from the cache's scores where they do not fit).  A radix search, 11
 // bits a pass over the cluster's summed histograms, finds the key of the last score
 // kept; then a warp lists the kept slots of a contiguous run of its own by ballots:
-// those above the key, the first few at it, and the newest.  2 x 131072 scores: 39 us;
-// 32 x 4096: 19 us (a cluster of 8 for each: 41).
+// those above the key, the first few at it, and the newest.  2 x 131072 scores: 25 us
+// (39 with a page looked up and a load waited for slot by slot, and a run a thread);
+// 32 x 4096: 16 us (a cluster of 8 for each, at that step: 41).
 __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const CacheView c, const EvictParams p)
 {
     namespace cg = cooperative_groups;
