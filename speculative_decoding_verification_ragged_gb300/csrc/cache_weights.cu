@@ -22,6 +22,7 @@ namespace specv {
 namespace {
 
 constexpr int kMaxTiles = 8;               // tiles of a CTA at most
+constexpr int kFew = 8;                    // requests whose lengths are taken as max_len
 
 template <typename T, int D_, int NT_> struct Weights {
     static constexpr int D = D_, NT = NT_, NH = NT / 2;
@@ -271,13 +272,28 @@ cudaError_t launch_one(const CacheView &c, const AttnParams &p, cudaStream_t s)
         if (e != cudaSuccess) return e;
         done[dev] = true;
     }
-    // tiles a CTA: two rounds of resident CTAs.  (Fewer stage a head's queries for
-    // more tiles, more even out ragged requests: with 1, 2, 3 and 5 rounds 64 requests
-    // x 5 rows, ragged up to 4096 tokens, took 84, 66, 81 and 92 us; 128 of 4096 tokens
-    // 174, 147, 175 and 193; 2 x 65533 tokens of 16 heads 70, 81, 85 and 85.)
+    // tiles a CTA: two rounds of resident CTAs where there are many requests, whose
+    // lengths differ.  (Fewer stage a head's queries for more tiles, more even out the
+    // lengths: with 1, 2, 3 and 5 rounds 64 requests x 5 rows, ragged up to 4096 tokens,
+    // took 84, 66, 81 and 92 us.)  A few requests are taken to be as long as max_len: the
+    // fewest rounds, each of them a CTA's tiles and two tiles' time for the queries.  (4
+    // requests x 5 rows x 16000 tokens 39 us against 56 in two rounds, 42 against 40 where
+    // they are ragged; 8 x 16000 55 against 65, ragged 53 against 51; 16 x 8000 63
+    // against 66, ragged 56 against 53.)
     const int tiles = (p.max_len + kTile - 1) / kTile, slots = 152 * A::CTAS * 2;
     const int64_t per = (static_cast<int64_t>(c.B) * tiles + slots - 1) / slots;
-    const int t = static_cast<int>(per < 1 ? 1 : (per > kMaxTiles ? kMaxTiles : per));
+    int t = static_cast<int>(per < 1 ? 1 : (per > kMaxTiles ? kMaxTiles : per));
+    if (c.B <= kFew) {
+        int64_t least = INT64_MAX;
+        for (int i = 1; i <= kMaxTiles; ++i) {
+            const int64_t ctas = static_cast<int64_t>(c.B) * ((tiles + i - 1) / i);
+            const int64_t cost = (2 * ctas + slots - 1) / slots * (i + 2);
+            if (cost < least) {
+                least = cost;
+                t = i;
+            }
+        }
+    }
     weights_kernel<T, D, NT><<<dim3((tiles + t - 1) / t, c.B), kAttnThreads + 64, A::SMEM, s>>>(c, p, t);
     return cudaGetLastError();
 }
