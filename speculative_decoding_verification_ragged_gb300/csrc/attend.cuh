@@ -309,14 +309,20 @@ __device__ __forceinline__ void load_products(uint32_t addr, float (&v)[N])
 }
 
 // cap * tanh(s / cap), s and the result in units of `unit` (1 or log2 e).  EXACT
-// (fp32 results): the library's tanh.  Else 1 - 2 / (1 + e^2z), within 2^-21 of
-// cap absolute.
+// (fp32 results): the library's tanh.  Else (e^2z - 1) / (e^2z + 1), and below 1/2,
+// where that cancels, Lambert's continued fraction to its fifth term (9e-11 off):
+// within 2^-20 of the result, relative, so that small scores under a large cap keep
+// the log-sum-exp's digits; one approximate quotient for the two.
 template <bool EXACT>
 __device__ __forceinline__ float cap_score(float y, float cap, float rcap)
 {
-    if (EXACT) return cap * tanhf(y * rcap);
-    const float t = 1.f + ex2(fminf(2.f * kLog2e * rcap * y, 126.f));
-    return cap - __fdividef(2.f * cap, t);
+    const float z = y * rcap;
+    if (EXACT) return cap * tanhf(z);
+    const float t = ex2(fminf(2.f * kLog2e * z, 60.f)), zz = z * z;
+    const bool small = fabsf(z) < 0.5f;
+    const float num = small ? z * fmaf(zz, zz + 105.f, 945.f) : t - 1.f;
+    const float den = small ? fmaf(zz, fmaf(zz, 15.f, 420.f), 945.f) : t + 1.f;
+    return cap * __fdividef(num, den);
 }
 
 // Columns of a column tile: the fewest of 16, 32, 64 that hold a request's

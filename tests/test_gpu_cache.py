@@ -503,6 +503,24 @@ def test_attention_is_deterministic_and_reuses_its_workspace():
     assert all(torch.equal(first[k], got[k]) for k in first)
 
 
+@pytest.mark.parametrize("gain", [0.01, 0.1, 1.0])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_attention_small_scores_under_a_large_cap(dtype, gain):
+    """The cap's error is relative to the score (2^-20 of it), not to the cap."""
+    sv = need_gpu()
+    rng = np.random.default_rng(23)
+    lens, cu = [700, 33, 129, 1], np.array([0, 2, 4, 6, 7])
+    c = quick_pool(rng, B=4, H=2, D=128, page=64, lens=lens)
+    q = queries(rng, 7, 8, 128, dtype, gain)
+    kw = dict(cap=500.0, scale=0.01)
+    res, _, status = run_attention(sv, c, q, cu, lens, 1, **kw)
+    assert status == 0
+    _, lse, _, S, _ = ref.attention(c, q.float().cpu().numpy(), cu, lens, **kw)
+    u = 2.0 ** -24
+    tol = (c.D * 2 * u + 4 * u + 2.0 ** -20) * S + 4 * u * np.abs(lse) + 2.0 ** -19
+    assert (np.abs(res["lse"].cpu().numpy().astype(np.float64) - lse) <= tol).all()
+
+
 @pytest.mark.parametrize("kw", [dict(), dict(cap=20.0, window=300, prefix=2)])
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_attention_with_nan_and_infinite_queries_ends(dtype, kw):
