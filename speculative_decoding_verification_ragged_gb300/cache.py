@@ -4,7 +4,9 @@ attend, weights, evict.
 Argument marshalling only, like binding.py.  Every function takes
 `prepared=True` to return a CacheCall instead of running: its arguments are
 marshalled once, each call launches on the then-current stream and returns the
-same result tensors, so a serving loop pays one ctypes call per launch.
+same result tensors, so a serving loop pays one ctypes call per launch.  `stream`
+runs a call on another stream than the current one: its inputs have to be ready
+there, and the caller waits for that stream before it uses the results elsewhere.
 """
 from __future__ import annotations
 
@@ -89,24 +91,72 @@ def new_cache(n_pages: int, H: int, D: int, page_tokens: int = 64, device=None, 
     return PagedCache(pages, k_scale, v_scale)
 
 
+def _tensors(x):
+    """The tensors of a call's arguments and results, wherever they are kept."""
+    if isinstance(x, torch.Tensor):
+        yield x
+    elif isinstance(x, PagedCache):
+        yield from _tensors((x.pages, x.k_scale, x.v_scale))
+    elif isinstance(x, (tuple, dict)):
+        for y in (x.values() if isinstance(x, dict) else x):
+            yield from _tensors(y)
+
+
 class CacheCall:
     """A library call with its arguments marshalled: calling it launches on the
-    current stream and returns its results.  Keeps its tensors alive."""
+    current stream (or `stream`) and returns its results.  Keeps its tensors alive.
 
-    def __init__(self, fn, args, result, keep, device):
+    Its results, and a workspace that it made itself, belong to the stream that it
+    was prepared for.  The first call on another stream waits for that workspace's
+    zeros, and from then on no memory of the call is given away before that stream is
+    through with it.  (Inputs have to be ready on the stream of the call, as for any
+    launch; a call that a graph captures is ordered by whoever replays it.)"""
+
+    def __init__(self, fn, args, result, keep, device, known, ready):
         self._fn, self._args, self._result, self._keep = fn, args, result, keep
         self._device = device
+        self._known, self._ready = known, ready      # streams that the tensors are safe on; the zeros' event
 
     def __call__(self, stream=None):
         s = torch.cuda.current_stream(self._device) if stream is None else stream
+        if s.cuda_stream not in self._known:
+            self._adopt(s)
         rc = self._fn(*self._args, s.cuda_stream)
         if rc:
             _check(rc)
         return self._result
 
+    def _adopt(self, s):
+        with torch.cuda.stream(s):
+            if torch.cuda.is_current_stream_capturing():
+                return
+        if self._ready is not None:
+            s.wait_event(self._ready)
+        for t in _tensors((self._keep, self._result)):
+            t.record_stream(s)
+        self._known.add(s.cuda_stream)
 
-def _finish(call: CacheCall, prepared: bool, stream):
-    return call if prepared else call(stream)
+
+def _run(fn, args, result, keep, device, prepared, stream, zeroed=False):
+    """The call, or a handle of it where `prepared`.  Results (and `zeroed`: a
+    workspace) were made under torch.cuda.stream(stream), so that their memory is
+    `stream`'s from the start."""
+    here = torch.cuda.current_stream(device)
+    away = stream is not None and stream.cuda_stream != here.cuda_stream
+    ready = None
+    if prepared and zeroed:
+        with torch.cuda.stream(stream):
+            if not torch.cuda.is_current_stream_capturing():
+                ready = torch.cuda.Event()
+                ready.record()
+    call = CacheCall(fn, args, result, keep, device, set() if away else {here.cuda_stream}, ready)
+    if prepared:
+        return call
+    call(stream)
+    if away:
+        for t in _tensors(result):
+            t.record_stream(here)        # the caller goes on with them here
+    return result
 
 
 def _same_device(a, *others):
@@ -167,8 +217,7 @@ def cache_append(cache: PagedCache, k, v, cu_rows, start, page_table, *, B: int,
                  _paged(slot_pos, "slot_pos", cache, torch.int32),
                  _per_request(pos0, "pos0", B), _dev(status, "status", torch.int32))
     keep = (cache, k, v, cu_rows, start, page_table, score, slot_pos, pos0, status, view, rows)
-    return _finish(CacheCall(L.spec_cache_append, (C.byref(view), C.byref(rows)), cache, keep,
-                             k.device), prepared, stream)
+    return _run(L.spec_cache_append, (C.byref(view), C.byref(rows)), cache, keep, k.device, prepared, stream)
 
 
 def cache_read(cache: PagedCache, cu_rows, start, page_table, *, B: int, max_rows: int,
@@ -182,15 +231,15 @@ def cache_read(cache: PagedCache, cu_rows, start, page_table, *, B: int, max_row
     view = cache._view(page_table, B)
     R_cap = B * max_rows if R_cap is None else int(R_cap)
     shape = (R_cap, cache.H, cache.D)
-    res = {n: torch.empty(shape, dtype=dtype, device=cache.pages.device) for n in ("k", "v")}
+    with torch.cuda.stream(stream):
+        res = {n: torch.empty(shape, dtype=dtype, device=cache.pages.device) for n in ("k", "v")}
     kp, kr, kh = _heads(res["k"], "k", cache.D)
     vp, vr, vh = _heads(res["v"], "v", cache.D)
     rows = _Rows(kp, vp, _float_code(dtype), kr, kh, vr, vh, R_cap, int(max_rows),
                  _per_request(cu_rows, "cu_rows", B + 1), _per_request(start, "start", B), None,
                  None, None, _dev(status, "status", torch.int32))
     keep = (cache, cu_rows, start, page_table, status, view, rows)
-    return _finish(CacheCall(L.spec_cache_read, (C.byref(view), C.byref(rows)), res, keep,
-                             cache.pages.device), prepared, stream)
+    return _run(L.spec_cache_read, (C.byref(view), C.byref(rows)), res, keep, cache.pages.device, prepared, stream)
 
 
 def cache_workspace_bytes(B: int, k_max: int, Hq: int, H: int, D: int, max_len: int) -> int:
@@ -233,14 +282,15 @@ def cache_attend(cache: PagedCache, q, cu_rows, cache_len, page_table, *, B: int
     L = load_library()
     view, attn = _attention(cache, q, cu_rows, cache_len, page_table, B, k_max, max_len, scale, cap,
                             slopes, window, prefix, slot_pos, status)
-    ws = workspace if workspace is not None else new_cache_workspace(
-        cache, page_table, B=B, k_max=k_max, Hq=q.shape[1], max_len=max_len)
-    res = {"out": torch.empty(q.shape, dtype=q.dtype, device=q.device),
-           "lse": torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)}
+    with torch.cuda.stream(stream):
+        ws = workspace if workspace is not None else new_cache_workspace(
+            cache, page_table, B=B, k_max=k_max, Hq=q.shape[1], max_len=max_len)
+        res = {"out": torch.empty(q.shape, dtype=q.dtype, device=q.device),
+               "lse": torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)}
     keep = (cache, q, cu_rows, cache_len, page_table, slopes, slot_pos, status, ws, view, attn)
     args = (C.byref(view), C.byref(attn), res["out"].data_ptr(), res["lse"].data_ptr(),
             _dev(ws, "workspace", torch.uint8), ws.numel())
-    return _finish(CacheCall(L.spec_cache_attend, args, res, keep, q.device), prepared, stream)
+    return _run(L.spec_cache_attend, args, res, keep, q.device, prepared, stream, zeroed=workspace is None)
 
 
 def cache_weights(cache: PagedCache, q, lse, cu_rows, cache_len, page_table, score, *, B: int,
@@ -259,7 +309,7 @@ def cache_weights(cache: PagedCache, q, lse, cu_rows, cache_len, page_table, sco
     keep = (cache, q, lse, cu_rows, cache_len, page_table, score, slopes, slot_pos, status, view, attn)
     args = (C.byref(view), C.byref(attn), _dev(lse, "lse", torch.float32),
             _paged(score, "score", cache, torch.float32))
-    return _finish(CacheCall(L.spec_cache_weights, args, score, keep, q.device), prepared, stream)
+    return _run(L.spec_cache_weights, args, score, keep, q.device, prepared, stream)
 
 
 def cache_evict(cache: PagedCache, score, cache_len, page_table, dst_table, *, B: int, budget: int,
@@ -273,8 +323,9 @@ def cache_evict(cache: PagedCache, score, cache_len, page_table, dst_table, *, B
     if dst_table.dim() != 2 or dst_table.shape[0] < B:
         raise SpecError("dst_table must be [B, pages]")
     dev = cache.pages.device
-    res = {"kept": torch.empty(B, int(budget), dtype=torch.int32, device=dev),
-           "new_len": torch.empty(B, dtype=torch.int32, device=dev)}
+    with torch.cuda.stream(stream):
+        res = {"kept": torch.empty(B, int(budget), dtype=torch.int32, device=dev),
+               "new_len": torch.empty(B, dtype=torch.int32, device=dev)}
     ev = _Eviction(_paged(score, "score", cache, torch.float32),
                    _paged(slot_pos, "slot_pos", cache, torch.int32),
                    _per_request(cache_len, "cache_len", B), int(budget), int(recent),
@@ -282,5 +333,4 @@ def cache_evict(cache: PagedCache, score, cache_len, page_table, dst_table, *, B
                    res["kept"].data_ptr(), res["new_len"].data_ptr(),
                    _dev(status, "status", torch.int32))
     keep = (cache, score, cache_len, page_table, dst_table, slot_pos, status, view, ev)
-    return _finish(CacheCall(L.spec_cache_evict, (C.byref(view), C.byref(ev)), res, keep, dev),
-                   prepared, stream)
+    return _run(L.spec_cache_evict, (C.byref(view), C.byref(ev)), res, keep, dev, prepared, stream)

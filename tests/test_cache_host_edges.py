@@ -1,0 +1,137 @@
+"""The 4-bit cache's binding and C entries, on the host alone: where tensors are
+made and how long they are kept when a call runs on another stream, and the
+refusals at the edges of the contract.  Devices, streams and the library are
+stood in for where a call would otherwise launch."""
+import warnings
+
+import pytest
+import torch
+from torch._subclasses.fake_tensor import FakeTensorMode
+
+from tests.test_cache_host import sv  # noqa: F401
+
+
+class Streams:
+    """Streams by name, the current one, and what was done on which."""
+
+    class One:
+        def __init__(self, log, n):
+            self.log, self.cuda_stream = log, n
+
+        def wait_event(self, e):
+            self.log.append(("wait", self.cuda_stream, e.on))
+
+    def __init__(self):
+        self.log = []
+        self.here, self.side, self.third = (self.One(self.log, n) for n in (1, 2, 3))
+        self.current = self.here
+
+    def enter(self, s):
+        streams = self
+
+        class Under:
+            def __enter__(self):
+                self.before, streams.current = streams.current, s or streams.current
+
+            def __exit__(self, *a):
+                streams.current = self.before
+        return Under()
+
+
+@pytest.fixture
+def faked(sv, monkeypatch):  # noqa: F811
+    """The binding over tensors of a device that is not there: (sv, streams)."""
+    import speculative_decoding_verification_ragged_gb300.cache as mod
+    st = Streams()
+
+    class Library:
+        def __getattr__(self, name):
+            if name == "spec_cache_workspace_bytes":
+                return lambda *a: 4096
+            return lambda *a: st.log.append(("launch", a[-1], name)) or 0
+
+    class Event:
+        def record(self):
+            self.on = st.current.cuda_stream
+
+    def made(f):
+        def g(*a, **kw):
+            st.log.append(("made", st.current.cuda_stream, f.__name__))
+            return f(*a, **kw)
+        return g
+
+    monkeypatch.setattr(mod, "load_library", lambda path=None: Library())
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: st.current)
+    monkeypatch.setattr(torch.cuda, "stream", st.enter)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    monkeypatch.setattr(torch.cuda, "Event", Event)
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: st.log.append(("lent", s.cuda_stream, tuple(t.shape))))
+    with FakeTensorMode(), warnings.catch_warnings():
+        warnings.simplefilter("ignore")
+        z = lambda *s, d=torch.int32, dev="cuda:0": torch.zeros(*s, dtype=d, device=dev)
+        st.cache = lambda **kw: sv.PagedCache(z(3, 1, 1, 36 * 64, d=torch.uint8), **kw)
+        st.z = z
+        st.args = (z(4, 2, 64, d=torch.float32), z(2), z(1), z(1, 3))
+        st.made = lambda: (monkeypatch.setattr(torch, "zeros", made(torch.zeros)), monkeypatch.setattr(torch, "empty", made(torch.empty)))
+        yield sv, st
+
+
+def test_a_call_on_another_stream_makes_its_tensors_there(faked):
+    """Workspace zeros and results on the stream of the launch; the inputs kept for
+    it, the results for the caller's."""
+    sv, st = faked
+    cache, score = st.cache(), st.z(3, 32, d=torch.float32)
+    st.made()
+    sv.cache_attend(cache, *st.args, B=1, k_max=3, stream=st.side)
+    assert {x[1] for x in st.log if x[0] == "made"} == {2} and sum(x[0] == "made" for x in st.log) >= 3
+    lent = [x for x in st.log if x[0] == "lent"]
+    assert {(2, (3, 1, 1, 36 * 64)), (2, (4, 2, 64)), (2, (1, 3)), (2, (4096,)), (1, (4, 2, 64)), (1, (4, 2))} <= {x[1:] for x in lent}
+    launch = st.log.index(("launch", 2, "spec_cache_attend"))
+    assert all(st.log.index(x) < launch for x in lent if x[1] == 2)
+    for call in (lambda: sv.cache_read(cache, st.args[1], st.args[2], st.args[3], B=1, max_rows=4, stream=st.side),
+                 lambda: sv.cache_evict(cache, score, st.args[2], st.args[3], st.args[3], B=1, budget=4, stream=st.side)):
+        del st.log[:]
+        call()
+        assert {x[1] for x in st.log if x[0] == "made"} == {2}
+        assert {x[1] for x in st.log if x[0] == "lent"} == {1, 2}
+
+
+def test_a_handle_orders_its_workspace_before_another_stream(faked):
+    sv, st = faked
+    call = sv.cache_attend(st.cache(), *st.args, B=1, k_max=3, prepared=True)
+    del st.log[:]
+    call()
+    assert st.log == [("launch", 1, "spec_cache_attend")]           # its own stream: nothing to do
+    for stream in (st.side, st.third):
+        del st.log[:]
+        call(stream)
+        n = stream.cuda_stream
+        assert st.log[0] == ("wait", n, 1) and st.log[-1] == ("launch", n, "spec_cache_attend")
+        assert sum(x[0] == "lent" for x in st.log) == len(st.log) - 2 >= 7
+        del st.log[:]
+        with st.enter(stream):
+            call()
+        assert st.log == [("launch", n, "spec_cache_attend")]       # from then on neither
+    # prepared for another stream than the current one: the current one waits too
+    call = sv.cache_attend(st.cache(), *st.args, B=1, k_max=3, prepared=True, stream=st.side)
+    del st.log[:]
+    call()
+    assert st.log[0] == ("wait", 1, 2)
+
+
+def test_a_handle_over_the_callers_workspace_waits_for_nothing(faked):
+    sv, st = faked
+    call = sv.cache_attend(st.cache(), *st.args, B=1, k_max=3, workspace=st.z(4096, d=torch.uint8), prepared=True)
+    del st.log[:]
+    call(st.side)
+    assert all(x[0] != "wait" for x in st.log)
+
+
+def test_a_captured_call_is_left_to_its_graph(faked, monkeypatch):
+    sv, st = faked
+    call = sv.cache_attend(st.cache(), *st.args, B=1, k_max=3, prepared=True)
+    del st.log[:]
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: st.current is st.side)
+    call(st.side)
+    assert st.log == [("launch", 2, "spec_cache_attend")]
