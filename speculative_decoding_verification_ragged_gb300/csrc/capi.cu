@@ -245,7 +245,8 @@ int check_attention(const spec_cache *cache, const spec_attention *a, CacheView 
     p.cap = a->cap;
     p.slopes = a->slopes;
     p.window = a->window;
-    p.prefix = a->prefix;
+    // no slot lies beyond room: a prefix of any size stays clear of 2^31 in the kernels' sums
+    p.prefix = static_cast<int32_t>(a->prefix < room ? a->prefix : room);
     p.slot_pos = a->slot_pos;
     p.status = a->status;
     p.q_aligned = rows_aligned(a->q, a->q_row, a->q_head, elt_bytes(a->dtype));

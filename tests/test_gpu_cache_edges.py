@@ -5,7 +5,7 @@ import numpy as np
 import pytest
 
 from tests._gpu import need_gpu
-from tests.test_gpu_cache import dev, gpu_cache, queries, quick_pool
+from tests.test_gpu_cache import check_attention, dev, gpu_cache, queries, quick_pool
 
 torch = pytest.importorskip("torch")
 
@@ -78,3 +78,18 @@ def test_inputs_dropped_after_a_call_on_another_stream_stay():
         side.synchronize()
         assert all(torch.equal(want[k], got[k]) for k in want)
         del late
+
+
+# ------------------------------------------------------- limits of the arguments ---
+
+@pytest.mark.parametrize("prefix", [2 ** 31 - 1, 2 ** 31 - 127, 2 ** 31 - 128, 1 << 30])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_a_prefix_beyond_every_slot_shows_all(dtype, prefix):
+    """A window with such a prefix hides nothing."""
+    sv = need_gpu()
+    rng = np.random.default_rng(41)
+    lens, cu = [700, 33, 1, 300], np.array([0, 3, 6, 7, 10])
+    c = quick_pool(rng, B=4, H=2, D=64, page=64, lens=lens)
+    q = queries(rng, 10, 4, 64, dtype)
+    *_, status = check_attention(sv, c, q, cu, lens, 2, window=20, prefix=prefix)
+    assert status == 0
