@@ -112,7 +112,8 @@ typedef struct {
     int32_t window;            /* > 0: only slots with pos_row - pos_slot < window ...        */
     int32_t prefix;            /* ... or slot < prefix                                        */
     const int32_t *slot_pos;   /* [n_pages, page_tokens] or NULL: position of a slot, not
-                                  decreasing over a request's slots; NULL: its index          */
+                                  decreasing over a request's slots, the last less than 2^31
+                                  beyond the first; NULL: its index                           */
     uint32_t *status;          /* [1] or NULL                                                 */
 } spec_attention;
 

@@ -50,7 +50,8 @@ __device__ __forceinline__ void visible_steps(const CacheView &c, const AttnPara
     if (p.window <= 0 || own <= 0) return;
     int first = max(own - p.window + 1, 0) / STEP;
     if (p.slot_pos) {
-        const int limit = slot_position(c, p, w.b, own) - p.window;
+        // (in 64 bits: positions can be negative, a window as wide as the type)
+        const int64_t limit = static_cast<int64_t>(slot_position(c, p, w.b, own)) - p.window;
         int lo = 0, hi = own / STEP;               // steps below lo are hidden, step hi is not
         while (lo < hi) {
             const int by = (hi - lo + 6) / 7;

@@ -12,6 +12,14 @@ torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 
 
+def gapped_positions(rng, c, first=0):
+    """Positions of every slot, rising by 1 to 3 from `first` in each request."""
+    pos = np.zeros((c.n_pages, c.page), np.int32)
+    for b in range(len(c.table)):
+        pos[c.table[b]] = (first + np.cumsum(rng.integers(1, 4, c.table.shape[1] * c.page)) - 1).reshape(-1, c.page)
+    return pos
+
+
 # --------------------------------------------------------------- streams ---
 
 def split_case(sv):
@@ -92,4 +100,16 @@ def test_a_prefix_beyond_every_slot_shows_all(dtype, prefix):
     c = quick_pool(rng, B=4, H=2, D=64, page=64, lens=lens)
     q = queries(rng, 10, 4, 64, dtype)
     *_, status = check_attention(sv, c, q, cu, lens, 2, window=20, prefix=prefix)
+    assert status == 0
+
+
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 30])
+def test_the_widest_window_over_negative_positions_shows_all(window):
+    sv = need_gpu()
+    rng = np.random.default_rng(42)
+    lens, cu = [700, 33, 300], np.array([0, 2, 4, 6])
+    c = quick_pool(rng, B=3, H=2, D=64, page=64, lens=lens)
+    pos = gapped_positions(rng, c, first=-5000)
+    q = queries(rng, 6, 4, 64, "bf16")
+    *_, status = check_attention(sv, c, q, cu, lens, 1, window=window, slot_pos=pos)
     assert status == 0
