@@ -309,6 +309,9 @@ __device__ __forceinline__ void load_products(uint32_t addr, float (&v)[N])
     }
 }
 
+// 1 / cap, finite for the smallest cap too (scores of 0 stay 0 under it)
+__device__ __forceinline__ float cap_reciprocal(float cap) { return fminf(1.f / cap, 3.4028234663852886e38f); }
+
 // cap * tanh(s / cap), s and the result in units of `unit` (1 or log2 e).  EXACT
 // (fp32 results): the library's tanh.  Else (e^2z - 1) / (e^2z + 1), and below 1/2,
 // where that cancels, Lambert's continued fraction to its fifth term (9e-11 off):

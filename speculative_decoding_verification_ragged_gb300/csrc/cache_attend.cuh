@@ -250,7 +250,7 @@ __device__ __forceinline__ void token_scores(const AttnParams &p, const Job &w, 
 #pragma unroll
         for (int q = 0; q < N; ++q) v[q] *= cs.mult[q0 + q];
         if (p.cap > 0.f) {
-            const float cap = p.cap * kLog2e, rcap = 1.f / cap;
+            const float cap = p.cap * kLog2e, rcap = cap_reciprocal(cap);
 #pragma unroll
             for (int q = 0; q < N; ++q) v[q] = cap_score<A::PIECES == 2>(v[q], cap, rcap);
         }

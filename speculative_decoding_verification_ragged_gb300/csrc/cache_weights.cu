@@ -172,7 +172,7 @@ weights_kernel(const CacheView c, const AttnParams p, const int tiles)
             const bool live = lane < valid;
             const int tpos = options && p.slot_pos && live ? slot_position(c, p, w.b, slot) : slot;
             const bool always = live && (p.window <= 0 || slot < p.prefix);
-            const float rcap = p.cap > 0.f ? 1.f / p.cap : 0.f;
+            const float rcap = p.cap > 0.f ? cap_reciprocal(p.cap) : 0.f;
 #pragma unroll
             for (int k = 0; k < NH; ++k) {
                 if (k >= real) break;

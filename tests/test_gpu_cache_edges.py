@@ -113,3 +113,16 @@ def test_the_widest_window_over_negative_positions_shows_all(window):
     q = queries(rng, 6, 4, 64, "bf16")
     *_, status = check_attention(sv, c, q, cu, lens, 1, window=window, slot_pos=pos)
     assert status == 0
+
+
+@pytest.mark.parametrize("cap", [1e-39, 1e-45])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_a_cap_too_small_for_its_reciprocal(dtype, cap):
+    """Scores of no size: every slot weighs the same, a row of zeros included."""
+    sv = need_gpu()
+    rng = np.random.default_rng(43)
+    lens, cu = [300, 33], np.array([0, 2, 4])
+    c = quick_pool(rng, B=2, H=2, D=128, page=64, lens=lens)
+    q = queries(rng, 4, 4, 128, dtype)
+    q[1] = 0
+    check_attention(sv, c, q, cu, lens, 1, cap=cap)
