@@ -130,8 +130,12 @@ SPEC_API size_t spec_cache_workspace_bytes(int32_t B, int32_t k_max, int32_t Hq,
  * j <= len_b - n_b + (r - cu_rows[b]), its own slot, so the rows of a step are
  * causal among themselves; with window > 0 also pos - pos_j < window or
  * j < prefix.  A row that sees no slot (a window that hides all, len_b < n_b,
- * a bad length) gets out = 0 and lse = -inf.  Slots that no row of the
- * request sees are not read, whatever their bytes.  out [R_cap, Hq, D], lse
+ * a bad length) gets out = 0 and lse = -inf.  What slots hold that no row of the
+ * request sees does not matter, NaN scales included (the scales of the others have
+ * to be numbers).  Pages whose slots a window hides from all rows can be given back
+ * and need no id: their entries are not looked at, and with slot_pos, where only
+ * positions tell, bad ids that follow hidden slots (or begin the cache, with
+ * position 0 hidden) count as such and are not reported.  out [R_cap, Hq, D], lse
  * [R_cap, Hq] or NULL, both contiguous; rows >= cu_rows[B] are not written.
  * Results do not depend on the order in which blocks run.  A query row with a
  * NaN or infinite value gets unspecified results, as can the request's other rows

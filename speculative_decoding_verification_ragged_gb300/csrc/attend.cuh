@@ -89,35 +89,75 @@ __device__ __forceinline__ bool load_job(const CacheView &c, const AttnParams &p
     return true;
 }
 
+// Whether the window hides the block from `slot0` on from every row of the request
+// (of slots that are their own positions; where slot_pos has those, it has to be read).
+__device__ __forceinline__ bool hidden_block(const AttnParams &p, const Job &w, int slot0)
+{
+    const int own = w.len - w.n;                       // the first row's
+    return p.window > 0 && !p.slot_pos && own > 0 && slot0 >= p.prefix && slot0 + kTok - 1 <= own - p.window;
+}
+
 // The next tile to fetch, its page ids asked for ahead: a fetch does not wait for
 // the page table (the ids are looked at only when the copies are issued).
 struct Fetch {
-    int h, slot, len, page;     // page: of this lane's block, as the table has it
+    int h, slot, n, page;       // n, page: of this lane's block, its tokens and the page as the table has it
 };
 
-__device__ __forceinline__ Fetch ask_pages(const CacheView &c, const Job &w, int h, int slot)
+// (WINDOW: there can be one)
+template <bool WINDOW>
+__device__ __forceinline__ Fetch ask_pages(const CacheView &c, const AttnParams &p, const Job &w, int h, int slot)
 {
     const int lane = threadIdx.x & 31, slot0 = slot + lane * kTok;
-    Fetch f = {h, slot, w.len, -1};
-    if (lane < 4 && slot0 < w.len)
+    Fetch f = {h, slot, 0, -1};
+    if (lane < 4 && slot0 < w.len && !(WINDOW && hidden_block(p, w, slot0))) {
+        f.n = min(w.len - slot0, kTok);
         f.page = __ldg(c.page_table + static_cast<int64_t>(w.b) * c.max_pages + slot0 / c.page_tokens);
+    }
     return f;
+}
+
+// Report the blocks `bad` of a tile, whose page id is none.  Where the window goes by
+// slot_pos, a page that it hides may have been given back, and then has no positions
+// that say so: a run of bad pages counts as hidden where the good page before it ends
+// hidden, or where it begins the cache and position 0 is hidden.  The pages of a run
+// lead back to its first one, so looking at the 32 pages before is enough: a run that
+// rows would see is reported by its first pages.
+template <bool WINDOW>
+__device__ __forceinline__ void report_pages(const CacheView &c, const AttnParams &p, const Job &w, int slot, uint32_t bad)
+{
+    const int lane = threadIdx.x & 31, own = w.len - w.n;
+    bool report = !WINDOW || p.window <= 0 || !p.slot_pos || own <= 0;
+    if (!report) {
+        const int64_t limit = static_cast<int64_t>(slot_position(c, p, w.b, own)) - p.window;
+        for (uint32_t left = bad & ~(bad << 1); left && !report; left &= left - 1) {
+            const int slot0 = slot + (__ffs(left) - 1) * kTok, index = slot0 / c.page_tokens, at = index - 1 - lane;
+            const int id = at >= 0 ? __ldg(c.page_table + static_cast<int64_t>(w.b) * c.max_pages + at) : -1;
+            const uint32_t good = __ballot_sync(0xFFFFFFFFu, id >= 0 && id < c.n_pages);
+            if (good)
+                report = slot_position(c, p, w.b, (index - __ffs(good) + 1) * c.page_tokens - 1) > limit;
+            else
+                report = index <= 32 && limit < 0;
+            report = report || slot0 < p.prefix;
+        }
+    }
+    if (report && lane == 0) set_status(p.status, SPEC_STATUS_BAD_PAGE);
 }
 
 // Copy the first BYTES of a tile's 4 blocks into a stage (all of a block, or its
 // keys); a lane of one warp per block.  nv: the tokens of each block that exist (0
-// for a bad page: its bytes are not fetched, and what the stage holds there is
-// masked); pages, where it is asked for: their page ids.
-template <int BYTES>
-__device__ __forceinline__ void load_tile(const CacheView &c, const Fetch &f, uint8_t *stage, uint64_t *full, int *nv,
-                                          uint32_t *status, int *pages = nullptr)
+// for a bad page, or a block that the window hides whole: its bytes are not fetched,
+// and what the stage holds there is masked); pages, where it is asked for: their page ids.
+template <int BYTES, bool WINDOW>
+__device__ __forceinline__ void load_tile(const CacheView &c, const AttnParams &p, const Job &w, const Fetch &f, uint8_t *stage,
+                                          uint64_t *full, int *nv, int *pages = nullptr)
 {
     const int lane = threadIdx.x & 31;
     const int slot0 = f.slot + lane * kTok;
-    int n = lane < 4 ? min(max(f.len - slot0, 0), kTok) : 0;
-    if (n > 0 && (f.page < 0 || f.page >= c.n_pages)) {
-        set_status(status, SPEC_STATUS_BAD_PAGE);
-        n = 0;
+    int n = f.n;
+    const uint32_t bad = __ballot_sync(0xFFFFFFFFu, n > 0 && (f.page < 0 || f.page >= c.n_pages));
+    if (bad) {
+        report_pages<WINDOW>(c, p, w, f.slot, bad);
+        if (bad >> lane & 1u) n = 0;
     }
     const uint32_t have = __ballot_sync(0xFFFFFFFFu, n > 0);
     if (lane < 4) nv[lane] = n;

@@ -103,6 +103,17 @@ __device__ __forceinline__ void value_scales(const uint8_t *tile, const int *nv,
     }
 }
 
+// Scales of 0 for the tokens that the window hides from all columns (lit: a bit for
+// each of a block's tokens that it does not hide).  Their weight is 0, but their bytes can be anything, NaN included.
+template <int D> __device__ __forceinline__ void hide_values(const uint32_t *lit, uint32_t *vs)
+{
+#pragma unroll
+    for (int i = threadIdx.x; i < D / 16 * 64; i += kAttnThreads) {
+        const uint32_t two = lit[i % 64 / 16] >> (i % 16 * 2);
+        vs[i] &= ((two & 1u) ? 0xFFFFu : 0u) | ((two & 2u) ? 0xFFFF0000u : 0u);
+    }
+}
+
 // The values of one channel over the 32 tokens of a block -> 16 columns
 template <int D, bool WIDE>
 __device__ __forceinline__ void decode_values(const uint8_t *blk, int d, const uint32_t *vs, uint32_t taddr)
@@ -514,6 +525,7 @@ attend_kernel(const CacheView c, const AttnParams p, const Layout lay)
     constexpr int kFirst = 1, kLast = 2, kEnd = 4;
     __shared__ int keys_are, weights_wide;
     __shared__ __align__(16) int nv[A::STAGES][4], pages[A::STAGES][4];
+    __shared__ __align__(16) uint32_t lit[2][4];      // tokens of a tile that the window does not hide from all columns
     const int tid = threadIdx.x, warp = warp_index(), lane = tid & 31;
     const int group = p.Hq / c.H;
 
@@ -571,12 +583,12 @@ attend_kernel(const CacheView c, const AttnParams p, const Layout lay)
                     s_phase ^= 1;
                 }
             }
-            if (any) next = ask_pages(c, seg.w, seg.w.h, tile_slot<OPT>(seg, k++));
+            if (any) next = ask_pages<OPT>(c, p, seg.w, seg.w.h, tile_slot<OPT>(seg, k++));
         };
         ask_next();
         while (any && !fail) {
             wait_or_fail(&empty[ring], phase, fail);
-            load_tile<block_bytes(D)>(c, next, stages + ring * A::STAGE, &full[ring], nv[ring], p.status,
+            load_tile<block_bytes(D), OPT>(c, p, seg.w, next, stages + ring * A::STAGE, &full[ring], nv[ring],
                                       OPT ? pages[ring] : nullptr);
             if (++ring == A::STAGES) {
                 ring = 0;
@@ -709,6 +721,13 @@ attend_kernel(const CacheView c, const AttnParams p, const Layout lay)
             wait_or_fail(&s_bar, s_phase, fail);
             s_phase ^= 1;
             tmem_fence_after();
+            if (OPT && p.window > 0 && half == 0) {
+                // (the first column's row sees no later slots than the others, and no fewer)
+                const bool dark = own_first >= 0 && t.slot >= p.prefix &&
+                                  t.pos <= static_cast<int64_t>(cs.pos[0]) - p.window;
+                const uint32_t seen = __ballot_sync(0xFFFFFFFFu, !dark);
+                if (lane == 0) lit[buf][quarter] = seen;
+            }
             float v[NH], x[NH];
             uint32_t hi[NH / 2];
             // weights, and whether they are fit for f16: none beyond 2^15 (the reference
@@ -758,6 +777,14 @@ attend_kernel(const CacheView c, const AttnParams p, const Layout lay)
                     for (int q = 0; q < OR; ++q) acc[q] *= cs.factor[half * NH + q % NH];
                 } else {
                     rescale_results<A>(cs, o_t + lane_off);
+                }
+            }
+            if (OPT && p.window > 0) {
+                // (the same for all: a barrier lies between)
+                const uint4 seen = *reinterpret_cast<const uint4 *>(lit[buf]);
+                if ((seen.x & seen.y & seen.z & seen.w) != 0xFFFFFFFFu) {
+                    hide_values<D>(lit[buf], vsk);
+                    csync();
                 }
             }
             // S^T is read, the keys' columns are free: on to the next tile's keys

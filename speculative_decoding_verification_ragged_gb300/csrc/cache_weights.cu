@@ -105,16 +105,16 @@ weights_kernel(const CacheView c, const AttnParams p, const int tiles)
         Step at = {0, 0, 0};
         int ring = 0;
         uint32_t phase = 1;                               // (a stage is empty at first)
-        Fetch next = ask_pages(c, w, 0, step_slot<kTile>(w, i0));
+        Fetch next = ask_pages<true>(c, p, w, 0, step_slot<kTile>(w, i0));
         for (int i = 0; i < steps && !fail; ++i) {
             wait_or_fail(&empty[ring], phase, fail);
-            load_tile<A::K_BYTES>(c, next, stages + ring * A::STAGE, &full[ring], nv[ring], p.status);
+            load_tile<A::K_BYTES, true>(c, p, w, next, stages + ring * A::STAGE, &full[ring], nv[ring]);
             if (++ring == A::STAGES) {
                 ring = 0;
                 phase ^= 1;
             }
             at.next(nt, qt_used);
-            if (i + 1 < steps) next = ask_pages(c, w, at.h, step_slot<kTile>(w, i0 + at.t));
+            if (i + 1 < steps) next = ask_pages<true>(c, p, w, at.h, step_slot<kTile>(w, i0 + at.t));
         }
         return;
     }
@@ -248,9 +248,10 @@ weights_kernel(const CacheView c, const AttnParams p, const int tiles)
         csync();
         for (int t = half; t < nt; t += 2) {
             const int slot = step_slot<kTile>(w, i0 + t) + tok;
-            const int page = slot < w.len ? page_of(c, w.b, slot) : -1;
-            if (page >= 0)
-                p.score[static_cast<int64_t>(page) * c.page_tokens + slot % c.page_tokens] += acc[t][0][tok] + acc[t][1][tok];
+            // (a slot that no row sees got 0, and its page may be another's by now)
+            const float got = acc[t][0][tok] + acc[t][1][tok];
+            const int page = slot < w.len && got != 0.f ? page_of(c, w.b, slot) : -1;
+            if (page >= 0) p.score[static_cast<int64_t>(page) * c.page_tokens + slot % c.page_tokens] += got;
         }
     }
     tmem_fence_before();

@@ -4,8 +4,9 @@ tests/test_gpu_cache.py derives."""
 import numpy as np
 import pytest
 
+from tests import _cache_ref as ref
 from tests._gpu import need_gpu
-from tests.test_gpu_cache import check_attention, dev, gpu_cache, queries, quick_pool
+from tests.test_gpu_cache import check_attention, dev, gpu_cache, queries, quick_pool, run_attention
 
 torch = pytest.importorskip("torch")
 
@@ -126,3 +127,109 @@ def test_a_cap_too_small_for_its_reciprocal(dtype, cap):
     q = queries(rng, 4, 4, 128, dtype)
     q[1] = 0
     check_attention(sv, c, q, cu, lens, 1, cap=cap)
+
+
+# -------------------------------------------------- slots that the window hides ---
+
+HIDDEN = [  # rows, window, prefix, positions with gaps
+    (1, 1, 0, False), (4, 33, 3, False), (3, 150, 40, False), (4, 100, 130, False),
+    (1, 1, 0, True), (4, 33, 3, True), (3, 150, 40, True), (4, 100, 130, True)]
+
+
+def hidden_case(rng, D, page, rows, window, prefix, gaps):
+    lens = [1000, 641, 300, 129, 128, 5]
+    n = [min(rows, x) for x in lens]
+    cu = np.concatenate([[0], np.cumsum(n)])
+    c = quick_pool(rng, B=len(lens), H=2, D=D, page=page, lens=lens)
+    pos = gapped_positions(rng, c) if gaps else None
+    hidden = []
+    for b, (L, r) in enumerate(zip(lens, n)):
+        i = np.arange(L)
+        at = i if pos is None else pos[c.table[b, i // page], i % page].astype(np.int64)
+        hidden.append(i[(at[L - r] - at >= window) & (i >= prefix) & (i < L - r)])
+    return c, lens, cu, pos, hidden
+
+
+def exact_bounds(c, q, cu, lens, **kw):
+    """out, lse of the definition and how far results may be from them."""
+    out, lse, A, S, w = ref.attention(c, q.float().cpu().numpy(), cu, lens, **kw)
+    u = 2.0 ** -24
+    ds = (c.D * 2 * u + 4 * u) * S
+    bf = q.dtype == torch.bfloat16
+    rel = 2 * ds + 2.0 ** -20 + 2.0 ** -23 * (max(lens) / 16 + 16) + (2.0 ** -11 if bf else 2.0 ** -20)
+    tol = A * rel[..., None] + (2.0 ** -8 * np.abs(out) if bf else 0) + 1e-30
+    return out, tol, lse, ds + 4 * u * np.abs(lse) + 2.0 ** -19, w
+
+
+@pytest.mark.parametrize("rows,window,prefix,gaps", HIDDEN)
+@pytest.mark.parametrize("D,page,dtype", [(64, 32, "bf16"), (128, 64, "f32"), (256, 96, "bf16"), (128, 32, "bf16")])
+def test_what_hidden_slots_hold_does_not_matter(D, page, dtype, rows, window, prefix, gaps):
+    """NaN scales and any codes in slots that no row sees, in the tiles that some row does."""
+    sv = need_gpu()
+    rng = np.random.default_rng(D + page + window)
+    c, lens, cu, pos, hidden = hidden_case(rng, D, page, rows, window, prefix, gaps)
+    assert any(len(h) for h in hidden)
+    for b, slots in enumerate(hidden):
+        for s in slots:
+            blk = c.pages[c.table[b, s // page], :, s % page // 32]
+            t = s % 32
+            blk[:, 16 * D + t * (D // 16):16 * D + (t + 1) * (D // 16)] = rng.choice(np.array([0x7F, 0xFF, 0x30], np.uint8), D // 16)
+            blk[:, 34 * D + t:36 * D:32] = rng.choice(np.array([0x7F, 0xFF], np.uint8), D // 16)
+    q = queries(rng, int(cu[-1]), 4, D, dtype)
+    *_, status = check_attention(sv, c, q, cu, lens, rows - 1, window=window, prefix=prefix, slot_pos=pos)
+    assert status == 0
+
+
+@pytest.mark.parametrize("rows,window,prefix,gaps", HIDDEN)
+@pytest.mark.parametrize("page,dtype", [(32, "bf16"), (64, "f32"), (96, "bf16")])
+def test_pages_that_the_window_hides_need_no_id(page, dtype, rows, window, prefix, gaps):
+    """Pages of which no row sees a slot, given back: their entries name no page,
+    nothing is reported, and the other slots count as before."""
+    sv = need_gpu()
+    rng = np.random.default_rng(page + window)
+    c, lens, cu, pos, hidden = hidden_case(rng, 64, page, rows, window, prefix, gaps)
+    q = queries(rng, int(cu[-1]), 4, 64, dtype)
+    kw = dict(window=window, prefix=prefix, slot_pos=pos)
+    out, tol, lse, lse_tol, w = exact_bounds(c, q, cu, lens, **kw)
+    cut = ref.Cache(c.pages, c.table)
+    gone = 0
+    for b, slots in enumerate(hidden):
+        for p in range(c.table.shape[1]):
+            if len(slots) and np.isin(np.arange(p * page, (p + 1) * page), slots).all():
+                cut.table[b, p] = (-1, c.n_pages, -2 ** 31)[p % 3]
+                gone += 1
+    assert gone
+    res, score, status = run_attention(sv, cut, q, cu, lens, rows - 1, **kw)
+    assert status == 0
+    assert (np.abs(res["out"].float().cpu().numpy() - out) <= tol).all()
+    assert (np.abs(res["lse"].cpu().numpy() - lse) <= lse_tol).all()
+    got = score.cpu().numpy()
+    for b, L in enumerate(lens):
+        i = np.arange(L)
+        ok = np.isin(i, hidden[b], invert=True)
+        np.testing.assert_allclose(got[c.table[b, i // page], i % page][ok], w[b][ok], rtol=1e-4, atol=1e-30)
+
+
+@pytest.mark.parametrize("gaps", [False, True])
+def test_a_bad_page_among_the_visible_ones_is_reported(gaps):
+    """... with a window too, and hides its own tokens alone."""
+    sv = need_gpu()
+    rng = np.random.default_rng(44)
+    L, page, window = 2000, 32, 1200
+    c = quick_pool(rng, B=1, H=1, D=64, page=page, lens=[L])
+    pos = gapped_positions(rng, c) if gaps else None
+    at = np.arange(L) if pos is None else pos[c.table[0, np.arange(L) // page], np.arange(L) % page].astype(np.int64)
+    first = int(np.argmax(at > at[L - 1] - window))                 # the first visible slot
+    q = queries(rng, 1, 2, 64, "f32")
+    k, v = c.get(0, 0, np.arange(L))
+    for p in (first // page + 1, (first + L) // 2 // page, L // page - 1):
+        cut = ref.Cache(c.pages, c.table)
+        cut.table[0, p] = -1
+        cut.table[0, :first // page] = -1                            # given back, all of them
+        res, _, status = run_attention(sv, cut, q, np.array([0, 1]), [L], 0, window=window, slot_pos=pos)
+        assert status == 0x400
+        see = (np.arange(L) >= first) & (np.arange(L) // page != p)
+        for h in range(2):
+            s = k[see] @ q[0, h].double().cpu().numpy() / 8
+            e = np.exp(s - s.max())
+            np.testing.assert_allclose(res["out"][0, h].cpu().numpy(), e @ v[see] / e.sum(), rtol=1e-4, atol=1e-4)
