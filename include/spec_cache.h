@@ -25,7 +25,8 @@
  *
  * Conventions are those of spec_verify.h: device pointers owned by the
  * caller, asynchronous on `stream`, no allocation, argument errors returned
- * before any launch, problems in device data OR-ed into *status.
+ * before any launch, problems in device data OR-ed into *status.  Arrays are
+ * aligned to their type, pages and workspace to 16 bytes; anything else is refused.
  */
 #ifndef SPEC_CACHE_H
 #define SPEC_CACHE_H
@@ -117,7 +118,7 @@ typedef struct {
     uint32_t *status;          /* [1] or NULL                                                 */
 } spec_attention;
 
-/* Workspace of spec_cache_attend, zero-filled once before its first use; any
+/* Workspace of spec_cache_attend, 16-byte aligned, zero-filled once before its first use; any
  * number of stream-ordered calls, of any shapes that it is large enough for, can
  * then share it (after SPEC_STATUS_TIMEOUT it has to be zeroed again).  0 for
  * invalid sizes. */

@@ -148,6 +148,12 @@ int noalloc_scratch(void **ptr)
 
 // ---- the 4-bit paged cache ----
 
+// whether device arrays of 32-bit values lie on their words (null: absent)
+template <typename... T> bool on_words(const T *...p)
+{
+    return ((reinterpret_cast<uintptr_t>(p) % 4 == 0) && ...);
+}
+
 int check_cache(const spec_cache *c, CacheView &v)
 {
     if (!c || !c->pages || !c->page_table) return SPEC_ERR_INVALID_ARG;
@@ -155,7 +161,8 @@ int check_cache(const spec_cache *c, CacheView &v)
         return SPEC_ERR_INVALID_ARG;
     if (c->page_tokens < SPEC_CACHE_BLOCK_TOKENS || c->page_tokens % SPEC_CACHE_BLOCK_TOKENS)
         return SPEC_ERR_INVALID_ARG;
-    if (reinterpret_cast<uintptr_t>(c->pages) % 16) return SPEC_ERR_INVALID_ARG;
+    if (reinterpret_cast<uintptr_t>(c->pages) % 16 || !on_words(c->k_scale, c->v_scale, c->page_table))
+        return SPEC_ERR_INVALID_ARG;
     if (c->D != 64 && c->D != 128 && c->D != 256) return SPEC_ERR_UNSUPPORTED;
     // slots are 32-bit; kv heads and requests are the y and z of the grids
     if (c->page_tokens > 65536 || c->H > 65535 || c->B > 65535) return SPEC_ERR_UNSUPPORTED;
@@ -190,7 +197,8 @@ int run_cache_rows(const spec_cache *cache, const spec_cache_rows *r, bool appen
     if (r->R_cap < 1 || r->max_rows < 1) return SPEC_ERR_INVALID_ARG;
     if (r->max_rows > (1 << 30)) return SPEC_ERR_UNSUPPORTED;
     const size_t elt = elt_bytes(r->dtype);
-    if (reinterpret_cast<uintptr_t>(r->k) % elt || reinterpret_cast<uintptr_t>(r->v) % elt)
+    if (reinterpret_cast<uintptr_t>(r->k) % elt || reinterpret_cast<uintptr_t>(r->v) % elt ||
+        !on_words(r->cu_rows, r->start, r->score, r->slot_pos, r->pos0, r->status))
         return SPEC_ERR_INVALID_ARG;
     CacheRows p;
     p.k = r->k;
@@ -226,7 +234,9 @@ int check_attention(const spec_cache *cache, const spec_attention *a, CacheView 
         return SPEC_ERR_INVALID_ARG;
     const int64_t room = static_cast<int64_t>(c.max_pages) * c.page_tokens;
     if (a->max_len < 0 || a->max_len > room) return SPEC_ERR_INVALID_ARG;
-    if (reinterpret_cast<uintptr_t>(a->q) % elt_bytes(a->dtype)) return SPEC_ERR_INVALID_ARG;
+    if (reinterpret_cast<uintptr_t>(a->q) % elt_bytes(a->dtype) ||
+        !on_words(a->cu_rows, a->len, a->slopes, a->slot_pos, a->status))
+        return SPEC_ERR_INVALID_ARG;
     // the work's units and their multiples stay far below 2^63
     const double units = static_cast<double>(c.B) * a->Hq * (a->k_max + 1) * (room / 128 + 16);
     if (units > 1e15) return SPEC_ERR_UNSUPPORTED;
@@ -504,7 +514,9 @@ int spec_cache_attend(const spec_cache *cache, const spec_attention *attn, void 
     const int rc = check_attention(cache, attn, c, p);
     if (rc != SPEC_OK) return rc;
     if (!out) return SPEC_ERR_INVALID_ARG;
-    if (reinterpret_cast<uintptr_t>(out) % elt_bytes(attn->dtype)) return SPEC_ERR_INVALID_ARG;
+    if (reinterpret_cast<uintptr_t>(out) % elt_bytes(attn->dtype) || !on_words(lse)) return SPEC_ERR_INVALID_ARG;
+    // (the parts of split tasks are read 16 bytes at a time)
+    if (reinterpret_cast<uintptr_t>(workspace) % 16) return SPEC_ERR_INVALID_ARG;
     if (!workspace || workspace_bytes < spec_cache_workspace_bytes(c.B, p.k_max, p.Hq, c.H, c.D, p.max_len))
         return SPEC_ERR_WORKSPACE;
     p.out = out;
@@ -521,7 +533,7 @@ int spec_cache_weights(const spec_cache *cache, const spec_attention *attn, cons
     AttnParams p;
     const int rc = check_attention(cache, attn, c, p);
     if (rc != SPEC_OK) return rc;
-    if (!lse || !score) return SPEC_ERR_INVALID_ARG;
+    if (!lse || !score || !on_words(lse, score)) return SPEC_ERR_INVALID_ARG;
     p.lse = const_cast<float *>(lse);
     p.score = score;
     const cudaError_t e = launch_cache_weights(c, p, attn->dtype, reinterpret_cast<cudaStream_t>(stream));
@@ -534,6 +546,8 @@ int spec_cache_evict(const spec_cache *cache, const spec_eviction *ev, spec_stre
     const int rc = check_cache(cache, c);
     if (rc != SPEC_OK) return rc;
     if (!ev || !ev->score || !ev->len || !ev->dst_table || !ev->kept || !ev->new_len)
+        return SPEC_ERR_INVALID_ARG;
+    if (!on_words(ev->score, ev->slot_pos, ev->len, ev->dst_table, ev->kept, ev->new_len, ev->status))
         return SPEC_ERR_INVALID_ARG;
     if (ev->budget < 1 || ev->recent < 0 || ev->recent > ev->budget || ev->dst_pages < 1)
         return SPEC_ERR_INVALID_ARG;

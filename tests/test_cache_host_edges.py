@@ -2,13 +2,14 @@
 made and how long they are kept when a call runs on another stream, and the
 refusals at the edges of the contract.  Devices, streams and the library are
 stood in for where a call would otherwise launch."""
+import ctypes as C
 import warnings
 
 import pytest
 import torch
 from torch._subclasses.fake_tensor import FakeTensorMode
 
-from tests.test_cache_host import sv  # noqa: F401
+from tests.test_cache_host import FAKE, _attn, _cache, _evict, _rows, sv  # noqa: F401
 
 
 class Streams:
@@ -135,3 +136,33 @@ def test_a_captured_call_is_left_to_its_graph(faked, monkeypatch):
     monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: st.current is st.side)
     call(st.side)
     assert st.log == [("launch", 2, "spec_cache_attend")]
+
+
+# ---------------------------------------------------------------- refusals ---
+
+ODD, HALF = C.c_void_p(0x10001), C.c_void_p(0x10002)
+
+
+def test_arrays_off_their_words_are_refused(sv):  # noqa: F811
+    """Device arrays of 32-bit values anywhere else, and a workspace off 16 bytes
+    (its parts are read by vectors): refused before a launch would touch them."""
+    L, n = sv.load_library(), 1 << 30
+    rows = lambda f, c, r: f(C.byref(c), C.byref(r), None)
+    attend = lambda c, a, lse=FAKE, ws=FAKE: L.spec_cache_attend(C.byref(c), C.byref(a), FAKE, lse, ws, n, None)
+    weights = lambda c, a, lse=FAKE, score=FAKE: L.spec_cache_weights(C.byref(c), C.byref(a), lse, score, None)
+    evict = lambda c, e: L.spec_cache_evict(C.byref(c), C.byref(e), None)
+    for off in (ODD, HALF):
+        for name in ("k_scale", "v_scale", "page_table"):
+            c = _cache(**{name: off})
+            assert rows(L.spec_cache_append, c, _rows()) == 1 and rows(L.spec_cache_read, c, _rows()) == 1, name
+            assert attend(c, _attn()) == 1 and weights(c, _attn()) == 1 and evict(c, _evict()) == 1, name
+        for name in ("cu_rows", "start", "score", "slot_pos", "pos0", "status"):
+            assert rows(L.spec_cache_append, _cache(), _rows(**{name: off})) == 1, name
+        for name in ("cu_rows", "len", "slopes", "slot_pos", "status"):
+            assert attend(_cache(), _attn(**{name: off})) == 1 and weights(_cache(), _attn(**{name: off})) == 1, name
+        assert attend(_cache(), _attn(), lse=off) == 1
+        assert weights(_cache(), _attn(), lse=off) == 1 and weights(_cache(), _attn(), score=off) == 1
+        for name in ("score", "slot_pos", "len", "dst_table", "kept", "new_len", "status"):
+            assert evict(_cache(), _evict(**{name: off})) == 1, name
+    for at in (0x10001, 0x10004, 0x10008):
+        assert attend(_cache(), _attn(), ws=C.c_void_p(at)) == 1
