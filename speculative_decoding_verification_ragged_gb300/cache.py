@@ -71,7 +71,7 @@ class PagedCache:
         self.pages, self.k_scale, self.v_scale = pages, k_scale, v_scale
 
     def _view(self, page_table, B: int) -> _Cache:
-        _same_device(self.pages, page_table)
+        _same_device(self.pages, page_table, self.k_scale, self.v_scale)
         if page_table.dim() != 2 or page_table.shape[0] < B:
             raise SpecError("page_table must be [B, max_pages]")
         return _Cache(_dev(self.pages, "pages", torch.uint8), self.n_pages, self.page_tokens, self.H,
@@ -280,6 +280,7 @@ def cache_attend(cache: PagedCache, q, cu_rows, cache_len, page_table, *, B: int
     window and prefix as in spec_cache.h.  Returns {"out" [R_cap, Hq, D],
     "lse" [R_cap, Hq]}; rows of no request are left unwritten."""
     L = load_library()
+    _same_device(cache.pages, workspace)
     view, attn = _attention(cache, q, cu_rows, cache_len, page_table, B, k_max, max_len, scale, cap,
                             slopes, window, prefix, slot_pos, status)
     with torch.cuda.stream(stream):

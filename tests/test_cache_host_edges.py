@@ -140,6 +140,40 @@ def test_a_captured_call_is_left_to_its_graph(faked, monkeypatch):
 
 # ---------------------------------------------------------------- refusals ---
 
+def test_tensors_of_another_device_are_refused(faked):
+    """... whichever argument they are: a pointer of another GPU must not reach a kernel."""
+    sv, st = faked
+    z, (q, cu, ln, tab) = st.z, st.args
+    f32, there = torch.float32, dict(dev="cuda:1")
+    kv, score, pos = z(4, 1, 64, d=f32), z(3, 32, d=f32), z(3, 32)
+    lse, ws = z(4, 2, d=f32), z(4096, d=torch.uint8)
+    call = dict(B=1)
+    attend = lambda c=None, q=q, cu=cu, ln=ln, tab=tab, **kw: sv.cache_attend(c or st.cache(), q, cu, ln, tab, k_max=3, **call, **kw)
+    weights = lambda c=None, q=q, lse=lse, tab=tab, score=score, **kw: sv.cache_weights(
+        c or st.cache(), q, lse, cu, ln, tab, score, k_max=3, **call, **kw)
+    append = lambda c=None, k=kv, v=kv, tab=tab, **kw: sv.cache_append(c or st.cache(), k, v, cu, ln, tab, max_rows=4, **call, **kw)
+    read = lambda c=None, cu=cu, tab=tab, **kw: sv.cache_read(c or st.cache(), cu, ln, tab, max_rows=4, **call, **kw)
+    evict = lambda c=None, score=score, tab=tab, dst=tab, **kw: sv.cache_evict(c or st.cache(), score, ln, tab, dst, budget=4, **call, **kw)
+    for f in (attend, weights, append, read, evict):
+        f()                                                          # all on one device: accepted
+        for kw in (dict(k_scale=z(1, d=f32, **there)), dict(v_scale=z(1, d=f32, **there))):
+            with pytest.raises(sv.SpecError, match="different devices"):
+                f(st.cache(**kw))
+        with pytest.raises(sv.SpecError, match="different devices"):
+            f(tab=z(1, 3, **there))
+        with pytest.raises(sv.SpecError, match="different devices"):
+            f(status=z(1, **there))
+    for f, kw in [(attend, dict(workspace=z(4096, d=torch.uint8, **there))), (attend, dict(q=z(4, 2, 64, d=f32, **there))),
+                  (attend, dict(slopes=z(2, d=f32, **there))), (attend, dict(slot_pos=z(3, 32, **there))),
+                  (weights, dict(lse=z(4, 2, d=f32, **there))), (weights, dict(score=z(3, 32, d=f32, **there))),
+                  (append, dict(v=z(4, 1, 64, d=f32, **there))), (append, dict(score=z(3, 32, d=f32, **there))),
+                  (append, dict(pos0=z(1, **there))), (read, dict(cu=z(2, **there))),
+                  (evict, dict(score=z(3, 32, d=f32, **there))), (evict, dict(dst=z(1, 3, **there))),
+                  (evict, dict(slot_pos=z(3, 32, **there)))]:
+        with pytest.raises(sv.SpecError, match="different devices"):
+            f(**kw)
+    attend(workspace=ws)
+
 ODD, HALF = C.c_void_p(0x10001), C.c_void_p(0x10002)
 
 
