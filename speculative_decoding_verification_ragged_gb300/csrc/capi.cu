@@ -148,6 +148,9 @@ int noalloc_scratch(void **ptr)
 
 // ---- the 4-bit paged cache ----
 
+// slots are 32-bit; kv heads and requests are the y and z of the grids
+constexpr int32_t kMostSlots = 1 << 30, kMostHeads = 65535, kMostRequests = 65535;
+
 // whether device arrays of 32-bit values lie on their words (null: absent)
 template <typename... T> bool on_words(const T *...p)
 {
@@ -164,9 +167,8 @@ int check_cache(const spec_cache *c, CacheView &v)
     if (reinterpret_cast<uintptr_t>(c->pages) % 16 || !on_words(c->k_scale, c->v_scale, c->page_table))
         return SPEC_ERR_INVALID_ARG;
     if (c->D != 64 && c->D != 128 && c->D != 256) return SPEC_ERR_UNSUPPORTED;
-    // slots are 32-bit; kv heads and requests are the y and z of the grids
-    if (c->page_tokens > 65536 || c->H > 65535 || c->B > 65535) return SPEC_ERR_UNSUPPORTED;
-    if (static_cast<int64_t>(c->max_pages) * c->page_tokens > (1 << 30)) return SPEC_ERR_UNSUPPORTED;
+    if (c->page_tokens > 65536 || c->H > kMostHeads || c->B > kMostRequests) return SPEC_ERR_UNSUPPORTED;
+    if (static_cast<int64_t>(c->max_pages) * c->page_tokens > kMostSlots) return SPEC_ERR_UNSUPPORTED;
     v.pages = static_cast<uint8_t *>(c->pages);
     v.n_pages = c->n_pages;
     v.page_tokens = c->page_tokens;
@@ -229,7 +231,7 @@ int check_attention(const spec_cache *cache, const spec_attention *a, CacheView 
     if (a->dtype != SPEC_F32 && a->dtype != SPEC_BF16) return SPEC_ERR_UNSUPPORTED;
     if (a->Hq < 1 || a->Hq % c.H || a->R_cap < 1 || a->k_max < 0 || a->window < 0 || a->prefix < 0)
         return SPEC_ERR_INVALID_ARG;
-    if (a->k_max > 31 || a->Hq > 65535) return SPEC_ERR_UNSUPPORTED;
+    if (a->k_max > 31 || a->Hq > kMostHeads) return SPEC_ERR_UNSUPPORTED;
     if (!(a->scale - a->scale == 0.f) || !(a->cap >= 0.f) || !(a->cap - a->cap == 0.f))
         return SPEC_ERR_INVALID_ARG;
     const int64_t room = static_cast<int64_t>(c.max_pages) * c.page_tokens;
@@ -503,6 +505,7 @@ size_t spec_cache_workspace_bytes(int32_t B, int32_t k_max, int32_t Hq, int32_t 
 {
     if (B < 1 || k_max < 0 || k_max > 31 || H < 1 || Hq < H || Hq % H || max_len < 1) return 0;
     if (D != 64 && D != 128 && D != 256) return 0;
+    if (B > kMostRequests || Hq > kMostHeads || max_len > kMostSlots) return 0;      // (no call accepts them)
     return cache_attend_workspace(B, k_max, Hq, H, D, max_len);
 }
 

@@ -200,3 +200,18 @@ def test_arrays_off_their_words_are_refused(sv):  # noqa: F811
             assert evict(_cache(), _evict(**{name: off})) == 1, name
     for at in (0x10001, 0x10004, 0x10008):
         assert attend(_cache(), _attn(), ws=C.c_void_p(at)) == 1
+
+
+def test_workspace_sizes_at_the_limits(sv):  # noqa: F811
+    """Every size that a call would accept has one, near that of the same grid of
+    blocks; sizes that no call accepts have none, with no sum wrapped on the way."""
+    L = sv.load_library()
+    full = L.spec_cache_workspace_bytes(4, 31, 64, 4, 128, 1 << 20)
+    assert 0 < full < 1 << 28
+    for ok in [(4, 31, 64, 4, 128, 1 << 30), (65535, 31, 64, 4, 128, 1 << 10), (4, 31, 65535, 65535, 128, 1 << 20)]:
+        assert 0 < L.spec_cache_workspace_bytes(*ok) <= full, ok
+    # one kv head for all: more columns, the widest tile
+    assert 0 < L.spec_cache_workspace_bytes(65535, 31, 65535, 1, 64, 1 << 20) < 1 << 28
+    for bad in [(4, 31, 64, 4, 128, 2 ** 31 - 1), (4, 31, 64, 4, 128, (1 << 30) + 1), (65536, 31, 64, 4, 128, 1024),
+                (4, 31, 2 ** 31 - 1, 1, 128, 1024), (4, 31, 65536, 4, 128, 1024), (4, 31, 2 ** 31 - 1, 2 ** 31 - 1, 128, 1024)]:
+        assert L.spec_cache_workspace_bytes(*bad) == 0, bad
