@@ -233,3 +233,42 @@ def test_a_bad_page_among_the_visible_ones_is_reported(gaps):
             s = k[see] @ q[0, h].double().cpu().numpy() / 8
             e = np.exp(s - s.max())
             np.testing.assert_allclose(res["out"][0, h].cpu().numpy(), e @ v[see] / e.sum(), rtol=1e-4, atol=1e-4)
+
+
+# ---------------------------------------------------------------------- read ---
+
+def to_bf16(x):
+    """x (64 bits, normal range) rounded once to bf16, ties to even."""
+    m, e = np.frexp(x)
+    return np.ldexp(np.rint(m * 256), e - 8)
+
+
+def test_read_rounds_once():
+    """Head scales that put products of up to 30 bits within a rounding to fp32 of a
+    tie of bf16: the values read are those of one rounding, all of them."""
+    sv = need_gpu()
+    rng = np.random.default_rng(45)
+    codes = np.unique(np.outer(ref.E2M1[1:], ref.E4M3[0x30:0x40]))    # what code * scale can be
+    g = []
+    while len(g) < 64:
+        a = rng.choice(codes)
+        tie = (2 * int(rng.integers(128, 256)) + 1) / 512               # half way between two bf16 values
+        x = np.float32(tie / a)
+        near = np.float64(x) * a
+        if near != tie and np.float64(np.float32(near)) == tie:
+            g.append(x)
+    g = np.array(g, np.float32)
+    c = quick_pool(rng, B=1, H=64, D=64, page=32, lens=[256])
+    live = rng.integers(0x30, 0x40, (c.n_pages, 64, 1, 2, 128), dtype=np.uint8)
+    c.pages[..., 16 * 64:18 * 64], c.pages[..., 34 * 64:] = live[..., 0, :], live[..., 1, :]
+    c.g = [g, g[::-1].copy()]
+    cache, twice = gpu_cache(sv, c), 0
+    args = (cache, dev(np.array([0, 256], np.int32)), dev(np.zeros(1, np.int32)), dev(c.table))
+    got = sv.cache_read(*args, B=1, max_rows=256, dtype=torch.bfloat16)
+    wide = sv.cache_read(*args, B=1, max_rows=256, dtype=torch.float32)
+    for h in range(64):
+        for name, x in zip("kv", c.get(0, h, np.arange(256))):
+            np.testing.assert_array_equal(got[name][:, h].double().cpu().numpy(), to_bf16(x))
+            np.testing.assert_array_equal(wide[name][:, h].cpu().numpy(), x.astype(np.float32))
+            twice += (to_bf16(x.astype(np.float32).astype(np.float64)) != to_bf16(x)).sum()
+    assert twice > 100                                               # (values that two roundings get wrong)
