@@ -3,8 +3,8 @@
 //
 // score_j += sum over rows and heads of exp(s_ij - lse_i): with S^T = K Q^T
 // (cache_attend.cuh) a token is a lane, and its sum over the columns and heads
-// stays in two threads (a half of the columns each), in a fixed order -- no
-// atomics, one read and one write of the score.  A CTA takes a few tiles of one
+// stays in two threads (a half of the columns each), in a fixed order, and is added to
+// the score once.  A CTA takes a few tiles of one
 // request through every kv head; the keys alone are read.  The product of a step
 // runs while the weights of the step before are summed and the next head's queries
 // are staged; warp 8 issues the products, warp 9 fetches, and the eight warps that
@@ -251,7 +251,8 @@ weights_kernel(const CacheView c, const AttnParams p, const int tiles)
             // (a slot that no row sees got 0, and its page may be another's by now)
             const float got = acc[t][0][tok] + acc[t][1][tok];
             const int page = slot < w.len && got != 0.f ? page_of(c, w.b, slot) : -1;
-            if (page >= 0) p.score[static_cast<int64_t>(page) * c.page_tokens + slot % c.page_tokens] += got;
+            // (requests can share a page: one addition that none of theirs falls into)
+            if (page >= 0) atomicAdd(p.score + static_cast<int64_t>(page) * c.page_tokens + slot % c.page_tokens, got);
         }
     }
     tmem_fence_before();

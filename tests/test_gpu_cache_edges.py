@@ -272,3 +272,32 @@ def test_read_rounds_once():
             np.testing.assert_array_equal(wide[name][:, h].cpu().numpy(), x.astype(np.float32))
             twice += (to_bf16(x.astype(np.float32).astype(np.float64)) != to_bf16(x)).sum()
     assert twice > 100                                               # (values that two roundings get wrong)
+
+
+# ------------------------------------------------------------------ sharing ---
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_requests_that_share_pages_all_count(dtype):
+    """48 requests behind one prompt: every one's weights arrive in its slots' scores."""
+    sv = need_gpu()
+    rng = np.random.default_rng(46)
+    B, page, shared = 48, 64, 512
+    lens = [shared + int(n) for n in rng.integers(2, 100, B)]
+    c = quick_pool(rng, B=B, H=2, D=64, page=page, lens=lens)
+    c.table[:, :shared // page] = c.table[0, :shared // page]
+    cu = np.arange(0, 2 * B + 1, 2)
+    q = queries(rng, 2 * B, 4, 64, dtype, 0.5)
+    cache, tab = gpu_cache(sv, c), dev(c.table)
+    cu_, ln = dev(cu.astype(np.int32)), dev(np.asarray(lens, np.int32))
+    res = sv.cache_attend(cache, q, cu_, ln, tab, B=B, k_max=1)
+    _, lse, _, S, w = ref.attention(c, q.float().cpu().numpy(), cu, lens)
+    want = np.zeros((c.n_pages, page))
+    for b, n in enumerate(lens):
+        np.add.at(want, (c.table[b, np.arange(n) // page], np.arange(n) % page), w[b])
+    u = 2.0 ** -24
+    # of each weight as for pages of one's own, and a rounding for every request's addition
+    rel = 2 * (64 * 2 * u + 4 * u) * S.max() + 4 * u * np.abs(lse).max() + 2.0 ** -18 + B * u
+    for _ in range(10):
+        score = torch.zeros(c.n_pages, page, device="cuda")
+        sv.cache_weights(cache, q, res["lse"], cu_, ln, tab, score, B=B, k_max=1)
+        assert (np.abs(score.cpu().numpy() - want) <= rel * want + 1e-30).all()
