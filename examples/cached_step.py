@@ -6,7 +6,7 @@ place of the target model and random tokens in the place of the draft's.
 
 Each step appends the k + 1 rows of every request, attends with them over the
 cache, verifies the drafts greedily, keeps the accepted prefix, and adds up the
-attention that the cached tokens got.  A request whose cache has outgrown its
+attention that the cached tokens got from the rows that stayed.  A request whose cache has outgrown its
 budget loses the tokens that got the least.
 """
 from __future__ import annotations
@@ -82,7 +82,10 @@ def run(steps: int = 12, B: int = 8, k: int = 4, V: int = 2048, Hq: int = 16, H:
         logits = att["out"].flatten(1) @ model.head
         check = torch.cat([drafts, drafts.new_zeros(B, 1)], 1).flatten().int()
         got = sv.verify_greedy(logits, cu, check, V=V, B=B, k_max=k)
-        sv.cache_weights(cache, query, att["lse"], cu, grown, tables[side], score, **options)
+        # rows of rejected drafts have no say in what is evicted: lse = -inf counts as 0
+        rejected = torch.arange(k + 1, device="cuda") > got["accepted_len"][:, None]
+        lse = att["lse"].view(B, k + 1, Hq).masked_fill(rejected[..., None], float("-inf")).flatten(0, 1)
+        sv.cache_weights(cache, query, lse, cu, grown, tables[side], score, **options)
         # the accepted drafts stay cached with the token before them; the next token
         # is not in the cache yet
         kept = got["accepted_len"] + 1

@@ -151,8 +151,9 @@ SPEC_API int spec_cache_attend(const spec_cache *cache, const spec_attention *at
 /*
  * score[slot] += sum over the request's rows r and all query heads h of
  * exp(s_rj - lse[r][h]) for every slot j that some row sees (s, masks and lse
- * as in spec_cache_attend, lse = -inf rows count 0): the attention each cached
- * token got this step.  score [n_pages, page_tokens].  A request's sum runs in a
+ * as in spec_cache_attend): the attention each cached token got this step.  Rows
+ * with lse = -inf count 0: those that saw nothing, and those that the caller marks
+ * so, as it should the rows of rejected drafts before weights that eviction goes by.  score [n_pages, page_tokens].  A request's sum runs in a
  * fixed order and is added to the slot's score once; requests that share a page (a
  * common prompt) all count, and which of them adds first is open: there, and there
  * alone, the last place can change from call to call.

@@ -301,3 +301,58 @@ def test_requests_that_share_pages_all_count(dtype):
         score = torch.zeros(c.n_pages, page, device="cuda")
         sv.cache_weights(cache, q, res["lse"], cu_, ln, tab, score, B=B, k_max=1)
         assert (np.abs(score.cpu().numpy() - want) <= rel * want + 1e-30).all()
+
+
+# ----------------------------------------------------------- rejected rows ---
+
+@pytest.mark.parametrize("kw", [dict(), dict(cap=20.0, window=50, prefix=2)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_rows_marked_by_an_infinite_lse_do_not_count(dtype, kw):
+    """The weights of the other rows alone, whatever the marked ones would have added."""
+    sv = need_gpu()
+    rng = np.random.default_rng(47)
+    lens, cu, took = [700, 33, 300], np.array([0, 4, 8, 12]), [1, 4, 2]
+    c = quick_pool(rng, B=3, H=2, D=64, page=64, lens=lens)
+    q = queries(rng, 12, 4, 64, dtype)
+    cache, tab = gpu_cache(sv, c), dev(c.table)
+    args = (dev(cu.astype(np.int32)), dev(np.asarray(lens, np.int32)), tab)
+    lse = sv.cache_attend(cache, q, *args, B=3, k_max=3, **kw)["lse"]
+    for b, n in enumerate(took):
+        lse[cu[b] + n:cu[b + 1]] = float("-inf")
+    score = torch.zeros(c.n_pages, 64, device="cuda")
+    sv.cache_weights(cache, q, lse, *args, score, B=3, k_max=3, **kw)
+    # the same rows by themselves: a cache that ends with the last one that stayed
+    short = [L - (4 - n) for L, n in zip(lens, took)]
+    rows = np.concatenate([np.arange(cu[b], cu[b] + n) for b, n in enumerate(took)])
+    _, exact, _, S, w = ref.attention(c, q[rows].float().cpu().numpy(), np.concatenate([[0], np.cumsum(took)]), short, **kw)
+    u = 2.0 ** -24
+    rel = 2 * ((64 * 2 * u + 4 * u) * S.max() + kw.get("cap", 0) * 2.0 ** -20) + 4 * u * np.abs(exact).max() + 2.0 ** -18
+    want = np.zeros((c.n_pages, 64))
+    for b, n in enumerate(short):
+        want[c.table[b, np.arange(n) // 64], np.arange(n) % 64] = w[b]
+    assert (np.abs(score.cpu().numpy() - want) <= rel * want + 1e-30).all()
+
+
+def test_the_example_leaves_rejected_rows_out(monkeypatch):
+    """What examples/cached_step.py passes to the weights: -inf for the rows after the
+    accepted prefix, a number for every other."""
+    sv = need_gpu()
+    from examples import cached_step
+    seen = []
+    verify, weights = sv.verify_greedy, sv.cache_weights
+
+    def verified(*a, **kw):
+        got = verify(*a, **kw)
+        seen.append(got["accepted_len"].tolist())
+        return got
+
+    def weighed(cache, q, lse, *a, **kw):
+        last = torch.isfinite(lse.view(8, 5, -1))
+        for b, n in enumerate(seen[-1]):
+            assert last[b, :n + 1].all() and not last[b, n + 1:].any()
+        return weights(cache, q, lse, *a, **kw)
+
+    monkeypatch.setattr(sv, "verify_greedy", verified)
+    monkeypatch.setattr(sv, "cache_weights", weighed)
+    cached_step.run(steps=6)
+    assert len(seen) == 6
