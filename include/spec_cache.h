@@ -142,7 +142,8 @@ SPEC_API size_t spec_cache_workspace_bytes(int32_t B, int32_t k_max, int32_t Hq,
  * NaN or infinite value gets unspecified results, as can the request's other rows
  * of the same kv head; every other row its own.  One launch.  bf16
  * outputs come from weights rounded to 11 bits, fp32 ones from 22 bits; sums of
- * weights, and so lse, are fp32.
+ * weights, and so lse, are fp32, and so are the sums of values, of which bf16's lose
+ * up to 2^-13 of themselves to truncation, over a cache of any length.
  */
 SPEC_API int spec_cache_attend(const spec_cache *cache, const spec_attention *attn, void *out,
                                float *lse, void *workspace, size_t workspace_bytes,
