@@ -10,6 +10,7 @@ there, and the caller waits for that stream before it uses the results elsewhere
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes as C
 import math
 from typing import Optional
@@ -91,6 +92,14 @@ def new_cache(n_pages: int, H: int, D: int, page_tokens: int = 64, device=None, 
     return PagedCache(pages, k_scale, v_scale)
 
 
+def _on(stream):
+    """The context in which a call for `stream` makes its tensors."""
+    return _HERE if stream is None else torch.cuda.stream(stream)
+
+
+_HERE = contextlib.nullcontext()
+
+
 def _tensors(x):
     """The tensors of a call's arguments and results, wherever they are kept."""
     if isinstance(x, torch.Tensor):
@@ -139,20 +148,20 @@ class CacheCall:
 
 def _run(fn, args, result, keep, device, prepared, stream, zeroed=False):
     """The call, or a handle of it where `prepared`.  Results (and `zeroed`: a
-    workspace) were made under torch.cuda.stream(stream), so that their memory is
-    `stream`'s from the start."""
+    workspace) were made under _on(stream), so that their memory is `stream`'s from
+    the start."""
     here = torch.cuda.current_stream(device)
     away = stream is not None and stream.cuda_stream != here.cuda_stream
     ready = None
     if prepared and zeroed:
-        with torch.cuda.stream(stream):
+        with _on(stream):
             if not torch.cuda.is_current_stream_capturing():
                 ready = torch.cuda.Event()
                 ready.record()
     call = CacheCall(fn, args, result, keep, device, set() if away else {here.cuda_stream}, ready)
     if prepared:
         return call
-    call(stream)
+    call(stream if away else here)
     if away:
         for t in _tensors(result):
             t.record_stream(here)        # the caller goes on with them here
@@ -231,7 +240,7 @@ def cache_read(cache: PagedCache, cu_rows, start, page_table, *, B: int, max_row
     view = cache._view(page_table, B)
     R_cap = B * max_rows if R_cap is None else int(R_cap)
     shape = (R_cap, cache.H, cache.D)
-    with torch.cuda.stream(stream):
+    with _on(stream):
         res = {n: torch.empty(shape, dtype=dtype, device=cache.pages.device) for n in ("k", "v")}
     kp, kr, kh = _heads(res["k"], "k", cache.D)
     vp, vr, vh = _heads(res["v"], "v", cache.D)
@@ -258,8 +267,8 @@ def new_cache_workspace(cache: PagedCache, page_table, *, B: int, k_max: int, Hq
 
 
 def _attention(cache, q, cu_rows, cache_len, page_table, B, k_max, max_len, scale, cap, slopes,
-               window, prefix, slot_pos, status):
-    _same_device(cache.pages, q, cu_rows, cache_len, slopes, slot_pos, status)
+               window, prefix, slot_pos, status, *more):
+    _same_device(cache.pages, q, cu_rows, cache_len, slopes, slot_pos, status, *more)
     view = cache._view(page_table, B)
     qp, qr, qh = _heads(q, "q", cache.D)
     return view, _Attention(
@@ -280,10 +289,9 @@ def cache_attend(cache: PagedCache, q, cu_rows, cache_len, page_table, *, B: int
     window and prefix as in spec_cache.h.  Returns {"out" [R_cap, Hq, D],
     "lse" [R_cap, Hq]}; rows of no request are left unwritten."""
     L = load_library()
-    _same_device(cache.pages, workspace)
     view, attn = _attention(cache, q, cu_rows, cache_len, page_table, B, k_max, max_len, scale, cap,
-                            slopes, window, prefix, slot_pos, status)
-    with torch.cuda.stream(stream):
+                            slopes, window, prefix, slot_pos, status, workspace)
+    with _on(stream):
         ws = workspace if workspace is not None else new_cache_workspace(
             cache, page_table, B=B, k_max=k_max, Hq=q.shape[1], max_len=max_len)
         res = {"out": torch.empty(q.shape, dtype=q.dtype, device=q.device),
@@ -300,11 +308,11 @@ def cache_weights(cache: PagedCache, q, lse, cu_rows, cache_len, page_table, sco
                   status=None, prepared: bool = False, stream=None):
     """spec_cache_weights: add to score [n_pages, page_tokens] the attention
     weight that each slot got from the rows of q, whose lse cache_attend gave
-    (same options).  Returns score."""
+    (same options); -inf there leaves a row out, as one of a rejected draft.  Returns
+    score."""
     L = load_library()
-    _same_device(cache.pages, lse, score)
     view, attn = _attention(cache, q, cu_rows, cache_len, page_table, B, k_max, max_len, scale, cap,
-                            slopes, window, prefix, slot_pos, status)
+                            slopes, window, prefix, slot_pos, status, lse, score)
     if lse.numel() != q.shape[0] * q.shape[1]:
         raise SpecError("lse must be [rows, Hq]")
     keep = (cache, q, lse, cu_rows, cache_len, page_table, score, slopes, slot_pos, status, view, attn)
@@ -324,7 +332,7 @@ def cache_evict(cache: PagedCache, score, cache_len, page_table, dst_table, *, B
     if dst_table.dim() != 2 or dst_table.shape[0] < B:
         raise SpecError("dst_table must be [B, pages]")
     dev = cache.pages.device
-    with torch.cuda.stream(stream):
+    with _on(stream):
         res = {"kept": torch.empty(B, int(budget), dtype=torch.int32, device=dev),
                "new_len": torch.empty(B, dtype=torch.int32, device=dev)}
     ev = _Eviction(_paged(score, "score", cache, torch.float32),
