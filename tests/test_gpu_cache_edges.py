@@ -131,6 +131,17 @@ def test_a_cap_too_small_for_its_reciprocal(dtype, cap):
 
 # -------------------------------------------------- slots that the window hides ---
 
+def poison(rng, c, hidden):
+    """NaN scales, and any others, in the given slots of each request."""
+    D = c.D
+    for b, slots in enumerate(hidden):
+        for s in slots:
+            blk = c.pages[c.table[b, s // c.page], :, s % c.page // 32]
+            t = s % 32
+            blk[:, 16 * D + t * (D // 16):16 * D + (t + 1) * (D // 16)] = rng.choice(np.array([0x7F, 0xFF, 0x30], np.uint8), D // 16)
+            blk[:, 34 * D + t:36 * D:32] = rng.choice(np.array([0x7F, 0xFF], np.uint8), D // 16)
+
+
 HIDDEN = [  # rows, window, prefix, positions with gaps
     (1, 1, 0, False), (4, 33, 3, False), (3, 150, 40, False), (4, 100, 130, False),
     (1, 1, 0, True), (4, 33, 3, True), (3, 150, 40, True), (4, 100, 130, True)]
@@ -169,14 +180,23 @@ def test_what_hidden_slots_hold_does_not_matter(D, page, dtype, rows, window, pr
     rng = np.random.default_rng(D + page + window)
     c, lens, cu, pos, hidden = hidden_case(rng, D, page, rows, window, prefix, gaps)
     assert any(len(h) for h in hidden)
-    for b, slots in enumerate(hidden):
-        for s in slots:
-            blk = c.pages[c.table[b, s // page], :, s % page // 32]
-            t = s % 32
-            blk[:, 16 * D + t * (D // 16):16 * D + (t + 1) * (D // 16)] = rng.choice(np.array([0x7F, 0xFF, 0x30], np.uint8), D // 16)
-            blk[:, 34 * D + t:36 * D:32] = rng.choice(np.array([0x7F, 0xFF], np.uint8), D // 16)
+    poison(rng, c, hidden)
     q = queries(rng, int(cu[-1]), 4, D, dtype)
     *_, status = check_attention(sv, c, q, cu, lens, rows - 1, window=window, prefix=prefix, slot_pos=pos)
+    assert status == 0
+
+
+@pytest.mark.parametrize("D,group,dtype", [(128, 12, "bf16"), (64, 16, "f32"), (256, 12, "bf16")])
+@pytest.mark.parametrize("gaps", [False, True])
+def test_what_hidden_slots_hold_over_many_columns(D, group, dtype, gaps):
+    """32 rows in several column tiles, each with hidden slots of its own: what is NaN
+    is hidden from all of them, what some row sees counts there."""
+    sv = need_gpu()
+    rng = np.random.default_rng(D + group)
+    c, lens, cu, pos, hidden = hidden_case(rng, D, 32, 32, 20, 5, gaps)
+    poison(rng, c, hidden)
+    q = queries(rng, int(cu[-1]), 2 * group, D, dtype, 0.5)
+    *_, status = check_attention(sv, c, q, cu, lens, 31, window=20, prefix=5, slot_pos=pos)
     assert status == 0
 
 
@@ -404,3 +424,45 @@ def test_long_sums_do_not_drift(D, H, B, rows, group, louder, cap):
     assert abs(float(err.mean())) <= 2.0 ** -5 + 5 / (3 * err.numel()) ** 0.5, float(err.mean())
     lse = got["lse"].view(B, rows, H, group)[:2, -1].double()
     assert float((lse - torch.log(den)).abs().max()) <= 1e-4
+
+
+# -------------------------------------------------- wide tables, large pages ---
+
+@pytest.mark.parametrize("kw", [dict(), dict(window=100, prefix=5), dict(window=100, prefix=5, gaps=True)])
+@pytest.mark.parametrize("page,dtype", [(32, "bf16"), (96, "f32"), (2048, "bf16"), (65536, "f32")])
+def test_a_table_for_far_longer_contexts(page, dtype, kw):
+    """Room for 131072 tokens and more, lengths up to 900: what the entries past a
+    length hold does not matter, for attention, weights and eviction alike."""
+    sv = need_gpu()
+    kw = dict(kw)
+    rng = np.random.default_rng(page)
+    lens, cu = [900, 33, 1, 300, 129], np.array([0, 3, 6, 7, 10, 12])
+    c = quick_pool(rng, B=5, H=2, D=64, page=page, lens=lens)
+    if kw.pop("gaps", False):
+        kw["slot_pos"] = gapped_positions(rng, c)
+    exact = c.table
+    wide = rng.integers(-2 ** 31, 2 ** 31, (5, 131072 // page + 3)).astype(np.int32)
+    for b, n in enumerate(lens):
+        used = -(-n // page)
+        wide[b, :used] = exact[b, :used]
+    c.table = wide
+    q = queries(rng, 12, 4, 64, dtype, 0.5)
+    *_, status = check_attention(sv, c, q, cu, lens, 2, **kw)
+    assert status == 0
+    budget, recent = 200, 16
+    per = -(-budget // page)
+    pool = np.concatenate([c.pages, np.zeros((5 * per, *c.pages.shape[1:]), np.uint8)])
+    score = rng.exponential(1, (len(pool), page)).astype(np.float32)
+    dst = np.arange(c.n_pages, len(pool)).reshape(5, per).astype(np.int32)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    cache = sv.PagedCache(dev(pool))
+    got = sv.cache_evict(cache, dev(score), dev(np.asarray(lens, np.int32)), dev(wide), dev(dst), B=5, budget=budget,
+                         recent=recent, status=status)
+    assert status.item() == 0
+    after = ref.Cache(cache.pages.cpu().numpy(), dst)
+    for b, n in enumerate(lens):
+        i = np.arange(n)
+        keep = ref.evict(score[wide[b, i // page], i % page], n, budget, recent)
+        np.testing.assert_array_equal(got["kept"][b].cpu().numpy(), np.concatenate([keep, np.full(budget - len(keep), -1)]))
+        for x, y in zip(after.get(b, 1, np.arange(len(keep))), c.get(b, 1, keep)):
+            np.testing.assert_array_equal(x, y)
