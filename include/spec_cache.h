@@ -41,7 +41,8 @@ extern "C" {
 
 /* further device status bits */
 #define SPEC_STATUS_BAD_PAGE   0x400u  /* page id outside [0, n_pages): its tokens are hidden / skipped */
-#define SPEC_STATUS_BAD_LENGTH 0x800u  /* length outside [0, max_pages * page_tokens]: request skipped  */
+#define SPEC_STATUS_BAD_LENGTH 0x800u  /* length outside [0, max_pages * page_tokens] (attention: [0,
+                                          max_len]): request skipped; its rows see nothing        */
 
 /* The cache as a batch of B requests sees it. */
 typedef struct {

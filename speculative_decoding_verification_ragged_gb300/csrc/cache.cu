@@ -91,7 +91,7 @@ __device__ __forceinline__ uint32_t quantise(const float (&x)[N], float g, uint3
 // CTA, so the value codes, two tokens to a byte, are read, merged and written
 // back without atomics.  A warp reads 512 bytes of a row's values per load; bound by
 // the instructions of the quantisation, about 1500 a warp and block: 27 k fp32 rows
-// of 8 heads of 64 take 49 us (2.3 TB/s of rows), and 82 with the read of them all.
+// of 8 heads of 64 take 62 us (1.8 TB/s of rows), and 95 with the read of them all.
 template <typename T, int D>
 __global__ void __launch_bounds__(kRowThreads) append_kernel(const CacheView c, const CacheRows r)
 {

@@ -12,7 +12,7 @@
 //
 // Bound by the latency of a step: 64 requests of 2 to 5 rows and 40 query heads over
 // up to 4096 tokens, ragged, take 66 us (1.2 TB/s of keys and scores), 128 x 5 rows x
-// 4096 tokens 147 us (2.1 TB/s).  With a barrier a step and fetches and products by
+// 4096 tokens 146 us (2.1 TB/s).  With a barrier a step and fetches and products by
 // the decoding warps those were 109 and 237 us (84 and 174 without, all CTAs in one
 // round; two rounds, which even out ragged requests, made the rest).
 #include "attend.cuh"
@@ -277,7 +277,8 @@ cudaError_t launch_one(const CacheView &c, const AttnParams &p, cudaStream_t s)
     // tiles a CTA: two rounds of resident CTAs where there are many requests, whose
     // lengths differ.  (Fewer stage a head's queries for more tiles, more even out the
     // lengths: with 1, 2, 3 and 5 rounds 64 requests x 5 rows, ragged up to 4096 tokens,
-    // took 84, 66, 81 and 92 us.)  A few requests are taken to be as long as max_len: the
+    // took 84, 66, 81 and 92 us; 2 x 65533 tokens of 16
+    // heads 70, and 81 with 2.)  A few requests are taken to be as long as max_len: the
     // fewest rounds, each of them a CTA's tiles and two tiles' time for the queries.  (4
     // requests x 5 rows x 16000 tokens 39 us against 56 in two rounds, 42 against 40 where
     // they are ragged; 8 x 16000 55 against 65, ragged 53 against 51; 16 x 8000 63
