@@ -7,7 +7,9 @@ device is present, the calls raise.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes as C
+import functools
 import os
 from typing import Optional
 
@@ -182,6 +184,46 @@ def _stream(stream) -> int:
     return s.cuda_stream
 
 
+_HERE = contextlib.nullcontext()
+
+
+def _on(stream):
+    """The context in which a call for `stream` makes its tensors: their memory is
+    that stream's from the start, and its zeros come before the launch."""
+    return _HERE if stream is None else torch.cuda.stream(stream)
+
+
+def _tensors(x):
+    """The tensors of a call's arguments and results, wherever they are kept."""
+    if isinstance(x, torch.Tensor):
+        yield x
+    elif isinstance(x, (tuple, list, dict)):
+        for y in (x.values() if isinstance(x, dict) else x):
+            yield from _tensors(y)
+    elif hasattr(x, "_tensors"):
+        yield from _tensors(x._tensors())
+
+
+def _streamed(f):
+    """A call's `stream`: workspace and results are made on it, and no memory of the
+    call is given away before the stream that uses it is through.  (Inputs have to be
+    ready there, and the caller waits for it before it uses the results elsewhere.)"""
+    @functools.wraps(f)
+    def call(*args, stream=None, **kw):
+        if stream is None:
+            return f(*args, **kw)
+        here = torch.cuda.current_stream()
+        with torch.cuda.stream(stream):
+            res = f(*args, stream=stream, **kw)
+        if stream.cuda_stream != here.cuda_stream:
+            for t in _tensors((args, kw)):
+                t.record_stream(stream)
+            for t in _tensors(res):
+                t.record_stream(here)
+        return res
+    return call
+
+
 def _logits_dtype(t: torch.Tensor) -> int:
     if t.dtype == torch.bfloat16 or t.dtype == torch.int16 or t.dtype == torch.uint16:
         return SPEC_BF16
@@ -259,6 +301,7 @@ def _outputs(B, k_max, R_cap, device, rows: bool, stats) -> tuple:
     return o, res
 
 
+@_streamed
 def verify_greedy(logits, cu_rows, draft_ids, *, V: int, B: int, k_max: int,
                   R_cap: Optional[int] = None, workspace=None, rows: bool = True, stats=None,
                   stream=None) -> dict:
@@ -277,6 +320,7 @@ def verify_greedy(logits, cu_rows, draft_ids, *, V: int, B: int, k_max: int,
     return res
 
 
+@_streamed
 def verify_greedy_noalloc(logits, cu_rows, draft_ids, *, V: int, B: int, k_max: int,
                           R_cap: Optional[int] = None, rows: bool = True, stats=None,
                           stream=None) -> dict:
@@ -299,6 +343,7 @@ def verify_greedy_noalloc(logits, cu_rows, draft_ids, *, V: int, B: int, k_max: 
     return res
 
 
+@_streamed
 def verify_relaxed_topk(logits, cu_rows, draft_ids, relaxed_k, *, V: int, B: int, k_max: int,
                         R_cap: Optional[int] = None, workspace=None, rows: bool = True,
                         stats=None, stream=None) -> dict:
@@ -314,6 +359,7 @@ def verify_relaxed_topk(logits, cu_rows, draft_ids, relaxed_k, *, V: int, B: int
     return res
 
 
+@_streamed
 def verify_greedy_active(logits, cu_rows, draft_ids, vocab_ids, *, V: int, B: int, k_max: int,
                          R_cap: Optional[int] = None, workspace=None, rows: bool = True,
                          stats=None, stream=None) -> dict:
@@ -333,6 +379,7 @@ def verify_greedy_active(logits, cu_rows, draft_ids, vocab_ids, *, V: int, B: in
     return res
 
 
+@_streamed
 def verify_greedy_margin(logits, cu_rows, draft_ids, margin, generated=None, protected_ids=None,
                          from_position: int = 0, after_tokens: int = 0, *, V: int, B: int,
                          k_max: int, R_cap: Optional[int] = None, workspace=None,
@@ -356,6 +403,7 @@ def verify_greedy_margin(logits, cu_rows, draft_ids, margin, generated=None, pro
     return res
 
 
+@_streamed
 def verify_sample(logits, cu_rows, draft_ids, temperature, top_k, top_p, min_p, seed,
                   request_id=None, step: int = 0, *, V: int, B: int, k_max: int,
                   R_cap: Optional[int] = None, workspace=None, rows: bool = True, stats=None,
@@ -379,6 +427,7 @@ def verify_sample(logits, cu_rows, draft_ids, temperature, top_k, top_p, min_p, 
     return res
 
 
+@_streamed
 def draft_confidence(draft_logits, *, V: int, B: int, k: int, selected=None,
                      threshold: float = 0.3, max_rows: int = 0, workspace=None,
                      stream=None) -> dict:
@@ -414,6 +463,7 @@ def draft_confidence(draft_logits, *, V: int, B: int, k: int, selected=None,
     return res
 
 
+@_streamed
 def restore_rows(compact: torch.Tensor, cu_rows, out: torch.Tensor, *, B: int, k_max: int,
                  status=None, stream=None) -> torch.Tensor:
     """spec_restore_rows: compact row cu_rows[b] + j goes to row
@@ -438,6 +488,7 @@ def restore_rows(compact: torch.Tensor, cu_rows, out: torch.Tensor, *, B: int, k
     return out
 
 
+@_streamed
 def prefix_stats(accepted_len, cu_rows, acc, ver, hist=None, status=None, *, B: int, k_max: int,
                  stream=None):
     """spec_prefix_stats: accumulate per-position prefix-acceptance counters
@@ -462,15 +513,16 @@ class PreparedSample:
                  workspace=None, rows: bool = True, stats=None, stream=None):
         self.L = load_library()
         R_cap = R_cap or B * (k_max + 1)
-        self.ws = workspace if workspace is not None else new_workspace(
-            R_cap, B, V, _logits_dtype(logits), logits.device, sampling=True)
+        with _on(stream):
+            self.ws = workspace if workspace is not None else new_workspace(
+                R_cap, B, V, _logits_dtype(logits), logits.device, sampling=True)
+            self.out, self.res = _outputs(B, k_max, R_cap, logits.device, rows, stats)
         self.batch = _batch(logits, V, B, k_max, R_cap, cu_rows, draft_ids)
         self.samp = Sampling(_dev(temperature, "temperature", torch.float32),
                              _dev(top_k, "top_k", torch.int32), _dev(top_p, "top_p", torch.float32),
                              _dev(min_p, "min_p", torch.float32), _dev(seed, "seed", torch.int64),
                              _dev(request_id, "request_id", torch.int32)
                              if request_id is not None else None, 0)
-        self.out, self.res = _outputs(B, k_max, R_cap, logits.device, rows, stats)
         self.stream = _stream(stream)
         self._keep = (logits, cu_rows, draft_ids, temperature, top_k, top_p, min_p, seed,
                       request_id, stats)

@@ -10,14 +10,13 @@ there, and the caller waits for that stream before it uses the results elsewhere
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes as C
 import math
 from typing import Optional
 
 import torch
 
-from .binding import SPEC_BF16, SPEC_F32, SpecError, _check, _dev, load_library
+from .binding import SPEC_BF16, SPEC_F32, SpecError, _check, _dev, _on, _tensors, load_library
 
 BLOCK_TOKENS = 32
 HEAD_CHANNELS = (64, 128, 256)
@@ -71,6 +70,9 @@ class PagedCache:
                 raise SpecError("%s needs one value per kv head" % what)
         self.pages, self.k_scale, self.v_scale = pages, k_scale, v_scale
 
+    def _tensors(self):
+        return self.pages, self.k_scale, self.v_scale
+
     def _view(self, page_table, B: int) -> _Cache:
         _same_device(self.pages, page_table, self.k_scale, self.v_scale)
         if page_table.dim() != 2 or page_table.shape[0] < B:
@@ -90,25 +92,6 @@ def new_cache(n_pages: int, H: int, D: int, page_tokens: int = 64, device=None, 
     pages = torch.zeros(n_pages, H, page_tokens // BLOCK_TOKENS, 36 * D, dtype=torch.uint8,
                         device=device or "cuda")
     return PagedCache(pages, k_scale, v_scale)
-
-
-def _on(stream):
-    """The context in which a call for `stream` makes its tensors."""
-    return _HERE if stream is None else torch.cuda.stream(stream)
-
-
-_HERE = contextlib.nullcontext()
-
-
-def _tensors(x):
-    """The tensors of a call's arguments and results, wherever they are kept."""
-    if isinstance(x, torch.Tensor):
-        yield x
-    elif isinstance(x, PagedCache):
-        yield from _tensors((x.pages, x.k_scale, x.v_scale))
-    elif isinstance(x, (tuple, dict)):
-        for y in (x.values() if isinstance(x, dict) else x):
-            yield from _tensors(y)
 
 
 class CacheCall:
