@@ -173,7 +173,7 @@ typedef struct {
     const int32_t *dst_table;  /* [B, dst_pages] pages that receive the kept tokens           */
     int32_t dst_pages;
     int32_t *kept;             /* [B, budget] kept slots, ascending, -1 padded                */
-    int32_t *new_len;          /* [B] min(len, budget)                                        */
+    int32_t *new_len;          /* [B] min(len, budget); can be len itself                     */
     uint32_t *status;          /* [1] or NULL                                                 */
 } spec_eviction;
 

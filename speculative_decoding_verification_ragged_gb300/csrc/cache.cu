@@ -329,7 +329,9 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const CacheVi
     }
     // (the same in every CTA of the cluster: none is left waiting)
     const int all = ctas * kSelThreads, me = rank * kSelThreads + tid;
+    // (new_len can be len: written when the cluster has read it)
     if (bad) {
+        cluster.sync();
         if (me == 0) {
             set_status(p.status, bad);
             p.new_len[b] = -1;
@@ -337,9 +339,10 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const CacheVi
         for (int i = me; i < p.budget; i += all) kept[i] = -1;
         return;
     }
-    if (me == 0) p.new_len[b] = keep;
     for (int i = keep + me; i < p.budget; i += all) kept[i] = -1;
     if (len <= p.budget) {
+        cluster.sync();
+        if (me == 0) p.new_len[b] = keep;
         for (int i = me; i < len; i += all) kept[i] = i;
         return;
     }
@@ -472,6 +475,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const CacheVi
     else
         select([&](int i) { return score_key(p.score[score_at(i)]); });
     for (int i = me; i < p.recent; i += all) kept[keep - p.recent + i] = old + i;
+    if (me == 0) p.new_len[b] = keep;
 }
 
 constexpr int kMoveThreads = 128;

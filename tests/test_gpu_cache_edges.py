@@ -466,3 +466,32 @@ def test_a_table_for_far_longer_contexts(page, dtype, kw):
         np.testing.assert_array_equal(got["kept"][b].cpu().numpy(), np.concatenate([keep, np.full(budget - len(keep), -1)]))
         for x, y in zip(after.get(b, 1, np.arange(len(keep))), c.get(b, 1, keep)):
             np.testing.assert_array_equal(x, y)
+
+
+# --------------------------------------------------------- lengths in place ---
+
+def test_eviction_can_update_the_lengths_in_place():
+    """new_len in the place of len, with clusters of 8 blocks a request: kept, cut,
+    and skipped requests alike, time and again."""
+    import ctypes as C
+    from speculative_decoding_verification_ragged_gb300.cache import _Eviction
+    sv = need_gpu()
+    rng = np.random.default_rng(48)
+    page, budget, recent = 128, 6000, 64
+    lens = [131072, 5000, 131072, 9000, -1, 100, 131072, 6000] * 4
+    B, per, dper = len(lens), 1024, -(-budget // page)
+    pages = torch.zeros(per + B * dper, 1, 4, 36 * 64, dtype=torch.uint8, device="cuda")
+    score = dev(rng.exponential(1, (len(pages), page)).astype(np.float32))
+    table = dev(np.tile(rng.permutation(per).astype(np.int32), (B, 1)))               # (read only: one prompt for all)
+    dst = dev(np.arange(per, len(pages)).reshape(B, dper).astype(np.int32))
+    cache = sv.PagedCache(pages)
+    before = dev(np.asarray(lens, np.int32))
+    want = sv.cache_evict(cache, score, before, table, dst, B=B, budget=budget, recent=recent)
+    view = cache._view(table, B)
+    for _ in range(10):
+        ln, kept = before.clone(), torch.empty_like(want["kept"])
+        ev = _Eviction(score.data_ptr(), None, ln.data_ptr(), budget, recent, dst.data_ptr(), dper, kept.data_ptr(),
+                       ln.data_ptr(), None)
+        assert sv.load_library().spec_cache_evict(C.byref(view), C.byref(ev), torch.cuda.current_stream().cuda_stream) == 0
+        torch.cuda.synchronize()
+        assert torch.equal(ln, want["new_len"]) and torch.equal(kept, want["kept"])
