@@ -138,7 +138,8 @@ SPEC_API size_t spec_cache_workspace_bytes(int32_t B, int32_t k_max, int32_t Hq,
  * and need no id: their entries are not looked at, and with slot_pos, where only
  * positions tell, bad ids that follow hidden slots (or begin the cache, with
  * position 0 hidden) count as such and are not reported.  out [R_cap, Hq, D], lse
- * [R_cap, Hq] or NULL, both contiguous; rows >= cu_rows[B] are not written.
+ * [R_cap, Hq] or NULL, both contiguous; rows >= cu_rows[B], and those of a request
+ * with malformed cu_rows (SPEC_STATUS_BAD_ROWS), are not written.
  * Results do not depend on the order in which blocks run.  A query row with a
  * NaN or infinite value gets unspecified results, as can the request's other rows
  * of the same kv head; every other row its own.  One launch.  bf16
