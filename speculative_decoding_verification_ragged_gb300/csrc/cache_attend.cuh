@@ -20,7 +20,10 @@
 // are rescaled then), so that P stays below 2^15 and keeps its 11 bits down to
 // x = -25.  A tile with a visible weight below that takes the product with bf16
 // operands instead (values exact in bf16 too, weights as a sum of two or three
-// bf16 terms): small weights keep their bits, whatever the largest is.
+// bf16 terms): small weights keep their bits, whatever the largest is.  (11 bits are
+// enough for bf16 outputs: a second f16 term took 147 us over 128 ragged requests and
+// 172 over 4 x 131071 tokens, against 139 and 163, and left the error against 64 bits
+// where it is, 0.0016 to 0.0017 in norm, that of the outputs' own rounding.)
 // bf16 queries are exact in f16 once scaled by a power of two; fp32 queries and
 // the weights of fp32 outputs are a sum of two f16 (22 bits), and their products
 // with V^T are added up tile by tile in fp32 registers (the tensor cores'
