@@ -152,6 +152,18 @@ SPEC_API int spec_cache_attend(const spec_cache *cache, const spec_attention *at
                                spec_stream stream);
 
 /*
+ * The same where a request's rows are the nodes of a tree: parent [R_cap] as in spec_tree.h.
+ * Row i of request b sees the slots before the step's, j < len_b - n_b, of the step's slots those of its
+ * ancestors and its own, and no others.  Its position is that of the root's slot plus its depth (a
+ * row that hangs on no other has depth 0), and so is its slot's, for slopes and window: with slot_pos, only
+ * the root's entry is read of the step's slots.  With len_b < n_b its rows see nothing
+ * (SPEC_STATUS_BAD_LENGTH).  Workspace as for spec_cache_attend; it may be shared.
+ */
+SPEC_API int spec_cache_attend_tree(const spec_cache *cache, const spec_attention *attn,
+                                    const int32_t *parent, void *out, float *lse, void *workspace,
+                                    size_t workspace_bytes, spec_stream stream);
+
+/*
  * score[slot] += sum over the request's rows r and all query heads h of
  * exp(s_rj - lse[r][h]) for every slot j that some row sees (s, masks and lse
  * as in spec_cache_attend): the attention each cached token got this step.  Rows

@@ -34,6 +34,11 @@ STATUS_BAD_RELAXED_K = 0x40
 STATUS_BAD_BUDGET = 0x80
 STATUS_TIMEOUT = 0x100
 STATUS_BAD_MARGIN = 0x200
+STATUS_BAD_PAGE = 0x400
+STATUS_BAD_LENGTH = 0x800
+STATUS_BAD_TREE = 0x1000
+STATUS_BAD_PENALTY = 0x2000
+STATUS_BAD_MASK = 0x4000
 
 EXPORTS = ["spec_workspace_bytes", "spec_draft_workspace_bytes", "spec_verify_greedy",
            "spec_verify_greedy_noalloc", "spec_verify_relaxed_topk",
@@ -43,7 +48,8 @@ EXPORTS = ["spec_workspace_bytes", "spec_draft_workspace_bytes", "spec_verify_gr
            "spec_step_state_bytes", "spec_step_init", "spec_step_update", "spec_step_query",
            "spec_step_cost_sps", "spec_step_cost_additive",
            "spec_cache_append", "spec_cache_read", "spec_cache_workspace_bytes",
-           "spec_cache_attend", "spec_cache_weights", "spec_cache_evict"]
+           "spec_cache_attend", "spec_cache_attend_tree", "spec_cache_weights", "spec_cache_evict",
+           "spec_prompt_workspace_bytes", "spec_prompt_attend", "spec_tree_accept", "spec_adjust_logits"]
 
 
 class SpecError(RuntimeError):
@@ -137,8 +143,14 @@ def load_library(path: Optional[str] = None) -> C.CDLL:
     L.spec_cache_attend.argtypes = [vp, vp, vp, vp, vp, C.c_size_t, vp]
     L.spec_cache_weights.argtypes = [vp, vp, vp, vp, vp]
     L.spec_cache_evict.argtypes = [vp, vp, vp]
-    for f in ["spec_cache_append", "spec_cache_read", "spec_cache_attend", "spec_cache_weights",
-              "spec_cache_evict"]:
+    L.spec_cache_attend_tree.argtypes = [vp, vp, vp, vp, vp, vp, C.c_size_t, vp]
+    L.spec_prompt_workspace_bytes.argtypes = [i32] * 4
+    L.spec_prompt_workspace_bytes.restype = C.c_size_t
+    L.spec_prompt_attend.argtypes = [vp, vp, vp, vp, C.c_size_t, vp]
+    L.spec_tree_accept.argtypes = [vp, vp]
+    L.spec_adjust_logits.argtypes = [vp, vp, i64, vp]
+    for f in ["spec_cache_append", "spec_cache_read", "spec_cache_attend", "spec_cache_attend_tree", "spec_cache_weights",
+              "spec_cache_evict", "spec_prompt_attend", "spec_tree_accept", "spec_adjust_logits"]:
         getattr(L, f).restype = C.c_int
     L.spec_step_state_bytes.restype = C.c_size_t
     L.spec_step_state_bytes.argtypes = []

@@ -1,5 +1,5 @@
 """Binding of the 4-bit paged cache (include/spec_cache.h): append, read,
-attend, weights, evict.
+attend (chains and trees of rows), weights, evict.
 
 Argument marshalling only, like binding.py.  Every function takes
 `prepared=True` to return a CacheCall instead of running: its arguments are
@@ -151,12 +151,12 @@ def _run(fn, args, result, keep, device, prepared, stream, zeroed=False):
     return result
 
 
-def _same_device(a, *others):
+def _same_device(a, *others, what="the cache"):
     if not a.is_cuda:
-        raise SpecError("the cache must be on a CUDA device")
+        raise SpecError("%s must be on a CUDA device" % what)
     if a.device.index != torch.cuda.current_device():
-        raise SpecError("the cache is on %s but the current device is cuda:%d"
-                        % (a.device, torch.cuda.current_device()))
+        raise SpecError("%s is on %s but the current device is cuda:%d"
+                        % (what, a.device, torch.cuda.current_device()))
     for t in others:
         if t is not None and t.device != a.device:
             raise SpecError("tensors on different devices: %s and %s" % (a.device, t.device))
@@ -184,6 +184,7 @@ def _paged(x, what: str, cache: PagedCache, dtype):
 
 
 def _per_request(x, what: str, n: int, dtype=torch.int32):
+    """The pointer of an array of n entries at least, or None."""
     if x is not None and x.numel() < n:
         raise SpecError("%s needs %d entries" % (what, n))
     return _dev(x, what, dtype)
@@ -283,6 +284,28 @@ def cache_attend(cache: PagedCache, q, cu_rows, cache_len, page_table, *, B: int
     args = (C.byref(view), C.byref(attn), res["out"].data_ptr(), res["lse"].data_ptr(),
             _dev(ws, "workspace", torch.uint8), ws.numel())
     return _run(L.spec_cache_attend, args, res, keep, q.device, prepared, stream, zeroed=workspace is None)
+
+
+def cache_attend_tree(cache: PagedCache, q, cu_rows, cache_len, page_table, parent, *, B: int, k_max: int,
+                      max_len: Optional[int] = None, scale: Optional[float] = None, cap: float = 0.0,
+                      slopes=None, window: int = 0, prefix: int = 0, slot_pos=None, workspace=None,
+                      status=None, prepared: bool = False, stream=None):
+    """spec_cache_attend_tree: cache_attend where a request's rows are the nodes of a
+    tree (parent [R_cap], as in spec_tree.h): a row sees the slots before the step's, its
+    ancestors' and its own.  Returns {"out" [R_cap, Hq, D], "lse" [R_cap, Hq]}; rows of no
+    request are left unwritten."""
+    L = load_library()
+    view, attn = _attention(cache, q, cu_rows, cache_len, page_table, B, k_max, max_len, scale, cap,
+                            slopes, window, prefix, slot_pos, status, parent, workspace)
+    with _on(stream):
+        ws = workspace if workspace is not None else new_cache_workspace(
+            cache, page_table, B=B, k_max=k_max, Hq=q.shape[1], max_len=max_len)
+        res = {"out": torch.empty(q.shape, dtype=q.dtype, device=q.device),
+               "lse": torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)}
+    keep = (cache, q, cu_rows, cache_len, page_table, parent, slopes, slot_pos, status, ws, view, attn)
+    args = (C.byref(view), C.byref(attn), _per_request(parent, "parent", q.shape[0]), res["out"].data_ptr(),
+            res["lse"].data_ptr(), _dev(ws, "workspace", torch.uint8), ws.numel())
+    return _run(L.spec_cache_attend_tree, args, res, keep, q.device, prepared, stream, zeroed=workspace is None)
 
 
 def cache_weights(cache: PagedCache, q, lse, cu_rows, cache_len, page_table, score, *, B: int,

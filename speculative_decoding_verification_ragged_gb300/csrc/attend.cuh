@@ -75,13 +75,14 @@ __device__ __forceinline__ void visible_steps(const CacheView &c, const AttnPara
 }
 
 // Rows and length of request w.b: false where it has no rows to attend with.
-// `status`: where to report what is wrong with it, or null.
-template <int STEP>
+// `status`: where to report what is wrong with it, or null.  TREE: the rows are a tree's, and
+// all of them have to be in the cache.
+template <int STEP, bool TREE = false>
 __device__ __forceinline__ bool load_job(const CacheView &c, const AttnParams &p, Job &w, uint32_t *status)
 {
     if (!request_rows(p.cu_rows, w.b, p.R_cap, p.k_max + 1, status, w.lo, w.n) || w.n == 0) return false;
     w.len = p.len[w.b];
-    if (w.len < 0 || w.len > p.max_len) {
+    if (w.len < (TREE ? w.n : 0) || w.len > p.max_len) {
         set_status(status, SPEC_STATUS_BAD_LENGTH);
         w.len = 0;
     }

@@ -19,8 +19,9 @@ size_t cache_attend_workspace(int B, int k_max, int Hq, int H, int D, int max_le
 
 cudaError_t launch_cache_attend(const CacheView &c, const AttnParams &p, int dtype, cudaStream_t s)
 {
-    if (p.cap > 0.f || p.slopes || p.window > 0) return launch_cache_attend_options(c, p, dtype, s);
-    return launch_attend<false>(c, p, dtype, s);
+    const bool options = p.cap > 0.f || p.slopes || p.window > 0;
+    if (p.parent) return options ? launch_cache_attend_tree_options(c, p, dtype, s) : launch_cache_attend_tree(c, p, dtype, s);
+    return options ? launch_cache_attend_options(c, p, dtype, s) : launch_attend<false, false>(c, p, dtype, s);
 }
 
 }  // namespace specv

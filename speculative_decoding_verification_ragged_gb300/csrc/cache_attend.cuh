@@ -1,7 +1,8 @@
 // cache_attend.cuh -- the kernel of the attention of packed verify rows over the
 // 4-bit paged cache (include/spec_cache.h); cache_attend.cu has it plain,
-// cache_attend_options.cu with the score options (each kernel's code stays small:
-// what runs once a segment is fetched anew each time).
+// cache_attend_options.cu with the score options, cache_attend_tree.cu and
+// cache_attend_tree_options.cu the same for rows that are a tree's (each kernel's code
+// stays small: what runs once a segment is fetched anew each time).
 //
 // For one request and kv head the step's query rows are columns of a matrix:
 // column j * group + g is row j of query head h * group + g.  Over tiles of 128
@@ -42,6 +43,7 @@
 #pragma once
 
 #include "attend.cuh"
+#include "tree.cuh"
 
 namespace specv {
 
@@ -226,7 +228,7 @@ template <int NT> struct Columns {
     float slope[NT];            // distance slope (log2 units)
     float factor[NT];           // rescale of a column whose reference moved
     float sum[NT];
-    int own[NT], pos[NT];       // last slot the column sees, its position
+    int own[NT], pos[NT];       // last slot the column sees (TREE: the nodes it sees, a bit each), its position
     float run[NT];              // ref of the sums over the runs of tiles so far
     int fresh[NT];              // reference: 0 set, 1 to be set to the tile's maximum, 2 nothing seen yet
     float red[4][NT];
@@ -237,15 +239,17 @@ struct Token {
     int slot, pos;
     bool live;                  // it exists
     bool edge;                  // some row may not see some token of the quarter
+    uint32_t node;              // TREE: its node's bit, or all bits where it lies before the step's slots
 };
 
 // Scores of a token in log2 units, the column's reference added (x + headroom),
 // for this thread's columns from q0 on; hidden ones -inf.
-template <typename A, bool OPT>
+template <typename A, bool OPT, bool TREE>
 __device__ __forceinline__ void token_scores(const AttnParams &p, const Job &w, const Columns<A::NT> &cs, uint32_t s_addr,
                                              int q0, const Token &t, float (&v)[A::NH])
 {
     constexpr int N = A::NH;
+    const auto seen = [&](int q) { return TREE ? (cs.own[q0 + q] & t.node) != 0 : t.slot <= cs.own[q0 + q]; };
     load_products<N, A::NT, A::PIECES>(s_addr + q0, v);
     if constexpr (!OPT) {
 #pragma unroll
@@ -260,7 +264,7 @@ __device__ __forceinline__ void token_scores(const AttnParams &p, const Job &w, 
         if (t.edge) {
 #pragma unroll
             for (int q = 0; q < N; ++q)
-                v[q] = t.live && t.slot <= cs.own[q0 + q] && q0 + q < w.ncols ? v[q] : -INFINITY;
+                v[q] = t.live && seen(q) && q0 + q < w.ncols ? v[q] : -INFINITY;
         }
     } else {
 #pragma unroll
@@ -274,7 +278,7 @@ __device__ __forceinline__ void token_scores(const AttnParams &p, const Job &w, 
 #pragma unroll
         for (int q = 0; q < N; ++q) {
             const int dist = cs.pos[q0 + q] - t.pos;
-            const bool see = t.slot <= cs.own[q0 + q] && (always || (t.live && dist < p.window)) && q0 + q < w.ncols;
+            const bool see = seen(q) && (always || (t.live && dist < p.window)) && q0 + q < w.ncols;
             v[q] = see ? v[q] - cs.slope[q0 + q] * static_cast<float>(dist) + cs.ref[q0 + q] : -INFINITY;
         }
     }
@@ -390,7 +394,7 @@ template <bool OPT> __device__ __forceinline__ int tile_slot(const Segment &s, i
 
 // A place in the line: task `task` (head * column tiles + column tile) of
 // request w.b, unit `unit` of it.
-template <int NT> struct Cursor {
+template <int NT, bool TREE> struct Cursor {
     Job w;
     int64_t at, end;            // units of the line: here, and where this CTA's range ends
     int qt, tasks, task, unit;
@@ -425,7 +429,7 @@ template <int NT> struct Cursor {
                         at = end;
                         break;
                     }
-                } while (!load_job<kTile>(c, p, w, nullptr));
+                } while (!load_job<kTile, TREE>(c, p, w, nullptr));
                 if (at < end) start(c, group);
             }
             if (some) return true;
@@ -435,7 +439,7 @@ template <int NT> struct Cursor {
 
 // Where this CTA's range begins: every thread takes a request at a time, a scan
 // of their units places them.
-template <int NT>
+template <int NT, bool TREE>
 __device__ __forceinline__ int64_t find_range(const CacheView &c, const AttnParams &p, const Layout &lay, int group,
                                               int &grid, int64_t &t0, Job &job, int64_t &off)
 {
@@ -446,7 +450,7 @@ __device__ __forceinline__ int64_t find_range(const CacheView &c, const AttnPara
     Job w;
     const auto weight = [&](int b, bool report) {
         w.b = b;
-        if (b >= c.B || !load_job<kTile>(c, p, w, report && blockIdx.x == 0 ? p.status : nullptr)) return static_cast<int64_t>(0);
+        if (b >= c.B || !load_job<kTile, TREE>(c, p, w, report && blockIdx.x == 0 ? p.status : nullptr)) return static_cast<int64_t>(0);
         return static_cast<int64_t>(c.H) * ((w.n * group + NT - 1) / NT) * (kTaskUnits + w.nsteps);
     };
     // inclusive scan over the CTA; `all`: its total
@@ -508,7 +512,7 @@ __device__ __forceinline__ int64_t find_range(const CacheView &c, const AttnPara
 // into weights (one barrier: do the references hold?), decode the next tile's
 // keys, then this tile's values; each product runs while they decode the other
 // operand, and they meet the other two at mbarriers only.
-template <typename T, int D, int NT, bool OPT>
+template <typename T, int D, int NT, bool OPT, bool TREE>
 __global__ void __launch_bounds__(kAttnThreads + 64, (Attn<T, D, NT>::CTAS))
 attend_kernel(const CacheView c, const AttnParams p, const Layout lay)
 {
@@ -530,6 +534,7 @@ attend_kernel(const CacheView c, const AttnParams p, const Layout lay)
     constexpr int kFirst = 1, kLast = 2, kEnd = 4;
     __shared__ int keys_are, weights_wide;
     __shared__ __align__(16) int nv[A::STAGES][4], pages[A::STAGES][4];
+    __shared__ int depth[TREE ? 32 : 1], root_pos;    // of the tree's nodes; the root's position
     __shared__ __align__(16) uint32_t lit[2][4];      // tokens of a tile that the window does not hide from all columns
     const int tid = threadIdx.x, warp = warp_index(), lane = tid & 31;
     const int group = p.Hq / c.H;
@@ -549,10 +554,10 @@ attend_kernel(const CacheView c, const AttnParams p, const Layout lay)
         mbar_init(&o_bar, 1);
         fence_mbar_init();
     }
-    Cursor<NT> cur;
+    Cursor<NT, TREE> cur;
     int grid;
     int64_t off;
-    const int64_t total = find_range<NT>(c, p, lay, group, grid, cur.at, cur.w, off);
+    const int64_t total = find_range<NT, TREE>(c, p, lay, group, grid, cur.at, cur.w, off);
     if (static_cast<int>(blockIdx.x) >= grid) return;
     if (warp == 0) tmem_alloc(&tmem_base, A::COLS);
     __syncthreads();
@@ -719,11 +724,25 @@ attend_kernel(const CacheView c, const AttnParams p, const Layout lay)
         const int n = seg.n;
         if (csync_count(fail || n < 0)) break;
         const float gk = c.k_scale ? c.k_scale[w.h] : 1.f, gv = c.v_scale ? c.v_scale[w.h] : 1.f;
+        const int root = w.len - w.n;                 // slot of the first row
+        uint32_t nodes = 0;
+        if (TREE && warp < (NT + 31) / 32) {
+            // a lane a node; then a lane a column
+            const uint32_t anc = tree_ancestors(tree_parent(p.parent, w.lo, w.n, p.status));
+            nodes = __shfl_sync(0xFFFFFFFFu, anc, min((w.col0 + tid) / group, w.n - 1));
+            if (warp == 0) depth[lane] = __popc(anc) - 1;
+            if (tid == 0) root_pos = w.len > 0 ? slot_position(c, p, w.b, root) : 0;
+        }
         if (tid < NT) {
             const int col = w.col0 + tid, j = min(col / group, w.n - 1);
             const int own = w.len > 0 ? w.len - w.n + j : -1;
-            cs.own[tid] = own;
-            cs.pos[tid] = own >= 0 ? slot_position(c, p, w.b, own) : 0;
+            if (TREE) {
+                cs.own[tid] = w.len > 0 ? nodes : 0u;
+                cs.pos[tid] = w.len > 0 ? slot_position(c, p, w.b, root) + __popc(nodes) - 1 : 0;
+            } else {
+                cs.own[tid] = own;
+                cs.pos[tid] = own >= 0 ? slot_position(c, p, w.b, own) : 0;
+            }
             cs.slope[tid] = p.slopes && tid < w.ncols ? p.slopes[w.h * group + col % group] * kLog2e : 0.f;
             cs.ref[tid] = kHeadroom;                  // (a padded column's results are unused)
             cs.fresh[tid] = 1;
@@ -737,7 +756,7 @@ attend_kernel(const CacheView c, const AttnParams p, const Layout lay)
         for (int i = 0; i < NH; ++i) l[i] = 0.f;
 #pragma unroll
         for (int i = 0; i < OR; ++i) acc[i] = 0.f;
-        const int own_first = cs.own[0];
+        const int own_first = TREE ? root - 1 : cs.own[0];        // last slot that all columns see, so far as the rows go
         if (n > 0) keys(ring, ring_phase, tile_slot<OPT>(seg, 0), kFirst | (n == 1 ? kLast : 0));
         // tiles in runs of kRun (fp32: all in one).  (Jumped back to: a loop around took
         // 166 us over 4 x 131071 tokens, and 140.3 over 128 ragged requests, against 163
@@ -755,6 +774,11 @@ attend_kernel(const CacheView c, const AttnParams p, const Layout lay)
             t.pos = pos;
             t.live = whole || lane < nv[ring][quarter];
             t.edge = !whole || slot0 + kTile - 1 > own_first;
+            if (TREE) {
+                const int node = t.slot - root;
+                t.node = node < 0 ? 0xFFFFFFFFu : (node < 32 ? 1u << node : 0u);
+                if (OPT && node >= 0 && node < w.n) t.pos = root_pos + depth[node];
+            }
             value_scales<D>(stage, nv[ring], whole, vsk);
             uint64_t *const done = &empty[ring];
             if (++ring == A::STAGES) {
@@ -767,7 +791,7 @@ attend_kernel(const CacheView c, const AttnParams p, const Layout lay)
             if (OPT && p.window > 0 && half == 0) {
                 // (the first column's row sees no later slots than the others, and no fewer)
                 const bool dark = own_first >= 0 && t.slot >= p.prefix &&
-                                  t.pos <= static_cast<int64_t>(cs.pos[0]) - p.window;
+                                  t.pos <= static_cast<int64_t>(TREE ? root_pos : cs.pos[0]) - p.window;
                 const uint32_t seen = __ballot_sync(0xFFFFFFFFu, !dark);
                 if (lane == 0) lit[buf][quarter] = seen;
             }
@@ -776,7 +800,7 @@ attend_kernel(const CacheView c, const AttnParams p, const Layout lay)
             // weights, and whether they are fit for f16: none beyond 2^15 (the reference
             // has to move) and no visible one without its bits (1: too large, 2: too small)
             const auto weigh = [&] {
-                token_scores<A, OPT>(p, w, cs, s_t + lane_off, half * NH, t, x);
+                token_scores<A, OPT, TREE>(p, w, cs, s_t + lane_off, half * NH, t, x);
 #pragma unroll
                 for (int q = 0; q < NH; ++q) v[q] = ex2(x[q]);
 #pragma unroll
@@ -1044,7 +1068,7 @@ template <typename A> size_t workspace_of(int B, int k_max, int Hq, int H, int m
     return kTicketBytes + static_cast<size_t>(l.grid) * 2 * A::NT * (A::D + 2) * 4;
 }
 
-template <typename T, int D, int NT, bool OPT>
+template <typename T, int D, int NT, bool OPT, bool TREE>
 cudaError_t launch_one(const CacheView &c, const AttnParams &p, cudaStream_t s)
 {
     using A = Attn<T, D, NT>;
@@ -1054,12 +1078,12 @@ cudaError_t launch_one(const CacheView &c, const AttnParams &p, cudaStream_t s)
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     if (!done[dev]) {
-        e = cudaFuncSetAttribute(attend_kernel<T, D, NT, OPT>, cudaFuncAttributeMaxDynamicSharedMemorySize, A::SMEM);
+        e = cudaFuncSetAttribute(attend_kernel<T, D, NT, OPT, TREE>, cudaFuncAttributeMaxDynamicSharedMemorySize, A::SMEM);
         if (e != cudaSuccess) return e;
         done[dev] = true;
     }
     const Layout l = layout_of<A>(c.B, p.k_max, p.Hq, c.H, p.max_len);
-    attend_kernel<T, D, NT, OPT><<<l.grid, kAttnThreads + 64, A::SMEM, s>>>(c, p, l);
+    attend_kernel<T, D, NT, OPT, TREE><<<l.grid, kAttnThreads + 64, A::SMEM, s>>>(c, p, l);
     return cudaGetLastError();
 }
 
@@ -1078,11 +1102,11 @@ template <typename F> auto with_kernel(int dtype, int D, int cols, F f)
     return nt == 16 ? f(Attn<B, 256, 16>()) : f(Attn<B, 256, 32>());
 }
 
-template <bool OPT> cudaError_t launch_attend(const CacheView &c, const AttnParams &p, int dtype, cudaStream_t s)
+template <bool OPT, bool TREE> cudaError_t launch_attend(const CacheView &c, const AttnParams &p, int dtype, cudaStream_t s)
 {
     return with_kernel(dtype, c.D, (p.k_max + 1) * (p.Hq / c.H), [&](auto a) {
         using A = decltype(a);
-        return launch_one<typename A::Type, A::D, A::NT, OPT>(c, p, s);
+        return launch_one<typename A::Type, A::D, A::NT, OPT, TREE>(c, p, s);
     });
 }
 

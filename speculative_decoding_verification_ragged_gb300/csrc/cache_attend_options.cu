@@ -6,7 +6,7 @@ namespace specv {
 
 cudaError_t launch_cache_attend_options(const CacheView &c, const AttnParams &p, int dtype, cudaStream_t s)
 {
-    return launch_attend<true>(c, p, dtype, s);
+    return launch_attend<true, false>(c, p, dtype, s);
 }
 
 }  // namespace specv

@@ -9,6 +9,8 @@
 #include "common.cuh"
 #include "internal.h"
 #include "spec_cache.h"
+#include "spec_prompt.h"
+#include "spec_tree.h"
 
 using namespace specv;
 
@@ -223,6 +225,53 @@ int run_cache_rows(const spec_cache *cache, const spec_cache_rows *r, bool appen
     return e == cudaSuccess ? SPEC_OK : cuda_fail(e);
 }
 
+bool finite_f32(float x) { return x - x == 0.f; }
+
+int check_prompt(const spec_prompt *a, PromptParams &p)
+{
+    if (!a || !a->q || !a->k || !a->v || !a->cu_rows) return SPEC_ERR_INVALID_ARG;
+    if (a->dtype != SPEC_F32 && a->dtype != SPEC_BF16) return SPEC_ERR_UNSUPPORTED;
+    if (a->H < 1 || a->Hq < 1 || a->Hq % a->H || a->B < 1 || a->R_cap < 1 || a->K_cap < 1 || a->window < 0 || a->prefix < 0)
+        return SPEC_ERR_INVALID_ARG;
+    if (!finite_f32(a->scale) || !finite_f32(a->cap) || a->cap < 0.f) return SPEC_ERR_INVALID_ARG;
+    const size_t elt = elt_bytes(a->dtype);
+    for (const void *x : {a->q, a->k, a->v})
+        if (reinterpret_cast<uintptr_t>(x) % elt) return SPEC_ERR_INVALID_ARG;
+    if (!on_words(a->cu_rows, a->cu_keys, a->slopes, a->status)) return SPEC_ERR_INVALID_ARG;
+    if (a->D != 64 && a->D != 128 && a->D != 256) return SPEC_ERR_UNSUPPORTED;
+    // rows and keys are 32-bit, and so are packed rows and tiles; kv heads are the y of the grid
+    if (a->H > kMostHeads || a->B > kMostRequests || a->R_cap > kMostSlots || a->K_cap > kMostSlots) return SPEC_ERR_UNSUPPORTED;
+    if (static_cast<int64_t>(a->R_cap) * (a->Hq / a->H) > INT32_MAX - 65536) return SPEC_ERR_UNSUPPORTED;
+    std::memset(&p, 0, sizeof p);
+    p.q = a->q;
+    p.k = a->k;
+    p.v = a->v;
+    p.q_row = a->q_row;
+    p.q_head = a->q_head;
+    p.k_row = a->k_row;
+    p.k_head = a->k_head;
+    p.v_row = a->v_row;
+    p.v_head = a->v_head;
+    p.Hq = a->Hq;
+    p.H = a->H;
+    p.D = a->D;
+    p.B = a->B;
+    p.R_cap = a->R_cap;
+    p.K_cap = a->K_cap;
+    p.cu_rows = a->cu_rows;
+    p.cu_keys = a->cu_keys;
+    p.scale = a->scale;
+    p.cap = a->cap;
+    p.slopes = a->slopes;
+    p.window = a->window;
+    p.prefix = a->prefix < kMostSlots ? a->prefix : kMostSlots;
+    p.status = a->status;
+    p.q_aligned = rows_aligned(a->q, a->q_row, a->q_head, elt);
+    p.k_aligned = rows_aligned(a->k, a->k_row, a->k_head, elt);
+    p.v_aligned = rows_aligned(a->v, a->v_row, a->v_head, elt);
+    return SPEC_OK;
+}
+
 int check_attention(const spec_cache *cache, const spec_attention *a, CacheView &c, AttnParams &p)
 {
     const int rc = check_cache(cache, c);
@@ -263,6 +312,28 @@ int check_attention(const spec_cache *cache, const spec_attention *a, CacheView 
     p.status = a->status;
     p.q_aligned = rows_aligned(a->q, a->q_row, a->q_head, elt_bytes(a->dtype));
     return SPEC_OK;
+}
+
+// attention over the cache of chains of rows, or of trees (parent)
+int run_attend(const spec_cache *cache, const spec_attention *attn, const int32_t *parent, void *out, float *lse,
+               void *workspace, size_t workspace_bytes, spec_stream stream)
+{
+    CacheView c;
+    AttnParams p;
+    const int rc = check_attention(cache, attn, c, p);
+    if (rc != SPEC_OK) return rc;
+    if (!out) return SPEC_ERR_INVALID_ARG;
+    if (reinterpret_cast<uintptr_t>(out) % elt_bytes(attn->dtype) || !on_words(lse)) return SPEC_ERR_INVALID_ARG;
+    // (the parts of split tasks are read 16 bytes at a time)
+    if (reinterpret_cast<uintptr_t>(workspace) % 16) return SPEC_ERR_INVALID_ARG;
+    if (!workspace || workspace_bytes < spec_cache_workspace_bytes(c.B, p.k_max, p.Hq, c.H, c.D, p.max_len))
+        return SPEC_ERR_WORKSPACE;
+    p.out = out;
+    p.lse = lse;
+    p.ws = workspace;
+    p.parent = parent;
+    const cudaError_t e = launch_cache_attend(c, p, attn->dtype, reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? SPEC_OK : cuda_fail(e);
 }
 
 }  // namespace
@@ -512,20 +583,112 @@ size_t spec_cache_workspace_bytes(int32_t B, int32_t k_max, int32_t Hq, int32_t 
 int spec_cache_attend(const spec_cache *cache, const spec_attention *attn, void *out, float *lse,
                       void *workspace, size_t workspace_bytes, spec_stream stream)
 {
-    CacheView c;
-    AttnParams p;
-    const int rc = check_attention(cache, attn, c, p);
+    return run_attend(cache, attn, nullptr, out, lse, workspace, workspace_bytes, stream);
+}
+
+int spec_cache_attend_tree(const spec_cache *cache, const spec_attention *attn, const int32_t *parent, void *out,
+                           float *lse, void *workspace, size_t workspace_bytes, spec_stream stream)
+{
+    if (!parent || !on_words(parent)) return SPEC_ERR_INVALID_ARG;
+    return run_attend(cache, attn, parent, out, lse, workspace, workspace_bytes, stream);
+}
+
+size_t spec_prompt_workspace_bytes(int32_t Hq, int32_t H, int32_t D, int32_t dtype)
+{
+    if (H < 1 || Hq < 1 || Hq % H || H > kMostHeads || (D != 64 && D != 128 && D != 256)) return 0;
+    if (dtype != SPEC_F32 && dtype != SPEC_BF16) return 0;
+    return 256;
+}
+
+int spec_prompt_attend(const spec_prompt *prompt, void *out, float *lse, void *workspace,
+                       size_t workspace_bytes, spec_stream stream)
+{
+    PromptParams p;
+    const int rc = check_prompt(prompt, p);
     if (rc != SPEC_OK) return rc;
-    if (!out) return SPEC_ERR_INVALID_ARG;
-    if (reinterpret_cast<uintptr_t>(out) % elt_bytes(attn->dtype) || !on_words(lse)) return SPEC_ERR_INVALID_ARG;
-    // (the parts of split tasks are read 16 bytes at a time)
+    if (!out || reinterpret_cast<uintptr_t>(out) % elt_bytes(prompt->dtype) || !on_words(lse)) return SPEC_ERR_INVALID_ARG;
     if (reinterpret_cast<uintptr_t>(workspace) % 16) return SPEC_ERR_INVALID_ARG;
-    if (!workspace || workspace_bytes < spec_cache_workspace_bytes(c.B, p.k_max, p.Hq, c.H, c.D, p.max_len))
-        return SPEC_ERR_WORKSPACE;
+    if (!workspace || workspace_bytes < spec_prompt_workspace_bytes(p.Hq, p.H, p.D, prompt->dtype)) return SPEC_ERR_WORKSPACE;
     p.out = out;
     p.lse = lse;
     p.ws = workspace;
-    const cudaError_t e = launch_cache_attend(c, p, attn->dtype, reinterpret_cast<cudaStream_t>(stream));
+    const cudaError_t e = launch_prompt_rows(p, prompt->dtype, reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? SPEC_OK : cuda_fail(e);
+}
+
+int spec_tree_accept(const spec_tree *t, spec_stream stream)
+{
+    if (!t || !t->cu_rows || !t->row_token || !t->node_token || !t->parent) return SPEC_ERR_INVALID_ARG;
+    if (!t->accepted_len || !t->out_tokens || !t->next_token) return SPEC_ERR_INVALID_ARG;
+    if (t->B < 1 || t->k_max < 0 || t->R_cap < 1) return SPEC_ERR_INVALID_ARG;
+    if (!on_words(t->cu_rows, t->row_token, t->node_token, t->parent, t->accepted_len, t->out_tokens, t->next_token,
+                  t->path_rows, t->status))
+        return SPEC_ERR_INVALID_ARG;
+    if (t->k_max > 31) return SPEC_ERR_UNSUPPORTED;
+    TreeParams p;
+    p.B = t->B;
+    p.k_max = t->k_max;
+    p.R_cap = t->R_cap;
+    p.cu_rows = t->cu_rows;
+    p.row_token = t->row_token;
+    p.node_token = t->node_token;
+    p.parent = t->parent;
+    p.accepted_len = t->accepted_len;
+    p.out_tokens = t->out_tokens;
+    p.next_token = t->next_token;
+    p.path_rows = t->path_rows;
+    p.status = t->status;
+    const cudaError_t e = launch_tree_accept(p, reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? SPEC_OK : cuda_fail(e);
+}
+
+int spec_adjust_logits(const spec_logit_rules *r, void *out, int64_t out_ld, spec_stream stream)
+{
+    if (!r || !r->logits || !r->cu_rows || !out) return SPEC_ERR_INVALID_ARG;
+    if (r->dtype != SPEC_F32 && r->dtype != SPEC_BF16) return SPEC_ERR_UNSUPPORTED;
+    if (r->V < 1 || r->ld < r->V || out_ld < r->V || r->B < 1 || r->R_cap < 1 || r->k_max < 0) return SPEC_ERR_INVALID_ARG;
+    const size_t elt = elt_bytes(r->dtype);
+    if (reinterpret_cast<uintptr_t>(r->logits) % elt || reinterpret_cast<uintptr_t>(out) % elt) return SPEC_ERR_INVALID_ARG;
+    if (out == r->logits && out_ld != r->ld) return SPEC_ERR_INVALID_ARG;
+    if (r->history && (!r->n_tokens || r->history_cap < 0 || r->history_ld < r->history_cap)) return SPEC_ERR_INVALID_ARG;
+    if (r->bias_cu && (r->n_bias < 0 || (r->n_bias > 0 && (!r->bias_ids || !r->bias_values)))) return SPEC_ERR_INVALID_ARG;
+    if (r->allowed && (r->n_allowed < 1 || r->allowed_ld < (static_cast<int64_t>(r->V) + 31) / 32)) return SPEC_ERR_INVALID_ARG;
+    if (!on_words(r->cu_rows, r->history, r->n_tokens, r->n_prompt, r->repetition, r->frequency, r->presence, r->node_token,
+                  r->parent, r->bias_cu, r->bias_ids, r->bias_values, r->allowed, r->allowed_row, r->status))
+        return SPEC_ERR_INVALID_ARG;
+    // requests are the y of the grid, counts leave two bits of their words
+    if (r->k_max > 31 || r->B > kMostRequests || r->V > kMostSlots || (r->history && r->history_cap > kMostSlots - 64))
+        return SPEC_ERR_UNSUPPORTED;
+    LogitParams p;
+    p.logits = r->logits;
+    p.ld = r->ld;
+    p.V = r->V;
+    p.B = r->B;
+    p.k_max = r->k_max;
+    p.R_cap = r->R_cap;
+    p.cu_rows = r->cu_rows;
+    p.history = r->history;
+    p.history_ld = r->history_ld;
+    p.history_cap = r->history_cap;
+    p.n_tokens = r->n_tokens;
+    p.n_prompt = r->n_prompt;
+    p.repetition = r->repetition;
+    p.frequency = r->frequency;
+    p.presence = r->presence;
+    p.node_token = r->node_token;
+    p.parent = r->parent;
+    p.bias_cu = r->bias_cu;
+    p.bias_ids = r->bias_ids;
+    p.bias_values = r->bias_values;
+    p.n_bias = r->n_bias;
+    p.allowed = r->allowed;
+    p.allowed_ld = r->allowed_ld;
+    p.n_allowed = r->n_allowed;
+    p.allowed_row = r->allowed_row;
+    p.status = r->status;
+    p.out = out;
+    p.out_ld = out_ld;
+    const cudaError_t e = launch_adjust_logits(p, r->dtype, reinterpret_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? SPEC_OK : cuda_fail(e);
 }
 

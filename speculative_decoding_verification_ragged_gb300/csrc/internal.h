@@ -126,8 +126,56 @@ struct AttnParams {
     void *out;
     float *lse;                  // attend: written; weights: read
     float *score;                // weights only
+    const int32_t *parent;       // the rows as a tree (or null: a chain)
     void *ws;
     bool q_aligned;              // every query starts on a 16-byte boundary
+};
+
+// Whole prompts over themselves (include/spec_prompt.h).
+struct PromptParams {
+    const void *q, *k, *v;
+    int64_t q_row, q_head, k_row, k_head, v_row, v_head;
+    int32_t Hq, H, D, B, R_cap, K_cap;
+    const int32_t *cu_rows, *cu_keys;    // cu_keys null: cu_rows
+    float scale, cap;
+    const float *slopes;
+    int32_t window, prefix;
+    uint32_t *status;
+    void *out;
+    float *lse;
+    void *ws;
+    bool q_aligned, k_aligned, v_aligned;    // every head starts on a 16-byte boundary
+};
+
+// Trees of drafts and the adjustment of logits (include/spec_tree.h).
+struct TreeParams {
+    int32_t B, k_max, R_cap;
+    const int32_t *cu_rows, *row_token, *node_token, *parent;
+    int32_t *accepted_len, *out_tokens, *next_token, *path_rows;
+    uint32_t *status;
+};
+
+struct LogitParams {
+    const void *logits;
+    int64_t ld;
+    int32_t V, B, k_max, R_cap;
+    const int32_t *cu_rows;
+    const int32_t *history;
+    int64_t history_ld;
+    int32_t history_cap;
+    const int32_t *n_tokens, *n_prompt;
+    const float *repetition, *frequency, *presence;
+    const int32_t *node_token, *parent;
+    const int32_t *bias_cu, *bias_ids;
+    const float *bias_values;
+    int32_t n_bias;
+    const uint32_t *allowed;
+    int64_t allowed_ld;
+    int32_t n_allowed;
+    const int32_t *allowed_row;
+    uint32_t *status;
+    void *out;
+    int64_t out_ld;
 };
 
 struct EvictParams {
@@ -145,13 +193,22 @@ cudaError_t launch_cache_rows(const CacheView &c, const CacheRows &r, int dtype,
                               cudaStream_t stream);
 cudaError_t launch_cache_attend(const CacheView &c, const AttnParams &p, int dtype,
                                 cudaStream_t stream);
-// the same with a cap, distance biases or a window (called by launch_cache_attend)
+// the same with a cap, distance biases or a window, and for trees of rows (called by
+// launch_cache_attend)
 cudaError_t launch_cache_attend_options(const CacheView &c, const AttnParams &p, int dtype,
                                         cudaStream_t stream);
+cudaError_t launch_cache_attend_tree(const CacheView &c, const AttnParams &p, int dtype,
+                                     cudaStream_t stream);
+cudaError_t launch_cache_attend_tree_options(const CacheView &c, const AttnParams &p, int dtype,
+                                             cudaStream_t stream);
 cudaError_t launch_cache_weights(const CacheView &c, const AttnParams &p, int dtype,
                                  cudaStream_t stream);
 // workspace bytes of the attention (for queries of either type)
 size_t cache_attend_workspace(int B, int k_max, int Hq, int H, int D, int max_len);
+// attention of prompts on the CUDA cores, either type
+cudaError_t launch_prompt_rows(const PromptParams &p, int dtype, cudaStream_t stream);
+cudaError_t launch_tree_accept(const TreeParams &p, cudaStream_t stream);
+cudaError_t launch_adjust_logits(const LogitParams &p, int dtype, cudaStream_t stream);
 cudaError_t launch_cache_evict(const CacheView &c, const EvictParams &p, cudaStream_t stream);
 
 // Host launchers (return cudaError_t of the launch).
