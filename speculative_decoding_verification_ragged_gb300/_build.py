@@ -12,7 +12,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OUT = os.path.join(PKG, "libspecverify.so")
 SOURCES = ["verify.cu", "rows.cu", "draft.cu", "cache.cu", "cache_attend.cu", "cache_attend_options.cu",
-           "cache_attend_tree.cu", "cache_attend_tree_options.cu", "cache_weights.cu", "prompt_rows.cu", "tree.cu",
+           "cache_attend_tree.cu", "cache_attend_tree_options.cu", "cache_weights.cu", "prompt_rows.cu",
+           "prompt_tiles.cu", "prompt_tiles_options.cu", "tree.cu",
            "capi.cu", "step_policy.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

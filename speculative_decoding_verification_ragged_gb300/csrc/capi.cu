@@ -263,7 +263,8 @@ int check_prompt(const spec_prompt *a, PromptParams &p)
     p.scale = a->scale;
     p.cap = a->cap;
     p.slopes = a->slopes;
-    p.window = a->window;
+    // (no key lies further before a row, nor further from the first: sums of these stay in 32 bits)
+    p.window = a->window < kMostSlots ? a->window : kMostSlots;
     p.prefix = a->prefix < kMostSlots ? a->prefix : kMostSlots;
     p.status = a->status;
     p.q_aligned = rows_aligned(a->q, a->q_row, a->q_head, elt);
@@ -597,7 +598,7 @@ size_t spec_prompt_workspace_bytes(int32_t Hq, int32_t H, int32_t D, int32_t dty
 {
     if (H < 1 || Hq < 1 || Hq % H || H > kMostHeads || (D != 64 && D != 128 && D != 256)) return 0;
     if (dtype != SPEC_F32 && dtype != SPEC_BF16) return 0;
-    return 256;
+    return prompt_workspace(D, dtype);
 }
 
 int spec_prompt_attend(const spec_prompt *prompt, void *out, float *lse, void *workspace,
@@ -612,7 +613,7 @@ int spec_prompt_attend(const spec_prompt *prompt, void *out, float *lse, void *w
     p.out = out;
     p.lse = lse;
     p.ws = workspace;
-    const cudaError_t e = launch_prompt_rows(p, prompt->dtype, reinterpret_cast<cudaStream_t>(stream));
+    const cudaError_t e = launch_prompt(p, prompt->dtype, reinterpret_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? SPEC_OK : cuda_fail(e);
 }
 

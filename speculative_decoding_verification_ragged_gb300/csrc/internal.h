@@ -205,7 +205,10 @@ cudaError_t launch_cache_weights(const CacheView &c, const AttnParams &p, int dt
                                  cudaStream_t stream);
 // workspace bytes of the attention (for queries of either type)
 size_t cache_attend_workspace(int B, int k_max, int Hq, int H, int D, int max_len);
-// attention of prompts on the CUDA cores, either type
+// attention of prompts, and its workspace
+cudaError_t launch_prompt(const PromptParams &p, int dtype, cudaStream_t stream);
+size_t prompt_workspace(int D, int dtype);
+// on the CUDA cores, either type (called by launch_prompt)
 cudaError_t launch_prompt_rows(const PromptParams &p, int dtype, cudaStream_t stream);
 cudaError_t launch_tree_accept(const TreeParams &p, cudaStream_t stream);
 cudaError_t launch_adjust_logits(const LogitParams &p, int dtype, cudaStream_t stream);

@@ -1,0 +1,548 @@
+// prompt_tiles.cuh -- the kernel of the attention of bf16 prompts over themselves on the tensor
+// cores (include/spec_prompt.h); prompt_tiles.cu has it plain, prompt_tiles_options.cu
+// with the score options.
+//
+// A work item is a kv head and NQ tiles of up to 128 packed rows (TT rows of all the query heads of the
+// kv head: g heads need a key once).  Over steps of KT keys
+//     S = Q K^T c,  P = 2^(S - m),  O += P V,
+// m a reference per row that moves only when a score passes it by 2^8: O, which lies in tensor
+// memory, is rescaled then and not with every step.  P is the tensor cores' A operand from tensor memory;
+// it is bf16 as V is (8 bits: the error it brings is of the size of the output's own rounding), the sums
+// of weights are taken in fp32 before that rounding.
+//
+// Warps: four for each tile's softmax (a thread a row), one that issues the products, one that fetches (tiled TMA
+// with the 128-byte swizzle) and hands out the items.  D = 64 and 128 keep two tiles in the CTA, whose products
+// alternate: one tile's weights are made while the other's products run.  D = 256 has room for one, and S twice: the
+// next step's S runs beside this step's weights.
+#pragma once
+
+#include "attend.cuh"
+#include "prompt.cuh"
+
+namespace specv {
+
+struct PromptMaps {
+    CUtensorMap q, k, v;
+};
+
+namespace {
+
+constexpr float kLazy = 8.f;               // log2 units a score may pass the reference by
+constexpr int kPromptSms = 152, kPromptTickets = 256;
+// Tensor memory truncates what it adds up: a run of keys at most, then the sum goes to fp32 in the
+// workspace.
+constexpr int kRunKeys = 16384;
+
+template <int D_> struct Prompt {
+    static constexpr int D = D_;
+    static constexpr int NQ = D == 256 ? 1 : 2;                // tiles of rows
+    static constexpr int NS = 2;                               // S in tensor memory: one a tile, or two of one
+    static constexpr int KT = D == 256 ? 64 : 128;             // keys of a step
+    static constexpr int RUN = kRunKeys / KT;
+    static constexpr int Q_TILE = 128 * D * 2, SLOT = KT * D * 2;
+    static constexpr int SLOTS = D == 64 ? 8 : 5;              // of K or V
+    static constexpr int SMEM = NQ * Q_TILE + SLOTS * SLOT + 1024;
+    static constexpr int SOFTMAX = NQ * 128, THREADS = SOFTMAX + 64;
+    // Tensor memory: S, O, P.  Products of one shape run in their order, so that at D = 128 P can take the place of
+    // its S, which the next S product then overwrites; at 64 and 256 the shapes differ, and P has columns of its own.
+    static constexpr int O_COL = NS * KT;
+    static constexpr int P_COL = D == 128 ? 0 : O_COL + NQ * D, P_STEP = D == 128 ? KT : KT / 2;
+    static_assert((D == 128 ? O_COL + NQ * D : P_COL + NS * P_STEP) <= 512, "tensor memory");
+};
+
+// A work item.
+struct Item {
+    PromptTile t;
+    int h, first;               // kv head (-1: there are no more); first row of the tiles
+    int n[2];                   // steps that each tile sees
+    int np, f0;                 // steps to visit: 0 .. np - 1, then f0, f0 + 1, ...
+};
+
+__device__ __forceinline__ int item_step(const Item &it, int i) { return i < it.np ? i : it.f0 + i - it.np; }
+
+// 2^x for a weight
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+template <int D, bool OPT>
+__global__ void __launch_bounds__(Prompt<D>::THREADS, 1)
+prompt_tiles_kernel(const PromptParams p, const __grid_constant__ PromptMaps maps)
+{
+    using A = Prompt<D>;
+    constexpr int NQ = A::NQ, KT = A::KT, SLOTS = A::SLOTS, kItems = 2;
+    constexpr int kIssuer = A::SOFTMAX / 32, kLoader = kIssuer + 1;
+    extern __shared__ uint8_t raw[];
+    uint8_t *const smem = raw + ((1024u - (smem_addr(raw) & 1023u)) & 1023u);
+    uint8_t *const qs = smem, *const slots = smem + NQ * A::Q_TILE;
+    __shared__ __align__(8) uint64_t q_full, q_empty, full[SLOTS], empty[SLOTS], tail, s_full[A::NS], p_full[A::NS], o_full[NQ],
+        item_full[kItems], item_empty[kItems];
+    __shared__ Item items[kItems];
+    __shared__ uint32_t tmem_base;
+    __shared__ int failed;
+    const int tid = threadIdx.x, warp = warp_index(), lane = tid & 31;
+    const int group = p.Hq / p.H, TT = 128 / group;
+
+    if (tid == 0) {
+        failed = 0;
+        mbar_init(&q_full, 1);
+        mbar_init(&q_empty, 1);
+        mbar_init(&tail, 1);
+        for (int i = 0; i < SLOTS; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < A::NS; ++i) {
+            mbar_init(&s_full[i], 1);
+            mbar_init(&p_full[i], 4);                 // (a warp may be a step ahead of another where S lies twice)
+        }
+        for (int i = 0; i < NQ; ++i) mbar_init(&o_full[i], 1);
+        for (int i = 0; i < kItems; ++i) {
+            mbar_init(&item_full[i], 1);
+            mbar_init(&item_empty[i], NQ * 4 + 1);
+        }
+        fence_mbar_init();
+    }
+    if (warp == 0) tmem_alloc(&tmem_base, 512);
+    __syncthreads();
+    tmem_fence_after();
+    const uint32_t s_t = __shfl_sync(0xFFFFFFFFu, tmem_base, 0), o_t = s_t + A::O_COL;
+    bool fail = false;
+    int ir = 0;
+    uint32_t i_phase = 0;
+    const auto next_item = [&] {
+        if (++ir == kItems) {
+            ir = 0;
+            i_phase ^= 1;
+        }
+    };
+
+    if (warp == kLoader) {
+        uint32_t *const ticket = static_cast<uint32_t *>(p.ws);        // items taken, CTAs that are done
+        if (lane == 0) {
+            tma_prefetch(&maps.q);
+            tma_prefetch(&maps.k);
+            tma_prefetch(&maps.v);
+        }
+        int ring = 0, b0 = 0;
+        uint32_t phase = 1, q_phase = 1, tail_phase = 0;
+        int64_t base = 0, index = blockIdx.x;         // tiles of the requests before b0; the item
+        const auto slot = [&](bool value, const Item &it, int step) {
+            const int k0 = step * KT;
+            wait_or_fail(&empty[ring], phase, fail);
+            uint8_t *const to = slots + ring * A::SLOT;
+            // values that no row of the request sees become zeros (0 x NaN would reach every row of the tile)
+            const int live = p.window > 0 ? max(it.t.m - it.t.n - p.window + 1, 0) : 0;
+            const bool part = value && (k0 + KT > it.t.m || (k0 < live && k0 + KT > p.prefix));
+            uint64_t *const bar = part ? &tail : &full[ring];
+            if (lane == 0) {
+                mbar_arrive_expect_tx(bar, A::SLOT);
+#pragma unroll
+                for (int x = 0; x < D; x += 64)
+                    tma_load_3d(to + x * KT * 2, value ? &maps.v : &maps.k, x, it.h, it.t.k_lo + k0, bar);
+            }
+            __syncwarp();
+            if (part) {
+                wait_or_fail(&tail, tail_phase, fail);
+                tail_phase ^= 1;
+                for (int e = lane; e < KT * D / 8; e += 32) {
+                    const int r = e / 8 % KT, j = k0 + r;
+                    if (j >= it.t.m || (j < live && j >= p.prefix))
+                        *reinterpret_cast<uint4 *>(to + static_cast<int64_t>(e) * 16) = make_uint4(0, 0, 0, 0);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&full[ring]);
+            }
+            if (++ring == SLOTS) {
+                ring = 0;
+                phase ^= 1;
+            }
+        };
+        for (;;) {
+            Item it;
+            it.h = -1;
+            const int64_t line = index / p.H;
+            // the request whose tiles hold `line`, its last (longest) tile first
+            while (b0 < p.B && !fail) {
+                PromptTile t;
+                int64_t mine = 0;
+                if (b0 + lane < p.B && prompt_request(p, b0 + lane, nullptr, t)) mine = (t.n + NQ * TT - 1) / (NQ * TT);
+                int64_t at = mine;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int64_t y = __shfl_up_sync(0xFFFFFFFFu, at, o);
+                    if (lane >= o) at += y;
+                }
+                const int64_t all = __shfl_sync(0xFFFFFFFFu, at, 31);
+                at += base;
+                const uint32_t hit = __ballot_sync(0xFFFFFFFFu, at - mine <= line && line < at);
+                if (hit) {
+                    const int from = __ffs(hit) - 1;
+                    it.t.b = b0 + from;
+                    it.t.lo = __shfl_sync(0xFFFFFFFFu, t.lo, from);
+                    it.t.n = __shfl_sync(0xFFFFFFFFu, t.n, from);
+                    it.t.k_lo = __shfl_sync(0xFFFFFFFFu, t.k_lo, from);
+                    it.t.m = __shfl_sync(0xFFFFFFFFu, t.m, from);
+                    it.first = static_cast<int>(__shfl_sync(0xFFFFFFFFu, at, from) - 1 - line) * (NQ * TT);
+                    it.h = static_cast<int>(index % p.H);
+                    break;
+                }
+                base += all;
+                b0 += 32;
+            }
+            if (it.h >= 0) {
+                const int own = it.t.m - it.t.n + it.first;            // last key of the first row
+                const int near = p.window > 0 ? max(own - p.window + 1, 0) / KT : 0;
+                it.f0 = near;
+                it.np = min((p.prefix + KT - 1) / KT, near);
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    const int rows = min(it.t.n - it.first - q * TT, TT);
+                    const int last = rows > 0 && q < NQ ? own + q * TT + rows - 1 : -1;
+                    it.n[q] = last < 0 ? 0 : it.np + last / KT + 1 - near;
+                }
+            }
+            wait_or_fail(&item_empty[ir], i_phase ^ 1, fail);
+            if (fail) it.h = -1;
+            if (lane == 0) {
+                items[ir] = it;
+                mbar_arrive(&item_full[ir]);
+            }
+            __syncwarp();
+            next_item();
+            if (it.h < 0) break;
+            // (asked for here, looked at after the item)
+            uint32_t taken = 0;
+            if (lane == 0) taken = atomicAdd(ticket, 1u);
+            const int n = max(it.n[0], it.n[1]);
+            if (n > 0) {
+                wait_or_fail(&q_empty, q_phase, fail);
+                q_phase ^= 1;
+                if (lane == 0) {
+                    const int tiles = it.n[1] > 0 ? 2 : 1;
+                    mbar_arrive_expect_tx(&q_full, tiles * TT * group * D * 2);
+                    for (int q = 0; q < tiles; ++q)
+#pragma unroll
+                        for (int x = 0; x < D; x += 64)
+                            tma_load_3d(qs + q * A::Q_TILE + x * 256, &maps.q, x, it.h * group, it.t.lo + it.first + q * TT, &q_full);
+                }
+                __syncwarp();
+                // in the order of the products
+                slot(false, it, item_step(it, 0));
+                for (int i = 0; i < n; ++i) {
+                    if (NQ == 2) slot(true, it, item_step(it, i));
+                    if (i + 1 < n) slot(false, it, item_step(it, i + 1));
+                    if (NQ == 1) slot(true, it, item_step(it, i));
+                }
+            }
+            index = static_cast<int64_t>(gridDim.x) + __shfl_sync(0xFFFFFFFFu, taken, 0);
+        }
+        // the last CTA leaves the tickets as it found them
+        if (lane == 0) {
+            fence_acq_rel_gpu();
+            if (atomicAdd(ticket + 1, 1u) == gridDim.x - 1) {
+                ticket[0] = 0u;
+                ticket[1] = 0u;
+            }
+        }
+    } else if (warp == kIssuer) {
+        const uint32_t q_addr = smem_addr(qs), slot_addr = smem_addr(slots);
+        int ring = 0;
+        uint32_t phase = 0, q_phase = 0, p_phase[A::NS] = {};
+        uint32_t steps = 0;                           // NQ = 1: steps so far, whose S alternates
+        const auto arrived = [&] {                    // the next slot of the ring: its place
+            wait_or_fail(&full[ring], phase, fail);
+            tmem_fence_after();
+            const int at = ring;
+            if (++ring == SLOTS) {
+                ring = 0;
+                phase ^= 1;
+            }
+            return at;
+        };
+        const auto scores = [&](int q, int s, int at) {
+            const uint32_t a = q_addr + q * A::Q_TILE, b = slot_addr + at * A::SLOT;
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k)
+                mma_f16_shared(s_t + s * KT, smem_desc_swizzled(a + k / 4 * (128 * 128) + k % 4 * 32, 16),
+                               smem_desc_swizzled(b + k / 4 * (KT * 128) + k % 4 * 32, 16), mma_f16_desc(KT, false, true), k > 0);
+            mma_commit(&s_full[s]);
+        };
+        const auto values = [&](int q, int s, int at, bool accumulate) {
+            const uint32_t b = slot_addr + at * A::SLOT;
+            wait_or_fail(&p_full[s], p_phase[s], fail);
+            p_phase[s] ^= 1;
+            tmem_fence_after();
+#pragma unroll
+            for (int k = 0; k < KT / 16; ++k)
+                mma_f16(o_t + q * D, s_t + A::P_COL + s * A::P_STEP + k * 8, smem_desc_swizzled(b + k * 2048, KT * 128),
+                        mma_f16_desc(D, true, true), accumulate || k > 0);
+            mma_commit(&o_full[q]);
+        };
+        for (;;) {
+            wait_or_fail(&item_full[ir], i_phase, fail);
+            const int h = *reinterpret_cast<volatile int *>(&items[ir].h);
+            const int n0 = *reinterpret_cast<volatile int *>(&items[ir].n[0]), n1 = *reinterpret_cast<volatile int *>(&items[ir].n[1]);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&item_empty[ir]);
+            next_item();
+            if (__shfl_sync(0xFFFFFFFFu, h < 0 || fail, 0)) break;
+            const int n = max(n0, n1);
+            if (n == 0) continue;
+            wait_or_fail(&q_full, q_phase, fail);
+            q_phase ^= 1;
+            int at = arrived();
+            if constexpr (NQ == 2) {
+                if (n0 > 0) scores(0, 0, at);
+                if (n1 > 0) scores(1, 1, at);
+            } else {
+                scores(0, steps & 1, at);
+            }
+            mma_commit(&empty[at]);
+            if (n == 1) mma_commit(&q_empty);
+            for (int i = 0; i < n; ++i) {
+                const bool more = i + 1 < n, accumulate = i % A::RUN != 0;
+                if constexpr (NQ == 2) {
+                    const int v = arrived();
+                    if (i < n0) values(0, 0, v, accumulate);
+                    if (more) at = arrived();
+                    if (i + 1 < n0) scores(0, 0, at);
+                    if (i < n1) values(1, 1, v, accumulate);
+                    mma_commit(&empty[v]);
+                    if (i + 1 < n1) scores(1, 1, at);
+                } else {
+                    if (more) {
+                        at = arrived();
+                        scores(0, (steps + 1) & 1, at);
+                    }
+                    const int v = arrived();
+                    values(0, steps & 1, v, accumulate);
+                    mma_commit(&empty[v]);
+                    ++steps;
+                }
+                if (more) mma_commit(&empty[at]);
+                if (i + 2 == n) mma_commit(&q_empty);
+            }
+        }
+    } else {
+        const int q = warp >> 2, row = tid & 127;     // tile, row of it
+        const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;
+        const uint32_t o_mine = o_t + q * D + lanes;
+        uint32_t count = 0;                           // steps of this tile so far
+        const float c = p.scale * kLog2e, cap = p.cap * kLog2e, rcap = p.cap > 0.f ? cap_reciprocal(cap) : 0.f;
+        // sums over the runs of keys so far, channel by channel
+        float *const sums = reinterpret_cast<float *>(static_cast<uint8_t *>(p.ws) + kPromptTickets) +
+                            (static_cast<int64_t>(blockIdx.x) * NQ + q) * 128 * D + row;
+        if (blockIdx.x == 0 && p.status) {
+            PromptTile t;
+            for (int b = tid; b < p.B; b += A::SOFTMAX) prompt_request(p, b, p.status, t);
+        }
+        for (;;) {
+            wait_or_fail(&item_full[ir], i_phase, fail);
+            const Item it = items[ir];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&item_empty[ir]);
+            next_item();
+            if (__shfl_sync(0xFFFFFFFFu, it.h < 0 || fail, 0)) break;
+            const int i_row = it.first + q * TT + row / group, head = it.h * group + row % group;
+            const bool real = row < TT * group && i_row < it.t.n;
+            const int own0 = it.t.m - it.t.n + it.first + q * TT;      // last key of the tile's first row
+            const int own = it.t.m - it.t.n + i_row;
+            const float slope = OPT && p.slopes && real ? p.slopes[head] * kLog2e : 0.f;
+            const int n = it.n[q];
+            float ref = -INFINITY, l = 0.f, run_ref = 0.f;
+            for (int i = 0; i < n; ++i) {
+                const int k0 = item_step(it, i) * KT;
+                const int sb = NQ == 2 ? q : count & 1;
+                wait_or_fail(&s_full[sb], (NQ == 2 ? count : count >> 1) & 1, fail);
+                tmem_fence_after();
+                const uint32_t s_mine = s_t + sb * KT + lanes;
+                float s[KT];
+#pragma unroll
+                for (int k = 0; k < KT; k += 32) tmem_ld32(s_mine + k, reinterpret_cast<uint32_t *>(s + k));
+                tmem_wait_ld();
+                if (OPT) {
+#pragma unroll
+                    for (int k = 0; k < KT; ++k) s[k] *= c;
+                    if (p.cap > 0.f) {
+#pragma unroll
+                        for (int k = 0; k < KT; ++k) s[k] = cap_score<false>(s[k], cap, rcap);
+                    }
+                    if (p.slopes) {
+                        const float far = static_cast<float>(own - k0);
+#pragma unroll
+                        for (int k = 0; k < KT; ++k) s[k] -= slope * (far - static_cast<float>(k));
+                    }
+                }
+                // keys that not all of the tile's rows see
+                if (k0 + KT - 1 > own0 || (p.window > 0 && k0 < own0 + TT - p.window)) {
+                    const int last = own - k0;
+                    if (p.window > 0) {
+                        const int64_t least = static_cast<int64_t>(last) - p.window;
+                        const int near = least < -1 ? -1 : static_cast<int>(least), always = p.prefix - k0;
+#pragma unroll
+                        for (int k = 0; k < KT; ++k) s[k] = k <= last && (k > near || k < always) ? s[k] : -INFINITY;
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < KT; ++k) s[k] = k <= last ? s[k] : -INFINITY;
+                    }
+                }
+                float top[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+                for (int k = 4; k < KT; ++k) top[k & 3] = fmaxf(top[k & 3], s[k]);
+                float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+                if (!OPT) most *= c;
+                const bool move = most > ref + kLazy, fresh = i % A::RUN == 0;
+                if (fresh && i > 0) {
+                    // a run's products to the sums
+                    wait_or_fail(&o_full[q], (count - 1) & 1, fail);
+                    tmem_fence_after();
+                    const float f = i == A::RUN ? 0.f : ex2(run_ref - ref);
+#pragma unroll 1
+                    for (int d = 0; d < D; d += 16) {
+                        uint32_t r[16];
+                        tmem_ld16(o_mine + d, r);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            float *const to = sums + (d + e) * 128;
+                            *to = __uint_as_float(r[e]) + (i == A::RUN ? 0.f : *to * f);
+                        }
+                    }
+                    run_ref = ref;
+                }
+                if (__any_sync(0xFFFFFFFFu, move)) {
+                    const float to = move ? most : ref, f = move ? ex2(ref - to) : 1.f;
+                    ref = to;
+                    l *= f;
+                    if (!fresh) {
+                        wait_or_fail(&o_full[q], (count - 1) & 1, fail);
+                        tmem_fence_after();
+#pragma unroll 1
+                        for (int d = 0; d < D; d += 16) {
+                            uint32_t r[16];
+                            tmem_ld16(o_mine + d, r);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * f);
+                            tmem_st16(o_mine + d, r);
+                        }
+                    }
+                }
+                const float down = ref == -INFINITY ? 0.f : -ref;
+                const uint64_t c2 = OPT ? f2_pack(1.f, 1.f) : f2_pack(c, c), down2 = f2_pack(down, down);
+                uint64_t sum = 0;
+#pragma unroll
+                for (int k = 0; k < KT; k += 32) {
+                    uint32_t w[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        float x, y;
+                        f2_unpack(f2_fma(f2_pack(s[k + 2 * e], s[k + 2 * e + 1]), c2, down2), x, y);
+                        x = ex2(x);
+                        y = ex2(y);
+                        sum = f2_add(sum, f2_pack(x, y));
+                        w[e] = pack_bf16(x, y);
+                    }
+                    tmem_st16(s_t + A::P_COL + sb * A::P_STEP + lanes + k / 2, w);
+                }
+                float x, y;
+                f2_unpack(sum, x, y);
+                l += x + y;
+                tmem_wait_st();
+                tmem_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_full[sb]);
+                ++count;
+            }
+            // the tile's results
+            const float inv = l > 0.f ? 1.f / l : 0.f;
+            if (n > 0) {
+                // (NQ = 1: the step before the last can be under way as well, and a wait is for the phase at hand or the one before)
+                if (NQ == 1) wait_or_fail(&o_full[q], count & 1, fail);
+                wait_or_fail(&o_full[q], (count - 1) & 1, fail);
+                tmem_fence_after();
+            }
+            const int64_t at = (static_cast<int64_t>(it.t.lo) + i_row) * p.Hq + head;
+            __nv_bfloat16 *const to = static_cast<__nv_bfloat16 *>(p.out) + at * D;
+            const float f = n > A::RUN ? ex2(run_ref - ref) : 0.f;
+#pragma unroll 1
+            for (int d = 0; d < D; d += 32) {
+                uint32_t r[32] = {};
+                if (n > 0) {
+                    tmem_ld32(o_mine + d, r);
+                    tmem_wait_ld();
+                }
+                if (real && !fail) {
+                    float v[32];
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(r[e]);
+                    if (n > A::RUN)
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) v[e] += sums[(d + e) * 128] * f;
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8) {
+                        uint4 w;
+                        w.x = pack_bf16(v[e] * inv, v[e + 1] * inv);
+                        w.y = pack_bf16(v[e + 2] * inv, v[e + 3] * inv);
+                        w.z = pack_bf16(v[e + 4] * inv, v[e + 5] * inv);
+                        w.w = pack_bf16(v[e + 6] * inv, v[e + 7] * inv);
+                        *reinterpret_cast<uint4 *>(to + d + e) = w;
+                    }
+                }
+                __syncwarp();
+            }
+            if (real && !fail && p.lse) p.lse[at] = l > 0.f ? (ref + log2f(l)) * kLn2 : -INFINITY;
+            tmem_fence_before();                      // (O is free with the next item's first weights)
+        }
+    }
+    if (fail) failed = 1;
+    tmem_fence_before();
+    __syncthreads();
+    if (failed && tid == 0) {
+        // a wait gave up: let the copies in flight land (bounded), then leave
+        for (int i = 0; i < SLOTS; ++i)
+            for (int ph = 0; ph < 2; ++ph) mbar_wait(&full[i], ph);
+        for (int ph = 0; ph < 2; ++ph) mbar_wait(&q_full, ph), mbar_wait(&tail, ph);
+        set_status(p.status, SPEC_STATUS_TIMEOUT);
+    }
+    __syncthreads();
+    tmem_fence_after();
+    if (warp == 0) tmem_free(s_t, 512);
+}
+
+template <int D, bool OPT> cudaError_t launch_tiles_of(const PromptParams &p, const PromptMaps &maps, cudaStream_t s)
+{
+    using A = Prompt<D>;
+    static bool done[64] = {false};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (!done[dev]) {
+        e = cudaFuncSetAttribute(prompt_tiles_kernel<D, OPT>, cudaFuncAttributeMaxDynamicSharedMemorySize, A::SMEM);
+        if (e != cudaSuccess) return e;
+        done[dev] = true;
+    }
+    const int rows = A::NQ * (128 / (p.Hq / p.H));
+    const int64_t items = (static_cast<int64_t>(p.R_cap) / rows + p.B) * p.H;
+    const int grid = static_cast<int>(items < kPromptSms ? items : kPromptSms);
+    prompt_tiles_kernel<D, OPT><<<grid, A::THREADS, A::SMEM, s>>>(p, maps);
+    return cudaGetLastError();
+}
+
+template <bool OPT> cudaError_t launch_tiles(const PromptParams &p, const PromptMaps &maps, cudaStream_t s)
+{
+    if (p.D == 64) return launch_tiles_of<64, OPT>(p, maps, s);
+    return p.D == 128 ? launch_tiles_of<128, OPT>(p, maps, s) : launch_tiles_of<256, OPT>(p, maps, s);
+}
+
+}  // namespace
+
+cudaError_t launch_prompt_tiles_options(const PromptParams &p, const PromptMaps &maps, cudaStream_t s);
+
+}  // namespace specv

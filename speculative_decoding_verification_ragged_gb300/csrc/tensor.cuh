@@ -4,9 +4,26 @@
 
 #include <cstdint>
 
+#include <cuda.h>
+
 #include "common.cuh"
 
 namespace specv {
+
+// A tiled TMA copy of a box of a 3-dimensional tensor into shared memory, completing on `bar`
+// (its innermost coordinate 0 or a multiple of 64 elements of 2 bytes: on 16 bytes).
+__device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, int x, int y, int z, uint64_t *bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
+        ::"r"(smem_addr(dst)), "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar))
+        : "memory");
+}
+
+__device__ __forceinline__ void tma_prefetch(const CUtensorMap *map)
+{
+    asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
 
 // the warp's index, known to be the same in all its lanes
 __device__ __forceinline__ int warp_index() { return __shfl_sync(0xFFFFFFFFu, static_cast<int>(threadIdx.x >> 5), 0); }
@@ -79,6 +96,20 @@ template <int N> __device__ __forceinline__ void tmem_ld(uint32_t addr, uint32_t
     }
 }
 
+__device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t *r)
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(addr)
+        : "memory");
+}
+
 __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t *r)
 {
     asm volatile(
@@ -105,6 +136,16 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo, uint3
            static_cast<uint64_t>(sbo >> 4) << 32 | static_cast<uint64_t>(1) << 46;
 }
 
+// Shared-memory operand in rows of 128 bytes with the 128-byte swizzle (as tiled TMA copies
+// leave it, from a multiple of 1024 bytes on): 8 rows follow 1024 bytes after the 8 before.  K-major: a row
+// holds 64 K values of one M or N index, `lbo` is not looked at.  N-major: a row holds 64 N values of one K index,
+// the next 64 lie `lbo` bytes further.
+__device__ __forceinline__ uint64_t smem_desc_swizzled(uint32_t addr, uint32_t lbo)
+{
+    return static_cast<uint64_t>((addr & 0x3FFFFu) >> 4) | static_cast<uint64_t>(lbo >> 4) << 16 |
+           static_cast<uint64_t>(1024 >> 4) << 32 | static_cast<uint64_t>(1) << 46 | static_cast<uint64_t>(2) << 61;
+}
+
 // Instruction descriptor: f16 x f16 -> f32 (or bf16 x bf16), M = 128, `n`
 // columns; b_n_major: B's N index is the contiguous one.
 __host__ __device__ constexpr uint32_t mma_f16_desc(int n, bool b_n_major, bool bf16 = false)
@@ -121,6 +162,16 @@ __device__ __forceinline__ void mma_f16(uint32_t d, uint32_t a, uint64_t b, uint
     asm volatile(
         "{\n\t.reg .pred p, q;\n\telect.sync _|q, 0xffffffff;\n\tsetp.ne.u32 p, %4, 0;\n\t"
         "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc),
+        "r"(static_cast<uint32_t>(accumulate))
+        : "memory");
+}
+
+// the same with A in shared memory
+__device__ __forceinline__ void mma_f16_shared(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\telect.sync _|q, 0xffffffff;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc),
         "r"(static_cast<uint32_t>(accumulate))
         : "memory");
 }

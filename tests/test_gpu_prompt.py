@@ -67,7 +67,7 @@ def check(sv, q, k, v, rows, keys=None, *, got=None, **kw):
     assert (err <= tol).all(), float((err / tol).max())
     w = rel + (2.0 ** -8 if dtype == "bf16" else 0.0)
     err, tol = np.abs(go - out), 1.01 * (A * w[..., None] + HALF[dtype] * np.abs(out)) + 1e-30
-    assert (err <= tol).all(), float((err / tol).max())
+    assert (err <= tol).all(), (float((err / tol).max()), np.argwhere((err > tol).any(-1))[:5])
     assert (go[~seen] == 0).all()
     return got
 
