@@ -1,6 +1,7 @@
 // tree.cu -- acceptance of a path through a tree of drafts, and the adjustment of the
 // rows' logits by penalties, biases and masks (include/spec_tree.h).
 #include "cache.cuh"
+#include "tensor.cuh"
 #include "tree.cuh"
 
 namespace specv {
@@ -50,13 +51,17 @@ __global__ void __launch_bounds__(kAcceptWarps * 32) tree_accept_kernel(const Tr
 
 // ---- logits ----
 
-// A CTA takes kSlice columns of a request's rows: the tokens so far are counted once, in
-// shared memory, for all rows.  A column's word: how often it was generated, whether it
-// was seen at all, whether one of the request's biases or nodes names it; a bit a column says
-// whether the word is anything but 0, so that most columns cost a byte of shared memory each 8.
-constexpr int kSlice = 8192, kLogitThreads = 256;
+// A CTA takes kSlice columns of a request's rows.  They stream by first, copied and masked; the
+// tokens so far are counted once for all rows, in shared memory, and the columns that have a count, a draft of
+// the paths or a bias ("touched") are written over, a thread each.  In place the touched columns come first, and only
+// rows with a mask stream by (a masked column is -inf whatever it was).
+//
+constexpr int kSlice = 8192;
+// A column's word: how often it was generated, whether it was seen at all, whether one of the request's biases or nodes
+// names it; a bit a column says whether the word is anything but 0.
 constexpr uint32_t kSeen = 1u << 31, kNamed = 1u << 30, kCount = kNamed - 1u;
 constexpr int kNear = 256;                            // biases of a slice kept in shared memory
+constexpr int kListed = 1024;                         // touched columns that are listed at a time
 
 template <typename T> struct LogitElt;
 template <> struct LogitElt<__nv_bfloat16> {
@@ -71,6 +76,16 @@ template <> struct LogitElt<__nv_bfloat16> {
             asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(x[2 * i + 1]), "f"(x[2 * i]));
         return v;
     }
+    // -inf where `may` has a bit clear
+    static __device__ __forceinline__ void hide(uint4 &v, uint32_t may)
+    {
+        uint32_t *w = &v.x;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t lo = may >> (2 * i) & 1u ? w[i] : 0xFF80u, hi = may >> (2 * i + 1) & 1u ? w[i] : 0xFF800000u;
+            w[i] = __byte_perm(lo, hi, 0x7610);
+        }
+    }
 };
 template <> struct LogitElt<float> {
     static constexpr int VEC = 4;
@@ -79,32 +94,35 @@ template <> struct LogitElt<float> {
     {
         return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
     }
+    static __device__ __forceinline__ void hide(uint4 &v, uint32_t may)
+    {
+        uint32_t *w = &v.x;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = may >> i & 1u ? w[i] : 0xFF800000u;
+    }
 };
 
-struct Slice {
+template <int kSlice> struct Slice {
+    static constexpr int kLogitThreads = kSlice / 32;
     uint32_t word[kSlice];
-    uint32_t touched[kSlice / 32 + 1];
+    uint32_t touched[kSlice / 32];
     int node_token[32];
     uint32_t path[32];                                // of each row: the nodes on it
+    int mask[32];                                     // of each row: its mask, -1 for none
     int bias_id[kNear];
     float bias_value[kNear];
     int scan[kLogitThreads / 32];
     int n_bias;
+    uint16_t column[kListed];
 };
-
-// N bits of a bit set from bit `i` on
-__device__ __forceinline__ uint32_t bits_at(const uint32_t *set, int i, int last_word)
-{
-    const int w = i >> 5;
-    return __funnelshift_r(set[w], w < last_word ? set[w + 1] : 0u, i & 31);
-}
 
 struct Penalty {
     float repetition, frequency, presence;
 };
 
 // one touched column (v: from the slice's first on) of a row with `path`
-__device__ __forceinline__ float adjust(const LogitParams &p, const Slice &s, const Penalty &pen, int c0, int v, int n, uint32_t path,
+template <int SLICE>
+__device__ __forceinline__ float adjust(const LogitParams &p, const Slice<SLICE> &s, const Penalty &pen, int c0, int v, int n, uint32_t path,
                                         int bias0, int bias1, float z)
 {
     const uint32_t w = s.word[v];
@@ -128,127 +146,64 @@ __device__ __forceinline__ float adjust(const LogitParams &p, const Slice &s, co
     return z;
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kLogitThreads) adjust_logits_kernel(const LogitParams p)
+template <typename T, int kSlice>
+__global__ void __launch_bounds__(kSlice / 32) adjust_logits_kernel(const LogitParams p)
 {
     using E = LogitElt<T>;
     constexpr int VEC = E::VEC;
-    __shared__ __align__(16) Slice s;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, b = blockIdx.y;
+    constexpr int kLogitThreads = Slice<kSlice>::kLogitThreads;
+    extern __shared__ __align__(16) uint8_t raw[];
+    Slice<kSlice> &s = *reinterpret_cast<Slice<kSlice> *>(raw);
+    const int tid = threadIdx.x, lane = tid & 31, warp = warp_index(), b = blockIdx.y;
     const int c0 = blockIdx.x * kSlice, cols = min(p.V - c0, kSlice);
     uint32_t *const report = blockIdx.x == 0 ? p.status : nullptr;      // (one CTA of a request speaks for it)
+    // What the request has is asked for at once, and what that leads to before the rows stream by: a CTA lives as long as
+    // its chain of loads.
+    Penalty pen = {p.repetition ? p.repetition[b] : 1.f, p.frequency ? p.frequency[b] : 0.f, p.presence ? p.presence[b] : 0.f};
+    int tokens = p.history ? p.n_tokens[b] : 0;
+    const int prompt = p.history && p.n_prompt ? p.n_prompt[b] : 0;
+    int bias0 = p.bias_cu ? p.bias_cu[b] : 0, bias1 = p.bias_cu ? p.bias_cu[b + 1] : 0;
     int lo, n;
     if (!request_rows(p.cu_rows, b, p.R_cap, p.k_max + 1, tid == 0 ? report : nullptr, lo, n) || n == 0) return;
-
-    for (int i = tid; i < kSlice / 4; i += kLogitThreads) reinterpret_cast<uint4 *>(s.word)[i] = make_uint4(0, 0, 0, 0);
-    for (int i = tid; i < kSlice / 32 + 1; i += kLogitThreads) s.touched[i] = 0;
-    const auto mark = [&](int v) { atomicOr(&s.touched[v >> 5], 1u << (v & 31)); };
-    // the request's penalties
-    Penalty pen = {p.repetition ? p.repetition[b] : 1.f, p.frequency ? p.frequency[b] : 0.f, p.presence ? p.presence[b] : 0.f};
     const auto finite = [](float x) { return x - x == 0.f; };
     bool bad = false;
     if (!finite(pen.repetition) || pen.repetition <= 0.f) pen.repetition = 1.f, bad = true;
     if (!finite(pen.frequency)) pen.frequency = 0.f, bad = true;
     if (!finite(pen.presence)) pen.presence = 0.f, bad = true;
+    if (bias0 < 0 || bias1 < bias0 || bias1 > p.n_bias) bad = bad || p.bias_cu, bias0 = bias1 = 0;
+    if (bad && tid == 0) set_status(report, SPEC_STATUS_BAD_PENALTY);
     const bool penal = pen.repetition != 1.f || pen.frequency != 0.f || pen.presence != 0.f;
-    int tokens = penal && p.history ? p.n_tokens[b] : 0;
+    if (!penal) tokens = 0;
     if (tokens < 0 || tokens > p.history_cap) {
         if (tid == 0) set_status(report, SPEC_STATUS_BAD_LENGTH);
         tokens = 0;
     }
-    const int prompt = tokens > 0 && p.n_prompt ? p.n_prompt[b] : 0;
-    int bias0 = 0, bias1 = 0;
-    if (p.bias_cu) {
-        bias0 = p.bias_cu[b];
-        bias1 = p.bias_cu[b + 1];
-        if (bias0 < 0 || bias1 < bias0 || bias1 > p.n_bias) bias0 = bias1 = 0, bad = true;
-    }
-    if (bad && tid == 0) set_status(report, SPEC_STATUS_BAD_PENALTY);
-    __syncthreads();
 
-    // the history
-    const int32_t *hist = p.history ? p.history + static_cast<int64_t>(b) * p.history_ld : nullptr;
-    const auto count = [&](int i, int t) {
-        const uint32_t v = static_cast<uint32_t>(t) - static_cast<uint32_t>(c0);
-        if (v < static_cast<uint32_t>(cols)) {
-            if (i < prompt) atomicOr(&s.word[v], kSeen);
-            else atomicAdd(&s.word[v], 1u);
-            mark(v);
-        }
-    };
-    for (int i = tid; i < tokens; i += 4 * kLogitThreads) {
-        int t[4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) t[u] = i + u * kLogitThreads < tokens ? __ldg(hist + i + u * kLogitThreads) : -1;
-#pragma unroll
-        for (int u = 0; u < 4; ++u) count(i + u * kLogitThreads, t[u]);
-    }
-    // the nodes and the rows' paths
-    if (warp == 0) {
-        const int parent = tree_parent(p.parent, lo, n, report);
-        const uint32_t hung = __ballot_sync(0xFFFFFFFFu, parent >= 0);
-        const bool have = penal && p.node_token && lane < n;
-        const int t = have && lane > 0 ? __ldg(p.node_token + lo + lane) : -1;
-        const uint32_t anc = tree_ancestors(parent);   // (the whole warp: it exchanges them)
-        s.path[lane] = have ? anc & hung : 0u;
-        s.node_token[lane] = t;
-        const uint32_t v = static_cast<uint32_t>(t) - static_cast<uint32_t>(c0);
-        if (parent >= 0 && t >= 0 && v < static_cast<uint32_t>(cols)) {
-            atomicOr(&s.word[v], kNamed);
-            mark(v);
-        }
-    }
-    // the biases of the slice, in their order
-    int near = 0;
-    for (int i0 = bias0; i0 < bias1; i0 += kLogitThreads) {
-        const int i = i0 + tid;
-        const uint32_t v = i < bias1 ? static_cast<uint32_t>(__ldg(p.bias_ids + i)) - static_cast<uint32_t>(c0) : 0xFFFFFFFFu;
-        const bool mine = v < static_cast<uint32_t>(cols);
-        const uint32_t vote = __ballot_sync(0xFFFFFFFFu, mine);
-        if (lane == 0) s.scan[warp] = __popc(vote);
-        __syncthreads();
-        int at = near + __popc(vote & ((1u << lane) - 1u));
-#pragma unroll
-        for (int w = 0; w < kLogitThreads / 32; ++w) {
-            at += w < warp ? s.scan[w] : 0;
-            near += s.scan[w];
-        }
-        if (mine) {
-            if (at < kNear) {
-                s.bias_id[at] = static_cast<int>(v);
-                s.bias_value[at] = __ldg(p.bias_values + i);
-            }
-            atomicOr(&s.word[v], kNamed);
-            mark(v);
-        }
-        __syncthreads();
-    }
-    if (tid == 0) s.n_bias = near;
-    __syncthreads();
-
+    const bool in_place = p.out == p.logits;
     const int mask_words = (p.V + 31) / 32;
-    for (int j = 0; j < n; ++j) {
-        const int row = lo + j;
-        const T *src = static_cast<const T *>(p.logits) + static_cast<int64_t>(row) * p.ld + c0;
-        T *dst = static_cast<T *>(p.out) + static_cast<int64_t>(row) * p.out_ld + c0;
-        const uint32_t path = s.path[j];
-        const uint32_t *allowed = nullptr;
-        if (p.allowed) {
-            const int m = p.allowed_row ? __ldg(p.allowed_row + row) : row;
-            if (m >= 0 && m < p.n_allowed) allowed = p.allowed + m * p.allowed_ld;
-            else if ((m != -1 || !p.allowed_row) && tid == 0) set_status(report, SPEC_STATUS_BAD_MASK);
-        }
-        const auto one = [&](int v) {
-            float z = to_f32<T>(src[v]);
-            if (s.touched[v >> 5] >> (v & 31) & 1u) z = adjust(p, s, pen, c0, v, n, path, bias0, bias1, z);
-            if (allowed && !(__ldg(allowed + ((c0 + v) >> 5)) >> ((c0 + v) & 31) & 1u)) z = -INFINITY;
-            dst[v] = from_f32<T>(z);
-        };
+    const auto source = [&](int row) { return static_cast<const T *>(p.logits) + static_cast<int64_t>(row) * p.ld + c0; };
+    const auto target = [&](int row) { return static_cast<T *>(p.out) + static_cast<int64_t>(row) * p.out_ld + c0; };
+    const auto mask_of = [&](int row) {
+        if (!p.allowed) return -1;
+        const int m = p.allowed_row ? __ldg(p.allowed_row + row) : row;
+        return m >= 0 && m < p.n_allowed ? m : (m == -1 ? -1 : -2);
+    };
+    const auto mask_at = [&](int m) -> const uint32_t * { return m >= 0 ? p.allowed + m * p.allowed_ld : nullptr; };
+    const auto hidden = [&](const uint32_t *allowed, int v) {
+        return allowed && !(__ldg(allowed + ((c0 + v) >> 5)) >> ((c0 + v) & 31) & 1u);
+    };
+    // a row as it streams by
+    const auto stream = [&](int row) {
+        const uint32_t *const allowed = mask_at(mask_of(row));
+        if (in_place && !allowed) return;
+        const T *const src = source(row);
+        T *const dst = target(row);
+        const auto one = [&](int v) { dst[v] = hidden(allowed, v) ? from_f32<T>(-INFINITY) : src[v]; };
         // 16-byte vectors where input and output lie alike, the columns before and after one by one
         const uint32_t off = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(src) & 15u);
         if (off != static_cast<uint32_t>(reinterpret_cast<uintptr_t>(dst) & 15u)) {
             for (int v = tid; v < cols; v += kLogitThreads) one(v);
-            continue;
+            return;
         }
         const int head = min(static_cast<int>((16u - off) % 16u / sizeof(T)), cols);
         const int vecs = (cols - head) / VEC, tail = head + vecs * VEC;
@@ -266,26 +221,155 @@ __global__ void __launch_bounds__(kLogitThreads) adjust_logits_kernel(const Logi
             for (int u = 0; u < U; ++u) {
                 const int i = i0 + u * kLogitThreads, v = head + i * VEC;
                 if (i >= vecs) break;
-                uint32_t hit = bits_at(s.touched, v, kSlice / 32) & ((1u << VEC) - 1u);
-                uint32_t may = (1u << VEC) - 1u;
                 if (allowed) {
                     const int w = (c0 + v) >> 5;
-                    may &= __funnelshift_r(__ldg(allowed + w), w + 1 < mask_words ? __ldg(allowed + w + 1) : 0u, (c0 + v) & 31);
+                    E::hide(x[u], __funnelshift_r(__ldg(allowed + w), w + 1 < mask_words ? __ldg(allowed + w + 1) : 0u, (c0 + v) & 31));
                 }
-                if (hit == 0 && may == (1u << VEC) - 1u) {
-                    *reinterpret_cast<uint4 *>(dst + v) = x[u];
-                    continue;
-                }
-                float z[VEC];
-                E::unpack(x[u], z);
-#pragma unroll
-                for (int k = 0; k < VEC; ++k) {
-                    if (hit >> k & 1u) z[k] = adjust(p, s, pen, c0, v + k, n, path, bias0, bias1, z[k]);
-                    if (!(may >> k & 1u)) z[k] = -INFINITY;
-                }
-                *reinterpret_cast<uint4 *>(dst + v) = E::pack(z);
+                *reinterpret_cast<uint4 *>(dst + v) = x[u];
             }
         }
+    };
+
+    // the first tokens, the nodes and the first biases: asked for here, looked at when the rows are through
+    const int32_t *const hist = p.history ? p.history + static_cast<int64_t>(b) * p.history_ld : nullptr;
+    int first_tokens[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+        const int i = u * kLogitThreads + tid;
+        first_tokens[u] = i < tokens ? __ldg(hist + i) : -1;
+    }
+    const int first_id = bias0 + tid < bias1 ? __ldg(p.bias_ids + bias0 + tid) : -1;
+    const float first_value = bias0 + tid < bias1 ? __ldg(p.bias_values + bias0 + tid) : 0.f;
+    int parent = -1, token = -1, mask = -1;
+    if (warp == 0 && lane < n) {
+        parent = tree_parent(p.parent, lo, n, report);
+        if (penal && p.node_token && lane > 0) token = __ldg(p.node_token + lo + lane);
+        mask = mask_of(lo + lane);
+        if (mask == -2) set_status(report, SPEC_STATUS_BAD_MASK);
+    }
+    for (int i = tid; i < kSlice / 4; i += kLogitThreads) reinterpret_cast<uint4 *>(s.word)[i] = make_uint4(0, 0, 0, 0);
+    s.touched[tid] = 0;
+    if (!in_place)
+        for (int j = 0; j < n; ++j) stream(lo + j);
+    __syncthreads();
+    // the history
+    const auto count = [&](int i, int t) {
+        const uint32_t v = static_cast<uint32_t>(t - c0);     // (ids below 0 are large as well: c0 + cols < 2^30)
+        if (v >= static_cast<uint32_t>(cols)) return;
+        // (most have been there before: a look instead of an atomic)
+        const uint32_t word = *const_cast<volatile uint32_t *>(&s.word[v]);
+        if (i >= prompt) atomicAdd(&s.word[v], 1u);
+        else if (!(word & kSeen)) atomicOr(&s.word[v], kSeen);
+        if (word == 0) atomicOr(&s.touched[v / 32], 1u << (v & 31));
+    };
+#pragma unroll
+    for (int u = 0; u < 4; ++u) count(u * kLogitThreads + tid, first_tokens[u]);
+    int done = 4 * kLogitThreads;
+    if (reinterpret_cast<uintptr_t>(hist) % 16 == 0) {
+        // (by vectors, what fills whole rounds of them)
+        constexpr int U = 4, ROUND = 4 * U * kLogitThreads;
+        for (; done <= tokens - ROUND; done += ROUND) {
+            int4 x[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) x[u] = __ldg(reinterpret_cast<const int4 *>(hist + done) + u * kLogitThreads + tid);
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int i = done + 4 * (u * kLogitThreads + tid);
+                const uint32_t least = min(min(static_cast<uint32_t>(x[u].x - c0), static_cast<uint32_t>(x[u].y - c0)),
+                                           min(static_cast<uint32_t>(x[u].z - c0), static_cast<uint32_t>(x[u].w - c0)));
+                if (least >= static_cast<uint32_t>(cols)) continue;
+                count(i, x[u].x);
+                count(i + 1, x[u].y);
+                count(i + 2, x[u].z);
+                count(i + 3, x[u].w);
+            }
+        }
+    }
+    for (; done < tokens; done += 4 * kLogitThreads) {
+        int t[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int i = done + u * kLogitThreads + tid;
+            t[u] = i < tokens ? __ldg(hist + i) : -1;
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) count(done + u * kLogitThreads + tid, t[u]);
+    }
+    // the nodes, the rows' paths and masks
+    if (warp == 0) {
+        const uint32_t hung = __ballot_sync(0xFFFFFFFFu, parent >= 0), anc = tree_ancestors(parent);
+        s.path[lane] = penal && p.node_token && lane < n ? anc & hung : 0u;
+        s.node_token[lane] = token;
+        s.mask[lane] = mask;
+        const uint32_t v = static_cast<uint32_t>(token - c0);
+        if (parent >= 0 && token >= 0 && v < static_cast<uint32_t>(cols)) {
+            atomicOr(&s.word[v], kNamed);
+            atomicOr(&s.touched[v / 32], 1u << (v & 31));
+        }
+    }
+    // the biases of the slice, in their order
+    int near = 0;
+    for (int64_t i0 = bias0; i0 < bias1; i0 += kLogitThreads) {
+        const int64_t i = i0 + tid;
+        const bool again = i0 > bias0;
+        const int id = !again ? first_id : (i < bias1 ? __ldg(p.bias_ids + i) : -1);
+        const uint32_t v = static_cast<uint32_t>(id - c0);
+        const bool mine = v < static_cast<uint32_t>(cols);
+        const uint32_t vote = __ballot_sync(0xFFFFFFFFu, mine);
+        if (lane == 0) s.scan[warp] = __popc(vote);
+        __syncthreads();
+        int at = near + __popc(vote & ((1u << lane) - 1u));
+#pragma unroll
+        for (int w = 0; w < kLogitThreads / 32; ++w) {
+            at += w < warp ? s.scan[w] : 0;
+            near += s.scan[w];
+        }
+        if (mine) {
+            if (at < kNear) {
+                s.bias_id[at] = static_cast<int>(v);
+                s.bias_value[at] = again ? __ldg(p.bias_values + i) : first_value;
+            }
+            atomicOr(&s.word[v], kNamed);
+            atomicOr(&s.touched[v / 32], 1u << (v & 31));
+        }
+        __syncthreads();
+    }
+    if (tid == 0) s.n_bias = near;
+    __syncthreads();
+
+    // the touched columns in their order, kListed at a time; a thread has 32 columns of the set
+    const uint32_t set = s.touched[tid];
+    int first = __popc(set), touched = 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xFFFFFFFFu, first, o);
+        if (lane >= o) first += y;
+    }
+    if (lane == 31) s.scan[warp] = first;
+    __syncthreads();
+    first -= __popc(set);
+#pragma unroll
+    for (int w = 0; w < kLogitThreads / 32; ++w) {
+        first += w < warp ? s.scan[w] : 0;
+        touched += s.scan[w];
+    }
+    for (int e0 = 0; e0 < touched; e0 += kListed) {
+        const int count = min(touched - e0, kListed);
+        if (e0 > 0) __syncthreads();
+        int at = first - e0;
+        for (uint32_t left = set; left; left &= left - 1, ++at)
+            if (at >= 0 && at < kListed) s.column[at] = static_cast<uint16_t>(tid * 32 + __ffs(left) - 1);
+        __syncthreads();
+        for (int e = tid; e < n * count; e += kLogitThreads) {
+            const int j = e / count, v = s.column[e - j * count], row = lo + j;
+            const float z = to_f32<T>(source(row)[v]);
+            const bool gone = hidden(mask_at(s.mask[j]), v);
+            target(row)[v] = from_f32<T>(gone ? -INFINITY : adjust(p, s, pen, c0, v, n, s.path[j], bias0, bias1, z));
+        }
+    }
+    if (in_place) {
+        __syncthreads();
+        for (int j = 0; j < n; ++j) stream(lo + j);
     }
 }
 
@@ -297,12 +381,31 @@ cudaError_t launch_tree_accept(const TreeParams &p, cudaStream_t s)
     return cudaGetLastError();
 }
 
+namespace {
+
+template <typename T, int SLICE> cudaError_t launch_logits(const LogitParams &p, cudaStream_t s)
+{
+    static bool done[64] = {false};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (!done[dev]) {
+        e = cudaFuncSetAttribute(adjust_logits_kernel<T, SLICE>, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(Slice<SLICE>));
+        if (e != cudaSuccess) return e;
+        done[dev] = true;
+    }
+    const dim3 grid((p.V + SLICE - 1) / SLICE, p.B);
+    adjust_logits_kernel<T, SLICE><<<grid, SLICE / 32, sizeof(Slice<SLICE>), s>>>(p);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
 cudaError_t launch_adjust_logits(const LogitParams &p, int dtype, cudaStream_t s)
 {
-    const dim3 grid((p.V + kSlice - 1) / kSlice, p.B);
-    if (dtype == SPEC_F32) adjust_logits_kernel<float><<<grid, kLogitThreads, 0, s>>>(p);
-    else adjust_logits_kernel<__nv_bfloat16><<<grid, kLogitThreads, 0, s>>>(p);
-    return cudaGetLastError();
+    if (dtype == SPEC_F32) return launch_logits<float, kSlice>(p, s);
+    return launch_logits<__nv_bfloat16, kSlice>(p, s);
 }
 
 }  // namespace specv
