@@ -10,10 +10,11 @@
 // it is bf16 as V is (8 bits: the error it brings is of the size of the output's own rounding), the sums
 // of weights are taken in fp32 before that rounding.
 //
-// Warps: four for each tile's softmax (a thread a row), one that issues the products, one that fetches (tiled TMA
+// Warps: eight for the softmax (a thread a row of its tile, or two that share its keys), one that issues the products, one that fetches (tiled TMA
 // with the 128-byte swizzle) and hands out the items.  D = 64 and 128 keep two tiles in the CTA, whose products
 // alternate: one tile's weights are made while the other's products run.  D = 256 has room for one, and S twice: the
-// next step's S runs beside this step's weights.
+// next step's S runs beside this step's weights; two threads share a row, half of a step's keys each, and half of the
+// channels of O (the shorter chain of a step: see the figures).
 #pragma once
 
 #include "attend.cuh"
@@ -42,7 +43,9 @@ template <int D_> struct Prompt {
     static constexpr int Q_TILE = 128 * D * 2, SLOT = KT * D * 2;
     static constexpr int SLOTS = D == 64 ? 8 : 5;              // of K or V
     static constexpr int SMEM = NQ * Q_TILE + SLOTS * SLOT + 1024;
-    static constexpr int SOFTMAX = NQ * 128, THREADS = SOFTMAX + 64;
+    static constexpr int SHARE = 2 / NQ;                       // threads of a row
+    static constexpr int KH = KT / SHARE, DH = D / SHARE;      // keys of a step, channels, of each
+    static constexpr int SOFTMAX = 256, THREADS = SOFTMAX + 64;
     // Tensor memory: S, O, P.  Products of one shape run in their order, so that at D = 128 P can take the place of
     // its S, which the next S product then overwrites; at 64 and 256 the shapes differ, and P has columns of its own.
     static constexpr int O_COL = NS * KT;
@@ -60,7 +63,7 @@ struct Item {
 
 __device__ __forceinline__ int item_step(const Item &it, int i) { return i < it.np ? i : it.f0 + i - it.np; }
 
-// 2^x for a weight
+// Two values as bf16, the first in the low half
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
 {
     uint32_t r;
@@ -68,12 +71,33 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
     return r;
 }
 
+// Barrier of the softmax warps, with a vote: whether any thread's `x` is true
+__device__ __forceinline__ bool softmax_any(bool x)
+{
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.or.pred q, 1, 256, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"(static_cast<uint32_t>(x))
+        : "memory");
+    return r != 0;
+}
+
+// cap * tanh(y / cap) = cap - 2 cap / (e^(2 y / cap) + 1), to 2^-21 of the cap: for caps of up to kPlainCap that is 3e-5 at
+// most, far below what the weights' 8 bits let through.  (Five instructions; cap_score keeps small scores' digits under
+// any cap, for three times that: see the figures.)
+constexpr float kPlainCap = 64.f;
+__device__ __forceinline__ float plain_cap(float y, float cap, float twice)
+{
+    return fmaf(-2.f * cap, __fdividef(1.f, ex2(y * twice) + 1.f), cap);
+}
+
 template <int D, bool OPT>
 __global__ void __launch_bounds__(Prompt<D>::THREADS, 1)
 prompt_tiles_kernel(const PromptParams p, const __grid_constant__ PromptMaps maps)
 {
     using A = Prompt<D>;
-    constexpr int NQ = A::NQ, KT = A::KT, SLOTS = A::SLOTS, kItems = 2;
+    constexpr int NQ = A::NQ, KT = A::KT, SLOTS = A::SLOTS, SHARE = A::SHARE, KH = A::KH, DH = A::DH, kItems = 2;
     constexpr int kIssuer = A::SOFTMAX / 32, kLoader = kIssuer + 1;
     extern __shared__ uint8_t raw[];
     uint8_t *const smem = raw + ((1024u - (smem_addr(raw) & 1023u)) & 1023u);
@@ -81,6 +105,7 @@ prompt_tiles_kernel(const PromptParams p, const __grid_constant__ PromptMaps map
     __shared__ __align__(8) uint64_t q_full, q_empty, full[SLOTS], empty[SLOTS], tail, s_full[A::NS], p_full[A::NS], o_full[NQ],
         item_full[kItems], item_empty[kItems];
     __shared__ Item items[kItems];
+    __shared__ float shared_row[SHARE == 2 ? 2 : 1][128];      // what the two threads of a row tell each other
     __shared__ uint32_t tmem_base;
     __shared__ int failed;
     const int tid = threadIdx.x, warp = warp_index(), lane = tid & 31;
@@ -97,12 +122,12 @@ prompt_tiles_kernel(const PromptParams p, const __grid_constant__ PromptMaps map
         }
         for (int i = 0; i < A::NS; ++i) {
             mbar_init(&s_full[i], 1);
-            mbar_init(&p_full[i], 4);                 // (a warp may be a step ahead of another where S lies twice)
+            mbar_init(&p_full[i], 4 * SHARE);               // (a warp may be a step ahead of another where S lies twice)
         }
         for (int i = 0; i < NQ; ++i) mbar_init(&o_full[i], 1);
         for (int i = 0; i < kItems; ++i) {
             mbar_init(&item_full[i], 1);
-            mbar_init(&item_empty[i], NQ * 4 + 1);
+            mbar_init(&item_empty[i], A::SOFTMAX / 32 + 1);
         }
         fence_mbar_init();
     }
@@ -329,14 +354,16 @@ prompt_tiles_kernel(const PromptParams p, const __grid_constant__ PromptMaps map
             }
         }
     } else {
-        const int q = warp >> 2, row = tid & 127;     // tile, row of it
+        const int q = SHARE == 2 ? 0 : warp >> 2, row = tid & 127;             // tile, row of it
+        const int part = SHARE == 2 ? warp >> 2 : 0;                           // which of the row's threads
         const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;
-        const uint32_t o_mine = o_t + q * D + lanes;
+        const uint32_t o_mine = o_t + q * D + part * DH + lanes;
         uint32_t count = 0;                           // steps of this tile so far
         const float c = p.scale * kLog2e, cap = p.cap * kLog2e, rcap = p.cap > 0.f ? cap_reciprocal(cap) : 0.f;
+        const float twice = 2.f * kLog2e * rcap;
         // sums over the runs of keys so far, channel by channel
         float *const sums = reinterpret_cast<float *>(static_cast<uint8_t *>(p.ws) + kPromptTickets) +
-                            (static_cast<int64_t>(blockIdx.x) * NQ + q) * 128 * D + row;
+                            ((static_cast<int64_t>(blockIdx.x) * NQ + q) * D + part * DH) * 128 + row;
         if (blockIdx.x == 0 && p.status) {
             PromptTile t;
             for (int b = tid; b < p.B; b += A::SOFTMAX) prompt_request(p, b, p.status, t);
@@ -347,7 +374,9 @@ prompt_tiles_kernel(const PromptParams p, const __grid_constant__ PromptMaps map
             __syncwarp();
             if (lane == 0) mbar_arrive(&item_empty[ir]);
             next_item();
-            if (__shfl_sync(0xFFFFFFFFu, it.h < 0 || fail, 0)) break;
+            // (threads that share rows leave together: they meet at barriers)
+            const bool stop = it.h < 0 || fail;
+            if (SHARE == 2 ? softmax_any(stop) : __any_sync(0xFFFFFFFFu, stop)) break;
             const int i_row = it.first + q * TT + row / group, head = it.h * group + row % group;
             const bool real = row < TT * group && i_row < it.t.n;
             const int own0 = it.t.m - it.t.n + it.first + q * TT;      // last key of the tile's first row
@@ -356,54 +385,58 @@ prompt_tiles_kernel(const PromptParams p, const __grid_constant__ PromptMaps map
             const int n = it.n[q];
             float ref = -INFINITY, l = 0.f, run_ref = 0.f;
             for (int i = 0; i < n; ++i) {
-                const int k0 = item_step(it, i) * KT;
+                const int step0 = item_step(it, i) * KT, k0 = step0 + part * KH;      // of the step, of this thread
                 const int sb = NQ == 2 ? q : count & 1;
                 wait_or_fail(&s_full[sb], (NQ == 2 ? count : count >> 1) & 1, fail);
                 tmem_fence_after();
-                const uint32_t s_mine = s_t + sb * KT + lanes;
-                float s[KT];
+                const uint32_t s_mine = s_t + sb * KT + part * KH + lanes;
+                float s[KH];
 #pragma unroll
-                for (int k = 0; k < KT; k += 32) tmem_ld32(s_mine + k, reinterpret_cast<uint32_t *>(s + k));
+                for (int k = 0; k < KH; k += 32) tmem_ld32(s_mine + k, reinterpret_cast<uint32_t *>(s + k));
                 tmem_wait_ld();
                 if (OPT) {
 #pragma unroll
-                    for (int k = 0; k < KT; ++k) s[k] *= c;
-                    if (p.cap > 0.f) {
+                    for (int k = 0; k < KH; ++k) s[k] *= c;
+                    if (p.cap > kPlainCap) {
 #pragma unroll
-                        for (int k = 0; k < KT; ++k) s[k] = cap_score<false>(s[k], cap, rcap);
+                        for (int k = 0; k < KH; ++k) s[k] = cap_score<false>(s[k], cap, rcap);
+                    } else if (p.cap > 0.f) {
+#pragma unroll
+                        for (int k = 0; k < KH; ++k) s[k] = plain_cap(s[k], cap, twice);
                     }
                     if (p.slopes) {
                         const float far = static_cast<float>(own - k0);
 #pragma unroll
-                        for (int k = 0; k < KT; ++k) s[k] -= slope * (far - static_cast<float>(k));
+                        for (int k = 0; k < KH; ++k) s[k] -= slope * (far - static_cast<float>(k));
                     }
                 }
                 // keys that not all of the tile's rows see
-                if (k0 + KT - 1 > own0 || (p.window > 0 && k0 < own0 + TT - p.window)) {
+                if (step0 + KT - 1 > own0 || (p.window > 0 && step0 < own0 + TT - p.window)) {
                     const int last = own - k0;
                     if (p.window > 0) {
                         const int64_t least = static_cast<int64_t>(last) - p.window;
                         const int near = least < -1 ? -1 : static_cast<int>(least), always = p.prefix - k0;
 #pragma unroll
-                        for (int k = 0; k < KT; ++k) s[k] = k <= last && (k > near || k < always) ? s[k] : -INFINITY;
+                        for (int k = 0; k < KH; ++k) s[k] = k <= last && (k > near || k < always) ? s[k] : -INFINITY;
                     } else {
 #pragma unroll
-                        for (int k = 0; k < KT; ++k) s[k] = k <= last ? s[k] : -INFINITY;
+                        for (int k = 0; k < KH; ++k) s[k] = k <= last ? s[k] : -INFINITY;
                     }
                 }
                 float top[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-                for (int k = 4; k < KT; ++k) top[k & 3] = fmaxf(top[k & 3], s[k]);
+                for (int k = 4; k < KH; ++k) top[k & 3] = fmaxf(top[k & 3], s[k]);
                 float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
                 if (!OPT) most *= c;
-                const bool move = most > ref + kLazy, fresh = i % A::RUN == 0;
+                bool move = most > ref + kLazy;
+                const bool fresh = i % A::RUN == 0;
                 if (fresh && i > 0) {
                     // a run's products to the sums
                     wait_or_fail(&o_full[q], (count - 1) & 1, fail);
                     tmem_fence_after();
                     const float f = i == A::RUN ? 0.f : ex2(run_ref - ref);
 #pragma unroll 1
-                    for (int d = 0; d < D; d += 16) {
+                    for (int d = 0; d < DH; d += 16) {
                         uint32_t r[16];
                         tmem_ld16(o_mine + d, r);
                         tmem_wait_ld();
@@ -415,7 +448,15 @@ prompt_tiles_kernel(const PromptParams p, const __grid_constant__ PromptMaps map
                     }
                     run_ref = ref;
                 }
-                if (__any_sync(0xFFFFFFFFu, move)) {
+                const bool any = SHARE == 2 ? softmax_any(move) : __any_sync(0xFFFFFFFFu, move);
+                if (any) {
+                    if (SHARE == 2) {
+                        // (both threads of a row take the same reference; the vote before keeps the places free)
+                        shared_row[part][row] = most;
+                        softmax_any(false);
+                        most = fmaxf(most, shared_row[part ^ 1][row]);
+                        move = most > ref + kLazy;
+                    }
                     const float to = move ? most : ref, f = move ? ex2(ref - to) : 1.f;
                     ref = to;
                     l *= f;
@@ -423,7 +464,7 @@ prompt_tiles_kernel(const PromptParams p, const __grid_constant__ PromptMaps map
                         wait_or_fail(&o_full[q], (count - 1) & 1, fail);
                         tmem_fence_after();
 #pragma unroll 1
-                        for (int d = 0; d < D; d += 16) {
+                        for (int d = 0; d < DH; d += 16) {
                             uint32_t r[16];
                             tmem_ld16(o_mine + d, r);
                             tmem_wait_ld();
@@ -437,7 +478,7 @@ prompt_tiles_kernel(const PromptParams p, const __grid_constant__ PromptMaps map
                 const uint64_t c2 = OPT ? f2_pack(1.f, 1.f) : f2_pack(c, c), down2 = f2_pack(down, down);
                 uint64_t sum = 0;
 #pragma unroll
-                for (int k = 0; k < KT; k += 32) {
+                for (int k = 0; k < KH; k += 32) {
                     uint32_t w[16];
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
@@ -448,7 +489,7 @@ prompt_tiles_kernel(const PromptParams p, const __grid_constant__ PromptMaps map
                         sum = f2_add(sum, f2_pack(x, y));
                         w[e] = pack_bf16(x, y);
                     }
-                    tmem_st16(s_t + A::P_COL + sb * A::P_STEP + lanes + k / 2, w);
+                    tmem_st16(s_t + A::P_COL + sb * A::P_STEP + part * (KH / 2) + lanes + k / 2, w);
                 }
                 float x, y;
                 f2_unpack(sum, x, y);
@@ -460,6 +501,13 @@ prompt_tiles_kernel(const PromptParams p, const __grid_constant__ PromptMaps map
                 ++count;
             }
             // the tile's results
+            if (SHARE == 2) {
+                softmax_any(false);
+                shared_row[part][row] = l;
+                softmax_any(false);
+                l += shared_row[part ^ 1][row];
+                softmax_any(false);
+            }
             const float inv = l > 0.f ? 1.f / l : 0.f;
             if (n > 0) {
                 // (NQ = 1: the step before the last can be under way as well, and a wait is for the phase at hand or the one before)
@@ -468,10 +516,10 @@ prompt_tiles_kernel(const PromptParams p, const __grid_constant__ PromptMaps map
                 tmem_fence_after();
             }
             const int64_t at = (static_cast<int64_t>(it.t.lo) + i_row) * p.Hq + head;
-            __nv_bfloat16 *const to = static_cast<__nv_bfloat16 *>(p.out) + at * D;
+            __nv_bfloat16 *const to = static_cast<__nv_bfloat16 *>(p.out) + at * D + part * DH;
             const float f = n > A::RUN ? ex2(run_ref - ref) : 0.f;
 #pragma unroll 1
-            for (int d = 0; d < D; d += 32) {
+            for (int d = 0; d < DH; d += 32) {
                 uint32_t r[32] = {};
                 if (n > 0) {
                     tmem_ld32(o_mine + d, r);
@@ -496,7 +544,7 @@ prompt_tiles_kernel(const PromptParams p, const __grid_constant__ PromptMaps map
                 }
                 __syncwarp();
             }
-            if (real && !fail && p.lse) p.lse[at] = l > 0.f ? (ref + log2f(l)) * kLn2 : -INFINITY;
+            if (real && !fail && p.lse && part == 0) p.lse[at] = l > 0.f ? (ref + log2f(l)) * kLn2 : -INFINITY;
             tmem_fence_before();                      // (O is free with the next item's first weights)
         }
     }
