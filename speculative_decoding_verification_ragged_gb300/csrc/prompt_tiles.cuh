@@ -41,8 +41,9 @@ template <int D_> struct Prompt {
     static constexpr int KT = D == 256 ? 64 : 128;             // keys of a step
     static constexpr int RUN = kRunKeys / KT;
     static constexpr int Q_TILE = 128 * D * 2, SLOT = KT * D * 2;
-    static constexpr int SLOTS = D == 64 ? 8 : 5;              // of K or V
-    static constexpr int SMEM = NQ * Q_TILE + SLOTS * SLOT + 1024;
+    static constexpr int SLOTS = D == 64 ? 8 : 4;              // of K or V
+    static constexpr int STAGE = 32 * 128;                     // results on their way out: 32 rows of 64 channels a warp
+    static constexpr int SMEM = NQ * Q_TILE + SLOTS * SLOT + 8 * STAGE + 1024;
     static constexpr int SHARE = 2 / NQ;                       // threads of a row
     static constexpr int KH = KT / SHARE, DH = D / SHARE;      // keys of a step, channels, of each
     static constexpr int SOFTMAX = 256, THREADS = SOFTMAX + 64;
@@ -83,13 +84,17 @@ __device__ __forceinline__ bool softmax_any(bool x)
     return r != 0;
 }
 
-// cap * tanh(y / cap) = cap - 2 cap / (e^(2 y / cap) + 1), to 2^-21 of the cap: for caps of up to kPlainCap that is 3e-5 at
-// most, far below what the weights' 8 bits let through.  (Five instructions; cap_score keeps small scores' digits under
-// any cap, for three times that: see the figures.)
-constexpr float kPlainCap = 64.f;
-__device__ __forceinline__ float plain_cap(float y, float cap, float twice)
+// tanh(z) for |z| <= kTame as z times a polynomial in z^2 (interpolated at Chebyshev's points of [0, kTame^2]: within
+// 2^-22 of the result), in packed pairs and without the special functions, which weights and quotients keep busy.
+constexpr float kTame = 0.75f;
+__device__ __forceinline__ uint64_t tame_tanh(uint64_t z)
 {
-    return fmaf(-2.f * cap, __fdividef(1.f, ex2(y * twice) + 1.f), cap);
+    constexpr float co[6] = {1.0f, -0.333329529f, 0.133253396f, -0.0533411168f, 0.0195762161f, -0.00471152226f};
+    const uint64_t t = f2_fma(z, z, 0);
+    uint64_t y = f2_pack(co[5], co[5]);
+#pragma unroll
+    for (int i = 4; i >= 0; --i) y = f2_fma(y, t, f2_pack(co[i], co[i]));
+    return f2_fma(y, z, 0);
 }
 
 template <int D, bool OPT>
@@ -102,7 +107,7 @@ prompt_tiles_kernel(const PromptParams p, const __grid_constant__ PromptMaps map
     extern __shared__ uint8_t raw[];
     uint8_t *const smem = raw + ((1024u - (smem_addr(raw) & 1023u)) & 1023u);
     uint8_t *const qs = smem, *const slots = smem + NQ * A::Q_TILE;
-    __shared__ __align__(8) uint64_t q_full, q_empty, full[SLOTS], empty[SLOTS], tail, s_full[A::NS], p_full[A::NS], o_full[NQ],
+    __shared__ __align__(8) uint64_t q_full, q_empty, full[SLOTS], empty[SLOTS], tail, s_full[A::NS], p_full[A::NS], o_full[A::NS],
         item_full[kItems], item_empty[kItems];
     __shared__ Item items[kItems];
     __shared__ float shared_row[SHARE == 2 ? 2 : 1][128];      // what the two threads of a row tell each other
@@ -122,9 +127,9 @@ prompt_tiles_kernel(const PromptParams p, const __grid_constant__ PromptMaps map
         }
         for (int i = 0; i < A::NS; ++i) {
             mbar_init(&s_full[i], 1);
+            mbar_init(&o_full[i], 1);
             mbar_init(&p_full[i], 4 * SHARE);               // (a warp may be a step ahead of another where S lies twice)
         }
-        for (int i = 0; i < NQ; ++i) mbar_init(&o_full[i], 1);
         for (int i = 0; i < kItems; ++i) {
             mbar_init(&item_full[i], 1);
             mbar_init(&item_empty[i], A::SOFTMAX / 32 + 1);
@@ -155,6 +160,10 @@ prompt_tiles_kernel(const PromptParams p, const __grid_constant__ PromptMaps map
         int ring = 0, b0 = 0;
         uint32_t phase = 1, q_phase = 1, tail_phase = 0;
         int64_t base = 0, index = blockIdx.x;         // tiles of the requests before b0; the item
+        // 32 requests from b0 on, a lane each, kept from item to item: their tiles up to and with this lane's
+        PromptTile t = {};
+        int known = -1;
+        int64_t mine = 0, upto = 0;
         const auto slot = [&](bool value, const Item &it, int step) {
             const int k0 = step * KT;
             wait_or_fail(&empty[ring], phase, fail);
@@ -193,17 +202,17 @@ prompt_tiles_kernel(const PromptParams p, const __grid_constant__ PromptMaps map
             const int64_t line = index / p.H;
             // the request whose tiles hold `line`, its last (longest) tile first
             while (b0 < p.B && !fail) {
-                PromptTile t;
-                int64_t mine = 0;
-                if (b0 + lane < p.B && prompt_request(p, b0 + lane, nullptr, t)) mine = (t.n + NQ * TT - 1) / (NQ * TT);
-                int64_t at = mine;
+                if (known != b0) {
+                    mine = b0 + lane < p.B && prompt_request(p, b0 + lane, nullptr, t) ? (t.n + NQ * TT - 1) / (NQ * TT) : 0;
+                    upto = mine;
 #pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const int64_t y = __shfl_up_sync(0xFFFFFFFFu, at, o);
-                    if (lane >= o) at += y;
+                    for (int o = 1; o < 32; o <<= 1) {
+                        const int64_t y = __shfl_up_sync(0xFFFFFFFFu, upto, o);
+                        if (lane >= o) upto += y;
+                    }
+                    known = b0;
                 }
-                const int64_t all = __shfl_sync(0xFFFFFFFFu, at, 31);
-                at += base;
+                const int64_t at = base + upto, all = __shfl_sync(0xFFFFFFFFu, upto, 31);
                 const uint32_t hit = __ballot_sync(0xFFFFFFFFu, at - mine <= line && line < at);
                 if (hit) {
                     const int from = __ffs(hit) - 1;
@@ -306,7 +315,7 @@ prompt_tiles_kernel(const PromptParams p, const __grid_constant__ PromptMaps map
             for (int k = 0; k < KT / 16; ++k)
                 mma_f16(o_t + q * D, s_t + A::P_COL + s * A::P_STEP + k * 8, smem_desc_swizzled(b + k * 2048, KT * 128),
                         mma_f16_desc(D, true, true), accumulate || k > 0);
-            mma_commit(&o_full[q]);
+            mma_commit(&o_full[s]);
         };
         for (;;) {
             wait_or_fail(&item_full[ir], i_phase, fail);
@@ -360,7 +369,6 @@ prompt_tiles_kernel(const PromptParams p, const __grid_constant__ PromptMaps map
         const uint32_t o_mine = o_t + q * D + part * DH + lanes;
         uint32_t count = 0;                           // steps of this tile so far
         const float c = p.scale * kLog2e, cap = p.cap * kLog2e, rcap = p.cap > 0.f ? cap_reciprocal(cap) : 0.f;
-        const float twice = 2.f * kLog2e * rcap;
         // sums over the runs of keys so far, channel by channel
         float *const sums = reinterpret_cast<float *>(static_cast<uint8_t *>(p.ws) + kPromptTickets) +
                             ((static_cast<int64_t>(blockIdx.x) * NQ + q) * D + part * DH) * 128 + row;
@@ -368,6 +376,13 @@ prompt_tiles_kernel(const PromptParams p, const __grid_constant__ PromptMaps map
             PromptTile t;
             for (int b = tid; b < p.B; b += A::SOFTMAX) prompt_request(p, b, p.status, t);
         }
+        // Wait for the products with V of the tile's step `j`.  (Where S lies twice, the step before can be under way too when
+        // this is asked, and a parity tells two phases apart: the steps take turns at two barriers, as with S and P.)
+        const auto values_done = [&](uint32_t j) {
+            wait_or_fail(&o_full[NQ == 2 ? q : j & 1], (NQ == 2 ? j : j >> 1) & 1, fail);
+            tmem_fence_after();
+        };
+        uint8_t *const stage = slots + SLOTS * A::SLOT + warp * A::STAGE;
         for (;;) {
             wait_or_fail(&item_full[ir], i_phase, fail);
             const Item it = items[ir];
@@ -394,35 +409,53 @@ prompt_tiles_kernel(const PromptParams p, const __grid_constant__ PromptMaps map
 #pragma unroll
                 for (int k = 0; k < KH; k += 32) tmem_ld32(s_mine + k, reinterpret_cast<uint32_t *>(s + k));
                 tmem_wait_ld();
-                if (OPT) {
+                // keys that not all of the tile's rows see: hidden ones get `x`
+                const auto hide = [&](float x) {
+                    if (step0 + KT - 1 > own0 || (p.window > 0 && step0 < own0 + TT - p.window)) {
+                        const int last = own - k0;
+                        if (p.window > 0) {
+                            const int64_t least = static_cast<int64_t>(last) - p.window;
+                            const int near = least < -1 ? -1 : static_cast<int>(least), always = p.prefix - k0;
 #pragma unroll
-                    for (int k = 0; k < KH; ++k) s[k] *= c;
-                    if (p.cap > kPlainCap) {
+                            for (int k = 0; k < KH; ++k) s[k] = k <= last && (k > near || k < always) ? s[k] : x;
+                        } else {
 #pragma unroll
-                        for (int k = 0; k < KH; ++k) s[k] = cap_score<false>(s[k], cap, rcap);
-                    } else if (p.cap > 0.f) {
+                            for (int k = 0; k < KH; ++k) s[k] = k <= last ? s[k] : x;
+                        }
+                    }
+                };
+                if constexpr (OPT) {
+                    // the scores in log2 units; the way of the tanh is chosen by what this row sees alone
+                    if (p.cap > 0.f) {
+                        hide(0.f);
+                        float large = 0.f;
 #pragma unroll
-                        for (int k = 0; k < KH; ++k) s[k] = plain_cap(s[k], cap, twice);
+                        for (int k = 0; k < KH; ++k) large = fmaxf(large, fabsf(s[k]));
+                        if (!real || large * fabsf(c * rcap) <= kTame) {
+                            const uint64_t z2 = f2_pack(c * rcap, c * rcap), cap2 = f2_pack(cap, cap);
+#pragma unroll
+                            for (int e = 0; e < KH / 2; ++e)
+                                f2_unpack(f2_fma(tame_tanh(f2_fma(f2_pack(s[2 * e], s[2 * e + 1]), z2, 0)), cap2, 0), s[2 * e], s[2 * e + 1]);
+                        } else {
+#pragma unroll
+                            for (int k = 0; k < KH; ++k) s[k] = cap_score<false>(s[k] * c, cap, rcap);
+                        }
+                        __syncwarp();
+                    } else {
+                        const uint64_t c2 = f2_pack(c, c);
+#pragma unroll
+                        for (int e = 0; e < KH / 2; ++e) f2_unpack(f2_fma(f2_pack(s[2 * e], s[2 * e + 1]), c2, 0), s[2 * e], s[2 * e + 1]);
                     }
                     if (p.slopes) {
-                        const float far = static_cast<float>(own - k0);
+                        const float far = -slope * static_cast<float>(own - k0);
+                        const uint64_t far2 = f2_pack(far, far), slope2 = f2_pack(slope, slope);
 #pragma unroll
-                        for (int k = 0; k < KH; ++k) s[k] -= slope * (far - static_cast<float>(k));
+                        for (int e = 0; e < KH / 2; ++e)
+                            f2_unpack(f2_add(f2_pack(s[2 * e], s[2 * e + 1]), f2_fma(slope2, f2_pack(2.f * e, 2.f * e + 1.f), far2)),
+                                      s[2 * e], s[2 * e + 1]);
                     }
                 }
-                // keys that not all of the tile's rows see
-                if (step0 + KT - 1 > own0 || (p.window > 0 && step0 < own0 + TT - p.window)) {
-                    const int last = own - k0;
-                    if (p.window > 0) {
-                        const int64_t least = static_cast<int64_t>(last) - p.window;
-                        const int near = least < -1 ? -1 : static_cast<int>(least), always = p.prefix - k0;
-#pragma unroll
-                        for (int k = 0; k < KH; ++k) s[k] = k <= last && (k > near || k < always) ? s[k] : -INFINITY;
-                    } else {
-#pragma unroll
-                        for (int k = 0; k < KH; ++k) s[k] = k <= last ? s[k] : -INFINITY;
-                    }
-                }
+                hide(-INFINITY);
                 float top[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
                 for (int k = 4; k < KH; ++k) top[k & 3] = fmaxf(top[k & 3], s[k]);
@@ -432,8 +465,7 @@ prompt_tiles_kernel(const PromptParams p, const __grid_constant__ PromptMaps map
                 const bool fresh = i % A::RUN == 0;
                 if (fresh && i > 0) {
                     // a run's products to the sums
-                    wait_or_fail(&o_full[q], (count - 1) & 1, fail);
-                    tmem_fence_after();
+                    values_done(count - 1);
                     const float f = i == A::RUN ? 0.f : ex2(run_ref - ref);
 #pragma unroll 1
                     for (int d = 0; d < DH; d += 16) {
@@ -461,8 +493,7 @@ prompt_tiles_kernel(const PromptParams p, const __grid_constant__ PromptMaps map
                     ref = to;
                     l *= f;
                     if (!fresh) {
-                        wait_or_fail(&o_full[q], (count - 1) & 1, fail);
-                        tmem_fence_after();
+                        values_done(count - 1);
 #pragma unroll 1
                         for (int d = 0; d < DH; d += 16) {
                             uint32_t r[16];
@@ -475,7 +506,7 @@ prompt_tiles_kernel(const PromptParams p, const __grid_constant__ PromptMaps map
                     }
                 }
                 const float down = ref == -INFINITY ? 0.f : -ref;
-                const uint64_t c2 = OPT ? f2_pack(1.f, 1.f) : f2_pack(c, c), down2 = f2_pack(down, down);
+                const uint64_t c2 = f2_pack(c, c), down2 = f2_pack(down, down);
                 uint64_t sum = 0;
 #pragma unroll
                 for (int k = 0; k < KH; k += 32) {
@@ -483,7 +514,8 @@ prompt_tiles_kernel(const PromptParams p, const __grid_constant__ PromptMaps map
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
                         float x, y;
-                        f2_unpack(f2_fma(f2_pack(s[k + 2 * e], s[k + 2 * e + 1]), c2, down2), x, y);
+                        const uint64_t two = f2_pack(s[k + 2 * e], s[k + 2 * e + 1]);
+                        f2_unpack(OPT ? f2_add(two, down2) : f2_fma(two, c2, down2), x, y);
                         x = ex2(x);
                         y = ex2(y);
                         sum = f2_add(sum, f2_pack(x, y));
@@ -510,37 +542,40 @@ prompt_tiles_kernel(const PromptParams p, const __grid_constant__ PromptMaps map
             }
             const float inv = l > 0.f ? 1.f / l : 0.f;
             if (n > 0) {
-                // (NQ = 1: the step before the last can be under way as well, and a wait is for the phase at hand or the one before)
-                if (NQ == 1) wait_or_fail(&o_full[q], count & 1, fail);
-                wait_or_fail(&o_full[q], (count - 1) & 1, fail);
-                tmem_fence_after();
+                values_done(count - 1);
             }
             const int64_t at = (static_cast<int64_t>(it.t.lo) + i_row) * p.Hq + head;
-            __nv_bfloat16 *const to = static_cast<__nv_bfloat16 *>(p.out) + at * D + part * DH;
             const float f = n > A::RUN ? ex2(run_ref - ref) : 0.f;
+            // 64 channels at a time by way of shared memory: 8 lanes then write a row's 128 bytes (a thread's own row
+            // by itself meets 32 lines with every store)
+            const int64_t place = real && !fail ? at * D + part * DH : -1;
 #pragma unroll 1
-            for (int d = 0; d < DH; d += 32) {
-                uint32_t r[32] = {};
-                if (n > 0) {
-                    tmem_ld32(o_mine + d, r);
-                    tmem_wait_ld();
-                }
-                if (real && !fail) {
+            for (int d = 0; d < DH; d += 64) {
+#pragma unroll
+                for (int d2 = 0; d2 < 64; d2 += 32) {
+                    uint32_t r[32] = {};
+                    if (n > 0) {
+                        tmem_ld32(o_mine + d + d2, r);
+                        tmem_wait_ld();
+                    }
                     float v[32];
 #pragma unroll
                     for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(r[e]);
                     if (n > A::RUN)
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) v[e] += sums[(d + e) * 128] * f;
+                        for (int e = 0; e < 32; ++e) v[e] += sums[(d + d2 + e) * 128] * f;
 #pragma unroll
-                    for (int e = 0; e < 32; e += 8) {
-                        uint4 w;
-                        w.x = pack_bf16(v[e] * inv, v[e + 1] * inv);
-                        w.y = pack_bf16(v[e + 2] * inv, v[e + 3] * inv);
-                        w.z = pack_bf16(v[e + 4] * inv, v[e + 5] * inv);
-                        w.w = pack_bf16(v[e + 6] * inv, v[e + 7] * inv);
-                        *reinterpret_cast<uint4 *>(to + d + e) = w;
-                    }
+                    for (int e = 0; e < 32; e += 8)
+                        *reinterpret_cast<uint4 *>(stage + lane * 128 + (((d2 + e) / 8) ^ (lane & 7)) * 16) =
+                            make_uint4(pack_bf16(v[e] * inv, v[e + 1] * inv), pack_bf16(v[e + 2] * inv, v[e + 3] * inv),
+                                       pack_bf16(v[e + 4] * inv, v[e + 5] * inv), pack_bf16(v[e + 6] * inv, v[e + 7] * inv));
+                }
+                __syncwarp();
+#pragma unroll
+                for (int r = lane / 8; r < 32; r += 4) {
+                    const int64_t to = __shfl_sync(0xFFFFFFFFu, place, r);
+                    const uint4 x = *reinterpret_cast<const uint4 *>(stage + r * 128 + ((lane & 7) ^ (r & 7)) * 16);
+                    if (to >= 0) *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.out) + to + d + (lane & 7) * 8) = x;
                 }
                 __syncwarp();
             }
