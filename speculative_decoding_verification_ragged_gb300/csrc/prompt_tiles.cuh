@@ -46,7 +46,10 @@ template <int D_> struct Prompt {
     static constexpr int SMEM = NQ * Q_TILE + SLOTS * SLOT + 8 * STAGE + 1024;
     static constexpr int SHARE = 2 / NQ;                       // threads of a row
     static constexpr int KH = KT / SHARE, DH = D / SHARE;      // keys of a step, channels, of each
-    static constexpr int SOFTMAX = 256, THREADS = SOFTMAX + 64;
+    // (The third warpgroup has two warps that idle: registers move between warpgroups.  384 threads launch with 168 each,
+    // 64512 in all = 256 x 208 + 128 x 88.)
+    static constexpr int SOFTMAX = 256, THREADS = SOFTMAX + 128, LAUNCH_REGS = 168, MORE_REGS = 208, LESS_REGS = 88;
+    static_assert(SOFTMAX * MORE_REGS + 128 * LESS_REGS == THREADS * LAUNCH_REGS, "no more registers than the launch has");
     // Tensor memory: S, O, P.  Products of one shape run in their order, so that at D = 128 P can take the place of
     // its S, which the next S product then overwrites; at 64 and 256 the shapes differ, and P has columns of its own.
     static constexpr int O_COL = NS * KT;
@@ -107,7 +110,7 @@ prompt_tiles_kernel(const PromptParams p, const __grid_constant__ PromptMaps map
     extern __shared__ uint8_t raw[];
     uint8_t *const smem = raw + ((1024u - (smem_addr(raw) & 1023u)) & 1023u);
     uint8_t *const qs = smem, *const slots = smem + NQ * A::Q_TILE;
-    __shared__ __align__(8) uint64_t q_full, q_empty, full[SLOTS], empty[SLOTS], tail, s_full[A::NS], p_full[A::NS], o_full[A::NS],
+    __shared__ __align__(8) uint64_t q_full[NQ], q_empty[NQ], full[SLOTS], empty[SLOTS], tail, s_full[A::NS], p_full[A::NS], o_full[A::NS],
         item_full[kItems], item_empty[kItems];
     __shared__ Item items[kItems];
     __shared__ float shared_row[SHARE == 2 ? 2 : 1][128];      // what the two threads of a row tell each other
@@ -118,9 +121,11 @@ prompt_tiles_kernel(const PromptParams p, const __grid_constant__ PromptMaps map
 
     if (tid == 0) {
         failed = 0;
-        mbar_init(&q_full, 1);
-        mbar_init(&q_empty, 1);
         mbar_init(&tail, 1);
+        for (int i = 0; i < NQ; ++i) {
+            mbar_init(&q_full[i], 1);
+            mbar_init(&q_empty[i], 1);
+        }
         for (int i = 0; i < SLOTS; ++i) {
             mbar_init(&full[i], 1);
             mbar_init(&empty[i], 1);
@@ -150,219 +155,236 @@ prompt_tiles_kernel(const PromptParams p, const __grid_constant__ PromptMaps map
         }
     };
 
-    if (warp == kLoader) {
-        uint32_t *const ticket = static_cast<uint32_t *>(p.ws);        // items taken, CTAs that are done
-        if (lane == 0) {
-            tma_prefetch(&maps.q);
-            tma_prefetch(&maps.k);
-            tma_prefetch(&maps.v);
-        }
-        int ring = 0, b0 = 0;
-        uint32_t phase = 1, q_phase = 1, tail_phase = 0;
-        int64_t base = 0, index = blockIdx.x;         // tiles of the requests before b0; the item
-        // 32 requests from b0 on, a lane each, kept from item to item: their tiles up to and with this lane's
-        PromptTile t = {};
-        int known = -1;
-        int64_t mine = 0, upto = 0;
-        const auto slot = [&](bool value, const Item &it, int step) {
-            const int k0 = step * KT;
-            wait_or_fail(&empty[ring], phase, fail);
-            uint8_t *const to = slots + ring * A::SLOT;
-            // values that no row of the request sees become zeros (0 x NaN would reach every row of the tile)
-            const int live = p.window > 0 ? max(it.t.m - it.t.n - p.window + 1, 0) : 0;
-            const bool part = value && (k0 + KT > it.t.m || (k0 < live && k0 + KT > p.prefix));
-            uint64_t *const bar = part ? &tail : &full[ring];
+    if (warp >= kIssuer) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(A::LESS_REGS));
+        if (warp == kLoader) {
+            uint32_t *const ticket = static_cast<uint32_t *>(p.ws);        // items taken, CTAs that are done
             if (lane == 0) {
-                mbar_arrive_expect_tx(bar, A::SLOT);
-#pragma unroll
-                for (int x = 0; x < D; x += 64)
-                    tma_load_3d(to + x * KT * 2, value ? &maps.v : &maps.k, x, it.h, it.t.k_lo + k0, bar);
+                tma_prefetch(&maps.q);
+                tma_prefetch(&maps.k);
+                tma_prefetch(&maps.v);
             }
-            __syncwarp();
-            if (part) {
-                wait_or_fail(&tail, tail_phase, fail);
-                tail_phase ^= 1;
-                for (int e = lane; e < KT * D / 8; e += 32) {
-                    const int r = e / 8 % KT, j = k0 + r;
-                    if (j >= it.t.m || (j < live && j >= p.prefix))
-                        *reinterpret_cast<uint4 *>(to + static_cast<int64_t>(e) * 16) = make_uint4(0, 0, 0, 0);
-                }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&full[ring]);
-            }
-            if (++ring == SLOTS) {
-                ring = 0;
-                phase ^= 1;
-            }
-        };
-        for (;;) {
-            Item it;
-            it.h = -1;
-            const int64_t line = index / p.H;
-            // the request whose tiles hold `line`, its last (longest) tile first
-            while (b0 < p.B && !fail) {
-                if (known != b0) {
-                    mine = b0 + lane < p.B && prompt_request(p, b0 + lane, nullptr, t) ? (t.n + NQ * TT - 1) / (NQ * TT) : 0;
-                    upto = mine;
-#pragma unroll
-                    for (int o = 1; o < 32; o <<= 1) {
-                        const int64_t y = __shfl_up_sync(0xFFFFFFFFu, upto, o);
-                        if (lane >= o) upto += y;
-                    }
-                    known = b0;
-                }
-                const int64_t at = base + upto, all = __shfl_sync(0xFFFFFFFFu, upto, 31);
-                const uint32_t hit = __ballot_sync(0xFFFFFFFFu, at - mine <= line && line < at);
-                if (hit) {
-                    const int from = __ffs(hit) - 1;
-                    it.t.b = b0 + from;
-                    it.t.lo = __shfl_sync(0xFFFFFFFFu, t.lo, from);
-                    it.t.n = __shfl_sync(0xFFFFFFFFu, t.n, from);
-                    it.t.k_lo = __shfl_sync(0xFFFFFFFFu, t.k_lo, from);
-                    it.t.m = __shfl_sync(0xFFFFFFFFu, t.m, from);
-                    it.first = static_cast<int>(__shfl_sync(0xFFFFFFFFu, at, from) - 1 - line) * (NQ * TT);
-                    it.h = static_cast<int>(index % p.H);
-                    break;
-                }
-                base += all;
-                b0 += 32;
-            }
-            if (it.h >= 0) {
-                const int own = it.t.m - it.t.n + it.first;            // last key of the first row
-                const int near = p.window > 0 ? max(own - p.window + 1, 0) / KT : 0;
-                it.f0 = near;
-                it.np = min((p.prefix + KT - 1) / KT, near);
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    const int rows = min(it.t.n - it.first - q * TT, TT);
-                    const int last = rows > 0 && q < NQ ? own + q * TT + rows - 1 : -1;
-                    it.n[q] = last < 0 ? 0 : it.np + last / KT + 1 - near;
-                }
-            }
-            wait_or_fail(&item_empty[ir], i_phase ^ 1, fail);
-            if (fail) it.h = -1;
-            if (lane == 0) {
-                items[ir] = it;
-                mbar_arrive(&item_full[ir]);
-            }
-            __syncwarp();
-            next_item();
-            if (it.h < 0) break;
-            // (asked for here, looked at after the item)
-            uint32_t taken = 0;
-            if (lane == 0) taken = atomicAdd(ticket, 1u);
-            const int n = max(it.n[0], it.n[1]);
-            if (n > 0) {
-                wait_or_fail(&q_empty, q_phase, fail);
-                q_phase ^= 1;
+            int ring = 0, b0 = 0;
+            uint32_t phase = 1, tail_phase = 0, q_phase[NQ];
+            for (int q = 0; q < NQ; ++q) q_phase[q] = 1;
+            int64_t base = 0, index = blockIdx.x;         // tiles of the requests before b0; the item
+            // 32 requests from b0 on, a lane each, kept from item to item: their tiles up to and with this lane's
+            PromptTile t = {};
+            int known = -1;
+            int64_t mine = 0, upto = 0;
+            const auto slot = [&](bool value, const Item &it, int step) {
+                const int k0 = step * KT;
+                wait_or_fail(&empty[ring], phase, fail);
+                uint8_t *const to = slots + ring * A::SLOT;
+                // values that no row of the request sees become zeros (0 x NaN would reach every row of the tile)
+                const int live = p.window > 0 ? max(it.t.m - it.t.n - p.window + 1, 0) : 0;
+                const bool part = value && (k0 + KT > it.t.m || (k0 < live && k0 + KT > p.prefix));
+                uint64_t *const bar = part ? &tail : &full[ring];
                 if (lane == 0) {
-                    const int tiles = it.n[1] > 0 ? 2 : 1;
-                    mbar_arrive_expect_tx(&q_full, tiles * TT * group * D * 2);
-                    for (int q = 0; q < tiles; ++q)
+                    mbar_arrive_expect_tx(bar, A::SLOT);
 #pragma unroll
-                        for (int x = 0; x < D; x += 64)
-                            tma_load_3d(qs + q * A::Q_TILE + x * 256, &maps.q, x, it.h * group, it.t.lo + it.first + q * TT, &q_full);
+                    for (int x = 0; x < D; x += 64)
+                        tma_load_3d(to + x * KT * 2, value ? &maps.v : &maps.k, x, it.h, it.t.k_lo + k0, bar);
                 }
                 __syncwarp();
-                // in the order of the products
-                slot(false, it, item_step(it, 0));
-                for (int i = 0; i < n; ++i) {
-                    if (NQ == 2) slot(true, it, item_step(it, i));
-                    if (i + 1 < n) slot(false, it, item_step(it, i + 1));
-                    if (NQ == 1) slot(true, it, item_step(it, i));
-                }
-            }
-            index = static_cast<int64_t>(gridDim.x) + __shfl_sync(0xFFFFFFFFu, taken, 0);
-        }
-        // the last CTA leaves the tickets as it found them
-        if (lane == 0) {
-            fence_acq_rel_gpu();
-            if (atomicAdd(ticket + 1, 1u) == gridDim.x - 1) {
-                ticket[0] = 0u;
-                ticket[1] = 0u;
-            }
-        }
-    } else if (warp == kIssuer) {
-        const uint32_t q_addr = smem_addr(qs), slot_addr = smem_addr(slots);
-        int ring = 0;
-        uint32_t phase = 0, q_phase = 0, p_phase[A::NS] = {};
-        uint32_t steps = 0;                           // NQ = 1: steps so far, whose S alternates
-        const auto arrived = [&] {                    // the next slot of the ring: its place
-            wait_or_fail(&full[ring], phase, fail);
-            tmem_fence_after();
-            const int at = ring;
-            if (++ring == SLOTS) {
-                ring = 0;
-                phase ^= 1;
-            }
-            return at;
-        };
-        const auto scores = [&](int q, int s, int at) {
-            const uint32_t a = q_addr + q * A::Q_TILE, b = slot_addr + at * A::SLOT;
-#pragma unroll
-            for (int k = 0; k < D / 16; ++k)
-                mma_f16_shared(s_t + s * KT, smem_desc_swizzled(a + k / 4 * (128 * 128) + k % 4 * 32, 16),
-                               smem_desc_swizzled(b + k / 4 * (KT * 128) + k % 4 * 32, 16), mma_f16_desc(KT, false, true), k > 0);
-            mma_commit(&s_full[s]);
-        };
-        const auto values = [&](int q, int s, int at, bool accumulate) {
-            const uint32_t b = slot_addr + at * A::SLOT;
-            wait_or_fail(&p_full[s], p_phase[s], fail);
-            p_phase[s] ^= 1;
-            tmem_fence_after();
-#pragma unroll
-            for (int k = 0; k < KT / 16; ++k)
-                mma_f16(o_t + q * D, s_t + A::P_COL + s * A::P_STEP + k * 8, smem_desc_swizzled(b + k * 2048, KT * 128),
-                        mma_f16_desc(D, true, true), accumulate || k > 0);
-            mma_commit(&o_full[s]);
-        };
-        for (;;) {
-            wait_or_fail(&item_full[ir], i_phase, fail);
-            const int h = *reinterpret_cast<volatile int *>(&items[ir].h);
-            const int n0 = *reinterpret_cast<volatile int *>(&items[ir].n[0]), n1 = *reinterpret_cast<volatile int *>(&items[ir].n[1]);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&item_empty[ir]);
-            next_item();
-            if (__shfl_sync(0xFFFFFFFFu, h < 0 || fail, 0)) break;
-            const int n = max(n0, n1);
-            if (n == 0) continue;
-            wait_or_fail(&q_full, q_phase, fail);
-            q_phase ^= 1;
-            int at = arrived();
-            if constexpr (NQ == 2) {
-                if (n0 > 0) scores(0, 0, at);
-                if (n1 > 0) scores(1, 1, at);
-            } else {
-                scores(0, steps & 1, at);
-            }
-            mma_commit(&empty[at]);
-            if (n == 1) mma_commit(&q_empty);
-            for (int i = 0; i < n; ++i) {
-                const bool more = i + 1 < n, accumulate = i % A::RUN != 0;
-                if constexpr (NQ == 2) {
-                    const int v = arrived();
-                    if (i < n0) values(0, 0, v, accumulate);
-                    if (more) at = arrived();
-                    if (i + 1 < n0) scores(0, 0, at);
-                    if (i < n1) values(1, 1, v, accumulate);
-                    mma_commit(&empty[v]);
-                    if (i + 1 < n1) scores(1, 1, at);
-                } else {
-                    if (more) {
-                        at = arrived();
-                        scores(0, (steps + 1) & 1, at);
+                if (part) {
+                    wait_or_fail(&tail, tail_phase, fail);
+                    tail_phase ^= 1;
+                    for (int e = lane; e < KT * D / 8; e += 32) {
+                        const int r = e / 8 % KT, j = k0 + r;
+                        if (j >= it.t.m || (j < live && j >= p.prefix))
+                            *reinterpret_cast<uint4 *>(to + static_cast<int64_t>(e) * 16) = make_uint4(0, 0, 0, 0);
                     }
-                    const int v = arrived();
-                    values(0, steps & 1, v, accumulate);
-                    mma_commit(&empty[v]);
-                    ++steps;
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&full[ring]);
                 }
-                if (more) mma_commit(&empty[at]);
-                if (i + 2 == n) mma_commit(&q_empty);
+                if (++ring == SLOTS) {
+                    ring = 0;
+                    phase ^= 1;
+                }
+            };
+            for (;;) {
+                Item it;
+                it.h = -1;
+                const int64_t line = index / p.H;
+                // the request whose tiles hold `line`, its last (longest) tile first
+                while (b0 < p.B && !fail) {
+                    if (known != b0) {
+                        mine = b0 + lane < p.B && prompt_request(p, b0 + lane, nullptr, t) ? (t.n + NQ * TT - 1) / (NQ * TT) : 0;
+                        upto = mine;
+#pragma unroll
+                        for (int o = 1; o < 32; o <<= 1) {
+                            const int64_t y = __shfl_up_sync(0xFFFFFFFFu, upto, o);
+                            if (lane >= o) upto += y;
+                        }
+                        known = b0;
+                    }
+                    const int64_t at = base + upto, all = __shfl_sync(0xFFFFFFFFu, upto, 31);
+                    const uint32_t hit = __ballot_sync(0xFFFFFFFFu, at - mine <= line && line < at);
+                    if (hit) {
+                        const int from = __ffs(hit) - 1;
+                        it.t.b = b0 + from;
+                        it.t.lo = __shfl_sync(0xFFFFFFFFu, t.lo, from);
+                        it.t.n = __shfl_sync(0xFFFFFFFFu, t.n, from);
+                        it.t.k_lo = __shfl_sync(0xFFFFFFFFu, t.k_lo, from);
+                        it.t.m = __shfl_sync(0xFFFFFFFFu, t.m, from);
+                        it.first = static_cast<int>(__shfl_sync(0xFFFFFFFFu, at, from) - 1 - line) * (NQ * TT);
+                        it.h = static_cast<int>(index % p.H);
+                        break;
+                    }
+                    base += all;
+                    b0 += 32;
+                }
+                if (it.h >= 0) {
+                    const int own = it.t.m - it.t.n + it.first;            // last key of the first row
+                    const int near = p.window > 0 ? max(own - p.window + 1, 0) / KT : 0;
+                    it.f0 = near;
+                    it.np = min((p.prefix + KT - 1) / KT, near);
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        const int rows = min(it.t.n - it.first - q * TT, TT);
+                        const int last = rows > 0 && q < NQ ? own + q * TT + rows - 1 : -1;
+                        it.n[q] = last < 0 ? 0 : it.np + last / KT + 1 - near;
+                    }
+                }
+                wait_or_fail(&item_empty[ir], i_phase ^ 1, fail);
+                if (fail) it.h = -1;
+                if (lane == 0) {
+                    items[ir] = it;
+                    mbar_arrive(&item_full[ir]);
+                }
+                __syncwarp();
+                next_item();
+                if (it.h < 0) break;
+                // (asked for here, looked at after the item)
+                uint32_t taken = 0;
+                if (lane == 0) taken = atomicAdd(ticket, 1u);
+                const int n = max(it.n[0], it.n[1]);
+                if (n > 0) {
+                    // in the order of the products (a tile's queries as soon as its last scores are through)
+#pragma unroll
+                    for (int q = 0; q < NQ; ++q) {
+                        if (it.n[q] > 0) {
+                            wait_or_fail(&q_empty[q], q_phase[q], fail);
+                            q_phase[q] ^= 1;
+                            if (lane == 0) {
+                                mbar_arrive_expect_tx(&q_full[q], TT * group * D * 2);
+#pragma unroll
+                                for (int x = 0; x < D; x += 64)
+                                    tma_load_3d(qs + q * A::Q_TILE + x * 256, &maps.q, x, it.h * group, it.t.lo + it.first + q * TT, &q_full[q]);
+                            }
+                            __syncwarp();
+                        }
+                        if (q == 0) slot(false, it, item_step(it, 0));
+                    }
+                    for (int i = 0; i < n; ++i) {
+                        if (NQ == 2) slot(true, it, item_step(it, i));
+                        if (i + 1 < n) slot(false, it, item_step(it, i + 1));
+                        if (NQ == 1) slot(true, it, item_step(it, i));
+                    }
+                }
+                index = static_cast<int64_t>(gridDim.x) + __shfl_sync(0xFFFFFFFFu, taken, 0);
+            }
+            // the last CTA leaves the tickets as it found them
+            if (lane == 0) {
+                fence_acq_rel_gpu();
+                if (atomicAdd(ticket + 1, 1u) == gridDim.x - 1) {
+                    ticket[0] = 0u;
+                    ticket[1] = 0u;
+                }
+            }
+        } else if (warp == kIssuer) {
+            const uint32_t q_addr = smem_addr(qs), slot_addr = smem_addr(slots);
+            int ring = 0;
+            uint32_t phase = 0, q_phase[NQ] = {}, p_phase[A::NS] = {};
+            uint32_t steps = 0;                           // NQ = 1: steps so far, whose S alternates
+            const auto arrived = [&] {                    // the next slot of the ring: its place
+                wait_or_fail(&full[ring], phase, fail);
+                tmem_fence_after();
+                const int at = ring;
+                if (++ring == SLOTS) {
+                    ring = 0;
+                    phase ^= 1;
+                }
+                return at;
+            };
+            const auto scores = [&](int q, int s, int at, bool last) {
+                const uint32_t a = q_addr + q * A::Q_TILE, b = slot_addr + at * A::SLOT;
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k)
+                    mma_f16_shared(s_t + s * KT, smem_desc_swizzled(a + k / 4 * (128 * 128) + k % 4 * 32, 16),
+                                   smem_desc_swizzled(b + k / 4 * (KT * 128) + k % 4 * 32, 16), mma_f16_desc(KT, false, true), k > 0);
+                mma_commit(&s_full[s]);
+                if (last) mma_commit(&q_empty[q]);
+            };
+            const auto values = [&](int q, int s, int at, bool accumulate) {
+                const uint32_t b = slot_addr + at * A::SLOT;
+                wait_or_fail(&p_full[s], p_phase[s], fail);
+                p_phase[s] ^= 1;
+                tmem_fence_after();
+#pragma unroll
+                for (int k = 0; k < KT / 16; ++k)
+                    mma_f16(o_t + q * D, s_t + A::P_COL + s * A::P_STEP + k * 8, smem_desc_swizzled(b + k * 2048, KT * 128),
+                            mma_f16_desc(D, true, true), accumulate || k > 0);
+                mma_commit(&o_full[s]);
+            };
+            for (;;) {
+                wait_or_fail(&item_full[ir], i_phase, fail);
+                const int h = *reinterpret_cast<volatile int *>(&items[ir].h);
+                const int n0 = *reinterpret_cast<volatile int *>(&items[ir].n[0]), n1 = *reinterpret_cast<volatile int *>(&items[ir].n[1]);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&item_empty[ir]);
+                next_item();
+                if (__shfl_sync(0xFFFFFFFFu, h < 0 || fail, 0)) break;
+                const int n = max(n0, n1);
+                if (n == 0) continue;
+                const auto queries = [&](int q) {
+                    wait_or_fail(&q_full[q], q_phase[q], fail);
+                    q_phase[q] ^= 1;
+                    tmem_fence_after();
+                };
+                int at = arrived();
+                if constexpr (NQ == 2) {
+                    if (n0 > 0) {
+                        queries(0);
+                        scores(0, 0, at, n0 == 1);
+                    }
+                    if (n1 > 0) {
+                        queries(1);
+                        scores(1, 1, at, n1 == 1);
+                    }
+                } else {
+                    queries(0);
+                    scores(0, steps & 1, at, n == 1);
+                }
+                mma_commit(&empty[at]);
+                for (int i = 0; i < n; ++i) {
+                    const bool more = i + 1 < n, accumulate = i % A::RUN != 0;
+                    if constexpr (NQ == 2) {
+                        const int v = arrived();
+                        if (i < n0) values(0, 0, v, accumulate);
+                        if (more) at = arrived();
+                        if (i + 1 < n0) scores(0, 0, at, i + 2 == n0);
+                        if (i < n1) values(1, 1, v, accumulate);
+                        mma_commit(&empty[v]);
+                        if (i + 1 < n1) scores(1, 1, at, i + 2 == n1);
+                    } else {
+                        if (more) {
+                            at = arrived();
+                            scores(0, (steps + 1) & 1, at, i + 2 == n);
+                        }
+                        const int v = arrived();
+                        values(0, steps & 1, v, accumulate);
+                        mma_commit(&empty[v]);
+                        ++steps;
+                    }
+                    if (more) mma_commit(&empty[at]);
+                }
             }
         }
     } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(A::MORE_REGS));
         const int q = SHARE == 2 ? 0 : warp >> 2, row = tid & 127;             // tile, row of it
         const int part = SHARE == 2 ? warp >> 2 : 0;                           // which of the row's threads
         const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;
@@ -551,31 +573,38 @@ prompt_tiles_kernel(const PromptParams p, const __grid_constant__ PromptMaps map
             const int64_t place = real && !fail ? at * D + part * DH : -1;
 #pragma unroll 1
             for (int d = 0; d < DH; d += 64) {
-#pragma unroll
+#pragma unroll 1
                 for (int d2 = 0; d2 < 64; d2 += 32) {
                     uint32_t r[32] = {};
                     if (n > 0) {
                         tmem_ld32(o_mine + d + d2, r);
                         tmem_wait_ld();
                     }
-                    float v[32];
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(r[e]);
                     if (n > A::RUN)
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) v[e] += sums[(d + d2 + e) * 128] * f;
+                        for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) + sums[(d + d2 + e) * 128] * f);
 #pragma unroll
-                    for (int e = 0; e < 32; e += 8)
-                        *reinterpret_cast<uint4 *>(stage + lane * 128 + (((d2 + e) / 8) ^ (lane & 7)) * 16) =
-                            make_uint4(pack_bf16(v[e] * inv, v[e + 1] * inv), pack_bf16(v[e + 2] * inv, v[e + 3] * inv),
-                                       pack_bf16(v[e + 4] * inv, v[e + 5] * inv), pack_bf16(v[e + 6] * inv, v[e + 7] * inv));
+                    for (int e = 0; e < 32; e += 8) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) w[k] = pack_bf16(__uint_as_float(r[e + 2 * k]) * inv, __uint_as_float(r[e + 2 * k + 1]) * inv);
+                        *reinterpret_cast<uint4 *>(stage + lane * 128 + (((d2 + e) / 8) ^ (lane & 7)) * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
                 }
                 __syncwarp();
 #pragma unroll
-                for (int r = lane / 8; r < 32; r += 4) {
-                    const int64_t to = __shfl_sync(0xFFFFFFFFu, place, r);
-                    const uint4 x = *reinterpret_cast<const uint4 *>(stage + r * 128 + ((lane & 7) ^ (r & 7)) * 16);
-                    if (to >= 0) *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.out) + to + d + (lane & 7) * 8) = x;
+                for (int k0 = 0; k0 < 8; k0 += 4) {
+                    uint4 x[4];
+                    int64_t to[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int from = (k0 + k) * 4 + lane / 8;
+                        to[k] = __shfl_sync(0xFFFFFFFFu, place, from);
+                        x[k] = *reinterpret_cast<const uint4 *>(stage + from * 128 + ((lane & 7) ^ (from & 7)) * 16);
+                    }
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        if (to[k] >= 0) *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.out) + to[k] + d + (lane & 7) * 8) = x[k];
                 }
                 __syncwarp();
             }
@@ -590,7 +619,10 @@ prompt_tiles_kernel(const PromptParams p, const __grid_constant__ PromptMaps map
         // a wait gave up: let the copies in flight land (bounded), then leave
         for (int i = 0; i < SLOTS; ++i)
             for (int ph = 0; ph < 2; ++ph) mbar_wait(&full[i], ph);
-        for (int ph = 0; ph < 2; ++ph) mbar_wait(&q_full, ph), mbar_wait(&tail, ph);
+        for (int ph = 0; ph < 2; ++ph) {
+            for (int i = 0; i < NQ; ++i) mbar_wait(&q_full[i], ph);
+            mbar_wait(&tail, ph);
+        }
         set_status(p.status, SPEC_STATUS_TIMEOUT);
     }
     __syncthreads();
