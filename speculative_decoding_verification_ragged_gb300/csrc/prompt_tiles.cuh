@@ -639,6 +639,11 @@ template <int D, bool OPT> cudaError_t launch_tiles_of(const PromptParams &p, co
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     if (!done[dev]) {
+        // (registers that move between warpgroups have to add up to what the launch has)
+        cudaFuncAttributes a;
+        e = cudaFuncGetAttributes(&a, prompt_tiles_kernel<D, OPT>);
+        if (e != cudaSuccess) return e;
+        if (a.numRegs != A::LAUNCH_REGS) return cudaErrorInvalidConfiguration;
         e = cudaFuncSetAttribute(prompt_tiles_kernel<D, OPT>, cudaFuncAttributeMaxDynamicSharedMemorySize, A::SMEM);
         if (e != cudaSuccess) return e;
         done[dev] = true;
