@@ -17,6 +17,8 @@
 extern "C" {
 #endif
 
+#define SPEC_PROMPT_MOST_KEYS (1 << 24)      /* keys of a call, of all requests */
+
 /* Packed prompts: request b's rows are cu_rows[b] .. cu_rows[b+1]-1 of q and out, its
  * keys cu_keys[b] .. cu_keys[b+1]-1 of k and v.  Its rows are the last of its keys: with
  * n rows and m >= n keys (a piece of a prompt over what came before) row i is key m - n + i. */
@@ -31,7 +33,8 @@ typedef struct {
     int64_t k_row, k_head;
     int64_t v_row, v_head;
     int32_t B;                 /* requests, >= 1                                              */
-    int32_t R_cap, K_cap;      /* host-known bounds on cu_rows[B], cu_keys[B], >= 1           */
+    int32_t R_cap, K_cap;      /* host-known bounds on cu_rows[B], cu_keys[B], >= 1; K_cap at
+                                  most SPEC_PROMPT_MOST_KEYS                                   */
     const int32_t *cu_rows;    /* [B+1]                                                       */
     const int32_t *cu_keys;    /* [B+1] or NULL: cu_rows                                      */
     float scale;               /* of q . k, finite                                            */
@@ -58,8 +61,11 @@ SPEC_API size_t spec_prompt_workspace_bytes(int32_t Hq, int32_t H, int32_t D, in
  * sees may hold anything; those that one of its rows sees have to be finite, as have
  * the queries (a row of another request never notices).  The scores have to stay within
  * fp32.  Results do not depend on the order in which blocks run.
+ * out and lse must not overlap the inputs.
  * bf16: products of bf16 in fp32, weights rounded to bf16 (8 bits) before they meet the values,
- * their sums, and so lse, in fp32.  f32: fp32 throughout.
+ * their sums, and so lse, in fp32.  They run on the tensor cores where q, k and v start on 16 bytes, their
+ * strides are positive multiples of 16 bytes, out starts on 16 bytes and Hq / H is at most 128; on the CUDA
+ * cores, many times slower, elsewhere, then with weights in fp32.  f32: fp32 throughout.
  */
 SPEC_API int spec_prompt_attend(const spec_prompt *prompt, void *out, float *lse, void *workspace,
                                 size_t workspace_bytes, spec_stream stream);

@@ -12,7 +12,8 @@
  * (spec_cache_attend_tree), adjusts the logits, takes a token for every row (row_token of
  * spec_verify_greedy or spec_verify_sample, whose own chain of drafts is not looked at) and
  * follows those tokens through the tree (spec_tree_accept).  Appending the keys and values of
- * path_rows again, from the root's slot on, leaves the accepted path in the cache.
+ * path_rows again, from the root's slot on, leaves the accepted path in the cache, where it is a
+ * chain (of spec_cache_weights too: the queries and lse of path_rows, with lse = -inf behind the path).
  *
  * Conventions are those of spec_verify.h.
  */
@@ -80,7 +81,7 @@ typedef struct {
     const int32_t *parent;     /* [R_cap] or NULL: a chain                                    */
     const int32_t *bias_cu;    /* [B+1] or NULL: request b's biases are bias_cu[b] ..         */
     const int32_t *bias_ids;   /* [n_bias] columns, in any order, repeated ones added up      */
-    const float *bias_values;  /* [n_bias]                                                    */
+    const float *bias_values;  /* [n_bias] finite, or -inf                                    */
     int32_t n_bias;
     const uint32_t *allowed;   /* [n_allowed, allowed_ld] or NULL: bit v % 32 of word v / 32
                                   says whether column v is allowed                            */

@@ -240,7 +240,9 @@ int check_prompt(const spec_prompt *a, PromptParams &p)
     if (!on_words(a->cu_rows, a->cu_keys, a->slopes, a->status)) return SPEC_ERR_INVALID_ARG;
     if (a->D != 64 && a->D != 128 && a->D != 256) return SPEC_ERR_UNSUPPORTED;
     // rows and keys are 32-bit, and so are packed rows and tiles; kv heads are the y of the grid
-    if (a->H > kMostHeads || a->B > kMostRequests || a->R_cap > kMostSlots || a->K_cap > kMostSlots) return SPEC_ERR_UNSUPPORTED;
+    if (a->H > kMostHeads || a->B > kMostRequests || a->R_cap > kMostSlots) return SPEC_ERR_UNSUPPORTED;
+    // (a row walks over its keys by itself, and the kernels' waits give up after about a second)
+    if (a->K_cap > SPEC_PROMPT_MOST_KEYS) return SPEC_ERR_UNSUPPORTED;
     if (static_cast<int64_t>(a->R_cap) * (a->Hq / a->H) > INT32_MAX - 65536) return SPEC_ERR_UNSUPPORTED;
     std::memset(&p, 0, sizeof p);
     p.q = a->q;

@@ -5,7 +5,7 @@
 //     S = Q K^T c,  P = 2^(S - m),  O += P V,  m the rows' running maximum.
 // 16 x 16 threads hold 4 x 4 scores and 4 x D/16 results each in registers; Q, K, V and P lie
 // in shared memory as fp32, rows 4 words apart in their banks, so that the 8 lanes of a 16-byte
-// load meet 32 different ones.
+// load meet 32 different ones.  fp32 keys and values come by asynchronous copies, a tile ahead.
 #include "attend.cuh"
 #include "prompt.cuh"
 
@@ -16,30 +16,50 @@ namespace {
 constexpr int kRows = 64, kKeys = 64, kRowThreads = 256;
 
 template <int D> constexpr int row_words = D + 4;
-template <int D> constexpr int rows_smem = (3 * kRows * row_words<D> + kRows * (kKeys + 4)) * 4;
+// keys and values lie twice where there is room: the next ones are fetched beside the arithmetic
+template <int D> constexpr int row_buffers = D == 256 ? 1 : 2;
+template <int D> constexpr int rows_smem = ((1 + 2 * row_buffers<D>) * kRows * row_words<D> + kRows * (kKeys + 4)) * 4;
 
 // `rows` rows of D channels into shared memory; row(i): where row i starts, null for zeros
-template <typename T, int D, typename F> __device__ __forceinline__ void stage_rows(float *to, bool aligned, float factor, F row)
+template <typename T, int D, typename F> __device__ __forceinline__ void stage_rows(float *to, bool aligned, F row)
 {
     for (int i = threadIdx.x; i < kRows * (D / 8); i += kRowThreads) {
         const int r = i / (D / 8), d = i % (D / 8) * 8;
         const T *src = row(r);
         float x[8] = {};
         if (src) load8<T>(src + d, aligned, x);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) x[k] *= factor;
         float4 *dst = reinterpret_cast<float4 *>(to + r * row_words<D> + d);
         dst[0] = make_float4(x[0], x[1], x[2], x[3]);
         dst[1] = make_float4(x[4], x[5], x[6], x[7]);
     }
 }
 
+// 16 bytes from global to shared memory, asynchronously; zeros where `have` is false
+__device__ __forceinline__ void fetch16(float *to, const void *from, bool have)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(to)), "l"(from), "r"(have ? 16 : 0) : "memory");
+}
+
+// the same as stage_rows for fp32 rows on 16 bytes, under way until rows_arrived
+template <int D, typename F> __device__ __forceinline__ void fetch_rows(float *to, const void *any, F row)
+{
+    for (int i = threadIdx.x; i < kRows * (D / 4); i += kRowThreads) {
+        const int r = i / (D / 4), d = i % (D / 4) * 4;
+        const float *const src = row(r);
+        fetch16(to + r * row_words<D> + d, src ? src + d : any, src != nullptr);
+    }
+}
+
+__device__ __forceinline__ void rows_asked() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void rows_arrived() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
 template <typename T, int D>
 __global__ void __launch_bounds__(kRowThreads) prompt_rows_kernel(const PromptParams p)
 {
     constexpr int W = row_words<D>, PW = kKeys + 4, OC = D / 16;
     extern __shared__ __align__(16) float sm[];
-    float *const qs = sm, *const ks = qs + kRows * W, *const vs = ks + kKeys * W, *const ps = vs + kKeys * W;
+    constexpr int BUF = row_buffers<D>;
+    float *const qs = sm, *const kv = qs + kRows * W, *const ps = kv + 2 * BUF * kKeys * W;
     const int group = p.Hq / p.H, h = blockIdx.y;
     PromptTile t;
     int tile;
@@ -52,7 +72,7 @@ __global__ void __launch_bounds__(kRowThreads) prompt_rows_kernel(const PromptPa
     // 64 packed rows: (row, head) of each
     const auto row_of = [&](int r) { return (first + r) / group; };
     const auto head_of = [&](int r) { return h * group + (first + r) % group; };
-    stage_rows<T, D>(qs, p.q_aligned, 1.f, [&](int r) {
+    stage_rows<T, D>(qs, p.q_aligned, [&](int r) {
         return r < count ? static_cast<const T *>(p.q) + static_cast<int64_t>(t.lo + row_of(r)) * p.q_row + head_of(r) * p.q_head : nullptr;
     });
     int own[4];                                       // last key that each of this thread's rows sees
@@ -74,19 +94,42 @@ __global__ void __launch_bounds__(kRowThreads) prompt_rows_kernel(const PromptPa
     const int near = p.window > 0 ? max(own0 + row_of(0) - p.window + 1, 0) : 0;
     const int live = p.window > 0 ? max(own0 - p.window + 1, 0) : 0;      // of the request's first row
     const float c = p.scale * kLog2e, cap = p.cap * kLog2e, rcap = p.cap > 0.f ? cap_reciprocal(cap) : 0.f;
-    for (int k0 = 0; k0 < end; k0 += kKeys) {
-        if (k0 >= p.prefix && k0 + kKeys <= near) continue;
-        __syncthreads();
-        const auto key = [&](const void *x, int64_t row, int64_t head) {
-            return [=, &p](int r) {
-                const int j = k0 + r;
-                return j < t.m && (j >= live || j < p.prefix)
-                           ? static_cast<const T *>(x) + (t.k_lo + static_cast<int64_t>(j)) * row + h * head : nullptr;
-            };
+    const auto next = [&](int k0) {                   // the tile of keys after this one that some row sees
+        do k0 += kKeys;
+        while (k0 < end && k0 >= p.prefix && k0 + kKeys <= near);
+        return k0;
+    };
+    const bool ahead = BUF == 2 && sizeof(T) == 4 && p.k_aligned && p.v_aligned;
+    const auto key = [&](const void *x, int64_t row, int64_t head, int k0) {
+        return [=, &p](int r) {
+            const int j = k0 + r;
+            return j < t.m && (j >= live || j < p.prefix)
+                       ? static_cast<const T *>(x) + (t.k_lo + static_cast<int64_t>(j)) * row + h * head : nullptr;
         };
-        stage_rows<T, D>(ks, p.k_aligned, 1.f, key(p.k, p.k_row, p.k_head));
-        stage_rows<T, D>(vs, p.v_aligned, 1.f, key(p.v, p.v_row, p.v_head));
-        __syncthreads();
+    };
+    const auto fetch = [&](int k0, int buf) {
+        if constexpr (sizeof(T) == 4) {
+            fetch_rows<D>(kv + 2 * buf * kKeys * W, p.k, key(p.k, p.k_row, p.k_head, k0));
+            fetch_rows<D>(kv + (2 * buf + 1) * kKeys * W, p.v, key(p.v, p.v_row, p.v_head, k0));
+            rows_asked();
+        }
+    };
+    int k0 = next(-kKeys), buf = 0;
+    if (ahead && k0 < end) fetch(k0, 0);
+    for (; k0 < end; k0 = next(k0)) {
+        const float *const ks = kv + 2 * buf * kKeys * W, *const vs = ks + kKeys * W;
+        if (ahead) {
+            rows_arrived();
+            __syncthreads();                          // (and the other buffer is read)
+            const int k1 = next(k0);
+            buf ^= 1;
+            if (k1 < end) fetch(k1, buf);
+        } else {
+            __syncthreads();
+            stage_rows<T, D>(kv, p.k_aligned, key(p.k, p.k_row, p.k_head, k0));
+            stage_rows<T, D>(kv + kKeys * W, p.v_aligned, key(p.v, p.v_row, p.v_head, k0));
+            __syncthreads();
+        }
         uint64_t s2[4][4] = {};
 #pragma unroll 4
         for (int d = 0; d < D; d += 4) {

@@ -42,7 +42,7 @@ def _rules(**over):
     (dict(prefix=-1), 1), (dict(scale=float("nan")), 1), (dict(scale=float("inf")), 1), (dict(cap=-1.0), 1),
     (dict(cap=float("nan")), 1), (dict(cap=float("inf")), 1), (dict(q=C.c_void_p(0x10001)), 1), (dict(dtype=0, k=ODD), 1),
     (dict(cu_rows=ODD), 1), (dict(cu_keys=ODD), 1), (dict(slopes=ODD), 1), (dict(status=ODD), 1), (dict(B=70000), 2),
-    (dict(H=70000, Hq=70000), 2), (dict(R_cap=(1 << 30) + 1), 2), (dict(K_cap=(1 << 30) + 1), 2), (dict(R_cap=1 << 30), 2)])
+    (dict(H=70000, Hq=70000), 2), (dict(R_cap=(1 << 30) + 1), 2), (dict(K_cap=(1 << 24) + 1), 2), (dict(R_cap=1 << 30), 2)])
 def test_prompt_is_checked(sv, over, rc):
     L, a = sv.load_library(), _prompt(**over)
     assert L.spec_prompt_attend(C.byref(a), FAKE, FAKE, FAKE, 1 << 40, None) == rc
