@@ -51,16 +51,25 @@ __global__ void __launch_bounds__(kAcceptWarps * 32) tree_accept_kernel(const Tr
 
 // ---- logits ----
 
-// A CTA takes kSlice columns of a request's rows.  They stream by first, copied and masked; the
+// A CTA takes kSlice columns of a request's rows (or of every few of them).  They stream by first, copied and masked; the
 // tokens so far are counted once for all rows, in shared memory, and the columns that have a count, a draft of
 // the paths or a bias ("touched") are written over, a thread each.  In place the touched columns come first, and only
 // rows with a mask stream by (a masked column is -inf whatever it was).
 //
 constexpr int kSlice = 8192;
+// Bound by HBM while the rows stream by (128 x 5 rows of 152064 bf16: 64 us without rules, 6.1 TB/s, 0.90 of the measured copy
+// rate), and by what a CTA does beside that (history, list, touched columns), a chain of loads that five CTAs an SM do not hide:
+// 96 us with histories of 4096 tokens and every second row masked (0.61).  A slice of 8192 columns: every slice reads the
+// history again, so that half of it took 120 us, and fewer CTAs have less in flight, so that twice took 105 and four times 117
+// (60000 tokens, one row of 64 requests: 93, 172, 83, 81).  Tried as well: four of the CTA's warps counting while the others
+// stream (105), a cluster that shares the history by distributed atomics (128, frequent tokens meet there), vectors of a row
+// ahead of the stores (120: registers for fewer CTAs), six CTAs an SM (119: fewer loads in flight in each).
+//
 // A column's word: how often it was generated, whether it was seen at all, whether one of the request's biases or nodes
 // names it; a bit a column says whether the word is anything but 0.
 constexpr uint32_t kSeen = 1u << 31, kNamed = 1u << 30, kCount = kNamed - 1u;
 constexpr int kNear = 256;                            // biases of a slice kept in shared memory
+constexpr int kFull = 152 * 5;                        // CTAs that are resident at once
 constexpr int kListed = 1024;                         // touched columns that are listed at a time
 
 template <typename T> struct LogitElt;
@@ -156,7 +165,7 @@ __global__ void __launch_bounds__(kSlice / 32) adjust_logits_kernel(const LogitP
     Slice<kSlice> &s = *reinterpret_cast<Slice<kSlice> *>(raw);
     const int tid = threadIdx.x, lane = tid & 31, warp = warp_index(), b = blockIdx.y;
     const int c0 = blockIdx.x * kSlice, cols = min(p.V - c0, kSlice);
-    uint32_t *const report = blockIdx.x == 0 ? p.status : nullptr;      // (one CTA of a request speaks for it)
+    uint32_t *const report = blockIdx.x == 0 && blockIdx.z == 0 ? p.status : nullptr;      // (one CTA of a request speaks for it)
     // What the request has is asked for at once, and what that leads to before the rows stream by: a CTA lives as long as
     // its chain of loads.
     Penalty pen = {p.repetition ? p.repetition[b] : 1.f, p.frequency ? p.frequency[b] : 0.f, p.presence ? p.presence[b] : 0.f};
@@ -164,7 +173,7 @@ __global__ void __launch_bounds__(kSlice / 32) adjust_logits_kernel(const LogitP
     const int prompt = p.history && p.n_prompt ? p.n_prompt[b] : 0;
     int bias0 = p.bias_cu ? p.bias_cu[b] : 0, bias1 = p.bias_cu ? p.bias_cu[b + 1] : 0;
     int lo, n;
-    if (!request_rows(p.cu_rows, b, p.R_cap, p.k_max + 1, tid == 0 ? report : nullptr, lo, n) || n == 0) return;
+    if (!request_rows(p.cu_rows, b, p.R_cap, p.k_max + 1, tid == 0 ? report : nullptr, lo, n) || n <= static_cast<int>(blockIdx.z)) return;
     const auto finite = [](float x) { return x - x == 0.f; };
     bool bad = false;
     if (!finite(pen.repetition) || pen.repetition <= 0.f) pen.repetition = 1.f, bad = true;
@@ -249,8 +258,9 @@ __global__ void __launch_bounds__(kSlice / 32) adjust_logits_kernel(const LogitP
     }
     for (int i = tid; i < kSlice / 4; i += kLogitThreads) reinterpret_cast<uint4 *>(s.word)[i] = make_uint4(0, 0, 0, 0);
     s.touched[tid] = 0;
+    const int z0 = blockIdx.z, dz = gridDim.z;        // this CTA's rows: z0, z0 + dz, ...
     if (!in_place)
-        for (int j = 0; j < n; ++j) stream(lo + j);
+        for (int j = z0; j < n; j += dz) stream(lo + j);
     __syncthreads();
     // the history
     const auto count = [&](int i, int t) {
@@ -360,8 +370,8 @@ __global__ void __launch_bounds__(kSlice / 32) adjust_logits_kernel(const LogitP
         for (uint32_t left = set; left; left &= left - 1, ++at)
             if (at >= 0 && at < kListed) s.column[at] = static_cast<uint16_t>(tid * 32 + __ffs(left) - 1);
         __syncthreads();
-        for (int e = tid; e < n * count; e += kLogitThreads) {
-            const int j = e / count, v = s.column[e - j * count], row = lo + j;
+        for (int e = tid; e < (n - z0 + dz - 1) / dz * count; e += kLogitThreads) {
+            const int i = e / count, v = s.column[e - i * count], j = z0 + i * dz, row = lo + j;
             const float z = to_f32<T>(source(row)[v]);
             const bool gone = hidden(mask_at(s.mask[j]), v);
             target(row)[v] = from_f32<T>(gone ? -INFINITY : adjust(p, s, pen, c0, v, n, s.path[j], bias0, bias1, z));
@@ -369,7 +379,7 @@ __global__ void __launch_bounds__(kSlice / 32) adjust_logits_kernel(const LogitP
     }
     if (in_place) {
         __syncthreads();
-        for (int j = 0; j < n; ++j) stream(lo + j);
+        for (int j = z0; j < n; j += dz) stream(lo + j);
     }
 }
 
@@ -395,7 +405,10 @@ template <typename T, int SLICE> cudaError_t launch_logits(const LogitParams &p,
         if (e != cudaSuccess) return e;
         done[dev] = true;
     }
-    const dim3 grid((p.V + SLICE - 1) / SLICE, p.B);
+    // A request's rows are dealt out to several CTAs, each with counts of its own, until the SMs are full (32 requests of up to
+    // 20 rows of 50257: 49 -> 27 us, one of 32 rows of 152064: 45 -> 10); a batch that fills them counts once a slice.
+    const int slices = (p.V + SLICE - 1) / SLICE, most = (kFull + slices * static_cast<int64_t>(p.B) - 1) / (slices * static_cast<int64_t>(p.B));
+    const dim3 grid(slices, p.B, most < p.k_max + 1 ? most : p.k_max + 1);
     adjust_logits_kernel<T, SLICE><<<grid, SLICE / 32, sizeof(Slice<SLICE>), s>>>(p);
     return cudaGetLastError();
 }
