@@ -1006,27 +1006,39 @@ attend_kernel(const CacheView c, const AttnParams p, const Layout lay)
                     if (p.lse) p.lse[out_row(tid)] = L > 0.f ? (M - kHeadroom + log2f(L)) * kLn2 : -INFINITY;
                 }
                 csync();
-                // a thread per four channels of a column
-                for (int e = tid; e < w.ncols * (D / 4); e += kAttnThreads) {
-                    const int col = e / (D / 4), d = e % (D / 4) * 4;
-                    const float M = cs.factor[col];
-                    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
+                // a thread per four channels of a column; for the many columns of a tree several at once, whose loads are
+                // in flight together
+                constexpr int U = TREE ? 4 : 1;
+                const int all = w.ncols * (D / 4);
+                for (int e0 = tid; e0 < all; e0 += U * kAttnThreads) {
+                    float4 o[U];
+#pragma unroll
+                    for (int u = 0; u < U; ++u) o[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll(TREE ? 2 : 4)
                     for (int s = 0; s < parts; ++s) {
-                        const float2 x = __ldcg(ml_all + slot_of(s) * NT + col);
-                        const float4 v = __ldcg(reinterpret_cast<const float4 *>(part_all + (slot_of(s) * NT + col) * D + d));
-                        const float f = x.y > 0.f ? ex2(x.x - M) : 0.f;
-                        o.x += f * v.x;
-                        o.y += f * v.y;
-                        o.z += f * v.z;
-                        o.w += f * v.w;
+#pragma unroll
+                        for (int u = 0; u < U; ++u) {
+                            const int e = U == 1 ? e0 : min(e0 + u * kAttnThreads, all - 1), col = e / (D / 4), d = e % (D / 4) * 4;
+                            const float2 x = __ldcg(ml_all + slot_of(s) * NT + col);
+                            const float4 v = __ldcg(reinterpret_cast<const float4 *>(part_all + (slot_of(s) * NT + col) * D + d));
+                            const float f = x.y > 0.f ? ex2(x.x - cs.factor[col]) : 0.f;
+                            o[u].x += f * v.x;
+                            o[u].y += f * v.y;
+                            o[u].z += f * v.z;
+                            o[u].w += f * v.w;
+                        }
                     }
-                    T *to = static_cast<T *>(p.out) + out_row(col) * D + d;
-                    const float g = cs.sum[col];
-                    to[0] = from_f32<T>(o.x * g);
-                    to[1] = from_f32<T>(o.y * g);
-                    to[2] = from_f32<T>(o.z * g);
-                    to[3] = from_f32<T>(o.w * g);
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        const int e = e0 + u * kAttnThreads, col = e / (D / 4), d = e % (D / 4) * 4;
+                        if (U > 1 && e >= all) break;
+                        T *to = static_cast<T *>(p.out) + out_row(col) * D + d;
+                        const float g = cs.sum[col];
+                        to[0] = from_f32<T>(o[u].x * g);
+                        to[1] = from_f32<T>(o[u].y * g);
+                        to[2] = from_f32<T>(o[u].z * g);
+                        to[3] = from_f32<T>(o[u].w * g);
+                    }
                 }
             }
         }
@@ -1102,11 +1114,17 @@ template <typename F> auto with_kernel(int dtype, int D, int cols, F f)
     return nt == 16 ? f(Attn<B, 256, 16>()) : f(Attn<B, 256, 32>());
 }
 
+// The rows of a chain are one column tile, of up to 64.  A tree's are several anyway, and go 32 at a time: 64 columns of bf16 heads
+// spill registers in the loop over the tiles and leave more of a last tile empty (64 trees of up to 26 nodes over 4096 tokens,
+// 40 / 8 heads: 213 us by 64 columns, 172 by 32, 233 by 16; of up to 8 nodes: 147, 85, 98; one of 13 nodes over 900
+// tokens: 27, 21, 19).  The workspace for chains is enough: twice the tiles of half the columns.
 template <bool OPT, bool TREE> cudaError_t launch_attend(const CacheView &c, const AttnParams &p, int dtype, cudaStream_t s)
 {
-    return with_kernel(dtype, c.D, (p.k_max + 1) * (p.Hq / c.H), [&](auto a) {
+    const int cols = (p.k_max + 1) * (p.Hq / c.H);
+    return with_kernel(dtype, c.D, TREE && cols > 32 ? 32 : cols, [&](auto a) {
         using A = decltype(a);
-        return launch_one<typename A::Type, A::D, A::NT, OPT, TREE>(c, p, s);
+        if constexpr (TREE && A::NT > 32) return cudaErrorInvalidValue;
+        else return launch_one<typename A::Type, A::D, A::NT, OPT, TREE>(c, p, s);
     });
 }
 

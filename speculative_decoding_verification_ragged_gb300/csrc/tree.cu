@@ -56,7 +56,6 @@ __global__ void __launch_bounds__(kAcceptWarps * 32) tree_accept_kernel(const Tr
 // the paths or a bias ("touched") are written over, a thread each.  In place the touched columns come first, and only
 // rows with a mask stream by (a masked column is -inf whatever it was).
 //
-constexpr int kSlice = 8192;
 // Bound by HBM while the rows stream by (128 x 5 rows of 152064 bf16: 64 us without rules, 6.1 TB/s, 0.90 of the measured copy
 // rate), and by what a CTA does beside that (history, list, touched columns), a chain of loads that five CTAs an SM do not hide:
 // 96 us with histories of 4096 tokens and every second row masked (0.61).  A slice of 8192 columns: every slice reads the
@@ -67,6 +66,7 @@ constexpr int kSlice = 8192;
 //
 // A column's word: how often it was generated, whether it was seen at all, whether one of the request's biases or nodes
 // names it; a bit a column says whether the word is anything but 0.
+constexpr int kSlice = 8192, kLogitThreads = 256;
 constexpr uint32_t kSeen = 1u << 31, kNamed = 1u << 30, kCount = kNamed - 1u;
 constexpr int kNear = 256;                            // biases of a slice kept in shared memory
 constexpr int kFull = 152 * 5;                        // CTAs that are resident at once
@@ -111,8 +111,7 @@ template <> struct LogitElt<float> {
     }
 };
 
-template <int kSlice> struct Slice {
-    static constexpr int kLogitThreads = kSlice / 32;
+struct Slice {
     uint32_t word[kSlice];
     uint32_t touched[kSlice / 32];
     int node_token[32];
@@ -130,8 +129,7 @@ struct Penalty {
 };
 
 // one touched column (v: from the slice's first on) of a row with `path`
-template <int SLICE>
-__device__ __forceinline__ float adjust(const LogitParams &p, const Slice<SLICE> &s, const Penalty &pen, int c0, int v, int n, uint32_t path,
+__device__ __forceinline__ float adjust(const LogitParams &p, const Slice &s, const Penalty &pen, int c0, int v, int n, uint32_t path,
                                         int bias0, int bias1, float z)
 {
     const uint32_t w = s.word[v];
@@ -155,14 +153,13 @@ __device__ __forceinline__ float adjust(const LogitParams &p, const Slice<SLICE>
     return z;
 }
 
-template <typename T, int kSlice>
-__global__ void __launch_bounds__(kSlice / 32) adjust_logits_kernel(const LogitParams p)
+template <typename T>
+__global__ void __launch_bounds__(kLogitThreads) adjust_logits_kernel(const LogitParams p)
 {
     using E = LogitElt<T>;
     constexpr int VEC = E::VEC;
-    constexpr int kLogitThreads = Slice<kSlice>::kLogitThreads;
     extern __shared__ __align__(16) uint8_t raw[];
-    Slice<kSlice> &s = *reinterpret_cast<Slice<kSlice> *>(raw);
+    Slice &s = *reinterpret_cast<Slice *>(raw);
     const int tid = threadIdx.x, lane = tid & 31, warp = warp_index(), b = blockIdx.y;
     const int c0 = blockIdx.x * kSlice, cols = min(p.V - c0, kSlice);
     uint32_t *const report = blockIdx.x == 0 && blockIdx.z == 0 ? p.status : nullptr;      // (one CTA of a request speaks for it)
@@ -348,6 +345,7 @@ __global__ void __launch_bounds__(kSlice / 32) adjust_logits_kernel(const LogitP
     __syncthreads();
 
     // the touched columns in their order, kListed at a time; a thread has 32 columns of the set
+    static_assert(kSlice == 32 * kLogitThreads && sizeof(Slice) <= 48 * 1024, "a word of the bit set a thread");
     const uint32_t set = s.touched[tid];
     int first = __popc(set), touched = 0;
 #pragma unroll
@@ -391,34 +389,15 @@ cudaError_t launch_tree_accept(const TreeParams &p, cudaStream_t s)
     return cudaGetLastError();
 }
 
-namespace {
-
-template <typename T, int SLICE> cudaError_t launch_logits(const LogitParams &p, cudaStream_t s)
-{
-    static bool done[64] = {false};
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    if (!done[dev]) {
-        e = cudaFuncSetAttribute(adjust_logits_kernel<T, SLICE>, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(Slice<SLICE>));
-        if (e != cudaSuccess) return e;
-        done[dev] = true;
-    }
-    // A request's rows are dealt out to several CTAs, each with counts of its own, until the SMs are full (32 requests of up to
-    // 20 rows of 50257: 49 -> 27 us, one of 32 rows of 152064: 45 -> 10); a batch that fills them counts once a slice.
-    const int slices = (p.V + SLICE - 1) / SLICE, most = (kFull + slices * static_cast<int64_t>(p.B) - 1) / (slices * static_cast<int64_t>(p.B));
-    const dim3 grid(slices, p.B, most < p.k_max + 1 ? most : p.k_max + 1);
-    adjust_logits_kernel<T, SLICE><<<grid, SLICE / 32, sizeof(Slice<SLICE>), s>>>(p);
-    return cudaGetLastError();
-}
-
-}  // namespace
-
 cudaError_t launch_adjust_logits(const LogitParams &p, int dtype, cudaStream_t s)
 {
-    if (dtype == SPEC_F32) return launch_logits<float, kSlice>(p, s);
-    return launch_logits<__nv_bfloat16, kSlice>(p, s);
+    // A request's rows are dealt out to several CTAs, each with counts of its own, until the SMs are full (32 requests of up to
+    // 20 rows of 50257: 49 -> 27 us, one of 32 rows of 152064: 45 -> 10); a batch that fills them counts once a slice.
+    const int64_t slices = (p.V + kSlice - 1) / kSlice, deals = (kFull + slices * p.B - 1) / (slices * p.B);
+    const dim3 grid(static_cast<unsigned>(slices), p.B, static_cast<unsigned>(deals < p.k_max + 1 ? deals : p.k_max + 1));
+    if (dtype == SPEC_F32) adjust_logits_kernel<float><<<grid, kLogitThreads, sizeof(Slice), s>>>(p);
+    else adjust_logits_kernel<__nv_bfloat16><<<grid, kLogitThreads, sizeof(Slice), s>>>(p);
+    return cudaGetLastError();
 }
 
 }  // namespace specv
