@@ -1,6 +1,7 @@
 """Speculative decoding with trees of drafts over a 4-bit paged cache: the loop of a
 serving engine around this library, with one attention layer of random weights in
-the place of the target model and its head without the attention as the draft.
+the place of the target model and its head without the attention as the draft (which
+random weights rarely let hit).
 
     python examples/tree_step.py [--steps 12]
 

@@ -171,6 +171,8 @@ __global__ void __launch_bounds__(kLogitThreads) adjust_logits_kernel(const Logi
     int bias0 = p.bias_cu ? p.bias_cu[b] : 0, bias1 = p.bias_cu ? p.bias_cu[b + 1] : 0;
     int lo, n;
     if (!request_rows(p.cu_rows, b, p.R_cap, p.k_max + 1, tid == 0 ? report : nullptr, lo, n) || n <= static_cast<int>(blockIdx.z)) return;
+    // a token's column of the slice; others, ids below 0 among them, come out beyond it
+    const auto column = [&](int t) { return static_cast<uint32_t>(t) - static_cast<uint32_t>(c0); };
     const auto finite = [](float x) { return x - x == 0.f; };
     bool bad = false;
     if (!finite(pen.repetition) || pen.repetition <= 0.f) pen.repetition = 1.f, bad = true;
@@ -261,7 +263,7 @@ __global__ void __launch_bounds__(kLogitThreads) adjust_logits_kernel(const Logi
     __syncthreads();
     // the history
     const auto count = [&](int i, int t) {
-        const uint32_t v = static_cast<uint32_t>(t - c0);     // (ids below 0 are large as well: c0 + cols < 2^30)
+        const uint32_t v = column(t);
         if (v >= static_cast<uint32_t>(cols)) return;
         // (most have been there before: a look instead of an atomic)
         const uint32_t word = *const_cast<volatile uint32_t *>(&s.word[v]);
@@ -282,8 +284,8 @@ __global__ void __launch_bounds__(kLogitThreads) adjust_logits_kernel(const Logi
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const int i = done + 4 * (u * kLogitThreads + tid);
-                const uint32_t least = min(min(static_cast<uint32_t>(x[u].x - c0), static_cast<uint32_t>(x[u].y - c0)),
-                                           min(static_cast<uint32_t>(x[u].z - c0), static_cast<uint32_t>(x[u].w - c0)));
+                const uint32_t least = min(min(column(x[u].x), column(x[u].y)),
+                                           min(column(x[u].z), column(x[u].w)));
                 if (least >= static_cast<uint32_t>(cols)) continue;
                 count(i, x[u].x);
                 count(i + 1, x[u].y);
@@ -308,7 +310,7 @@ __global__ void __launch_bounds__(kLogitThreads) adjust_logits_kernel(const Logi
         s.path[lane] = penal && p.node_token && lane < n ? anc & hung : 0u;
         s.node_token[lane] = token;
         s.mask[lane] = mask;
-        const uint32_t v = static_cast<uint32_t>(token - c0);
+        const uint32_t v = column(token);
         if (parent >= 0 && token >= 0 && v < static_cast<uint32_t>(cols)) {
             atomicOr(&s.word[v], kNamed);
             atomicOr(&s.touched[v / 32], 1u << (v & 31));
@@ -320,7 +322,7 @@ __global__ void __launch_bounds__(kLogitThreads) adjust_logits_kernel(const Logi
         const int64_t i = i0 + tid;
         const bool again = i0 > bias0;
         const int id = !again ? first_id : (i < bias1 ? __ldg(p.bias_ids + i) : -1);
-        const uint32_t v = static_cast<uint32_t>(id - c0);
+        const uint32_t v = column(id);
         const bool mine = v < static_cast<uint32_t>(cols);
         const uint32_t vote = __ballot_sync(0xFFFFFFFFu, mine);
         if (lane == 0) s.scan[warp] = __popc(vote);
