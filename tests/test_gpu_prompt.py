@@ -250,14 +250,17 @@ def test_streams_graphs_and_shared_workspaces(sv):
         assert torch.equal(got["out"], want["out"])
 
 
-@pytest.mark.parametrize("opt", [dict(), dict(window=3000, prefix=4)])
-def test_long_prompts_by_samples_of_their_rows(sv, opt):
-    """A long prompt and a piece over a long context: some rows against the definition."""
+@pytest.mark.parametrize("opt,D", [(dict(), 128), (dict(window=3000, prefix=4), 128), (dict(), 64), (dict(), 256),
+                                   (dict(cap=20.0, window=20000), 64), (dict(cap=20.0, slopes=[1e-4, 0.0, 1e-5, 1e-3]), 256)])
+def test_long_prompts_by_samples_of_their_rows(sv, opt, D):
+    """A long prompt and a piece over a long context (longer than tensor memory adds up at once): some rows against the
+    definition."""
     rng = np.random.default_rng(25)
-    n, m, Hq, H, D = 5003, 30011, 4, 1, 128
+    n, m, Hq, H = 5003, 36011, 4, 1
+    given = {**opt, "slopes": torch.tensor(opt["slopes"], device="cuda")} if "slopes" in opt else opt
     q, k, v = rand(rng, n, Hq, D), rand(rng, m, H, D), rand(rng, m, H, D)
-    got = sv.prompt_attend(q, k, v, i32([0, n]), B=1, cu_keys=i32([0, m]), **opt)
-    own = sv.prompt_attend(q, k[-n:], v[-n:], i32([0, n]), B=1, **opt)
+    got = sv.prompt_attend(q, k, v, i32([0, n]), B=1, cu_keys=i32([0, m]), **given)
+    own = sv.prompt_attend(q, k[-n:], v[-n:], i32([0, n]), B=1, **given)
     for i in [0, 1, 127, 2048, 4095, 5002]:
         upto = m - n + i + 1
         res = {x: got[x][i:i + 1] for x in got}

@@ -270,6 +270,13 @@ def test_logits(sv, rows, V, dtype):
     check_logits(sv, rng, rows, V, dtype, history=3000, few=50, bias=700, tree=False)
 
 
+@pytest.mark.parametrize("in_place", [False, True])
+def test_logits_of_many_requests(sv, in_place):
+    """So many that no request's rows are dealt out to several CTAs."""
+    rng = np.random.default_rng(37)
+    check_logits(sv, rng, [2, 1] * 200, 8203, "bf16", history=60, bias=4, in_place=in_place)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("kw", [dict(penalties=False), dict(path=False), dict(mask=False), dict(penalties=False, mask=False, bias=3),
                                 dict(penalties=False, mask=False, path=False), dict(in_place=True), dict(in_place=True, ld=9011),
