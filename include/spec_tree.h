@@ -71,7 +71,7 @@ typedef struct {
     const int32_t *history;    /* [B, history_ld] or NULL: each request's tokens so far (the
                                   root's token among them); ids outside [0, V) count nowhere  */
     int64_t history_ld;
-    int32_t history_cap;       /* columns of history                                          */
+    int32_t history_cap;       /* columns of history, at most 2^28 - 64                        */
     const int32_t *n_tokens;   /* [B] how many there are, 0..history_cap                      */
     const int32_t *n_prompt;   /* [B] or NULL (0): how many of them are the prompt's          */
     const float *repetition;   /* [B] or NULL (1): finite, > 0                                */

@@ -627,7 +627,7 @@ int spec_tree_accept(const spec_tree *t, spec_stream stream)
     if (!on_words(t->cu_rows, t->row_token, t->node_token, t->parent, t->accepted_len, t->out_tokens, t->next_token,
                   t->path_rows, t->status))
         return SPEC_ERR_INVALID_ARG;
-    if (t->k_max > 31) return SPEC_ERR_UNSUPPORTED;
+    if (t->k_max > 31 || t->B > kMostSlots) return SPEC_ERR_UNSUPPORTED;
     TreeParams p;
     p.B = t->B;
     p.k_max = t->k_max;
@@ -659,9 +659,9 @@ int spec_adjust_logits(const spec_logit_rules *r, void *out, int64_t out_ld, spe
     if (!on_words(r->cu_rows, r->history, r->n_tokens, r->n_prompt, r->repetition, r->frequency, r->presence, r->node_token,
                   r->parent, r->bias_cu, r->bias_ids, r->bias_values, r->allowed, r->allowed_row, r->status))
         return SPEC_ERR_INVALID_ARG;
-    // requests are the y of the grid, counts leave two bits of their words
-    if (r->k_max > 31 || r->B > kMostRequests || r->V > kMostSlots || (r->history && r->history_cap > kMostSlots - 64))
-        return SPEC_ERR_UNSUPPORTED;
+    // requests are the y of the grid, counts leave four bits of their words
+    if (r->k_max > 31 || r->B > kMostRequests || r->V > kMostSlots) return SPEC_ERR_UNSUPPORTED;
+    if ((r->history && r->history_cap > kMostSlots / 4 - 64) || (r->bias_cu && r->n_bias > kMostSlots)) return SPEC_ERR_UNSUPPORTED;
     LogitParams p;
     p.logits = r->logits;
     p.ld = r->ld;

@@ -64,13 +64,13 @@ __global__ void __launch_bounds__(kAcceptWarps * 32) tree_accept_kernel(const Tr
 // stream (105), a cluster that shares the history by distributed atomics (128, frequent tokens meet there), vectors of a row
 // ahead of the stores (120: registers for fewer CTAs), six CTAs an SM (119: fewer loads in flight in each).
 //
-// A column's word: how often it was generated, whether it was seen at all, whether one of the request's biases or nodes
-// names it; a bit a column says whether the word is anything but 0.
+// A column's word: how often it was generated, whether it was seen at all, whether one of the request's nodes names it, one of
+// its biases, more than one; a bit a column says whether the word is anything but 0.
 constexpr int kSlice = 8192, kLogitThreads = 256;
-constexpr uint32_t kSeen = 1u << 31, kNamed = 1u << 30, kCount = kNamed - 1u;
+constexpr uint32_t kSeen = 1u << 31, kNamed = 1u << 30, kBiased = 1u << 29, kTwice = 1u << 28, kCount = kTwice - 1u;
 constexpr int kNear = 256;                            // biases of a slice kept in shared memory
 constexpr int kFull = 152 * 5;                        // CTAs that are resident at once
-constexpr int kListed = 1024;                         // touched columns that are listed at a time
+constexpr int kListed = 1024, kListedBiased = 2 * kNear;      // touched columns that are listed at a time; with more biases than kNear
 
 template <typename T> struct LogitElt;
 template <> struct LogitElt<__nv_bfloat16> {
@@ -117,10 +117,16 @@ struct Slice {
     int node_token[32];
     uint32_t path[32];                                // of each row: the nodes on it
     int mask[32];                                     // of each row: its mask, -1 for none
-    int bias_id[kNear];
-    float bias_value[kNear];
+    union {
+        struct {
+            int bias_id[kNear];
+            float bias_value[kNear];
+        };
+        float bias_sum[kListedBiased];                // of each listed column, where the biases are too many
+    };
+    uint16_t before[kLogitThreads];                   // touched columns before each word of the bit set
     int scan[kLogitThreads / 32];
-    int n_bias;
+    int n_bias, twice;                                // biases of the slice; whether a column has several
     uint16_t column[kListed];
 };
 
@@ -128,9 +134,8 @@ struct Penalty {
     float repetition, frequency, presence;
 };
 
-// one touched column (v: from the slice's first on) of a row with `path`
-__device__ __forceinline__ float adjust(const LogitParams &p, const Slice &s, const Penalty &pen, int c0, int v, int n, uint32_t path,
-                                        int bias0, int bias1, float z)
+// one touched column (v: from the slice's first on; `at`: its place in the list) of a row with `path`
+__device__ __forceinline__ float adjust(const Slice &s, const Penalty &pen, int c0, int v, int at, int n, uint32_t path, float z)
 {
     const uint32_t w = s.word[v];
     int count = static_cast<int>(w & kCount);
@@ -141,12 +146,12 @@ __device__ __forceinline__ float adjust(const LogitParams &p, const Slice &s, co
     seen |= count > 0;
     if (seen) z = z > 0.f ? z / pen.repetition : z * pen.repetition;
     if (count > 0) z = z - pen.frequency * static_cast<float>(count) - pen.presence;
-    if (w & kNamed) {
+    if (w & kBiased) {
         float add = 0.f;
         if (s.n_bias <= kNear) {
             for (int i = 0; i < s.n_bias; ++i) add += s.bias_id[i] == v ? s.bias_value[i] : 0.f;
         } else {
-            for (int i = bias0; i < bias1; ++i) add += __ldg(p.bias_ids + i) == c0 + v ? __ldg(p.bias_values + i) : 0.f;
+            add = s.bias_sum[at];
         }
         z += add;
     }
@@ -181,11 +186,11 @@ __global__ void __launch_bounds__(kLogitThreads) adjust_logits_kernel(const Logi
     if (bias0 < 0 || bias1 < bias0 || bias1 > p.n_bias) bad = bad || p.bias_cu, bias0 = bias1 = 0;
     if (bad && tid == 0) set_status(report, SPEC_STATUS_BAD_PENALTY);
     const bool penal = pen.repetition != 1.f || pen.frequency != 0.f || pen.presence != 0.f;
-    if (!penal) tokens = 0;
     if (tokens < 0 || tokens > p.history_cap) {
         if (tid == 0) set_status(report, SPEC_STATUS_BAD_LENGTH);
         tokens = 0;
     }
+    if (!penal) tokens = 0;
 
     const bool in_place = p.out == p.logits;
     const int mask_words = (p.V + 31) / 32;
@@ -257,6 +262,7 @@ __global__ void __launch_bounds__(kLogitThreads) adjust_logits_kernel(const Logi
     }
     for (int i = tid; i < kSlice / 4; i += kLogitThreads) reinterpret_cast<uint4 *>(s.word)[i] = make_uint4(0, 0, 0, 0);
     s.touched[tid] = 0;
+    if (tid == 0) s.twice = 0;
     const int z0 = blockIdx.z, dz = gridDim.z;        // this CTA's rows: z0, z0 + dz, ...
     if (!in_place)
         for (int j = z0; j < n; j += dz) stream(lo + j);
@@ -338,7 +344,10 @@ __global__ void __launch_bounds__(kLogitThreads) adjust_logits_kernel(const Logi
                 s.bias_id[at] = static_cast<int>(v);
                 s.bias_value[at] = again ? __ldg(p.bias_values + i) : first_value;
             }
-            atomicOr(&s.word[v], kNamed);
+            if (atomicOr(&s.word[v], kBiased) & kBiased) {
+                atomicOr(&s.word[v], kTwice);
+                s.twice = 1;
+            }
             atomicOr(&s.touched[v / 32], 1u << (v & 31));
         }
         __syncthreads();
@@ -346,7 +355,7 @@ __global__ void __launch_bounds__(kLogitThreads) adjust_logits_kernel(const Logi
     if (tid == 0) s.n_bias = near;
     __syncthreads();
 
-    // the touched columns in their order, kListed at a time; a thread has 32 columns of the set
+    // the touched columns in their order, some at a time; a thread has 32 columns of the set
     static_assert(kSlice == 32 * kLogitThreads && sizeof(Slice) <= 48 * 1024, "a word of the bit set a thread");
     const uint32_t set = s.touched[tid];
     int first = __popc(set), touched = 0;
@@ -363,18 +372,61 @@ __global__ void __launch_bounds__(kLogitThreads) adjust_logits_kernel(const Logi
         first += w < warp ? s.scan[w] : 0;
         touched += s.scan[w];
     }
-    for (int e0 = 0; e0 < touched; e0 += kListed) {
-        const int count = min(touched - e0, kListed);
-        if (e0 > 0) __syncthreads();
+    s.before[tid] = static_cast<uint16_t>(first);
+    const bool many = near > kNear;
+    const int listed = many ? kListedBiased : kListed;
+    for (int e0 = 0; e0 < touched; e0 += listed) {
+        const int count = min(touched - e0, listed);
+        __syncthreads();
         int at = first - e0;
         for (uint32_t left = set; left; left &= left - 1, ++at)
-            if (at >= 0 && at < kListed) s.column[at] = static_cast<uint16_t>(tid * 32 + __ffs(left) - 1);
+            if (at >= 0 && at < listed) s.column[at] = static_cast<uint16_t>(tid * 32 + __ffs(left) - 1);
+        if (many) {
+            // Too many biases to compare every column with each: every bias goes to its column's sum, those of a column that has
+            // several one after another (5 rows of 152064, a bias a column: 2.4 ms, 166 by comparing; two a column: 10).
+            s.bias_sum[tid] = s.bias_sum[tid + kNear] = 0.f;
+            __syncthreads();
+            // the place in the list of a bias on column `id`, and whether the column has others, or -1
+            const auto place_of = [&](int id, bool &again) {
+                const uint32_t v = column(id);
+                if (v >= static_cast<uint32_t>(cols)) return -1;
+                const int to = s.before[v / 32] + __popc(s.touched[v / 32] & ((1u << (v & 31)) - 1u)) - e0;
+                again = (s.word[v] & kTwice) != 0;
+                return to >= 0 && to < count ? to : -1;
+            };
+            for (int64_t i0 = static_cast<int64_t>(bias0) + tid; i0 < bias1; i0 += 4 * kLogitThreads) {
+                int id[4];
+#pragma unroll
+                for (int u = 0; u < 4; ++u) id[u] = i0 + u * kLogitThreads < bias1 ? __ldg(p.bias_ids + i0 + u * kLogitThreads) : -1;
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    bool again = false;
+                    const int to = place_of(id[u], again);
+                    if (to >= 0 && !again) s.bias_sum[to] = __ldg(p.bias_values + i0 + u * kLogitThreads);
+                }
+            }
+            for (int64_t i0 = s.twice ? bias0 : bias1; i0 < bias1; i0 += kLogitThreads) {
+                bool again = false;
+                const int to = place_of(i0 + tid < bias1 ? __ldg(p.bias_ids + i0 + tid) : -1, again);
+                again = again && to >= 0;
+                if (!__syncthreads_or(again)) continue;
+                for (int w = 0; w < kLogitThreads / 32; ++w) {
+                    if (w == warp) {
+                        for (uint32_t left = __ballot_sync(0xFFFFFFFFu, again); left; left &= left - 1) {
+                            if (lane == __ffs(left) - 1) s.bias_sum[to] += __ldg(p.bias_values + i0 + tid);
+                            __syncwarp();
+                        }
+                    }
+                    __syncthreads();
+                }
+            }
+        }
         __syncthreads();
         for (int e = tid; e < (n - z0 + dz - 1) / dz * count; e += kLogitThreads) {
-            const int i = e / count, v = s.column[e - i * count], j = z0 + i * dz, row = lo + j;
+            const int i = e / count, place = e - i * count, v = s.column[place], j = z0 + i * dz, row = lo + j;
             const float z = to_f32<T>(source(row)[v]);
             const bool gone = hidden(mask_at(s.mask[j]), v);
-            target(row)[v] = from_f32<T>(gone ? -INFINITY : adjust(p, s, pen, c0, v, n, s.path[j], bias0, bias1, z));
+            target(row)[v] = from_f32<T>(gone ? -INFINITY : adjust(s, pen, c0, v, place, n, s.path[j], z));
         }
     }
     if (in_place) {

@@ -208,7 +208,7 @@ def test_acceptance_of_malformed_requests(sv):
 # ------------------------------------------------------------------ logits ---
 
 def check_logits(sv, rng, rows, V, dtype, *, ld=None, history=0, penalties=True, path=True, tree=True, bias=0, mask=True,
-                 in_place=False, shift=0, out_ld=None, few=None):
+                 in_place=False, shift=0, out_ld=None, few=None, bias_top=None):
     B, R, cu = len(rows), max(sum(rows), 1), offsets(rows)
     ld = ld or V
     z = torch.from_numpy((3 * rng.standard_normal(R * ld + shift)).astype(np.float32)).to(DT[dtype]).cuda()[shift:].view(R, ld)
@@ -230,9 +230,11 @@ def check_logits(sv, rng, rows, V, dtype, *, ld=None, history=0, penalties=True,
             opt["parent"] = i32(kw["parent"])
     if bias:
         counts = rng.integers(0, bias + 1, B)
-        ids, vals = rng.integers(-1, min(V + 2, 40), counts.sum()), rng.standard_normal(counts.sum()).astype(np.float32)
+        ids, vals = rng.integers(-1, bias_top or min(V + 2, 40), counts.sum()), rng.standard_normal(counts.sum()).astype(np.float32)
         bc = offsets(counts)
         kw["bias"] = [(ids[bc[b]:bc[b + 1]], vals[bc[b]:bc[b + 1]]) for b in range(B)]
+        if bias_top:                                                    # how many meet at a column at most
+            bias = max([int(np.bincount(x + 1).max()) for x, _ in kw["bias"] if len(x)], default=0)
         opt.update(bias_cu=i32(bc), bias_ids=i32(ids), bias_values=dev(vals))
     if mask:
         kw["allowed"] = rng.integers(-2 ** 31, 2 ** 31, (max(R // 2, 1), (V + 31) // 32 + 1)).astype(np.int32)
@@ -275,6 +277,81 @@ def test_logits_of_many_requests(sv, in_place):
     """So many that no request's rows are dealt out to several CTAs."""
     rng = np.random.default_rng(37)
     check_logits(sv, rng, [2, 1] * 200, 8203, "bf16", history=60, bias=4, in_place=in_place)
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("kw", [dict(history=20000), dict(history=20000, bias=300, bias_top=8900), dict(bias=9000, bias_top=9011),
+                                dict(bias=20000, bias_top=600, history=5000), dict(bias=3000, penalties=False, path=False)])
+def test_logits_of_many_touched_columns(sv, kw, in_place):
+    """More tokens, and more biases, than are kept or listed at a time; biases one a column and many."""
+    rng = np.random.default_rng(39)
+    check_logits(sv, rng, [3, 2], 9007, "f32", in_place=in_place, **kw)
+    check_logits(sv, rng, [1], 9007, "bf16", in_place=in_place, **kw)
+
+
+def test_a_bias_for_every_column(sv):
+    """Sums of small integers: exact; repeated runs give the same bits."""
+    rng = np.random.default_rng(41)
+    V, B = 20011, 3
+    z = torch.from_numpy(rng.integers(-50, 50, (B * 4, V)).astype(np.float32)).cuda()
+    ids = np.concatenate([rng.permutation(V), rng.permutation(np.repeat(np.arange(V), 2)), rng.integers(0, 5, 700)])
+    val = rng.integers(-9, 9, len(ids)).astype(np.float32)
+    cu = np.array([0, V, 3 * V, 3 * V + 700])
+    got = sv.adjust_logits(z, i32(np.arange(0, 13, 4)), V=V, B=B, k_max=3, bias_cu=i32(cu), bias_ids=i32(ids), bias_values=dev(val))["logits"]
+    for b in range(B):
+        add = np.zeros(V)
+        np.add.at(add, ids[cu[b]:cu[b + 1]], val[cu[b]:cu[b + 1]])
+        assert np.array_equal(got[4 * b:4 * b + 4].double().cpu().numpy(), z[4 * b:4 * b + 4].double().cpu().numpy() + add), b
+    val = dev(rng.standard_normal(len(ids)).astype(np.float32))
+    runs = [sv.adjust_logits(z, i32(np.arange(0, 13, 4)), V=V, B=B, k_max=3, bias_cu=i32(cu), bias_ids=i32(ids), bias_values=val)["logits"]
+            for _ in range(3)]
+    assert torch.equal(runs[0], runs[1]) and torch.equal(runs[0], runs[2])
+
+
+def test_lengths_are_looked_at_without_penalties(sv):
+    z = torch.zeros(2, 40, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for n, is_bad in ((3, False), (4, True), (-1, True)):
+        status.zero_()
+        got = sv.adjust_logits(z, i32([0, 2]), V=40, B=1, k_max=1, history=i32([[1, 2, 3]]), n_tokens=i32([n]), status=status)["logits"]
+        assert int(status) == (0x800 if is_bad else 0) and torch.equal(got, z)
+
+
+def test_chains_and_trees_share_a_workspace_and_graphs(sv):
+    """Both attentions and the acceptance captured, replayed in turn on one workspace, and on another stream."""
+    rng = np.random.default_rng(43)
+    rows, lens = [26, 9, 1], [1500, 400, 90]
+    c = quick_pool(rng, B=3, H=2, D=128, page=64, lens=lens)
+    q = torch.from_numpy(rng.standard_normal((36, 8, 128)).astype(np.float32)).to(torch.bfloat16).cuda()
+    parent = random_trees(rng, rows)
+    args = (gpu_cache(sv, c), q, i32(offsets(rows)), i32(lens), dev(c.table))
+    kw = dict(B=3, k_max=31)
+    want = [sv.cache_attend(*args, **kw), sv.cache_attend_tree(*args, i32(parent), **kw), sv.cache_attend_tree(*args, i32(parent), window=70, **kw)]
+    ws = sv.new_cache_workspace(args[0], args[4], Hq=8, **kw)
+    token, node = i32(rng.integers(0, 2, 36)), i32(rng.integers(0, 2, 36))
+    want.append(sv.tree_accept(token, node, i32(parent), args[2], **kw))
+    calls = [sv.cache_attend(*args, workspace=ws, prepared=True, **kw), sv.cache_attend_tree(*args, i32(parent), workspace=ws, prepared=True, **kw),
+             sv.cache_attend_tree(*args, i32(parent), workspace=ws, prepared=True, window=70, **kw),
+             sv.tree_accept(token, node, i32(parent), args[2], prepared=True, **kw)]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graphs = []
+    for call in calls:
+        call(stream=side)
+        side.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            call()
+        graphs.append(g)
+    held = [call() for call in calls]                                   # where each writes
+    for _ in range(3):
+        for res in held:
+            for x in res.values():
+                x.fill_(0)
+        for g in graphs:
+            g.replay()
+        for res, w in zip(held, want):
+            assert all(torch.equal(res[x], w[x]) for x in w)
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])

@@ -66,7 +66,7 @@ def test_prompt_outputs_and_workspace_are_checked(sv):
 @pytest.mark.parametrize("over,rc", [
     (dict(cu_rows=None), 1), (dict(row_token=None), 1), (dict(node_token=None), 1), (dict(parent=None), 1),
     (dict(accepted_len=None), 1), (dict(out_tokens=None), 1), (dict(next_token=None), 1), (dict(B=0), 1), (dict(k_max=-1), 1),
-    (dict(k_max=32), 2), (dict(R_cap=0), 1), (dict(parent=ODD), 1), (dict(path_rows=ODD), 1), (dict(status=ODD), 1)])
+    (dict(k_max=32), 2), (dict(B=(1 << 30) + 1), 2), (dict(R_cap=0), 1), (dict(parent=ODD), 1), (dict(path_rows=ODD), 1), (dict(status=ODD), 1)])
 def test_tree_is_checked(sv, over, rc):
     L, a = sv.load_library(), _tree(**over)
     assert L.spec_tree_accept(C.byref(a), None) == rc
@@ -93,6 +93,8 @@ def test_tree_attention_is_checked(sv):
     (dict(history=FAKE, history_ld=10, history_cap=10), 1), (dict(history=FAKE, n_tokens=FAKE, history_ld=9, history_cap=10), 1),
     (dict(history=FAKE, n_tokens=FAKE, history_ld=10, history_cap=-1), 1), (dict(history=ODD, n_tokens=FAKE), 1),
     (dict(history=FAKE, n_tokens=FAKE, history_ld=1 << 31, history_cap=(1 << 31) - 1), 2),
+    (dict(history=FAKE, n_tokens=FAKE, history_ld=1 << 28, history_cap=(1 << 28) - 63), 2),
+    (dict(bias_cu=FAKE, n_bias=(1 << 30) + 1, bias_ids=FAKE, bias_values=FAKE), 2),
     (dict(bias_cu=FAKE, n_bias=-1), 1), (dict(bias_cu=FAKE, n_bias=3, bias_ids=FAKE), 1),
     (dict(bias_cu=FAKE, n_bias=3, bias_values=FAKE), 1), (dict(allowed=FAKE, n_allowed=0, allowed_ld=32), 1),
     (dict(allowed=FAKE, n_allowed=1, allowed_ld=31), 1), (dict(repetition=ODD), 1), (dict(parent=ODD), 1), (dict(status=ODD), 1)])
