@@ -57,7 +57,8 @@ SPEC_API size_t spec_prompt_workspace_bytes(int32_t Hq, int32_t H, int32_t D, in
  * no key (m < n) gets out = 0 and lse = -inf, as do all rows of a request with malformed
  * cu_keys (SPEC_STATUS_BAD_LENGTH).  out [R_cap, Hq, D] and lse [R_cap, Hq] or NULL, both
  * contiguous; rows >= cu_rows[B], and those of a request with malformed cu_rows
- * (SPEC_STATUS_BAD_ROWS), are not written.  Keys and values that no row of their request
+ * (SPEC_STATUS_BAD_ROWS), are not written; where offsets go back, so that rows lie in two requests, those may hold either's
+ * results or be left.  Keys and values that no row of their request
  * sees may hold anything; those that one of its rows sees have to be finite, as have
  * the queries (a row of another request never notices).  The scores have to stay within
  * fp32.  Results do not depend on the order in which blocks run.

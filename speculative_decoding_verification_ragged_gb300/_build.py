@@ -13,8 +13,8 @@ INCLUDE = os.path.join(ROOT, "include")
 OUT = os.path.join(PKG, "libspecverify.so")
 SOURCES = ["verify.cu", "rows.cu", "draft.cu", "cache.cu", "cache_attend.cu", "cache_attend_options.cu",
            "cache_attend_tree.cu", "cache_attend_tree_options.cu", "cache_weights.cu", "prompt_rows.cu",
-           "prompt_tiles.cu", "prompt_tiles_options.cu", "tree.cu",
-           "capi.cu", "step_policy.cpp"]
+           "prompt_tiles.cu", "prompt_tiles_options.cu", "prompt_tiles_split.cu", "prompt_tiles_split_options.cu",
+           "tree.cu", "capi.cu", "step_policy.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -37,12 +37,26 @@ bool map_of(CUtensorMap *m, const void *x, bool aligned, int D, int heads, int r
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+cudaError_t launch_prompt_tiles(const PromptParams &p, const PromptMaps &maps, cudaStream_t s)
+{
+    // At most this many items (of requests that do not overlap).  Where they leave SMs idle each is split, into as many parts
+    // as fit and as its steps can pay for.
+    const int rows = (p.D == 256 ? 1 : 2) * (128 / (p.Hq / p.H));
+    const int64_t items = (p.R_cap + static_cast<int64_t>(p.B) * (rows - 1)) / rows * p.H;
+    const int64_t steps = p.K_cap / (p.D == 256 ? 64 : 128) + 1;
+    const int grid = static_cast<int>(items < kPromptSms ? items : kPromptSms);
+    const int split = parts_of(steps, static_cast<int>(items > kPromptSms ? 1 : min(kPromptSms / items, static_cast<int64_t>(kMostParts))));
+    const bool options = p.cap > 0.f || p.slopes || p.scale <= 0.f;
+    if (split > 1) return options ? launch_prompt_tiles_split_options(p, maps, grid, split, s) : launch_prompt_tiles_split(p, maps, grid, split, s);
+    return options ? launch_prompt_tiles_options(p, maps, grid, s) : launch_tiles<false, false>(p, maps, grid, 1, s);
+}
+
 }  // namespace
 
 size_t prompt_workspace(int D, int dtype)
 {
     if (dtype == SPEC_F32) return kPromptTickets;
-    return kPromptTickets + static_cast<size_t>(kPromptSms) * (D == 256 ? 1 : 2) * 128 * D * 4;
+    return kPromptTickets + static_cast<size_t>(kPromptSms) * (D == 256 ? 1 : 2) * 128 * (D * 4 + 8);
 }
 
 cudaError_t launch_prompt(const PromptParams &p, int dtype, cudaStream_t s)
@@ -54,7 +68,7 @@ cudaError_t launch_prompt(const PromptParams &p, int dtype, cudaStream_t s)
         map_of(&maps.q, p.q, p.q_aligned, p.D, p.Hq, p.R_cap, p.q_head, p.q_row, group, 128 / group) &&
         map_of(&maps.k, p.k, p.k_aligned, p.D, p.H, p.K_cap, p.k_head, p.k_row, 1, p.D == 256 ? 64 : 128) &&
         map_of(&maps.v, p.v, p.v_aligned, p.D, p.H, p.K_cap, p.v_head, p.v_row, 1, p.D == 256 ? 64 : 128))
-        return p.cap > 0.f || p.slopes || p.scale <= 0.f ? launch_prompt_tiles_options(p, maps, s) : launch_tiles<false>(p, maps, s);
+        return launch_prompt_tiles(p, maps, s);
     return launch_prompt_rows(p, dtype, s);
 }
 

@@ -1,6 +1,6 @@
 // prompt_tiles.cuh -- the kernel of the attention of bf16 prompts over themselves on the tensor
 // cores (include/spec_prompt.h); prompt_tiles.cu has it plain, prompt_tiles_options.cu
-// with the score options.
+// with the score options, prompt_tiles_split.cu and prompt_tiles_split_options.cu the same for few items, split along the keys.
 //
 // A work item is a kv head and NQ tiles of up to 128 packed rows (TT rows of all the query heads of the
 // kv head: g heads need a key once).  Over steps of KT keys
@@ -35,10 +35,22 @@ struct PromptMaps {
 namespace {
 
 constexpr float kLazy = 8.f;               // log2 units a score may pass the reference by
+// The workspace: tickets, a CTA's sums over keys, its rows' references and weights.
 constexpr int kPromptSms = 152, kPromptTickets = 256;
 // Tensor memory truncates what it adds up: a run of keys at most, then the sum goes to fp32 in the
 // workspace.
 constexpr int kRunKeys = 16384;
+// Where a call has too few items for the SMs, items of many steps are split along the keys; the parts of an item are a cluster of
+// CTAs, which join their sums together.  That costs as much as 8 steps (8 to 10 us): split into parts of at least 3 steps
+// from 12 steps on, 128 rows over 2000 keys take 27 us for 33 (over 8000: 43 for 99, over 60000: 156 for 643); from 8 on,
+// over 1000 keys, 25 to 27 for 23.
+constexpr int kSplitSteps = 12, kPartSteps = 3, kMostParts = 16;
+
+// parts of an item of n steps, of `most`
+__host__ __device__ __forceinline__ int parts_of(int64_t n, int most)
+{
+    return n < kSplitSteps ? 1 : static_cast<int>(n / kPartSteps < most ? n / kPartSteps : most);
+}
 
 template <int D_> struct Prompt {
     static constexpr int D = D_;
@@ -69,9 +81,14 @@ struct Item {
     int h, first;               // kv head (-1: there are no more); first row of the tiles
     int n[2];                   // steps that each tile sees
     int np, f0;                 // steps to visit: 0 .. np - 1, then f0, f0 + 1, ...
+    int part, parts, from;      // of the item's parts; the steps before it
 };
 
-__device__ __forceinline__ int item_step(const Item &it, int i) { return i < it.np ? i : it.f0 + i - it.np; }
+template <bool SPLIT> __device__ __forceinline__ int item_step(const Item &it, int i)
+{
+    if (SPLIT) i += it.from;
+    return i < it.np ? i : it.f0 + i - it.np;
+}
 
 // Two values as bf16, the first in the low half
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
@@ -79,6 +96,12 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
     uint32_t r;
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
+}
+
+// Barrier of all threads of the cluster's CTAs: none of them leaves before it, whatever fails
+__device__ __forceinline__ void cluster_barrier()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 // Barrier of the softmax warps, with a vote: whether any thread's `x` is true
@@ -106,9 +129,9 @@ __device__ __forceinline__ uint64_t tame_tanh(uint64_t z)
     return f2_fma(y, z, 0);
 }
 
-template <int D, bool OPT>
+template <int D, bool OPT, bool SPLIT>
 __global__ void __launch_bounds__(Prompt<D>::THREADS, 1)
-prompt_tiles_kernel(const PromptParams p, const __grid_constant__ PromptMaps maps)
+prompt_tiles_kernel(const PromptParams p, const __grid_constant__ PromptMaps maps, const int parts_most)
 {
     using A = Prompt<D>;
     constexpr int NQ = A::NQ, KT = A::KT, SLOTS = A::SLOTS, SHARE = A::SHARE, KH = A::KH, DH = A::DH, kItems = 2;
@@ -123,7 +146,7 @@ prompt_tiles_kernel(const PromptParams p, const __grid_constant__ PromptMaps map
     __shared__ uint32_t tmem_base;
     __shared__ int failed;
     const int tid = threadIdx.x, warp = warp_index(), lane = tid & 31;
-    const int group = p.Hq / p.H, TT = 128 / group;
+    const int group = p.Hq / p.H, TT = 128 / group, split = SPLIT ? parts_most : 1;
 
     if (tid == 0) {
         failed = 0;
@@ -211,9 +234,9 @@ prompt_tiles_kernel(const PromptParams p, const __grid_constant__ PromptMaps map
                 }
             };
             for (;;) {
-                Item it;
+                Item it = {};
                 it.h = -1;
-                const int64_t line = index / p.H;
+                const int64_t number = index / split, line = number / p.H;
                 // the request whose tiles hold `line`, its last (longest) tile first
                 while (b0 < p.B && !fail) {
                     if (known != b0) {
@@ -236,7 +259,7 @@ prompt_tiles_kernel(const PromptParams p, const __grid_constant__ PromptMaps map
                         it.t.k_lo = __shfl_sync(0xFFFFFFFFu, t.k_lo, from);
                         it.t.m = __shfl_sync(0xFFFFFFFFu, t.m, from);
                         it.first = static_cast<int>(__shfl_sync(0xFFFFFFFFu, at, from) - 1 - line) * (NQ * TT);
-                        it.h = static_cast<int>(index % p.H);
+                        it.h = static_cast<int>(number % p.H);
                         break;
                     }
                     base += all;
@@ -252,6 +275,20 @@ prompt_tiles_kernel(const PromptParams p, const __grid_constant__ PromptMaps map
                         const int rows = min(it.t.n - it.first - q * TT, TT);
                         const int last = rows > 0 && q < NQ ? own + q * TT + rows - 1 : -1;
                         it.n[q] = last < 0 ? 0 : it.np + last / KT + 1 - near;
+                    }
+                    // parts of about as many steps, as many as pay for their joining
+                    it.part = static_cast<int>(index % split);
+                    it.parts = 1;
+                    it.from = 0;
+                    if (SPLIT) {
+                        const int n = max(it.n[0], it.n[1]);
+                        it.parts = parts_of(n, split);
+                        it.from = static_cast<int>(static_cast<int64_t>(n) * it.part / it.parts);
+                        const int to = static_cast<int>(static_cast<int64_t>(n) * (it.part + 1) / it.parts);
+#pragma unroll
+                        for (int q = 0; q < 2; ++q) it.n[q] = max(min(it.n[q], to) - it.from, 0);
+                        // (a part's sums stay where they are until they are joined: its CTA takes no other)
+                        if (index >= gridDim.x || it.part >= it.parts) it.h = -1;
                     }
                 }
                 wait_or_fail(&item_empty[ir], i_phase ^ 1, fail);
@@ -282,12 +319,12 @@ prompt_tiles_kernel(const PromptParams p, const __grid_constant__ PromptMaps map
                             }
                             __syncwarp();
                         }
-                        if (q == 0) slot(false, it, item_step(it, 0));
+                        if (q == 0) slot(false, it, item_step<SPLIT>(it, 0));
                     }
                     for (int i = 0; i < n; ++i) {
-                        if (NQ == 2) slot(true, it, item_step(it, i));
-                        if (i + 1 < n) slot(false, it, item_step(it, i + 1));
-                        if (NQ == 1) slot(true, it, item_step(it, i));
+                        if (NQ == 2) slot(true, it, item_step<SPLIT>(it, i));
+                        if (i + 1 < n) slot(false, it, item_step<SPLIT>(it, i + 1));
+                        if (NQ == 1) slot(true, it, item_step<SPLIT>(it, i));
                     }
                 }
                 index = static_cast<int64_t>(gridDim.x) + __shfl_sync(0xFFFFFFFFu, taken, 0);
@@ -389,6 +426,10 @@ prompt_tiles_kernel(const PromptParams p, const __grid_constant__ PromptMaps map
                 }
             }
         }
+        if (SPLIT) {
+            __syncwarp();
+            cluster_barrier();                        // (with the softmax warps of all parts)
+        }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(A::MORE_REGS));
         const int q = SHARE == 2 ? 0 : warp >> 2, row = tid & 127;             // tile, row of it
@@ -400,6 +441,9 @@ prompt_tiles_kernel(const PromptParams p, const __grid_constant__ PromptMaps map
         // sums over the runs of keys so far, channel by channel
         float *const sums = reinterpret_cast<float *>(static_cast<uint8_t *>(p.ws) + kPromptTickets) +
                             ((static_cast<int64_t>(blockIdx.x) * NQ + q) * D + part * DH) * 128 + row;
+        // reference and weight of each row of each CTA's items that are split
+        float2 *const stats = reinterpret_cast<float2 *>(static_cast<uint8_t *>(p.ws) + kPromptTickets +
+                                                         static_cast<int64_t>(kPromptSms) * NQ * D * 512);
         if (blockIdx.x == 0 && p.status) {
             PromptTile t;
             for (int b = tid; b < p.B; b += A::SOFTMAX) prompt_request(p, b, p.status, t);
@@ -417,9 +461,9 @@ prompt_tiles_kernel(const PromptParams p, const __grid_constant__ PromptMaps map
             __syncwarp();
             if (lane == 0) mbar_arrive(&item_empty[ir]);
             next_item();
-            // (threads that share rows leave together: they meet at barriers)
+            // (threads that share rows, or join parts, leave together: they meet at barriers)
             const bool stop = it.h < 0 || fail;
-            if (SHARE == 2 ? softmax_any(stop) : __any_sync(0xFFFFFFFFu, stop)) break;
+            if (SHARE == 2 || SPLIT ? softmax_any(stop) : __any_sync(0xFFFFFFFFu, stop)) break;
             const int i_row = it.first + q * TT + row / group, head = it.h * group + row % group;
             const bool real = row < TT * group && i_row < it.t.n;
             const int own0 = it.t.m - it.t.n + it.first + q * TT;      // last key of the tile's first row
@@ -428,7 +472,7 @@ prompt_tiles_kernel(const PromptParams p, const __grid_constant__ PromptMaps map
             const int n = it.n[q];
             float ref = -INFINITY, l = 0.f, run_ref = 0.f;
             for (int i = 0; i < n; ++i) {
-                const int step0 = item_step(it, i) * KT, k0 = step0 + part * KH;      // of the step, of this thread
+                const int step0 = item_step<SPLIT>(it, i) * KT, k0 = step0 + part * KH;      // of the step, of this thread
                 const int sb = NQ == 2 ? q : count & 1;
                 wait_or_fail(&s_full[sb], (NQ == 2 ? count : count >> 1) & 1, fail);
                 tmem_fence_after();
@@ -568,12 +612,32 @@ prompt_tiles_kernel(const PromptParams p, const __grid_constant__ PromptMaps map
                 l += shared_row[part ^ 1][row];
                 softmax_any(false);
             }
-            const float inv = l > 0.f ? 1.f / l : 0.f;
             if (n > 0) {
                 values_done(count - 1);
             }
             const int64_t at = (static_cast<int64_t>(it.t.lo) + i_row) * p.Hq + head;
             const float f = n > A::RUN ? ex2(run_ref - ref) : 0.f;
+            if (SPLIT && it.parts > 1) {
+                // this part's sums to the workspace, to be joined when all are through
+#pragma unroll 1
+                for (int d = 0; d < DH; d += 16) {
+                    uint32_t r[16] = {};
+                    if (n > 0) {
+                        tmem_ld16(o_mine + d, r);
+                        tmem_wait_ld();
+                    }
+                    if (real) {
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            float *const to = sums + (d + e) * 128;
+                            *to = __uint_as_float(r[e]) + (n > A::RUN ? *to * f : 0.f);
+                        }
+                    }
+                }
+                if (part == 0) stats[(static_cast<int64_t>(blockIdx.x) * NQ + q) * 128 + row] = make_float2(ref, l);
+                continue;
+            }
+            const float inv = l > 0.f ? 1.f / l : 0.f;
             // 64 channels at a time by way of shared memory: 8 lanes then write a row's 128 bytes (a thread's own row
             // by itself meets 32 lines with every store)
             const int64_t place = real && !fail ? at * D + part * DH : -1;
@@ -617,6 +681,42 @@ prompt_tiles_kernel(const PromptParams p, const __grid_constant__ PromptMaps map
             if (real && !fail && p.lse && part == 0) p.lse[at] = l > 0.f ? (ref + log2f(l)) * kLn2 : -INFINITY;
             tmem_fence_before();                      // (O is free with the next item's first weights)
         }
+        if (SPLIT) {
+            // The parts of the item, in their order: each CTA of the cluster joins its share, a warp 32 rows of 16 channels at a
+            // time.  (A CTA of a split call takes one item, which still lies in the first place.)
+            fence_acq_rel_gpu();
+            __syncwarp();
+            cluster_barrier();
+            const Item &it = items[0];
+            const bool join = !fail && it.h >= 0 && it.parts > 1;      // (else the item's fields say nothing)
+            for (int u = join ? it.part * (A::SOFTMAX / 32) + warp : NQ * 4 * (D / 16); u < NQ * 4 * (D / 16); u += it.parts * (A::SOFTMAX / 32)) {
+                const int d = u % (D / 16) * 16, q = u / (D / 16) / 4, row = u / (D / 16) % 4 * 32 + lane;
+                const int i_row = it.first + q * TT + row / group, head = it.h * group + row % group;
+                if (row >= TT * group || i_row >= it.t.n) continue;
+                const int64_t first = (static_cast<int64_t>(blockIdx.x) - it.part) * NQ + q;     // of the parts' places, NQ apart
+                const float2 *const st = stats + first * 128 + row;
+                const float *const from = reinterpret_cast<const float *>(static_cast<const uint8_t *>(p.ws) + kPromptTickets) +
+                                          (first * D + d) * 128 + row;
+                float ref = -INFINITY, l = 0.f, o[16] = {};
+                for (int s = 0; s < it.parts; ++s) ref = fmaxf(ref, __ldcg(st + s * NQ * 128).x);
+#pragma unroll 2
+                for (int s = 0; s < it.parts; ++s) {
+                    const float2 x = __ldcg(st + s * NQ * 128);
+                    const float f = x.y > 0.f ? ex2(x.x - ref) : 0.f;
+                    l += x.y * f;
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) o[e] += __ldcg(from + (static_cast<int64_t>(s) * NQ * D + e) * 128) * f;
+                }
+                const float inv = l > 0.f ? 1.f / l : 0.f;
+                const int64_t at = (static_cast<int64_t>(it.t.lo) + i_row) * p.Hq + head;
+                uint4 *const to = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.out) + at * D + d);
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+                    to[k] = make_uint4(pack_bf16(o[8 * k] * inv, o[8 * k + 1] * inv), pack_bf16(o[8 * k + 2] * inv, o[8 * k + 3] * inv),
+                                       pack_bf16(o[8 * k + 4] * inv, o[8 * k + 5] * inv), pack_bf16(o[8 * k + 6] * inv, o[8 * k + 7] * inv));
+                if (p.lse && d == 0) p.lse[at] = l > 0.f ? (ref + log2f(l)) * kLn2 : -INFINITY;
+            }
+        }
     }
     if (fail) failed = 1;
     tmem_fence_before();
@@ -636,10 +736,26 @@ prompt_tiles_kernel(const PromptParams p, const __grid_constant__ PromptMaps map
     if (warp == 0) tmem_free(s_t, 512);
 }
 
-template <int D, bool OPT> cudaError_t launch_tiles_of(const PromptParams &p, const PromptMaps &maps, cudaStream_t s)
+template <int D> void split_config(cudaLaunchConfig_t &c, cudaLaunchAttribute &a, int grid, int split, cudaStream_t s)
+{
+    a.id = cudaLaunchAttributeClusterDimension;
+    a.val.clusterDim.x = static_cast<unsigned>(split);
+    a.val.clusterDim.y = a.val.clusterDim.z = 1;
+    c = {};
+    c.gridDim = dim3(static_cast<unsigned>(grid));
+    c.blockDim = dim3(Prompt<D>::THREADS);
+    c.dynamicSmemBytes = Prompt<D>::SMEM;
+    c.stream = s;
+    c.attrs = &a;
+    c.numAttrs = 1;
+}
+
+// `split`: parts that the items' steps can be split into at most; as many are taken as let all clusters run at once
+template <int D, bool OPT, bool SPLIT> cudaError_t launch_tiles_as(const PromptParams &p, const PromptMaps &maps, int grid, int split, cudaStream_t s)
 {
     using A = Prompt<D>;
     static bool done[64] = {false};
+    static int fit[SPLIT ? 64 : 1][kMostParts + 1];            // clusters of a size that run at once
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
@@ -647,28 +763,51 @@ template <int D, bool OPT> cudaError_t launch_tiles_of(const PromptParams &p, co
     if (!done[dev]) {
         // (registers that move between warpgroups have to add up to what the launch has)
         cudaFuncAttributes a;
-        e = cudaFuncGetAttributes(&a, prompt_tiles_kernel<D, OPT>);
+        e = cudaFuncGetAttributes(&a, prompt_tiles_kernel<D, OPT, SPLIT>);
         if (e != cudaSuccess) return e;
         if (a.numRegs != A::LAUNCH_REGS) return cudaErrorInvalidConfiguration;
-        e = cudaFuncSetAttribute(prompt_tiles_kernel<D, OPT>, cudaFuncAttributeMaxDynamicSharedMemorySize, A::SMEM);
+        e = cudaFuncSetAttribute(prompt_tiles_kernel<D, OPT, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize, A::SMEM);
+        if (e == cudaSuccess && SPLIT) e = cudaFuncSetAttribute(prompt_tiles_kernel<D, OPT, SPLIT>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
         if (e != cudaSuccess) return e;
+        if (SPLIT) {
+            for (int n = 2; n <= kMostParts; ++n) {
+                cudaLaunchConfig_t c;
+                cudaLaunchAttribute a;
+                split_config<D>(c, a, n, n, s);
+                int most = 0;
+                if (cudaOccupancyMaxActiveClusters(&most, prompt_tiles_kernel<D, OPT, SPLIT>, &c) != cudaSuccess) {
+                    cudaGetLastError();               // (a size that the GPU does not have)
+                    most = 0;
+                }
+                fit[dev][n] = most;
+            }
+        }
         done[dev] = true;
     }
-    const int rows = A::NQ * (128 / (p.Hq / p.H));
-    const int64_t items = (static_cast<int64_t>(p.R_cap) / rows + p.B) * p.H;
-    const int grid = static_cast<int>(items < kPromptSms ? items : kPromptSms);
-    prompt_tiles_kernel<D, OPT><<<grid, A::THREADS, A::SMEM, s>>>(p, maps);
-    return cudaGetLastError();
+    if constexpr (SPLIT) {
+        const int items = grid;
+        while (split > 1 && fit[dev][split] < items) --split;
+        grid = items * split;
+        cudaLaunchConfig_t c;
+        cudaLaunchAttribute a;
+        split_config<D>(c, a, grid, split, s);
+        return cudaLaunchKernelEx(&c, prompt_tiles_kernel<D, OPT, SPLIT>, p, maps, split);
+    } else {
+        prompt_tiles_kernel<D, OPT, SPLIT><<<grid, A::THREADS, A::SMEM, s>>>(p, maps, split);
+        return cudaGetLastError();
+    }
 }
 
-template <bool OPT> cudaError_t launch_tiles(const PromptParams &p, const PromptMaps &maps, cudaStream_t s)
+template <bool OPT, bool SPLIT> cudaError_t launch_tiles(const PromptParams &p, const PromptMaps &maps, int grid, int split, cudaStream_t s)
 {
-    if (p.D == 64) return launch_tiles_of<64, OPT>(p, maps, s);
-    return p.D == 128 ? launch_tiles_of<128, OPT>(p, maps, s) : launch_tiles_of<256, OPT>(p, maps, s);
+    if (p.D == 64) return launch_tiles_as<64, OPT, SPLIT>(p, maps, grid, split, s);
+    return p.D == 128 ? launch_tiles_as<128, OPT, SPLIT>(p, maps, grid, split, s) : launch_tiles_as<256, OPT, SPLIT>(p, maps, grid, split, s);
 }
 
 }  // namespace
 
-cudaError_t launch_prompt_tiles_options(const PromptParams &p, const PromptMaps &maps, cudaStream_t s);
+cudaError_t launch_prompt_tiles_options(const PromptParams &p, const PromptMaps &maps, int grid, cudaStream_t s);
+cudaError_t launch_prompt_tiles_split(const PromptParams &p, const PromptMaps &maps, int grid, int split, cudaStream_t s);
+cudaError_t launch_prompt_tiles_split_options(const PromptParams &p, const PromptMaps &maps, int grid, int split, cudaStream_t s);
 
 }  // namespace specv

@@ -4,9 +4,9 @@
 
 namespace specv {
 
-cudaError_t launch_prompt_tiles_options(const PromptParams &p, const PromptMaps &maps, cudaStream_t s)
+cudaError_t launch_prompt_tiles_options(const PromptParams &p, const PromptMaps &maps, int grid, cudaStream_t s)
 {
-    return launch_tiles<true>(p, maps, s);
+    return launch_tiles<true, false>(p, maps, grid, 1, s);
 }
 
 }  // namespace specv

@@ -1,0 +1,13 @@
+// prompt_tiles_split_options.cu -- attention of a few bf16 prompts on the tensor cores with a cap, distance
+// biases or a scale that is not positive, whose items are
+// split along the keys (prompt_tiles.cuh has the kernel).
+#include "prompt_tiles.cuh"
+
+namespace specv {
+
+cudaError_t launch_prompt_tiles_split_options(const PromptParams &p, const PromptMaps &maps, int grid, int split, cudaStream_t s)
+{
+    return launch_tiles<true, true>(p, maps, grid, split, s);
+}
+
+}  // namespace specv

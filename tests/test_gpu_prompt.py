@@ -266,3 +266,74 @@ def test_long_prompts_by_samples_of_their_rows(sv, opt, D):
         res = {x: got[x][i:i + 1] for x in got}
         check(sv, q[i:i + 1], k[:upto], v[:upto], [1], [upto], got=res, **opt)
         check(sv, q[i:i + 1], k[m - n:upto], v[m - n:upto], [1], [i + 1], got={x: own[x][i:i + 1] for x in own}, **opt)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("opt", [dict(), dict(window=900, prefix=70), dict(cap=15.0, slopes=[0.01, 0.02, 0.0, 0.003], window=3000)])
+def test_few_rows_over_long_contexts(sv, opt, D):
+    """So few rows that they are split along the keys: one row, a group that does not divide a tile, tiles whose first sees fewer
+    keys than its second, rows that see nothing, a request whose keys are too few to split."""
+    rng = np.random.default_rng(27)
+    for rows, keys, Hq, H in [([1], [9001], 4, 1), ([140], [2600], 4, 4), ([70, 3, 0, 5], [5000, 90, 700, 2], 4, 2)]:
+        check(sv, rand(rng, sum(rows), Hq, D), rand(rng, sum(keys), H, D), rand(rng, sum(keys), H, D), rows, keys, **opt)
+    if "slopes" not in opt:
+        check(sv, rand(rng, 300, 3, D), rand(rng, 2500, 1, D), rand(rng, 2500, 1, D), [300], [2500], **opt)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_split_prompts_repeat_and_share_a_workspace(sv, D):
+    """The same bits every time, next to calls that are not split, captured and on another stream."""
+    rng = np.random.default_rng(29)
+    ws = sv.new_prompt_workspace(4, 1, D)
+    calls = []
+    for rows, keys in [([5], [30000]), ([900] * 30, [900] * 30), ([200], [4000]), ([2, 2], [40000, 300]), ([4], [16])]:
+        q, k, v = rand(rng, sum(rows), 4, D), rand(rng, sum(keys), 1, D), rand(rng, sum(keys), 1, D)
+        args = (q, k, v, i32(offsets(rows)))
+        want = sv.prompt_attend(*args, B=len(rows), cu_keys=i32(offsets(keys)))
+        calls.append((sv.prompt_attend(*args, B=len(rows), cu_keys=i32(offsets(keys)), workspace=ws, prepared=True), want))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for call, _ in calls:
+        call(stream=side)
+    side.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        held = [call() for call, _ in calls]
+    for _ in range(5):
+        for res in held:
+            for x in res.values():
+                x.fill_(0)
+        g.replay()
+        for res, (_, want) in zip(held, calls):
+            assert torch.equal(res["out"], want["out"]) and torch.equal(res["lse"], want["lse"])
+    long = [sv.prompt_attend(q[:1], k, v, i32([0, 1]), B=1, cu_keys=i32([0, 300])) for _ in range(20)]
+    assert all(torch.equal(x["out"], long[0]["out"]) for x in long)
+
+
+def test_malformed_offsets_of_split_prompts(sv):
+    rng = np.random.default_rng(31)
+    q, k, v = rand(rng, 60, 2, 64), rand(rng, 5000, 1, 64), rand(rng, 5000, 1, 64)
+    good = check(sv, q, k, v, [20, 40], [2500, 2500])
+    for cu, cuk, is_status in [([0, 20, 61], [0, 2500, 5000], 0x10), ([0, 20, 60], [0, 2500, 5001], 0x800), ([0, 20, 10], [0, 2500, 5000], 0x10)]:
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        got = sv.prompt_attend(q, k, v, i32(cu), B=2, cu_keys=i32(cuk), status=status)
+        assert int(status) == is_status and torch.equal(got["out"][:20], good["out"][:20])
+        if is_status == 0x800:
+            assert bool((got["out"][20:] == 0).all()) and bool((got["lse"][20:] == float("-inf")).all())
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_split_prompts_with_fewer_items_than_could_be(sv, D):
+    """Requests and rows of a padded batch leave whole groups of CTAs without an item."""
+    rng = np.random.default_rng(33)
+    rows, keys, R = [1, 1, 0, 21, 3, 105], [90, 2, 0, 3000, 90, 2500], 300
+    q, k, v = rand(rng, R, 3, D), rand(rng, 8000, 1, D), rand(rng, 8000, 1, D)
+    for opt in (dict(), dict(cap=20.0), dict(window=2000, prefix=3)):
+        check(sv, q, k, v, rows, keys, **opt)
+    check(sv, q, k, v, [0, 0, 0, 0, 0, 1], [9, 0, 5, 0, 0, 2000])
+    none = sv.prompt_attend(q, k, v, i32([0, 0, 0]), B=2, cu_keys=i32([0, 3000, 8000]), prepared=True)
+    res = none()
+    for x in res.values():
+        x.fill_(5)
+    none()
+    assert all(bool((x == 5).all()) for x in res.values())
