@@ -66,7 +66,8 @@ SPEC_API size_t spec_prompt_workspace_bytes(int32_t Hq, int32_t H, int32_t D, in
  * bf16: products of bf16 in fp32, weights rounded to bf16 (8 bits) before they meet the values,
  * their sums, and so lse, in fp32.  They run on the tensor cores where q, k and v start on 16 bytes, their
  * strides are positive multiples of 16 bytes, out starts on 16 bytes and Hq / H is at most 128; on the CUDA
- * cores, many times slower, elsewhere, then with weights in fp32.  f32: fp32 throughout.
+ * cores, many times slower, elsewhere, then with weights in fp32.  f32: fp32 throughout.  On the CUDA cores the sums of
+ * weights and of values lose at most 2^-17 of their terms' magnitudes to roundings, over any number of keys.
  */
 SPEC_API int spec_prompt_attend(const spec_prompt *prompt, void *out, float *lse, void *workspace,
                                 size_t workspace_bytes, spec_stream stream);

@@ -2,12 +2,17 @@
 // fp32 rows, and bf16 rows that the tensor memory accelerator cannot fetch.
 //
 // A CTA takes 64 packed rows of a kv head and walks over the keys, 64 at a time:
-//     S = Q K^T c,  P = 2^(S - m),  O += P V,  m the rows' running maximum.
+//     S = Q K^T c,  P = 2^(S - m),  O += P V,  m a reference per row that moves when a score passes it by 2.
+// Sums run over up to 2^24 keys.  Added one after another they would lose up to keys x 2^-24 of themselves, and do where weights
+// and values are alike (1e-2 at 2^20 keys); so a tile's sum goes to the total by a sum that keeps its error (Knuth's), and the error
+// begins the next tile's sum: 64 terms' roundings are left, whatever the number of keys.  References that move by a factor of 2 or more
+// keep the roundings of rescaling a geometric series.
 // 16 x 16 threads hold 4 x 4 scores and 4 x D/16 results each in registers; Q, K, V and P lie
 // in shared memory as fp32, rows 4 words apart in their banks, so that the 8 lanes of a 16-byte
 // load meet 32 different ones.  fp32 keys and values come by asynchronous copies, a tile ahead.
 // Bound by those loads (12 an SM's clock for 32 packed products): 4 prompts of 2000 tokens, 16 / 4 heads of 128, fp32, take
-// 2.1 ms, 31 TFLOP/s of visible pairs; 5 small ones (up to 700 tokens, 12 heads of 64) 83 us.
+// 2.02 ms, 32 TFLOP/s of visible pairs (2.15 with one sum a channel, rescaled with every tile); of 64 channels 1.06 (1.01).  As bf16 in
+// rows that TMA cannot fetch 2.73 ms, where the tensor cores take 0.075.
 #include "attend.cuh"
 #include "prompt.cuh"
 
@@ -16,6 +21,24 @@ namespace specv {
 namespace {
 
 constexpr int kRows = 64, kKeys = 64, kRowThreads = 256;
+constexpr float kMove = 1.f;                          // log2 units a score may pass the reference by
+
+// total += sum; sum = what that rounded away
+__device__ __forceinline__ void to_total(float &total, float &sum)
+{
+    const float t = __fadd_rn(total, sum), z = __fsub_rn(t, total);
+    sum = __fadd_rn(__fsub_rn(total, __fsub_rn(t, z)), __fsub_rn(sum, z));
+    total = t;
+}
+
+__device__ __forceinline__ void to_total(uint64_t &total, uint64_t &sum)
+{
+    const uint64_t minus = f2_pack(-1.f, -1.f);
+    const auto sub = [&](uint64_t a, uint64_t b) { return f2_fma(b, minus, a); };
+    const uint64_t t = f2_add(total, sum), z = sub(t, total);
+    sum = f2_add(sub(total, sub(t, z)), sub(sum, z));
+    total = t;
+}
 
 template <int D> constexpr int row_words = D + 4;
 // keys and values lie twice where there is room: the next ones are fetched beside the arithmetic
@@ -78,17 +101,17 @@ __global__ void __launch_bounds__(kRowThreads) prompt_rows_kernel(const PromptPa
         return r < count ? static_cast<const T *>(p.q) + static_cast<int64_t>(t.lo + row_of(r)) * p.q_row + head_of(r) * p.q_head : nullptr;
     });
     int own[4];                                       // last key that each of this thread's rows sees
-    float slope[4], m[4], l[4];
-    uint64_t o[4][OC / 2];
+    float slope[4], m[4], l[4], l_all[4];             // l, o: of the tile, from what the totals lack on
+    uint64_t o[4][OC / 2], o_all[4][OC / 2];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int r = ty * 4 + i;
         own[i] = r < count ? own0 + row_of(r) : -1;
         slope[i] = p.slopes && r < count ? p.slopes[head_of(r)] * kLog2e : 0.f;
         m[i] = -INFINITY;
-        l[i] = 0.f;
+        l[i] = l_all[i] = 0.f;
 #pragma unroll
-        for (int j = 0; j < OC / 2; ++j) o[i][j] = 0;
+        for (int j = 0; j < OC / 2; ++j) o[i][j] = o_all[i][j] = 0;
     }
     // keys that some row of the tile sees: up to the last row's own, a window's from the first row's on
     // (those that no row of the request sees are taken as zeros, whatever they hold)
@@ -162,18 +185,26 @@ __global__ void __launch_bounds__(kRowThreads) prompt_rows_kernel(const PromptPa
             }
 #pragma unroll
             for (int x = 8; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, x));
-            top = fmaxf(top, m[i]);
-            const float ref = top == -INFINITY ? 0.f : top, f = exp2f(m[i] - ref);
-            m[i] = top;
-            l[i] *= f;
+            if (top > m[i] + kMove) {
+                const float f = exp2f(m[i] - top);
+                const uint64_t f2 = f2_pack(f, f);
+                m[i] = top;
+                l[i] *= f;
+                l_all[i] *= f;
 #pragma unroll
-            for (int j = 0; j < OC / 2; ++j) o[i][j] = f2_fma(o[i][j], f2_pack(f, f), 0);
+                for (int j = 0; j < OC / 2; ++j) {
+                    o[i][j] = f2_fma(o[i][j], f2, 0);
+                    o_all[i][j] = f2_fma(o_all[i][j], f2, 0);
+                }
+            }
+            const float ref = m[i] == -INFINITY ? 0.f : m[i];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const float w = exp2f(s[j] - ref);
                 l[i] += w;
                 ps[(ty * 4 + i) * PW + tx + 16 * j] = w;
             }
+            to_total(l_all[i], l[i]);
         }
         __syncwarp();                                 // (a warp's rows are its own)
 #pragma unroll 2
@@ -196,9 +227,14 @@ __global__ void __launch_bounds__(kRowThreads) prompt_rows_kernel(const PromptPa
                 }
             }
         }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < OC / 2; ++j) to_total(o_all[i][j], o[i][j]);
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
+        l[i] += l_all[i];
 #pragma unroll
         for (int x = 8; x > 0; x >>= 1) l[i] += __shfl_xor_sync(0xFFFFFFFFu, l[i], x);
         const int r = ty * 4 + i;
@@ -211,7 +247,7 @@ __global__ void __launch_bounds__(kRowThreads) prompt_rows_kernel(const PromptPa
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 float x, y;
-                f2_unpack(o[i][2 * j + e], x, y);
+                f2_unpack(f2_add(o_all[i][2 * j + e], o[i][2 * j + e]), x, y);
                 to[j * 64 + tx * 4 + 2 * e] = from_f32<T>(x * inv);
                 to[j * 64 + tx * 4 + 2 * e + 1] = from_f32<T>(y * inv);
             }
