@@ -19,7 +19,7 @@
 // Bound by the tensor cores: one prompt of 20011 tokens, 32 / 8 heads of 128, takes 1944 us (1.69 PFLOP/s of visible pairs,
 // 0.88 of the measured matrix rate; the pipe is active 72 % of the time), one of 8192 tokens and 40 / 8 heads 441.  An item costs
 // about 3 us beside its steps, so that 16 ragged prompts of up to 4096 tokens (35 items a CTA) are at 709 us, 0.67.  D = 64 has half
-// the products for as many weights: 295 us for 8192 tokens of 32 / 8 heads, 0.49.  Distance biases cost 657 us for 441,
+// the products for as many weights: 301 us for 8192 tokens of 32 / 8 heads, 0.48.  Distance biases cost 657 us for 441,
 // caps 788 (more instructions a score than the products leave time for).
 #pragma once
 
@@ -470,7 +470,7 @@ prompt_tiles_kernel(const PromptParams p, const __grid_constant__ PromptMaps map
             const int own = it.t.m - it.t.n + i_row;
             const float slope = OPT && p.slopes && real ? p.slopes[head] * kLog2e : 0.f;
             const int n = it.n[q];
-            float ref = -INFINITY, l = 0.f, run_ref = 0.f;
+            float ref = -INFINITY, l = 0.f, l_low = 0.f, run_ref = 0.f;       // (l_low: what l lacks)
             for (int i = 0; i < n; ++i) {
                 const int step0 = item_step<SPLIT>(it, i) * KT, k0 = step0 + part * KH;      // of the step, of this thread
                 const int sb = NQ == 2 ? q : count & 1;
@@ -564,6 +564,7 @@ prompt_tiles_kernel(const PromptParams p, const __grid_constant__ PromptMaps map
                     const float to = move ? most : ref, f = move ? ex2(ref - to) : 1.f;
                     ref = to;
                     l *= f;
+                    l_low *= f;
                     if (!fresh) {
                         values_done(count - 1);
 #pragma unroll 1
@@ -597,7 +598,11 @@ prompt_tiles_kernel(const PromptParams p, const __grid_constant__ PromptMaps map
                 }
                 float x, y;
                 f2_unpack(sum, x, y);
-                l += x + y;
+                // (a step's weights to l with the error kept: up to 2^18 steps, whose roundings go one way where weights are alike)
+                l_low += x + y;
+                const float l_new = __fadd_rn(l, l_low);
+                l_low = __fsub_rn(l_low, __fsub_rn(l_new, l));
+                l = l_new;
                 tmem_wait_st();
                 tmem_fence_before();
                 __syncwarp();
@@ -605,6 +610,7 @@ prompt_tiles_kernel(const PromptParams p, const __grid_constant__ PromptMaps map
                 ++count;
             }
             // the tile's results
+            l += l_low;
             if (SHARE == 2) {
                 softmax_any(false);
                 shared_row[part][row] = l;

@@ -110,3 +110,12 @@ def test_one_key_many_times(sv, dtype):
         assert (got["lse"][i].double() - lse).abs().max() <= WEIGHT + 70 * U + 4 * U * lse
         err = ((got["out"][i].double() - v[0].double()).abs() / v[0].double()).max()
         assert float(err) <= 2 * (WEIGHT + 70 * U) + 3 * U + 1.01 * HALF[dtype], float(err)
+
+
+@pytest.mark.parametrize("kind,D", [("first", 64), ("first", 128), ("waves", 64), ("first", 256)])
+def test_sums_of_prompts_on_the_tensor_cores(sv, kind, D):
+    """So many rows that their keys are not split."""
+    m, n = 1048583, 77 * (128 if D == 256 else 256)
+    q, k, v = inputs(scores_of(kind, m), D, n, torch.bfloat16)
+    got = sv.prompt_attend(q, k, v, i32([0, n]), B=1, cu_keys=i32([0, m]), scale=1.0)
+    check(got, k, v, [0, 1, n - 1], n, 90 * U, 2.0 ** -8 + 2.0 ** -13)
