@@ -109,7 +109,7 @@ typedef struct {
     const int32_t *len;        /* [B] tokens in the cache, this step's rows included          */
     int32_t max_len;           /* host-known bound on len (0: max_pages * page_tokens)        */
     float scale;               /* of q . k, finite                                            */
-    float cap;                 /* > 0: s = cap * tanh(s / cap); 0: off                        */
+    float cap;                 /* > 0: s = cap * tanh(s / cap) (above 2^120: as 2^120); 0: off */
     const float *slopes;       /* [Hq] or NULL: s -= slope * (pos_row - pos_slot)             */
     int32_t window;            /* > 0: only slots with pos_row - pos_slot < window ...        */
     int32_t prefix;            /* ... or slot < prefix                                        */

@@ -38,7 +38,7 @@ typedef struct {
     const int32_t *cu_rows;    /* [B+1]                                                       */
     const int32_t *cu_keys;    /* [B+1] or NULL: cu_rows                                      */
     float scale;               /* of q . k, finite                                            */
-    float cap;                 /* > 0: s = cap * tanh(s / cap); 0: off                        */
+    float cap;                 /* > 0: s = cap * tanh(s / cap) (above 2^120: as 2^120); 0: off */
     const float *slopes;       /* [Hq] or NULL: s -= slope * (row's key - key)                */
     int32_t window;            /* > 0: only keys less than `window` before the row's own ...   */
     int32_t prefix;            /* ... or among the first `prefix`                             */

@@ -227,6 +227,10 @@ int run_cache_rows(const spec_cache *cache, const spec_cache_rows *r, bool appen
 
 bool finite_f32(float x) { return x - x == 0.f; }
 
+// The kernels take a cap times log2 e, which has to stay finite, and the reciprocal of that, which has to keep its bits: a cap
+// above 2^120 counts as 2^120 (scores below 2^108 come out the same under either).
+float fit_cap(float cap) { return std::fmin(cap, 0x1p120f); }
+
 int check_prompt(const spec_prompt *a, PromptParams &p)
 {
     if (!a || !a->q || !a->k || !a->v || !a->cu_rows) return SPEC_ERR_INVALID_ARG;
@@ -263,7 +267,7 @@ int check_prompt(const spec_prompt *a, PromptParams &p)
     p.cu_rows = a->cu_rows;
     p.cu_keys = a->cu_keys;
     p.scale = a->scale;
-    p.cap = a->cap;
+    p.cap = fit_cap(a->cap);
     p.slopes = a->slopes;
     // (no key lies further before a row, nor further from the first: sums of these stay in 32 bits)
     p.window = a->window < kMostSlots ? a->window : kMostSlots;
@@ -306,7 +310,7 @@ int check_attention(const spec_cache *cache, const spec_attention *a, CacheView 
     p.max_len = a->max_len ? a->max_len : static_cast<int32_t>(room);
     p.scale = a->scale;
     p.scale_log2 = static_cast<float>(std::fabs(static_cast<double>(a->scale)) * 1.4426950408889634);
-    p.cap = a->cap;
+    p.cap = fit_cap(a->cap);
     p.slopes = a->slopes;
     p.window = a->window;
     // no slot lies beyond room: a prefix of any size stays clear of 2^31 in the kernels' sums
