@@ -108,7 +108,7 @@ typedef struct {
     const int32_t *cu_rows;    /* [B+1]                                                       */
     const int32_t *len;        /* [B] tokens in the cache, this step's rows included          */
     int32_t max_len;           /* host-known bound on len (0: max_pages * page_tokens)        */
-    float scale;               /* of q . k, finite                                            */
+    float scale;               /* of q . k; finite, and so times log2(e)                      */
     float cap;                 /* > 0: s = cap * tanh(s / cap) (above 2^120: as 2^120); 0: off */
     const float *slopes;       /* [Hq] or NULL: s -= slope * (pos_row - pos_slot)             */
     int32_t window;            /* > 0: only slots with pos_row - pos_slot < window ...        */

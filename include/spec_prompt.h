@@ -37,7 +37,7 @@ typedef struct {
                                   most SPEC_PROMPT_MOST_KEYS                                   */
     const int32_t *cu_rows;    /* [B+1]                                                       */
     const int32_t *cu_keys;    /* [B+1] or NULL: cu_rows                                      */
-    float scale;               /* of q . k, finite                                            */
+    float scale;               /* of q . k; finite, and so times log2(e)                      */
     float cap;                 /* > 0: s = cap * tanh(s / cap) (above 2^120: as 2^120); 0: off */
     const float *slopes;       /* [Hq] or NULL: s -= slope * (row's key - key)                */
     int32_t window;            /* > 0: only keys less than `window` before the row's own ...   */

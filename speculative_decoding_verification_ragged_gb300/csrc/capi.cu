@@ -231,13 +231,16 @@ bool finite_f32(float x) { return x - x == 0.f; }
 // above 2^120 counts as 2^120 (scores below 2^108 come out the same under either).
 float fit_cap(float cap) { return std::fmin(cap, 0x1p120f); }
 
+// Scales are taken times log2 e as well: one that leaves fp32 then would turn a score of 0 into NaN.
+bool fit_scale(float scale) { return finite_f32(scale * kLog2e); }
+
 int check_prompt(const spec_prompt *a, PromptParams &p)
 {
     if (!a || !a->q || !a->k || !a->v || !a->cu_rows) return SPEC_ERR_INVALID_ARG;
     if (a->dtype != SPEC_F32 && a->dtype != SPEC_BF16) return SPEC_ERR_UNSUPPORTED;
     if (a->H < 1 || a->Hq < 1 || a->Hq % a->H || a->B < 1 || a->R_cap < 1 || a->K_cap < 1 || a->window < 0 || a->prefix < 0)
         return SPEC_ERR_INVALID_ARG;
-    if (!finite_f32(a->scale) || !finite_f32(a->cap) || a->cap < 0.f) return SPEC_ERR_INVALID_ARG;
+    if (!fit_scale(a->scale) || !finite_f32(a->cap) || a->cap < 0.f) return SPEC_ERR_INVALID_ARG;
     const size_t elt = elt_bytes(a->dtype);
     for (const void *x : {a->q, a->k, a->v})
         if (reinterpret_cast<uintptr_t>(x) % elt) return SPEC_ERR_INVALID_ARG;
@@ -288,7 +291,7 @@ int check_attention(const spec_cache *cache, const spec_attention *a, CacheView 
     if (a->Hq < 1 || a->Hq % c.H || a->R_cap < 1 || a->k_max < 0 || a->window < 0 || a->prefix < 0)
         return SPEC_ERR_INVALID_ARG;
     if (a->k_max > 31 || a->Hq > kMostHeads) return SPEC_ERR_UNSUPPORTED;
-    if (!(a->scale - a->scale == 0.f) || !(a->cap >= 0.f) || !(a->cap - a->cap == 0.f))
+    if (!fit_scale(a->scale) || !(a->cap >= 0.f) || !(a->cap - a->cap == 0.f))
         return SPEC_ERR_INVALID_ARG;
     const int64_t room = static_cast<int64_t>(c.max_pages) * c.page_tokens;
     if (a->max_len < 0 || a->max_len > room) return SPEC_ERR_INVALID_ARG;
