@@ -519,11 +519,12 @@ prompt_tiles_kernel(const PromptParams p, const __grid_constant__ PromptMaps map
                         for (int e = 0; e < KH / 2; ++e) f2_unpack(f2_fma(f2_pack(s[2 * e], s[2 * e + 1]), c2, 0), s[2 * e], s[2 * e + 1]);
                     }
                     if (p.slopes) {
-                        const float far = -slope * static_cast<float>(own - k0);
-                        const uint64_t far2 = f2_pack(far, far), slope2 = f2_pack(slope, slope);
+                        // (the distance first, which is exact: the row's own key has no bias, however steep the slope)
+                        const float at = -static_cast<float>(own - k0);
+                        const uint64_t at2 = f2_pack(at, at), slope2 = f2_pack(slope, slope);
 #pragma unroll
                         for (int e = 0; e < KH / 2; ++e)
-                            f2_unpack(f2_add(f2_pack(s[2 * e], s[2 * e + 1]), f2_fma(slope2, f2_pack(2.f * e, 2.f * e + 1.f), far2)),
+                            f2_unpack(f2_fma(slope2, f2_add(f2_pack(2.f * e, 2.f * e + 1.f), at2), f2_pack(s[2 * e], s[2 * e + 1])),
                                       s[2 * e], s[2 * e + 1]);
                     }
                 }
