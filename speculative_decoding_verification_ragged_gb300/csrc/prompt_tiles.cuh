@@ -23,6 +23,8 @@
 // caps 788 (more instructions a score than the products leave time for).
 #pragma once
 
+#include <atomic>
+
 #include "attend.cuh"
 #include "prompt.cuh"
 
@@ -761,13 +763,14 @@ template <int D> void split_config(cudaLaunchConfig_t &c, cudaLaunchAttribute &a
 template <int D, bool OPT, bool SPLIT> cudaError_t launch_tiles_as(const PromptParams &p, const PromptMaps &maps, int grid, int split, cudaStream_t s)
 {
     using A = Prompt<D>;
-    static bool done[64] = {false};
-    static int fit[SPLIT ? 64 : 1][kMostParts + 1];            // clusters of a size that run at once
+    // (the table decides in how many parts a call is split, and with that its bits: a thread that finds `done` finds the table too)
+    static std::atomic<bool> done[64];
+    static std::atomic<int> fit[SPLIT ? 64 : 1][kMostParts + 1];           // clusters of a size that run at once
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    if (!done[dev]) {
+    if (!done[dev].load(std::memory_order_acquire)) {
         // (registers that move between warpgroups have to add up to what the launch has)
         cudaFuncAttributes a;
         e = cudaFuncGetAttributes(&a, prompt_tiles_kernel<D, OPT, SPLIT>);
@@ -786,14 +789,14 @@ template <int D, bool OPT, bool SPLIT> cudaError_t launch_tiles_as(const PromptP
                     cudaGetLastError();               // (a size that the GPU does not have)
                     most = 0;
                 }
-                fit[dev][n] = most;
+                fit[dev][n].store(most, std::memory_order_relaxed);
             }
         }
-        done[dev] = true;
+        done[dev].store(true, std::memory_order_release);
     }
     if constexpr (SPLIT) {
         const int items = grid;
-        while (split > 1 && fit[dev][split] < items) --split;
+        while (split > 1 && fit[dev][split].load(std::memory_order_relaxed) < items) --split;
         grid = items * split;
         cudaLaunchConfig_t c;
         cudaLaunchAttribute a;
