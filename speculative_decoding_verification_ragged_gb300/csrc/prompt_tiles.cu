@@ -63,12 +63,15 @@ cudaError_t launch_prompt(const PromptParams &p, int dtype, cudaStream_t s)
 {
     const int group = p.Hq / p.H;
     PromptMaps maps;
-    // bf16 goes to the tensor cores where TMA can fetch it and a tile holds the heads of a row; else by the CUDA cores
+    // bf16 goes to the tensor cores where TMA can fetch it, a tile holds the heads of a row and the kernel was built as it has to be; else
+    // to the CUDA cores
     if (dtype == SPEC_BF16 && group <= 128 && reinterpret_cast<uintptr_t>(p.out) % 16 == 0 &&
         map_of(&maps.q, p.q, p.q_aligned, p.D, p.Hq, p.R_cap, p.q_head, p.q_row, group, 128 / group) &&
         map_of(&maps.k, p.k, p.k_aligned, p.D, p.H, p.K_cap, p.k_head, p.k_row, 1, p.D == 256 ? 64 : 128) &&
-        map_of(&maps.v, p.v, p.v_aligned, p.D, p.H, p.K_cap, p.v_head, p.v_row, 1, p.D == 256 ? 64 : 128))
-        return launch_prompt_tiles(p, maps, s);
+        map_of(&maps.v, p.v, p.v_aligned, p.D, p.H, p.K_cap, p.v_head, p.v_row, 1, p.D == 256 ? 64 : 128)) {
+        const cudaError_t e = launch_prompt_tiles(p, maps, s);
+        if (e != cudaErrorNotSupported) return e;
+    }
     return launch_prompt_rows(p, dtype, s);
 }
 

@@ -759,7 +759,8 @@ template <int D> void split_config(cudaLaunchConfig_t &c, cudaLaunchAttribute &a
     c.numAttrs = 1;
 }
 
-// `split`: parts that the items' steps can be split into at most; as many are taken as let all clusters run at once
+// `split`: parts that the items' steps can be split into at most; as many are taken as let all clusters run at once.
+// cudaErrorNotSupported: a compiler gave the kernel other registers than its warpgroups share out.
 template <int D, bool OPT, bool SPLIT> cudaError_t launch_tiles_as(const PromptParams &p, const PromptMaps &maps, int grid, int split, cudaStream_t s)
 {
     using A = Prompt<D>;
@@ -771,11 +772,11 @@ template <int D, bool OPT, bool SPLIT> cudaError_t launch_tiles_as(const PromptP
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     if (!done[dev].load(std::memory_order_acquire)) {
-        // (registers that move between warpgroups have to add up to what the launch has)
+        // (registers that move between warpgroups have to add up to what the launch has, or their warps would wait for ever)
         cudaFuncAttributes a;
         e = cudaFuncGetAttributes(&a, prompt_tiles_kernel<D, OPT, SPLIT>);
         if (e != cudaSuccess) return e;
-        if (a.numRegs != A::LAUNCH_REGS) return cudaErrorInvalidConfiguration;
+        if (a.numRegs != A::LAUNCH_REGS) return cudaErrorNotSupported;
         e = cudaFuncSetAttribute(prompt_tiles_kernel<D, OPT, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize, A::SMEM);
         if (e == cudaSuccess && SPLIT) e = cudaFuncSetAttribute(prompt_tiles_kernel<D, OPT, SPLIT>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
         if (e != cudaSuccess) return e;
