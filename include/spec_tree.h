@@ -107,7 +107,8 @@ typedef struct {
  * allows nothing comes out as -inf alone.  Rows >= cu_rows[B], and those of a malformed
  * request (n_b < 0, n_b > k_max + 1, rows outside [0, R_cap]: SPEC_STATUS_BAD_ROWS), are not
  * written; an n_tokens out of range counts as 0 (SPEC_STATUS_BAD_LENGTH).
- * One launch; the logits are read and written once.
+ * One launch: the rows are copied and masked in one pass (in place only those with a mask), and the
+ * columns that have a token's count or a bias are read and written once more.
  */
 SPEC_API int spec_adjust_logits(const spec_logit_rules *rules, void *out, int64_t out_ld,
                                 spec_stream stream);
