@@ -14,14 +14,13 @@ namespace specv {
 
 // A tile of a request's packed rows.
 struct PromptTile {
-    int b, lo, n;               // request, its first packed row, its rows
-    int k_lo, m;                // its first key, its keys
+    int lo, n;                  // its request's first packed row and rows
+    int k_lo, m;                // and its first key and keys
 };
 
 // Rows and keys of request b: false where it has no rows.  Malformed keys count as none.
 __device__ __forceinline__ bool prompt_request(const PromptParams &p, int b, uint32_t *status, PromptTile &t)
 {
-    t.b = b;
     if (!request_rows(p.cu_rows, b, p.R_cap, p.R_cap, status, t.lo, t.n) || t.n == 0) return false;
     t.k_lo = p.cu_keys ? p.cu_keys[b] : t.lo;
     const int64_t m = p.cu_keys ? static_cast<int64_t>(p.cu_keys[b + 1]) - t.k_lo : t.n;

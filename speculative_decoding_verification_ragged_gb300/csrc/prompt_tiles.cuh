@@ -255,7 +255,6 @@ prompt_tiles_kernel(const PromptParams p, const __grid_constant__ PromptMaps map
                     const uint32_t hit = __ballot_sync(0xFFFFFFFFu, at - mine <= line && line < at);
                     if (hit) {
                         const int from = __ffs(hit) - 1;
-                        it.t.b = b0 + from;
                         it.t.lo = __shfl_sync(0xFFFFFFFFu, t.lo, from);
                         it.t.n = __shfl_sync(0xFFFFFFFFu, t.n, from);
                         it.t.k_lo = __shfl_sync(0xFFFFFFFFu, t.k_lo, from);

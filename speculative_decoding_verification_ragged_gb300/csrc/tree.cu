@@ -75,16 +75,6 @@ constexpr int kListed = 1024, kListedBiased = 2 * kNear;      // touched columns
 template <typename T> struct LogitElt;
 template <> struct LogitElt<__nv_bfloat16> {
     static constexpr int VEC = 8;
-    static __device__ __forceinline__ void unpack(uint4 v, float (&x)[8]) { Elt<uint16_t>::unpack(v, x); }
-    static __device__ __forceinline__ uint4 pack(const float (&x)[8])
-    {
-        uint4 v;
-        uint32_t *w = &v.x;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(x[2 * i + 1]), "f"(x[2 * i]));
-        return v;
-    }
     // -inf where `may` has a bit clear
     static __device__ __forceinline__ void hide(uint4 &v, uint32_t may)
     {
@@ -98,11 +88,6 @@ template <> struct LogitElt<__nv_bfloat16> {
 };
 template <> struct LogitElt<float> {
     static constexpr int VEC = 4;
-    static __device__ __forceinline__ void unpack(uint4 v, float (&x)[4]) { Elt<float>::unpack(v, x); }
-    static __device__ __forceinline__ uint4 pack(const float (&x)[4])
-    {
-        return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
-    }
     static __device__ __forceinline__ void hide(uint4 &v, uint32_t may)
     {
         uint32_t *w = &v.x;
