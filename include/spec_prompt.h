@@ -58,10 +58,11 @@ SPEC_API size_t spec_prompt_workspace_bytes(int32_t Hq, int32_t H, int32_t D, in
  * cu_keys (SPEC_STATUS_BAD_LENGTH).  out [R_cap, Hq, D] and lse [R_cap, Hq] or NULL, both
  * contiguous; rows >= cu_rows[B], and those of a request with malformed cu_rows
  * (SPEC_STATUS_BAD_ROWS), are not written; where offsets go back, so that rows lie in two requests, those may hold either's
- * results or be left.  Keys and values that no row of their request
+ * results or be left, and rows of the requests after them may be left too.  Keys and values that no row of their request
  * sees may hold anything; those that one of its rows sees have to be finite, as have
  * the queries (a row of another request never notices).  The scores have to stay within
- * fp32.  Results do not depend on the order in which blocks run.
+ * fp32.  Results do not depend on the order in which blocks run; into how many parts a bf16 row's keys are split goes by B, R_cap, K_cap,
+ * the heads, D, the options and the GPU, so that its last bits can be others in a padded or a larger batch.
  * out and lse must not overlap the inputs.
  * bf16: products of bf16 in fp32, weights rounded to bf16 (8 bits) before they meet the values,
  * their sums, and so lse, in fp32.  They run on the tensor cores where q, k and v start on 16 bytes, their
