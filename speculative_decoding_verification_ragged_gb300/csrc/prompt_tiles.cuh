@@ -16,11 +16,15 @@
 // the next step's S runs beside this step's weights; two threads share a row, half of a step's keys each, and half of the
 // channels of O (one thread a row: 540 us where two take 244, 6 pieces of up to 1000 rows with a cap and a window).
 //
-// Bound by the tensor cores: one prompt of 20011 tokens, 32 / 8 heads of 128, takes 1944 us (1.69 PFLOP/s of visible pairs,
-// 0.88 of the measured matrix rate; the pipe is active 72 % of the time), one of 8192 tokens and 40 / 8 heads 441.  An item costs
-// about 3 us beside its steps, so that 16 ragged prompts of up to 4096 tokens (35 items a CTA) are at 709 us, 0.67.  D = 64 has half
-// the products for as many weights: 301 us for 8192 tokens of 32 / 8 heads, 0.48.  Distance biases cost 657 us for 441,
-// caps 788 (more instructions a score than the products leave time for).
+// Bound by the tensor cores: one prompt of 20011 tokens, 32 / 8 heads of 128, takes 1944 to 2049 us from run to run (1.69 to 1.60
+// PFLOP/s of visible pairs, 0.88 to 0.83 of the measured matrix rate), one of 8192 tokens and 40 / 8 heads 427 (its pipe is active
+// 72 % of the time).  An item costs about 3 us beside its steps, 1.4 of them the softmax warps' own writing of the results while the
+// next scores lie ready, so that 16 ragged prompts of up to 4096 tokens (35 items a CTA) are at 709 to 755 us, 0.67 to 0.63, and 65535 prompts
+// of one row, 8 heads of 64, at 9.9 ms.  Elsewhere no unit is full, and the chain of a row's thread (scores from tensor memory,
+// weights, weights to tensor memory) with two such warps a scheduler is the bound: at D = 64, which has half the
+// products for as many weights, 301 us for 8192 tokens of 32 / 8 heads, 0.48 (tensor pipe 36 % active, special functions 33 %, issue 42 %);
+// distance biases 664 us for 427 (41, 21, 48 %), caps 795 (35, 18, 45 %; the FMA pipe 50 %).  D = 64 and 128 spill some 50 bytes a
+// thread at 168 registers, with options 100 to 115.
 #pragma once
 
 #include <atomic>

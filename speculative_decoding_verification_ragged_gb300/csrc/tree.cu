@@ -60,7 +60,8 @@ __global__ void __launch_bounds__(kAcceptWarps * 32) tree_accept_kernel(const Tr
 // rate), and by what a CTA does beside that (history, list, touched columns), a chain of loads that five CTAs an SM do not hide:
 // 96 us with histories of 4096 tokens and every second row masked (0.61).  A slice of 8192 columns: every slice reads the
 // history again, so that half of it took 120 us, and fewer CTAs have less in flight, so that twice took 105 and four times 117
-// (60000 tokens, one row of 64 requests: 93, 172, 83, 81).  Tried as well: four of the CTA's warps counting while the others
+// (60000 tokens, one row of 64 requests: 93, 172, 83, 81).  Each call alone over a cold L2: 117 us; in place 93, and 68
+// without masks, where only touched columns are read and written.  Tried as well: four of the CTA's warps counting while the others
 // stream (105), a cluster that shares the history by distributed atomics (128, frequent tokens meet there), vectors of a row
 // ahead of the stores (120: registers for fewer CTAs), six CTAs an SM (119: fewer loads in flight in each).
 //
@@ -368,7 +369,7 @@ __global__ void __launch_bounds__(kLogitThreads) adjust_logits_kernel(const Logi
             if (at >= 0 && at < listed) s.column[at] = static_cast<uint16_t>(tid * 32 + __ffs(left) - 1);
         if (many) {
             // Too many biases to compare every column with each: every bias goes to its column's sum, those of a column that has
-            // several one after another (5 rows of 152064, a bias a column: 2.4 ms, 166 by comparing; two a column: 10).
+            // several one after another (5 rows of 152064, a bias a column: 2.4 ms, 166 by comparing; two a column: 10 to 16).
             s.bias_sum[tid] = s.bias_sum[tid + kNear] = 0.f;
             __syncthreads();
             // the place in the list of a bias on column `id`, and whether the column has others, or -1

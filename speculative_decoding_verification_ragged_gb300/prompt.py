@@ -41,7 +41,8 @@ def prompt_attend(q, k, v, cu_rows, *, B: int, cu_keys=None, scale: Optional[flo
     """spec_prompt_attend: causal softmax attention of the packed prompts q [R_cap, Hq, D]
     over their own keys and values k, v [K_cap, H, D].  With cu_keys a request has keys
     cu_keys[b] .., and its rows are the last of them.  scale defaults to 1/sqrt(D); cap,
-    slopes, window and prefix as in spec_prompt.h.  Returns {"out" [R_cap, Hq, D],
+    slopes, window and prefix as in spec_prompt.h.  workspace: new_prompt_workspace's, which a caller
+    keeps (without one, up to 20 MB are zeroed with every call).  Returns {"out" [R_cap, Hq, D],
     "lse" [R_cap, Hq]}; rows of no request are left unwritten."""
     L = load_library()
     _same_device(q, k, v, cu_rows, cu_keys, slopes, workspace, status, what="q")
