@@ -60,12 +60,12 @@ SPEC_API size_t spec_prompt_workspace_bytes(int32_t Hq, int32_t H, int32_t D, in
  * (SPEC_STATUS_BAD_ROWS), are not written; where offsets go back, so that rows lie in two requests, those may hold either's
  * results or be left, and rows of the requests after them may be left too.  Keys and values that no row of their request
  * sees may hold anything; those that one of its rows sees have to be finite, as have
- * the queries (a row of another request never notices).  The scores have to stay within
- * fp32.  Results do not depend on the order in which blocks run; into how many parts a bf16 row's keys are split goes by B, R_cap, K_cap,
+ * the queries (a row of another request never notices).  The scores, times log2(e), have to stay within
+ * fp32, and values below 2^95 (2^24 of them, with weights of up to 2^8, are added up in fp32).  Results do not depend on the order in which blocks run; into how many parts a bf16 row's keys are split goes by B, R_cap, K_cap,
  * the heads, D, the options and the GPU, so that its last bits can be others in a padded or a larger batch.
  * out and lse must not overlap the inputs.
  * bf16: products of bf16 in fp32, weights rounded to bf16 (8 bits) before they meet the values,
- * their sums, and so lse, in fp32.  They run on the tensor cores where q, k and v start on 16 bytes, their
+ * their sums, and so lse, in fp32, as are the sums of values, which lose up to 2^-12 of themselves to truncation.  They run on the tensor cores where q, k and v start on 16 bytes, their
  * strides are positive multiples of 16 bytes, out starts on 16 bytes and Hq / H is at most 128; on the CUDA
  * cores, many times slower, elsewhere, then with weights in fp32.  f32: fp32 throughout.  On the CUDA cores the sums of
  * weights and of values lose at most 2^-17 of their terms' magnitudes to roundings, over any number of keys.
